@@ -1,0 +1,399 @@
+// Device row cache: writing raw token rows into a paged cache (norm, rotation,
+// encoding), reading cache rows back as bf16, and the 8-bit norm that makes
+// indexer keys.  All three stream rows once: they are bound by HBM.
+//
+// One warp per cache row.  Lane l holds the 16-byte units l and 32 + l of the
+// 512 latents (dims 8l .. 8l + 7 and 256 + 8l ..), so every load and store
+// instruction of a warp covers consecutive bytes whatever the format: 16, 8 or
+// 4 bytes a lane for bf16, e4m3 and e2m1.
+#include <cmath>
+
+#include "ess_rows.cuh"
+
+namespace ess {
+namespace {
+
+constexpr int kRowWarps = 8;          // rows in flight per CTA
+
+struct RopeFreq {
+  // turns per position as a binary fraction of 2^64: position * fraction
+  // modulo 2^64 is the angle, exact at any position, with no range reduction
+  unsigned long long f[32];
+};
+
+struct WriteArgs {
+  const uint16_t* kv;
+  long long stride;
+  long long n;
+  const uint16_t* gamma;
+  float eps;
+  const int32_t* pos;      // null: no rotation
+  int halves;
+  const int64_t* slots;
+  uint8_t* rows;
+  long long n_rows;
+  int* status;
+};
+
+template <int FMT>
+__global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
+    const WriteArgs a, const __grid_constant__ RopeFreq fr) {
+  pdl_wait_previous();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long i = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  if (i >= a.n) return;
+  const long long slot = a.slots[i];
+  const uint16_t* x = a.kv + i * a.stride;
+  const uint4* xv = reinterpret_cast<const uint4*>(x);
+  const uint4 u0 = xv[lane], u1 = xv[32 + lane];
+  if (slot < 0) return;
+  if (slot >= a.n_rows) {
+    if (lane == 0) set_status(a.status, ESS_ERR_DEVICE_CHECK);
+    return;
+  }
+  // k^R: lane l turns pair l
+  uint32_t ra, rb;
+  if (a.halves) {
+    ra = x[kLatent + lane];
+    rb = x[kLatent + 32 + lane];
+  } else {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(x + kLatent + 2 * lane);
+    ra = w & 0xffffu;
+    rb = w >> 16;
+  }
+  float y[16];
+  unpack8(u0, y);
+  unpack8(u1, y + 8);
+  if (a.gamma) {
+    SumSq s;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s.add(y[e]);
+    s.warp_reduce<32>();
+    const float r = s.rsqrt_mean(kLatent, a.eps);
+    const uint4* gv = reinterpret_cast<const uint4*>(a.gamma);
+    float g[16];
+    unpack8(gv[lane], g);
+    unpack8(gv[32 + lane], g + 8);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[e] = __fmul_rn(__fmul_rn(y[e], r), g[e]);
+  }
+  if (a.pos) {
+    const unsigned long long turn =
+        static_cast<unsigned long long>(static_cast<long long>(a.pos[i])) * fr.f[lane];
+    // the top 32 bits as a signed fraction of a turn, in half turns
+    const float h = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+    float sn, cs;
+    sincospif(h, &sn, &cs);
+    const float xa = bf16_lo(ra), xb = bf16_lo(rb);
+    ra = bf16_bits(xa * cs - xb * sn);
+    rb = bf16_bits(xa * sn + xb * cs);
+  }
+  uint8_t* row = a.rows + slot * row_bytes_of(FMT);
+  uint16_t* rope;
+  if (FMT == ESS_ROW_BF16) {
+    uint4* o = reinterpret_cast<uint4*>(row);
+    o[lane] = pack8_bf16(y);
+    o[32 + lane] = pack8_bf16(y + 8);
+    rope = reinterpret_cast<uint16_t*>(row + 1024);
+  } else if (FMT == ESS_ROW_COMPACT) {
+    // a tile of 128 dims is 16 lanes of one unit
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float m = group_max<16>(amax8(y + 8 * h));
+      const int e = scale_exp(m, 448.0f);
+      const float inv = exp2i(-e);
+      reinterpret_cast<uint2*>(row)[32 * h + lane] = pack8_e4m3(y + 8 * h, inv);
+      if ((lane & 15) == 0)
+        reinterpret_cast<float*>(row + 512)[2 * h + (lane >> 4)] = exp2i(e);
+    }
+    rope = reinterpret_cast<uint16_t*>(row + 528);
+  } else {
+    // a block of 32 dims is 4 lanes of one unit
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float m = group_max<4>(amax8(y + 8 * h));
+      const int e = min(max(scale_exp(m, 6.0f), kQ4MinExp), kQ4MaxExp);
+      const float inv = exp2i(-e);
+      reinterpret_cast<uint32_t*>(row)[32 * h + lane] = pack8_e2m1(y + 8 * h, inv);
+      if ((lane & 3) == 0) row[256 + 8 * h + (lane >> 2)] = static_cast<uint8_t>(e + 127);
+    }
+    rope = reinterpret_cast<uint16_t*>(row + 272);
+  }
+  if (a.halves) {
+    rope[lane] = static_cast<uint16_t>(ra);
+    rope[32 + lane] = static_cast<uint16_t>(rb);
+  } else {
+    reinterpret_cast<uint32_t*>(rope)[lane] = ra | (rb << 16);
+  }
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kRowWarps * 32) cache_read_kernel(
+    const uint8_t* __restrict__ rows, long long n_rows, const int64_t* __restrict__ slots,
+    long long n, uint16_t* __restrict__ out, int* status) {
+  pdl_wait_previous();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long i = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  if (i >= n) return;
+  const long long slot = slots[i];
+  uint4* o = reinterpret_cast<uint4*>(out + i * kRowDim);
+  if (slot < 0 || slot >= n_rows) {
+    if (slot >= n_rows && lane == 0) set_status(status, ESS_ERR_DEVICE_CHECK);
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    o[lane] = z;
+    o[32 + lane] = z;
+    if (lane < 8) o[64 + lane] = z;
+    return;
+  }
+  const uint8_t* row = rows + slot * row_bytes_of(FMT);
+  constexpr int kRopeOff = row_bytes_of(FMT) - 128;
+  uint4 rope = make_uint4(0u, 0u, 0u, 0u);
+  if (lane < 8) rope = reinterpret_cast<const uint4*>(row + kRopeOff)[lane];
+  if (FMT == ESS_ROW_BF16) {
+    const uint4* s = reinterpret_cast<const uint4*>(row);
+    const uint4 u0 = s[lane], u1 = s[32 + lane];
+    o[lane] = u0;
+    o[32 + lane] = u1;
+  } else if (FMT == ESS_ROW_COMPACT) {
+    const uint2* s = reinterpret_cast<const uint2*>(row);
+    const uint2 c0 = s[lane], c1 = s[32 + lane];
+    const float* sc = reinterpret_cast<const float*>(row + 512);
+    const float s0 = sc[lane >> 4], s1 = sc[2 + (lane >> 4)];
+    o[lane] = widen8_e4m3(c0, s0);
+    o[32 + lane] = widen8_e4m3(c1, s1);
+  } else {
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(row);
+    const uint32_t c0 = s[lane], c1 = s[32 + lane];
+    const int b0 = row[256 + (lane >> 2)], b1 = row[264 + (lane >> 2)];
+    o[lane] = widen8_e2m1(c0, b0);
+    o[32 + lane] = widen8_e2m1(c1, b1);
+  }
+  if (lane < 8) o[64 + lane] = rope;
+}
+
+struct NormArgs {
+  const uint16_t* x;
+  long long x_stride;
+  const uint16_t* res;
+  long long res_stride;
+  const uint16_t* gamma;
+  float eps;
+  long long n;
+  int dim;
+  uint16_t* res_out;
+  uint8_t* codes;
+  float* scales;
+};
+
+// TPR threads hold one row, UNITS 16-byte units (8 values) each: unit u of the
+// row sits in thread u % TPR, so 16 neighbouring lanes hold one group of 128.
+template <int TPR, int UNITS, bool RES>
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const NormArgs a) {
+  constexpr int kThreads = TPR > 256 ? TPR : 256;
+  constexpr int kRows = kThreads / TPR;
+  pdl_wait_previous();
+  pdl_launch_dependents();
+  const int t = threadIdx.x % TPR;
+  const long long i = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / TPR;
+  const bool live = i < a.n;
+  const int units = a.dim >> 3;
+  float h[UNITS][8];
+  SumSq s;
+#pragma unroll
+  for (int u = 0; u < UNITS; ++u) {
+    const int c = u * TPR + t;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u), w = v;
+    if (live && c < units) {
+      v = reinterpret_cast<const uint4*>(a.x + i * a.x_stride)[c];
+      if (RES) w = reinterpret_cast<const uint4*>(a.res + i * a.res_stride)[c];
+    }
+    unpack8(v, h[u]);
+    if (RES) {
+      float r[8];
+      unpack8(w, r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[u][e] += r[e];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < UNITS; ++u) {
+    if (RES) {
+      const int c = u * TPR + t;
+      if (a.res_out && live && c < units)
+        reinterpret_cast<uint4*>(a.res_out + i * a.res_stride)[c] = pack8_bf16(h[u]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s.add(h[u][e]);
+  }
+  s.template warp_reduce<(TPR < 32 ? TPR : 32)>();
+  if (TPR > 32) {
+    __shared__ float2 part[kThreads / 32];
+    const int w = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) part[w] = make_float2(s.hi, s.lo);
+    __syncthreads();
+    const int w0 = (threadIdx.x / TPR) * (TPR / 32);
+    s = SumSq();
+#pragma unroll
+    for (int q = 0; q < TPR / 32; ++q) s.merge(part[w0 + q].x, part[w0 + q].y);
+  }
+  const float r = s.rsqrt_mean(a.dim, a.eps);
+  const int groups = (a.dim + 127) >> 7;
+#pragma unroll
+  for (int u = 0; u < UNITS; ++u) {
+    const int c = u * TPR + t;
+    float y[8], g[8];
+    unpack8(c < units ? reinterpret_cast<const uint4*>(a.gamma)[c] : make_uint4(0u, 0u, 0u, 0u),
+            g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(__fmul_rn(h[u][e], r), g[e]);
+    const float m = group_max<16>(amax8(y));
+    const int e = scale_exp(m, 448.0f);
+    if (live && c < units) {
+      reinterpret_cast<uint2*>(a.codes + i * a.dim)[c] = pack8_e4m3(y, exp2i(-e));
+      if ((c & 15) == 0) a.scales[i * groups + (c >> 4)] = exp2i(e);
+    }
+  }
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <int TPR, int UNITS>
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
+  constexpr int kThreads = TPR > 256 ? TPR : 256;
+  constexpr int kRows = kThreads / TPR;
+  const dim3 grid(static_cast<unsigned>((a.n + kRows - 1) / kRows));
+  return a.res ? launch_pdl(norm_quant_kernel<TPR, UNITS, true>, grid, dim3(kThreads), 0, st, a)
+               : launch_pdl(norm_quant_kernel<TPR, UNITS, false>, grid, dim3(kThreads), 0, st, a);
+}
+
+// rows of one launch: the grid's x extent is a 31-bit number of CTAs
+constexpr long long kMaxRows = 1LL << 33;
+
+}  // namespace
+}  // namespace ess
+
+using namespace ess;
+
+extern "C" {
+
+ess_status ess_row_bytes(int32_t format, int32_t* bytes) {
+  if (!bytes || format < ESS_ROW_BF16 || format > ESS_ROW_Q4) return ESS_ERR_INVALID_ARG;
+  *bytes = row_bytes_of(format);
+  return ESS_OK;
+}
+
+ess_status ess_cache_write(const void* kv, int64_t kv_stride, int64_t n, const void* gamma,
+                           float eps, const double* inv_freq, const int32_t* pos, int32_t pairs,
+                           const int64_t* slots, void* rows, int64_t n_rows, int32_t format,
+                           int32_t* status, ess_stream_t stream) {
+  if (format < ESS_ROW_BF16 || format > ESS_ROW_Q4 || n < 0 || n > kMaxRows || n_rows < 0)
+    return ESS_ERR_INVALID_ARG;
+  if (kv_stride < kRowDim || kv_stride % 8 != 0 || !(eps >= 0.0f)) return ESS_ERR_INVALID_ARG;
+  if (pairs != ESS_ROPE_ADJACENT && pairs != ESS_ROPE_HALVES) return ESS_ERR_INVALID_ARG;
+  RopeFreq fr = {};
+  if (inv_freq) {
+    for (int i = 0; i < 32; ++i) {
+      if (!std::isfinite(inv_freq[i])) return ESS_ERR_INVALID_ARG;
+      // radians -> turns in [0, 1) -> a 64-bit binary fraction
+      const double turns = inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
+      const double part = turns - std::floor(turns);
+      const double hi = std::floor(std::ldexp(part, 32));
+      const double lo = std::ldexp(std::ldexp(part, 32) - hi, 32);
+      fr.f[i] = (static_cast<unsigned long long>(hi) << 32) + static_cast<unsigned long long>(lo);
+    }
+  }
+  if (n == 0) return ESS_OK;
+  if (!kv || !slots || !rows || (inv_freq && !pos) || !aligned16(kv) || !aligned16(rows) ||
+      (gamma && !aligned16(gamma)))
+    return ESS_ERR_INVALID_ARG;
+  WriteArgs a;
+  a.kv = static_cast<const uint16_t*>(kv);
+  a.stride = kv_stride;
+  a.n = n;
+  a.gamma = static_cast<const uint16_t*>(gamma);
+  a.eps = eps;
+  a.pos = inv_freq ? pos : nullptr;
+  a.halves = pairs == ESS_ROPE_HALVES;
+  a.slots = slots;
+  a.rows = static_cast<uint8_t*>(rows);
+  a.n_rows = n_rows;
+  a.status = status;
+  const dim3 grid(static_cast<unsigned>((n + kRowWarps - 1) / kRowWarps));
+  const dim3 block(kRowWarps * 32);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (format == ESS_ROW_BF16)
+    e = launch_pdl(cache_write_kernel<ESS_ROW_BF16>, grid, block, 0, st, a, fr);
+  else if (format == ESS_ROW_COMPACT)
+    e = launch_pdl(cache_write_kernel<ESS_ROW_COMPACT>, grid, block, 0, st, a, fr);
+  else
+    e = launch_pdl(cache_write_kernel<ESS_ROW_Q4>, grid, block, 0, st, a, fr);
+  return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
+}
+
+ess_status ess_cache_read(const void* rows, int64_t n_rows, int32_t format, const int64_t* slots,
+                          int64_t n, void* out, int32_t* status, ess_stream_t stream) {
+  if (format < ESS_ROW_BF16 || format > ESS_ROW_Q4 || n < 0 || n > kMaxRows || n_rows < 0)
+    return ESS_ERR_INVALID_ARG;
+  if (n == 0) return ESS_OK;
+  if (!rows || !slots || !out || !aligned16(rows) || !aligned16(out)) return ESS_ERR_INVALID_ARG;
+  const dim3 grid(static_cast<unsigned>((n + kRowWarps - 1) / kRowWarps));
+  const dim3 block(kRowWarps * 32);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const uint8_t* r = static_cast<const uint8_t*>(rows);
+  uint16_t* o = static_cast<uint16_t*>(out);
+  cudaError_t e;
+  if (format == ESS_ROW_BF16)
+    e = launch_pdl(cache_read_kernel<ESS_ROW_BF16>, grid, block, 0, st, r, n_rows, slots, n, o,
+                   status);
+  else if (format == ESS_ROW_COMPACT)
+    e = launch_pdl(cache_read_kernel<ESS_ROW_COMPACT>, grid, block, 0, st, r, n_rows, slots, n, o,
+                   status);
+  else
+    e = launch_pdl(cache_read_kernel<ESS_ROW_Q4>, grid, block, 0, st, r, n_rows, slots, n, o,
+                   status);
+  return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
+}
+
+ess_status ess_norm_quant(const void* x, int64_t x_stride, const void* residual,
+                          int64_t residual_stride, const void* gamma, float eps, int64_t n,
+                          int32_t dim, void* residual_out, void* codes, float* scales,
+                          ess_stream_t stream) {
+  if (n < 0 || n > kMaxRows || dim < 1 || !(eps >= 0.0f) || x_stride < dim ||
+      (residual && residual_stride < dim) || (residual_out && !residual))
+    return ESS_ERR_INVALID_ARG;
+  if (dim % 8 != 0 || dim > 16384) return ESS_ERR_UNSUPPORTED;
+  if (x_stride % 8 != 0 || (residual && residual_stride % 8 != 0)) return ESS_ERR_INVALID_ARG;
+  if (n == 0) return ESS_OK;
+  if (!x || !gamma || !codes || !scales || !aligned16(x) || !aligned16(gamma) ||
+      !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u) ||
+      (residual && !aligned16(residual)) || (residual_out && !aligned16(residual_out)))
+    return ESS_ERR_INVALID_ARG;
+  NormArgs a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.x_stride = x_stride;
+  a.res = static_cast<const uint16_t*>(residual);
+  a.res_stride = residual_stride;
+  a.gamma = static_cast<const uint16_t*>(gamma);
+  a.eps = eps;
+  a.n = n;
+  a.dim = dim;
+  a.res_out = static_cast<uint16_t*>(residual_out);
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = scales;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dim <= 128) e = launch_norm<16, 1>(a, st);
+  else if (dim <= 256) e = launch_norm<32, 1>(a, st);
+  else if (dim <= 512) e = launch_norm<64, 1>(a, st);
+  else if (dim <= 1024) e = launch_norm<128, 1>(a, st);
+  else if (dim <= 2048) e = launch_norm<128, 2>(a, st);
+  else if (dim <= 4096) e = launch_norm<256, 2>(a, st);
+  else if (dim <= 8192) e = launch_norm<512, 2>(a, st);
+  else e = launch_norm<512, 4>(a, st);
+  return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -27,6 +27,8 @@ ESS_FP8_E4M3 = 0
 ESS_BF16 = 1
 
 ESS_EVICT_LRU, ESS_EVICT_RANDOM, ESS_EVICT_SCORE, ESS_EVICT_LIM = range(4)
+ESS_ROW_BF16, ESS_ROW_COMPACT, ESS_ROW_Q4 = range(3)
+ESS_ROPE_ADJACENT, ESS_ROPE_HALVES = range(2)
 ESS_MISS_FUSED = 0
 ESS_MISS_STAGED = 1
 
@@ -42,7 +44,8 @@ EXPORTS = (
     "ess_pipeline_step", "ess_pool_get_state", "ess_pool_set_state", "ess_pool_get_rows",
     "ess_pool_read_stats", "ess_pool_poll", "ess_pool_kernel_launches", "ess_prefill_plan",
     "ess_compact_rows", "ess_replay_misses", "ess_host_gather", "ess_pool_set_eviction",
-    "ess_pool_bind_layer_compact", "ess_prefill_run",
+    "ess_pool_bind_layer_compact", "ess_prefill_run", "ess_row_bytes", "ess_cache_write",
+    "ess_cache_read", "ess_cache_mla_bytes", "ess_cache_mla", "ess_norm_quant",
 )
 
 # void (*)(void* user, int32_t layer, void* buffer, void* stream)
@@ -87,6 +90,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     P = ctypes.c_void_p
     I = ctypes.c_int
+    L = ctypes.c_int64
+    F = ctypes.c_float
     lib.ess_status_string.restype = ctypes.c_char_p
     lib.ess_status_string.argtypes = [I]
     sigs = {
@@ -122,6 +127,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "ess_pool_bind_layer_compact": [P, I, P, P, P, P, P],
         "ess_prefill_run": [I, P, I, I, P, ctypes.c_size_t, ctypes.c_size_t, ctypes.c_size_t, P,
                             PREFILL_COMPUTE_FN, P, P, P, P],
+        "ess_row_bytes": [I, ctypes.POINTER(ctypes.c_int32)],
+        "ess_cache_write": [P, L, L, P, F, P, P, I, P, P, L, I, P, P],
+        "ess_cache_read": [P, L, I, P, L, P, P, P],
+        "ess_cache_mla_bytes": [I, I, I, ctypes.POINTER(ctypes.c_size_t)],
+        "ess_cache_mla": [P, P, L, I, P, I, I, P, I, I, I, P, I, F, P, P, P, ctypes.c_size_t, P,
+                          P],
+        "ess_norm_quant": [P, L, P, L, P, F, L, I, P, P, P, P],
     }
     for name, args in sigs.items():
         f = getattr(lib, name)
@@ -410,3 +422,45 @@ def ess_prefill_run(onload_layer_map, host_kv, layer_bytes: int, buffers, comput
                                  int(layer_bytes), int(wb_offset), int(wb), bf, cb, None,
                                  _stream(compute_stream), _stream(h2d_stream),
                                  _stream(d2h_stream)), "ess_prefill_run")
+
+
+def ess_row_bytes(fmt: int) -> int:
+    n = ctypes.c_int32(0)
+    check(load().ess_row_bytes(int(fmt), ctypes.byref(n)), "ess_row_bytes")
+    return n.value
+
+
+def ess_cache_write(kv, kv_stride: int, n: int, gamma, eps: float, inv_freq, pos, pairs: int,
+                    slots, rows, n_rows: int, fmt: int, status=None, stream=None) -> None:
+    """inv_freq: a (ctypes.c_double * 32) array of radians per position, or None."""
+    check(load().ess_cache_write(_p(kv), kv_stride, n, _p(gamma), eps, inv_freq, _p(pos), pairs,
+                                 _p(slots), _p(rows), n_rows, fmt, _p(status), _stream(stream)),
+          "ess_cache_write")
+
+
+def ess_cache_read(rows, n_rows: int, fmt: int, slots, n: int, out, status=None,
+                   stream=None) -> None:
+    check(load().ess_cache_read(_p(rows), n_rows, fmt, _p(slots), n, _p(out), _p(status),
+                                _stream(stream)), "ess_cache_read")
+
+
+def ess_cache_mla_bytes(batch: int, ways: int, heads: int) -> int:
+    n = ctypes.c_size_t(0)
+    check(load().ess_cache_mla_bytes(batch, ways, heads, ctypes.byref(n)), "ess_cache_mla_bytes")
+    return n.value
+
+
+def ess_cache_mla(q, rows, n_rows: int, fmt: int, page_table, max_pages: int, page: int, T,
+                  batch: int, ways: int, heads: int, tokens, k: int, sm_scale: float, out, lse,
+                  workspace, ws_bytes: int, status=None, stream=None) -> None:
+    check(load().ess_cache_mla(_p(q), _p(rows), n_rows, fmt, _p(page_table), max_pages, page,
+                               _p(T), batch, ways, heads, _p(tokens), k, sm_scale, _p(out),
+                               _p(lse), _p(workspace), ws_bytes, _p(status), _stream(stream)),
+          "ess_cache_mla")
+
+
+def ess_norm_quant(x, x_stride: int, residual, residual_stride: int, gamma, eps: float, n: int,
+                   dim: int, residual_out, codes, scales, stream=None) -> None:
+    check(load().ess_norm_quant(_p(x), x_stride, _p(residual), residual_stride, _p(gamma), eps, n,
+                                dim, _p(residual_out), _p(codes), _p(scales), _stream(stream)),
+          "ess_norm_quant")

@@ -505,6 +505,142 @@ ess_status ess_prefill_run(int32_t n_layers, const int32_t* onload_layer_map, in
                            ess_stream_t compute_stream, ess_stream_t h2d_stream,
                            ess_stream_t d2h_stream);
 
+/* ---------------------------------------------------------------------------
+ * Device row cache: latent rows that stay on the GPU, in one of three formats,
+ * behind a page table, with the calls that fill, read and attend to them.  A
+ * row is c^KV[512] + k^R[64] as in the host copy.  These calls need no pool:
+ * every buffer is the caller's, each call is asynchronous on stream on the
+ * current device, allocates nothing and may be captured into a graph.
+ *
+ * ESS_ROW_BF16     1152 bytes: the 576 values (the rows of ess_append).
+ * ESS_ROW_COMPACT   656 bytes: the format of ess_compact_rows.
+ * ESS_ROW_Q4        400 bytes: bytes 0..255 the 512 latent values as e2m1
+ *                   codes, value 2i in the low half of byte i; bytes 256..271
+ *                   one exponent byte for each block of 32 values, the
+ *                   block's scale being 2^(byte - 127); bytes 272..399 the 64
+ *                   RoPE values as bf16.  A block's scale is the smallest
+ *                   power of two at or above fl32(amax / 6) (1 for an
+ *                   all-zero block), its exponent kept within -23..13 so that
+ *                   every value is exact in fp16 as in bf16; a value's code
+ *                   is e2m1(x / scale), nearest with ties to the even code,
+ *                   saturating at +-6.  The format has no infinity and no
+ *                   NaN: an infinity saturates and a NaN becomes 6 * scale.
+ *                   Exponent bytes outside 104..140 are read as the nearest
+ *                   of the two.
+ *
+ * status is a device int32, or NULL: the first device-side error of the calls
+ * that share it is put there when it holds ESS_OK; the caller clears it. */
+enum { ESS_ROW_BF16 = 0, ESS_ROW_COMPACT = 1, ESS_ROW_Q4 = 2 };
+
+/* Bytes of one row of a format (a multiple of 16).
+ * Errors: ESS_ERR_INVALID_ARG for an unknown format. */
+ess_status ess_row_bytes(int32_t format, int32_t* bytes);
+
+/* Which of the 64 RoPE values turn together: (2i, 2i + 1) or (i, i + 32). */
+enum { ESS_ROPE_ADJACENT = 0, ESS_ROPE_HALVES = 1 };
+
+/* Append token rows to a device row cache, normalised and rotated on the way.
+ *   kv        device bf16, n rows of 576 values, kv_stride elements apart
+ *             (>= 576, a multiple of 8), 16-byte aligned: the projection's
+ *             c^KV before its norm, then k^R before its rotation
+ *   gamma     device bf16 [512], 16-byte aligned: y = x * r * gamma with
+ *             r = 1 / sqrt(mean(x^2) + eps) over the 512; NULL: y = x
+ *   inv_freq  host double [32], radians per position of each of the 32
+ *             pairs, read before the call returns: pair i turns by
+ *             pos * inv_freq[i] (kept to 2^-32 of a turn at any position);
+ *             NULL: k^R as it is (pos is then ignored and may be NULL)
+ *   pos       device int32 [n]
+ *   pairs     ESS_ROPE_ADJACENT or ESS_ROPE_HALVES
+ *   slots     device int64 [n]: the cache row of each token (page * page size
+ *             + offset), or negative for a token that is not written
+ *   rows      device [n_rows][row bytes of format], 16-byte aligned
+ * Rows that no token names are left as they were.  The slots of one call are
+ * distinct; of a row named twice the bytes of either token may stay.  y and
+ * the rotated k^R are formed in fp32 (the mean to about 48 bits) and rounded
+ * once, to the row's format.  A slot at or past n_rows writes nothing and
+ * reports ESS_ERR_DEVICE_CHECK in status.  n = 0 launches nothing.
+ * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or negative argument, an
+ * unknown format or pairs, a frequency that is not finite, or eps < 0. */
+ess_status ess_cache_write(const void* kv, int64_t kv_stride, int64_t n, const void* gamma,
+                           float eps, const double* inv_freq, const int32_t* pos, int32_t pairs,
+                           const int64_t* slots, void* rows, int64_t n_rows, int32_t format,
+                           int32_t* status, ess_stream_t stream);
+
+/* Rows of a device row cache as bf16 rows, exactly (the prefix of a chunked
+ * prompt, or a check of what the cache holds).
+ *   slots  device int64 [n]: the cache row of each output row; a negative one
+ *          gives a row of zeros, one at or past n_rows too, with
+ *          ESS_ERR_DEVICE_CHECK in status
+ *   out    device bf16 [n][576], 16-byte aligned
+ * Errors: as ess_cache_write. */
+ess_status ess_cache_read(const void* rows, int64_t n_rows, int32_t format, const int64_t* slots,
+                          int64_t n, void* out, int32_t* status, ess_stream_t stream);
+
+/* Bytes of device workspace that ess_cache_mla needs for batch requests of
+ * ways queries x heads.  Errors: as ess_cache_mla for these three. */
+ess_status ess_cache_mla_bytes(int32_t batch, int32_t ways, int32_t heads, size_t* bytes);
+
+/* Absorbed-MLA attention over a device row cache: every token of a request
+ * (the layer without an indexer, or a context no longer than k), or the
+ * tokens that ess_select_manage / ess_indexer_topk selected.
+ *   q          device bf16 [batch][ways][heads][576], 16-byte aligned
+ *   rows       device [n_rows][400], 16-byte aligned; format ESS_ROW_Q4
+ *   page_table device int32 [batch][max_pages]: token t of request b is row
+ *              page_table[b][t / page] * page + t % page.  Entries past the
+ *              last token are not read.
+ *   T          device int32 [batch]: tokens of each request, the `ways` newest
+ *              included, 0 <= T <= max_pages * page
+ *   tokens     NULL: way m attends to the tokens t < T_b - (ways - 1) + m, so
+ *              the newest tokens attend causally to one another.  Otherwise
+ *              device int32 [batch][ways][k]: way m attends to its first
+ *              min(k, T_b) entries, whatever their order; a negative entry is
+ *              no token.
+ *   out        device bf16 [batch][ways][heads][512], 16-byte aligned:
+ *              softmax(sm_scale * q . row) @ row[:512]
+ *   lse        device float [batch][ways][heads], or NULL: the natural
+ *              logarithm of the softmax's sum (to join it with attention over
+ *              other tokens)
+ *   workspace  device, 256-byte aligned, at least ess_cache_mla_bytes; calls
+ *              that share one are ordered by the caller
+ * A query that attends to nothing gets zeros and lse = -infinity.  Scores,
+ * softmax and sums are fp32; the softmax numerators go into the second product
+ * as fp16 (11 bits), beside the latents, which fp16 holds exactly.
+ * A length outside its range, a token at or past T_b and a page outside the
+ * cache report ESS_ERR_DEVICE_CHECK in status; such a token is left out.
+ * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or non-positive
+ * argument; ESS_ERR_UNSUPPORTED for more than 4 ways or 128 heads, another
+ * format, or more than 2^31 - 1 rows or tokens of a request; ESS_ERR_OOM for
+ * a workspace that is too small. */
+ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_t format,
+                         const int32_t* page_table, int32_t max_pages, int32_t page,
+                         const int32_t* T, int32_t batch, int32_t ways, int32_t heads,
+                         const int32_t* tokens, int32_t k, float sm_scale, void* out, float* lse,
+                         void* workspace, size_t ws_bytes, int32_t* status, ess_stream_t stream);
+
+/* Root-mean-square norm with the residual's addition and e4m3 output.
+ *   x             device bf16, n rows of dim values, x_stride elements apart
+ *   residual      device bf16, n rows, residual_stride apart, or NULL
+ *   gamma         device bf16 [dim]
+ *   residual_out  device bf16, residual_stride apart: bf16(x + residual); it
+ *                 may be x or residual itself.  NULL: not stored
+ *   codes         device [n][dim] e4m3
+ *   scales        device float [n][ceil(dim / 128)]
+ * h = x + residual in fp32; y = h * r * gamma with r = 1 / sqrt(mean(h^2) +
+ * eps), the mean to about 48 bits; each 128 values (the last group may be
+ * shorter) get the scale of ess_compact_rows, the smallest power of two at or
+ * above fl32(amax / 448) (1 for zeros, at least 2^-126), and the codes
+ * e4m3(y / scale).  With dim = 128 a row is an indexer key with its key scale:
+ * codes and scales are ess_append's key_row and key_scale, or rows of the bound
+ * idx_keys and idx_scale for a prompt.
+ * n = 0 launches nothing.  Pointers and strides are 16-byte aligned (scales
+ * 4-byte).  Errors: ESS_ERR_INVALID_ARG for a null, misaligned or negative
+ * argument, a stride below dim, residual_out without residual, or eps < 0;
+ * ESS_ERR_UNSUPPORTED when dim is not a multiple of 8 in 8..16384. */
+ess_status ess_norm_quant(const void* x, int64_t x_stride, const void* residual,
+                          int64_t residual_stride, const void* gamma, float eps, int64_t n,
+                          int32_t dim, void* residual_out, void* codes, float* scales,
+                          ess_stream_t stream);
+
 /* Synchronise stream, return the first device-side error since the last
  * poll (ESS_OK if none) and clear it. */
 ess_status ess_pool_poll(ess_pool* pool, ess_stream_t stream);

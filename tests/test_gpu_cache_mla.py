@@ -1,0 +1,288 @@
+"""Attention over the 4-bit device row cache against float64.
+
+The tolerance follows from the kernel's roundings.  A score is an fp32 sum of
+576 exact products: off by at most 576 * 2^-24 of the sum of their magnitudes
+(dz, after the scale, in nats), so a weight is off by dz relative, the weights'
+sum too, and the fp16 numerator by 2^-11 more (values under 2^-14 of the row's
+largest by 2^-25 of it).  With A = sum p |v| / sum p an output is off by at most
+(2 dz + 2^-11 + 2^-18) A, and its bf16 rounding by 2^-8 of itself.  The 2^-18
+covers the exponential's own error and fp32 sums.
+"""
+import numpy as np
+import pytest
+import torch
+
+from host_latent_cache_gb300 import ess
+from oracle import row_cache as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from host_latent_cache_gb300 import build as B
+    B.build()
+    assert torch.cuda.is_available()
+    ess.load()
+
+
+class Case:
+    """A cache of random 4-bit rows behind a shuffled page table, with queries."""
+
+    def __init__(self, seed, lens, ways, heads, page=64, max_pages=None, extra=3, qscale=0.5):
+        from host_latent_cache_gb300 import rows
+        rng = np.random.default_rng(seed)
+        self.lens, self.ways, self.heads, self.page = list(lens), ways, heads, page
+        self.batch = len(self.lens)
+        per = max_pages or max(1, -(-max(self.lens) // page))
+        n_pages = self.batch * per + extra
+        y = rng.normal(size=(n_pages * page, 512)) * (0.5 + rng.random(512))
+        packed, exps = R.q4_encode(y)
+        rope = torch.from_numpy(rng.normal(size=(n_pages * page, 64)).astype(np.float32)).to(torch.bfloat16)
+        self.raw = np.concatenate([packed, exps, rope.view(torch.uint8).numpy()], axis=1)
+        self.table = rng.permutation(n_pages)[: self.batch * per].reshape(self.batch, per).astype(np.int32)
+        q = torch.from_numpy((qscale * rng.normal(size=(self.batch, ways, heads, 576))).astype(np.float32))
+        self.q = q.to(torch.bfloat16).cuda()
+        self.scale = 1.0 / 24.0
+        self.rng = rng
+        self.cache = rows.RowCache(torch.from_numpy(self.raw).cuda(), "q4", page=page)
+        self.T = torch.tensor(self.lens, dtype=torch.int32, device="cuda")
+        self.dev_table = torch.from_numpy(self.table).cuda()
+
+    def attend(self, tokens=None, **kw):
+        tok = None if tokens is None else torch.from_numpy(tokens).cuda()
+        return self.cache.attend(self.q, self.dev_table, self.T, self.scale, tokens=tok, **kw)
+
+    def rows_of(self, b, t):
+        return R.row_values(self.raw[self.table[b, t // self.page].astype(np.int64) * self.page
+                                     + t % self.page], "q4")
+
+    def check(self, out, lse, tokens=None, skip=()):
+        out, lse = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+        q = self.q.float().cpu().numpy().astype(np.float64)
+        for b, T in enumerate(self.lens):
+            for m in range(self.ways):
+                if tokens is None:
+                    t = np.arange(max(0, T - (self.ways - 1) + m))
+                else:
+                    t = tokens[b, m][: min(tokens.shape[2], T)].astype(np.int64)
+                    t = t[(t >= 0) & (t < T)]
+                t = np.array([x for x in t if (b, int(x)) not in skip], dtype=np.int64) if skip else t
+                got, gl = out[b, m], lse[b, m]
+                if t.size == 0:
+                    assert (got == 0).all() and (gl == -np.inf).all(), (b, m)
+                    continue
+                k = self.rows_of(b, t)
+                want, wl, size = R.attention(q[b, m], k, self.scale, np.ones((self.heads, t.size), bool))
+                dz = (576 * 2.0 ** -24) * (np.abs(q[b, m]) @ np.abs(k).T).max(axis=1) * self.scale
+                tol = (2 * dz[:, None] + 2.0 ** -11 + 2.0 ** -18) * size + 2.0 ** -8 * np.abs(want)
+                err = np.abs(got - want)
+                assert (err <= tol).all(), (b, m, float((err / tol).max()))
+                assert (np.abs(gl - wl) <= dz + 2.0 ** -20 * (1 + np.abs(wl))).all(), (b, m)
+
+
+@pytest.mark.parametrize("lens,ways,heads", [
+    ([1], 1, 1), ([2], 1, 16), ([127, 128, 129], 1, 128), ([4096], 1, 16), ([0, 1, 63, 700], 1, 20),
+    ([5, 0, 1, 1000], 4, 128), ([64, 65], 2, 64), ([300, 2, 257], 3, 33), ([2500, 31, 640], 1, 96),
+    ([1, 1, 1, 1, 1], 2, 7), ([3000] * 7, 1, 128), ([20000], 1, 128),
+], ids=lambda v: str(v).replace(" ", "")[:24])
+def test_dense(lens, ways, heads):
+    c = Case(sum(lens) + heads, lens, ways, heads)
+    out, lse = c.attend()
+    assert c.cache.poll() == ess.ESS_OK
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("page", [1, 7, 16, 100, 256])
+def test_page_sizes(page):
+    c = Case(page, [513, 130, 3], 2, 24, page=page)
+    out, lse = c.attend()
+    assert c.cache.poll() == ess.ESS_OK
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("lens,ways,heads,k", [
+    ([1000, 3, 0], 1, 128, 256), ([4000, 2000], 2, 16, 512), ([5000], 4, 128, 2048), ([40], 1, 8, 64),
+    ([300, 300], 1, 128, 1),
+], ids=lambda v: str(v).replace(" ", "")[:24])
+def test_listed_tokens(lens, ways, heads, k):
+    c = Case(k, lens, ways, heads)
+    tok = np.full((len(lens), ways, k), 12345678, dtype=np.int32)   # entries past min(k, T) are not read
+    for b, T in enumerate(lens):
+        for m in range(ways):
+            n = min(k, T)
+            tok[b, m, :n] = c.rng.permutation(T)[:n]
+            if n > 4:
+                tok[b, m, c.rng.integers(0, n, n // 4)] = -1        # holes anywhere
+    if lens[0] == 1000:
+        tok[0, 0, :256] = -7                                        # a list that holds nothing
+    out, lse = c.attend(tok)
+    assert c.cache.poll() == ess.ESS_OK
+    c.check(out, lse, tok)
+
+
+def test_a_listed_token_counts_as_often_as_it_is_listed():
+    c = Case(5, [10], 1, 4)
+    tok = np.array([[[3, 3, 3, 5]]], dtype=np.int32)
+    out, lse = c.attend(tok)
+    c.check(out, lse, tok)
+
+
+def test_peaked_and_rising_scores():
+    """Running maxima that keep growing along the tokens, and single tokens that take it all."""
+    c = Case(8, [3000], 1, 64, qscale=6.0)
+    k = c.rows_of(0, np.arange(3000))
+    q = c.q.float().cpu().numpy()
+    order = np.argsort(k @ q[0, 0, 0])                  # ascending scores of head 0
+    tok = order.astype(np.int32).reshape(1, 1, -1)
+    for t in (tok, tok[:, :, ::-1].copy()):
+        out, lse = c.attend(t)
+        c.check(out, lse, t)
+
+
+def test_what_lies_behind_the_last_token_does_not_matter():
+    c = Case(9, [70, 129], 2, 16, max_pages=5)
+    want = c.attend()
+    rows = c.cache.rows.clone()
+    used = torch.zeros(rows.shape[0], dtype=torch.bool, device="cuda")
+    for b, T in enumerate(c.lens):
+        t = np.arange(T)
+        used[torch.from_numpy(c.table[b, t // 64].astype(np.int64) * 64 + t % 64).cuda()] = True
+    rows[~used] = 0xFF                                  # NaN in k^R, the largest codes and exponents
+    from host_latent_cache_gb300.rows import RowCache
+    table = c.dev_table.clone()
+    table[0, 2:] = 1 << 30                              # pages past the last token are not read
+    table[1, 3:] = -9
+    cache = RowCache(rows, "q4")
+    got = cache.attend(c.q, table, c.T, c.scale)
+    assert cache.poll() == ess.ESS_OK
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_infinite_and_nan_queries_stay_in_their_row():
+    c = Case(10, [200, 200], 1, 16)
+    want, _ = c.attend()
+    c.q[0, 0, 3, 5] = float("nan")
+    c.q[1, 0, 15, 0] = float("inf")
+    out, lse = c.attend()
+    bad = torch.zeros(2, 1, 16, dtype=torch.bool, device="cuda")
+    bad[0, 0, 3] = bad[1, 0, 15] = True
+    assert torch.equal(out[~bad], want[~bad])
+    assert torch.isnan(out[bad]).all()
+
+
+def test_device_checks():
+    c = Case(11, [100, 200], 1, 8)
+    tok = np.full((2, 1, 50), -1, dtype=np.int32)
+    tok[0, 0, :3] = [5, 100, 7]                          # 100 is past the request's last token
+    tok[1, 0, :2] = [199, 0]
+    out, lse = c.attend(tok)
+    assert c.cache.poll() == ess.ESS_ERR_DEVICE_CHECK
+    c.check(out, lse, tok)
+    c.dev_table[1, 1] = 1 << 30                          # a page outside the cache: its tokens are left out
+    out, lse = c.attend()
+    assert c.cache.poll() == ess.ESS_ERR_DEVICE_CHECK
+    c.check(out, lse, skip={(1, t) for t in range(64, 128)})
+    c.dev_table[1, 1] = int(c.table[1, 1])
+    for bad, as_if in ((-3, 0), (1 << 20, 256)):         # a length outside its range is clamped
+        c.T[1] = bad
+        c.lens[1] = as_if
+        out, lse = c.attend()
+        assert c.cache.poll() == ess.ESS_ERR_DEVICE_CHECK
+        c.check(out, lse)
+
+
+def test_runs_are_the_same_and_a_workspace_may_be_dirty():
+    c = Case(12, [5000, 17, 900], 2, 128)
+    ws = c.cache.workspace(3, 2, 128)
+    ws.fill_(0xFF)
+    a = c.attend(workspace=ws)
+    b = c.attend()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_captured_calls_follow_the_lengths():
+    c = Case(13, [700, 300], 1, 128, max_pages=12)
+    out = torch.empty(2, 1, 128, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(2, 1, 128, device="cuda")
+    ws = c.cache.workspace(2, 1, 128)
+    c.attend(out=out, lse=lse, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.attend(out=out, lse=lse, workspace=ws)
+    for lens in ([700, 300], [1, 768], [0, 0], [64, 640]):
+        c.lens = lens
+        c.T.copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check(out, lse)
+    assert c.cache.poll() == ess.ESS_OK
+
+
+def test_two_streams_beside_one_another():
+    a, b = Case(14, [6000] * 3, 1, 128), Case(15, [4000] * 4, 2, 64)
+    want = a.attend(), b.attend()
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(sa):
+            ga = a.attend()
+        with torch.cuda.stream(sb):
+            gb = b.attend()
+    torch.cuda.synchronize()
+    for g, w in zip((ga, gb), want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+def test_arguments_are_refused():
+    c = Case(16, [50], 1, 4)
+    ok = dict(q=c.q, page_table=c.dev_table, T=c.T, sm_scale=c.scale)
+    for change in (dict(q=c.q.float()), dict(q=c.q[..., :575]), dict(q=c.q.cpu()),
+                   dict(T=c.T.long()), dict(T=c.T.repeat(2)), dict(page_table=c.dev_table.long()),
+                   dict(page_table=c.dev_table[0]), dict(tokens=c.T), dict(out=c.q),
+                   dict(q=c.q.transpose(1, 2).expand(1, 4, 3, 576))):
+        with pytest.raises(ValueError):
+            c.cache.attend(**{**ok, **change})
+    for change in (dict(sm_scale=0.0), dict(sm_scale=float("nan")), dict(q=c.q.expand(1, 1, 4, 576).repeat(1, 5, 1, 1)),
+                   dict(workspace=c.cache.workspace(1, 1, 4)[:0])):
+        with pytest.raises(ess.EssError):
+            c.cache.attend(**{**ok, **change})
+    from host_latent_cache_gb300.rows import RowCache
+    with pytest.raises(ess.EssError):
+        RowCache(torch.zeros(64, 656, dtype=torch.uint8, device="cuda"), "compact").attend(**ok)
+
+
+def test_written_rows_are_attended_and_read():
+    """Prompt rows and then a decode step's rows into the cache, attention over
+    all of them, and the rows read back: as a server runs them."""
+    from host_latent_cache_gb300.rows import RowCache
+    g = torch.Generator(device="cuda").manual_seed(17)
+    page, lens = 64, [130, 257]
+    table = torch.tensor([[4, 0, 7, 9, 11], [1, 8, 2, 3, 5]], dtype=torch.int32, device="cuda")
+    cache = RowCache(torch.zeros(12 * page, 400, dtype=torch.uint8, device="cuda"), "q4", page=page)
+    gamma = torch.ones(512, dtype=torch.bfloat16, device="cuda")
+    freq = [10000.0 ** (-i / 32.0) for i in range(32)]
+
+    def put(b, t0, n):
+        t = torch.arange(t0, t0 + n, device="cuda")
+        slots = table[b, t // page].long() * page + t % page
+        kv = torch.randn(n, 576, generator=g, device="cuda").to(torch.bfloat16)
+        cache.write(kv, slots, gamma=gamma, pos=t.int(), inv_freq=freq)
+        return slots
+    slots = [put(b, 0, n) for b, n in enumerate(lens)]
+    for step in range(3):
+        for b in range(2):
+            slots[b] = torch.cat([slots[b], put(b, lens[b] + step, 1)])
+        T = torch.tensor([n + step + 1 for n in lens], dtype=torch.int32, device="cuda")
+        q = torch.randn(2, 1, 32, 576, generator=g, device="cuda").to(torch.bfloat16)
+        out, lse = cache.attend(q, table, T, 1 / 24.0)
+        for b in range(2):
+            k = cache.read(slots[b]).double()
+            z = q[b, 0].double() @ k.T / 24.0
+            want = torch.softmax(z, 1) @ k[:, :512]
+            size = torch.softmax(z, 1) @ k[:, :512].abs()
+            dz = 576 * 2.0 ** -24 * (q[b, 0].double().abs() @ k.abs().T).amax(1, keepdim=True) / 24
+            tol = (2 * dz + 2.0 ** -11 + 2.0 ** -18) * size + 2.0 ** -8 * want.abs()
+            assert ((out[b, 0].double() - want).abs() <= tol).all()
+            assert ((lse[b, 0].double() - torch.logsumexp(z, 1)).abs() <= dz[:, 0] + 2.0 ** -16).all()
+    assert cache.poll() == ess.ESS_OK
