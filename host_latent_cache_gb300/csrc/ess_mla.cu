@@ -1,11 +1,32 @@
 // Absorbed-MLA attention over a device row cache held in 4 bits.
 //
 // For every query row (b, m, h): softmax_t(sm_scale * q . row_t) @ row_t[:512]
-// over the tokens of request b that way m sees, in one pass with the running
+// over the tokens of request b that way m sees, in one pass with a running
 // maximum and sum.
 //
-// One warp per query row, eight heads of one (request, way) per CTA: a tile of
-// 32 tokens is widened to fp32 in shared memory and shared by the eight warps.
+// With 128 heads a cached token costs 278 kflop and 400 bytes, so the tensor
+// cores bound it.  A pair of CTAs (cta_group::2) shares one tile of 128 tokens
+// and 128 query rows, 64 rows a CTA: the pair form with M = 128 keeps each
+// CTA's O[64][512] in 256 TMEM columns (lanes 64..127 hold the second half of
+// the columns), which leaves room for two score buffers, where one CTA with
+// 128 rows would fill TMEM with O alone.  Both products run at the full rate
+// of N = 256 (PV) and 70 % of it at N = 128 (QK), as measured.
+//
+//   S[128 rows][128 tokens] = Q K^T   bf16: each CTA widens its 64 tokens of K
+//   O[128 rows][512]       += P V     fp16: each CTA widens its 256 dims of V
+//
+// The rows' 4-bit codes are widened exactly: to bf16 beside the bf16 queries,
+// to fp16 beside P, which so keeps 11 bits.  Eight warps gather and widen
+// (raw rows of the next phase are in registers before this phase's buffer is
+// free), four run the softmax (thread = row and half of the tile's tokens),
+// one thread of the even CTA issues the MMAs: QK of tile i + 1, then PV of
+// tile i, so the softmax of a tile and the widening of the next run beside
+// them.  O is rescaled only when a row's maximum grows by more than 2^8.
+//
+// All tiles of all requests are dealt evenly to the pairs (lengths are read on
+// the device, so captured calls follow them); a request cut by a boundary
+// leaves fp32 partials, which a second kernel joins.
+#include <algorithm>
 #include <cmath>
 
 #include "ess_rows.cuh"
@@ -13,110 +34,709 @@
 namespace ess {
 namespace {
 
-constexpr int kTile = 32;
-constexpr int kHeadsPerCta = 8;
 constexpr int kMaxCacheWays = 4;
 constexpr int kMaxCacheHeads = 128;
+constexpr int kMt = 128;              // tokens per tile
+constexpr int kPairRows = 128;        // query rows per pair
+constexpr int kCtaRows = 64;          // of them per CTA
+constexpr int kMaxPairs = 76;         // one pair per two SMs
+
+constexpr int kSoftWarps = 4;
+constexpr int kMmaWarp = 4;
+constexpr int kWidenWarp0 = 5;
+constexpr int kWidenWarps = 8;
+constexpr int kMlaThreads = (kWidenWarp0 + kWidenWarps) * 32;
+
+constexpr uint32_t kKBlk = 8192;      // [64 rows][64 dims], 128-byte swizzled
+constexpr uint32_t kVBlk = 16384;     // [128 tokens][64 dims]
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffK = 9 * kKBlk;
+constexpr uint32_t kOffV = kOffK + 9 * kKBlk;
+constexpr uint32_t kOffP = kOffV + 4 * kVBlk;
+constexpr uint32_t kOffMisc = kOffP + 2 * kKBlk;
+
+constexpr uint32_t kColO = 0;         // TMEM columns: O, then two score buffers
+constexpr uint32_t kColS = 256;
+constexpr float kGrow = 8.0f;         // log2 of the growth of a maximum that O absorbs unscaled
+
+struct Misc {
+  uint64_t q_full, q_ready, q_free, k_full, v_full, p_full, qk_done[2], pv_done;
+  uint32_t tmem;
+  int abort;
+  int start_v;
+  int pad;
+  long long start_off, lo, hi;
+  long long scan[16];
+  uint32_t mask[2][4];                // tokens of a tile that exist
+  int32_t row[2][kMt];                // cache rows of a tile's tokens, -1: none
+  float xch[2][kMt];                  // row statistics of a thread for its partner
+};
+constexpr uint32_t kMlaSmem = 232448;
+static_assert(kOffMisc + sizeof(Misc) <= kMlaSmem, "shared memory of one CTA");
 
 struct MlaArgs {
-  const uint16_t* q;
   const uint8_t* rows;
-  long long n_rows;
+  int n_rows;
   const int32_t* page_table;
   int max_pages, page;
   const int32_t* T;
   int batch, ways, heads;
   const int32_t* tokens;
   int k;
+  int entries;             // dense: requests; listed: (request, way)
+  int row_tiles;           // pairs' row tiles per entry
+  int entry_rows;          // query rows per entry
   float c2;                // sm_scale * log2(e)
   uint16_t* out;
   float* lse;
+  int2* span;              // [entries][row_tiles]: first pair * 2 + slot, last pair
+  float* part_o;           // [pairs][2][128][512]
+  float2* part_ml;         // [pairs][2][128]
   int* status;
 };
 
-__global__ void __launch_bounds__(kHeadsPerCta * 32) cache_mla_kernel(const MlaArgs a) {
-  extern __shared__ float tile[];   // [kTile][576]
-  __shared__ int live[kTile];
-  pdl_wait_previous();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int m = blockIdx.y, b = blockIdx.z;
-  const int h = blockIdx.x * kHeadsPerCta + warp;
+__device__ __forceinline__ int request_len(const MlaArgs& a, int b) {
   const long long cap = static_cast<long long>(a.max_pages) * a.page;
-  int Tb = a.T[b];
-  if (Tb < 0 || Tb > cap) {
-    if (threadIdx.x == 0) set_status(a.status, ESS_ERR_DEVICE_CHECK);
-    Tb = Tb < 0 ? 0 : static_cast<int>(cap);
+  const int T = a.T[b];
+  return T < 0 ? 0 : (T > cap ? static_cast<int>(cap) : T);
+}
+__device__ __forceinline__ int entry_len(const MlaArgs& a, int v) {
+  return a.tokens ? min(a.k, request_len(a, v / a.ways)) : request_len(a, v);
+}
+
+// ---------------------------------------------------------------- pair PTX
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
+               "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrive on the barrier at this offset in both CTAs when all prior MMAs are done
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait.  When it gives up (or another warp has) the role goes on
+// without waiting, so that every block-wide barrier is still reached; the
+// results are garbage and status says so.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Misc* mi,
+                                              int* status) {
+  const uint32_t addr = smem_u32(bar);
+  if (mbar_try_wait_cluster(addr, parity)) return true;
+  volatile int* stop = &mi->abort;
+  const long long t0 = clock64();
+  while (!*stop) {
+    if (mbar_try_wait_cluster(addr, parity)) return true;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      set_status(status, ESS_ERR_TIMEOUT);
+      *stop = 1;
+    }
   }
-  const int32_t* list =
-      a.tokens ? a.tokens + (static_cast<size_t>(b) * a.ways + m) * a.k : nullptr;
-  const int n = list ? min(a.k, Tb) : max(0, Tb - (a.ways - 1) + m);
-  const size_t qrow = (static_cast<size_t>(b) * a.ways + m) * a.heads + min(h, a.heads - 1);
-  float q[18], o[16];
+  return false;
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// The tiles of one pair, in order: entry v, row tile rt, token tile.
+struct Tiles {
+  long long u, lo, hi;
+  int v, rt, tile, nt, len;
+
+  __device__ __forceinline__ Tiles(const MlaArgs& a, const Misc* mi) {
+    lo = u = mi->lo;
+    hi = mi->hi;
+    v = mi->start_v;
+    load(a);
+    rt = static_cast<int>(mi->start_off / nt);
+    tile = static_cast<int>(mi->start_off % nt);
+  }
+  __device__ __forceinline__ void load(const MlaArgs& a) {
+    len = entry_len(a, v);
+    nt = (len + kMt - 1) / kMt;
+  }
+  __device__ __forceinline__ bool more() const { return u < hi; }
+  __device__ __forceinline__ bool first() const { return u == lo || tile == 0; }
+  __device__ __forceinline__ bool last() const { return u + 1 == hi || tile + 1 == nt; }
+  __device__ __forceinline__ void next(const MlaArgs& a) {
+    ++u;
+    if (++tile == nt && u < hi) {
+      tile = 0;
+      if (++rt == a.row_tiles) {
+        rt = 0;
+        do {   // a tile is left, so an entry that has one follows
+          ++v;
+          load(a);
+        } while (nt == 0);
+      }
+    }
+  }
+};
+
+// The cache row of token e of the tile's entry, or -1.
+__device__ __forceinline__ int token_row(const MlaArgs& a, int v, int len, int e) {
+  if (e >= len) return -1;
+  int b = v, t = e;
+  if (a.tokens) {
+    b = v / a.ways;
+    t = a.tokens[static_cast<size_t>(v) * a.k + e];
+    if (t < 0) return -1;
+    if (t >= request_len(a, b)) {
+      set_status(a.status, ESS_ERR_DEVICE_CHECK);
+      return -1;
+    }
+  }
+  const int pg = a.page_table[static_cast<size_t>(b) * a.max_pages + t / a.page];
+  const long long row = static_cast<long long>(pg) * a.page + t % a.page;
+  if (row < 0 || row >= a.n_rows) {
+    set_status(a.status, ESS_ERR_DEVICE_CHECK);
+    return -1;
+  }
+  return static_cast<int>(row);
+}
+
+// 32 codes (one block) -> four 16-byte units of bf16 (K) or fp16 (V)
+__device__ __forceinline__ void widen_block(const uint4& codes, int byte, bool to_bf16,
+                                            uint4* unit) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+  const int eb = q4_exp_byte(byte);
+  if (to_bf16) {
+    const uint32_t s2 = q4_bf16_scale(eb);
 #pragma unroll
-  for (int j = 0; j < 18; ++j) q[j] = bf16_lo(a.q[qrow * kRowDim + 32 * j + lane]);
+    for (int q = 0; q < 4; ++q) {
+      uint32_t h[4];
+      e2m1_to_f16x2(w[q], h);
+      unit[q] = make_uint4(q4_bf16x2(h[0], s2), q4_bf16x2(h[1], s2), q4_bf16x2(h[2], s2),
+                           q4_bf16x2(h[3], s2));
+    }
+  } else {
+    const __half2 s2 = __float2half2_rn(__uint_as_float(static_cast<uint32_t>(eb) << 23));
 #pragma unroll
-  for (int j = 0; j < 16; ++j) o[j] = 0.0f;
+    for (int q = 0; q < 4; ++q) {
+      uint32_t h[4];
+      e2m1_to_f16x2(w[q], h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), s2);
+        h[e] = *reinterpret_cast<const uint32_t*>(&r);
+      }
+      unit[q] = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+  }
+}
+__device__ __forceinline__ int byte_of(uint32_t w, int i) {
+  return static_cast<int>((w >> (8 * i)) & 0xffu);
+}
+
+// ---------------------------------------------------------------- roles
+// Eight warps: gather the rows of a tile and widen them, K of this CTA's 64
+// tokens, then V of its 256 dims of all 128 tokens.
+__device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc* mi,
+                                           uint32_t rank) {
+  const int wt = threadIdx.x - kWidenWarp0 * 32;   // 0..255
+  const int w = wt >> 5, lane = wt & 31;
+  const int r8 = lane & 7, cq = lane >> 3;
+  const uint32_t k_full = dsmem_addr(smem_u32(&mi->k_full), 0);
+  const uint32_t v_full = dsmem_addr(smem_u32(&mi->v_full), 0);
+  uint8_t* sk = smem + kOffK;
+  uint8_t* sv = smem + kOffV;
+  Tiles it(a, mi);
+
+  auto publish = [&](int buf, int row) {   // 128 threads, one token each
+    mi->row[buf][wt] = row;
+    const uint32_t m = __ballot_sync(0xffffffffu, row >= 0);
+    if (lane == 0) mi->mask[buf][w] = m;
+  };
+  if (wt < kMt) publish(0, token_row(a, it.v, it.len, it.tile * kMt + wt));
+  named_sync(3, kWidenWarps * 32);
+
+  uint4 kc[4], ks, kr[2];     // raw K row: codes, exponents, RoPE units
+  uint4 vc[2][2];
+  uint2 vs[2];
+  const int krow = 8 * w + r8;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  auto load_k = [&](int buf) {
+    const int row = mi->row[buf][rank * kCtaRows + krow];
+    const uint8_t* s = a.rows + static_cast<size_t>(max(row, 0)) * kQ4RowBytes;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      kc[j] = row < 0 ? zero : reinterpret_cast<const uint4*>(s)[4 * j + cq];
+    ks = row < 0 ? zero : reinterpret_cast<const uint4*>(s + 256)[0];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      kr[j] = row < 0 ? zero : reinterpret_cast<const uint4*>(s + 272)[4 * j + cq];
+  };
+  auto load_v = [&](int buf) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int row = mi->row[buf][16 * w + 8 * g + r8];
+      const uint8_t* s = a.rows + static_cast<size_t>(max(row, 0)) * kQ4RowBytes;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        vc[g][j] = row < 0 ? zero : reinterpret_cast<const uint4*>(s + 128 * rank)[4 * j + cq];
+      vs[g] = row < 0 ? make_uint2(0u, 0u)
+                      : reinterpret_cast<const uint2*>(s + 256 + 8 * rank)[0];
+    }
+  };
+  load_k(0);
+  for (int g = 0; it.more(); ++g) {
+    const int buf = g & 1;
+    load_v(buf);
+    // K: free once QK of the tile before is done
+    if (g > 0) wait_or_abort(&mi->qk_done[(g - 1) & 1], ((g - 1) >> 1) & 1, mi, a.status);
+    {
+      const uint32_t ew[4] = {ks.x, ks.y, ks.z, ks.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint4 unit[4];
+        widen_block(kc[j], byte_of(ew[j], cq), true, unit);
+        const int c = 4 * j + cq;
+        uint8_t* d = sk + (c >> 1) * kKBlk;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(d + sw128_off(krow, (c & 1) * 4 + q)) = unit[q];
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<uint4*>(sk + 8 * kKBlk + sw128_off(krow, 4 * j + cq)) = kr[j];
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_remote(k_full);
+    // the next tile's rows (page table loads in flight while V is waited for)
+    it.next(a);
+    int nrow = -1;
+    const bool more = it.more();
+    if (more && wt < kMt) nrow = token_row(a, it.v, it.len, it.tile * kMt + wt);
+    // V: free once PV of the tile before is done, as are that tile's masks
+    if (g > 0) wait_or_abort(&mi->pv_done, (g - 1) & 1, mi, a.status);
+    if (more) {
+      if (wt < kMt) publish(buf ^ 1, nrow);
+      named_sync(3, kWidenWarps * 32);
+      load_k(buf ^ 1);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int tok = 16 * w + 8 * h + r8;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint4 unit[4];
+        widen_block(vc[h][j], byte_of(j ? vs[h].y : vs[h].x, cq), false, unit);
+        const int c = 4 * j + cq;
+        uint8_t* d = sv + (c >> 1) * kVBlk;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(d + sw128_off(tok, (c & 1) * 4 + q)) = unit[q];
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_remote(v_full);
+  }
+}
+
+// One thread per CTA loads the queries; that of the even CTA issues the MMAs.
+__device__ __forceinline__ void mma_role(const MlaArgs& a, const CUtensorMap* qmap, uint8_t* smem,
+                                         Misc* mi, uint32_t rank, uint32_t tmem) {
+  const uint32_t q_ready = dsmem_addr(smem_u32(&mi->q_ready), 0);
+  const uint32_t sq = smem_u32(smem + kOffQ), sk = smem_u32(smem + kOffK);
+  const uint32_t sv = smem_u32(smem + kOffV), sp = smem_u32(smem + kOffP);
+  const uint32_t idesc_qk = make_idesc(kFmtBF16, kFmtBF16, 0, kMt, kPairRows);
+  const uint32_t idesc_pv = make_idesc(kFmtF16, kFmtF16, 1, 256, kPairRows);
+  bool ok = true;
+  auto pv = [&](int g, bool accumulate) {
+    ok = wait_or_abort(&mi->v_full, g & 1, mi, a.status) && ok;
+    ok = wait_or_abort(&mi->p_full, g & 1, mi, a.status) && ok;
+    if (ok) {
+      tc_fence_after();
+#pragma unroll 1
+      for (int kt = 0; kt < 8; ++kt) {
+        const uint64_t ad = make_sdesc_sw128(sp + (kt >> 2) * kKBlk + (kt & 3) * 32, 16, 1024);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          umma_f16_pair(tmem + kColO + j * 128, ad,
+                        make_sdesc_sw128(sv + j * 2 * kVBlk + kt * 2048, kVBlk, 1024), idesc_pv,
+                        accumulate || kt > 0);
+      }
+      umma_commit_pair(smem_u32(&mi->pv_done));
+    }
+  };
+  int seg = 0;
+  bool acc = false;   // the tile before was not the first of its segment
+  Tiles it(a, mi);
+  for (int g = 0; it.more(); ++g) {
+    const bool first = it.first(), last = it.last();
+    if (first) {
+      if (seg > 0) ok = wait_or_abort(&mi->q_free, (seg - 1) & 1, mi, a.status) && ok;
+      mbar_arrive_expect_tx(smem_u32(&mi->q_full), 9 * kKBlk);
+      const int y = it.v * a.entry_rows + it.rt * kPairRows + rank * kCtaRows;
+      for (int kb = 0; kb < 9; ++kb)
+        tma_load_2d(sq + kb * kKBlk, qmap, smem_u32(&mi->q_full), kb * 64, y);
+      if (rank == 0 && g > 0) pv(g - 1, acc);
+      ok = wait_or_abort(&mi->q_full, seg & 1, mi, a.status) && ok;
+      mbar_arrive_remote(q_ready);
+      if (rank == 0) ok = wait_or_abort(&mi->q_ready, seg & 1, mi, a.status) && ok;
+      ++seg;
+    }
+    if (rank == 0) {
+      ok = wait_or_abort(&mi->k_full, g & 1, mi, a.status) && ok;
+      if (ok) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int kb = 0; kb < 9; ++kb)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f16_pair(tmem + kColS + (g & 1) * 64,
+                          make_sdesc_sw128(sq + kb * kKBlk + kk * 32, 16, 1024),
+                          make_sdesc_sw128(sk + kb * kKBlk + kk * 32, 16, 1024), idesc_qk,
+                          (kb | kk) != 0);
+        umma_commit_pair(smem_u32(&mi->qk_done[g & 1]));
+        if (last) umma_commit_pair(smem_u32(&mi->q_free));
+      }
+      if (!first) pv(g - 1, acc);
+    }
+    acc = !first;
+    it.next(a);
+    if (rank == 0 && !it.more()) pv(g, acc);
+  }
+  // the last arrival on this CTA's q_free, which nothing else waits for
+  wait_or_abort(&mi->q_free, (seg - 1) & 1, mi, a.status);
+}
+
+// Four warps: thread = one query row and half of a tile's tokens, or half of
+// the row's output dims.
+__device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Misc* mi,
+                                             uint32_t rank, uint32_t tmem, int pair) {
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int r = tid & 63, half = tid >> 6;
+  const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+  const uint32_t p_full = dsmem_addr(smem_u32(&mi->p_full), 0);
+  uint8_t* sp = smem + kOffP + half * kKBlk;
+  const int bar_id = 1 + (warp & 1);   // warps w and w + 2 hold the same rows
+  float m = -INFINITY, l = 0.0f;
+  int limit = 0, seg_first_tile = 0;
+  long long seg_u = 0;
+  Tiles it(a, mi);
+  for (int g = 0; it.more(); ++g) {
+    const bool first = it.first(), last = it.last();
+    if (first) {
+      const int row = it.rt * kPairRows + static_cast<int>(rank) * kCtaRows + r;
+      limit = row >= a.entry_rows ? 0 : it.len;
+      if (!a.tokens && limit) limit = it.len - (a.ways - 1) + row / a.heads;
+      m = -INFINITY;
+      l = 0.0f;
+      seg_first_tile = it.tile;
+      seg_u = it.u;
+    }
+    bool ok = wait_or_abort(&mi->qk_done[g & 1], (g >> 1) & 1, mi, a.status);
+    tc_fence_after();
+    const uint32_t ts = tmem + lanes + kColS + (g & 1) * 64;
+    uint32_t live[2] = {mi->mask[g & 1][2 * half], mi->mask[g & 1][2 * half + 1]};
+    const int nv = limit - it.tile * kMt - half * 64;   // tokens of this half before the limit
+    if (nv < 64) {
+      live[0] = nv <= 0 ? 0u : (nv < 32 ? live[0] & ((1u << nv) - 1u) : live[0]);
+      live[1] = nv <= 32 ? 0u : live[1] & ((1u << (nv - 32)) - 1u);
+    }
+    float mt = -INFINITY;
+#pragma unroll
+    for (int c2 = 0; c2 < 2; ++c2) {
+      float s[32];
+      tmem_ld32(ts + 32 * c2, s);
+      if (live[c2] == 0xffffffffu) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) mt = fmaxf(mt, s[c]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) mt = fmaxf(mt, (live[c2] >> c) & 1u ? s[c] : -INFINITY);
+      }
+    }
+    mi->xch[g & 1][tid] = mt;
+    named_sync(bar_id, 64);
+    mt = fmaxf(mt, mi->xch[g & 1][tid ^ 64]) * a.c2;
+    float f = 1.0f;
+    if (m == -INFINITY) {
+      m = mt;   // nothing summed yet: O's row is zero
+    } else if (mt > m + kGrow) {
+      f = ex2_approx(m - mt);
+      m = mt;
+    }
+    const float base = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f;
+    uint32_t p[32];
+#pragma unroll
+    for (int c2 = 0; c2 < 2; ++c2) {
+      float s[32];
+      tmem_ld32(ts + 32 * c2, s);
+      if (live[c2] != 0xffffffffu) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) s[c] = (live[c2] >> c) & 1u ? s[c] : -INFINITY;
+      }
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float p0 = ex2_approx(fmaf(s[2 * c], a.c2, -base));
+        const float p1 = ex2_approx(fmaf(s[2 * c + 1], a.c2, -base));
+        sum += p0 + p1;
+        p[16 * c2 + c] = half2_bits(p0, p1);
+      }
+    }
+    l = fmaf(l, f, sum);
+    // P and O are free once PV of the tile before is done
+    if (g > 0) ok = wait_or_abort(&mi->pv_done, (g - 1) & 1, mi, a.status) && ok;
+    if (!first && __any_sync(0xffffffffu, f != 1.0f)) {
+      tc_fence_after();
+      for (int c = 0; c < 8; ++c) {
+        float o[32];
+        tmem_ld32(tmem + lanes + kColO + 32 * c, o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] *= f;
+        tmem_st32(tmem + lanes + kColO + 32 * c, o);
+      }
+      tmem_wait_st();
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      *reinterpret_cast<uint4*>(sp + sw128_off(r, u)) =
+          make_uint4(p[4 * u], p[4 * u + 1], p[4 * u + 2], p[4 * u + 3]);
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if ((tid & 31) == 0) mbar_arrive_remote(p_full);
+
+    if (last) {
+      // the whole row's sum, then O out of TMEM: final, or a partial
+      mi->xch[(g & 1) ^ 1][tid] = l;
+      named_sync(bar_id, 64);
+      const float lt = l + mi->xch[(g & 1) ^ 1][tid ^ 64];
+      named_sync(bar_id, 64);
+      const bool whole = seg_first_tile == 0 && it.tile + 1 == it.nt;
+      const int slot = pair * 2 + (seg_u == it.lo ? 0 : 1);
+      ok = wait_or_abort(&mi->pv_done, g & 1, mi, a.status) && ok;
+      tc_fence_after();
+      const int row = it.rt * kPairRows + static_cast<int>(rank) * kCtaRows + r;
+      const bool mine = row < a.entry_rows;
+      const size_t orow = static_cast<size_t>(it.v) * a.entry_rows + row;
+      const float inv = !whole ? 1.0f : (lt > 0.0f || lt != lt ? 1.0f / lt : 0.0f);
+      const int prow = static_cast<int>(rank) * kCtaRows + r;
+      for (int c = 0; c < 8; ++c) {
+        float o[32];
+        tmem_ld32(tmem + lanes + kColO + 32 * c, o);
+        const int d0 = half * 256 + 32 * c;
+        if (whole) {
+          if (mine) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * kLatent + d0);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= inv;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) dst[q] = pack8_bf16(o + 8 * q);
+          }
+        } else {
+          float4* dst = reinterpret_cast<float4*>(
+              a.part_o + (static_cast<size_t>(slot) * kPairRows + prow) * kLatent + d0);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        }
+      }
+      if (half == 0) {
+        if (whole) {
+          if (mine && a.lse)
+            a.lse[orow] = lt > 0.0f || lt != lt ? (m + log2f(lt)) * 0.69314718055994531f
+                                                : -INFINITY;
+        } else {
+          a.part_ml[static_cast<size_t>(slot) * kPairRows + prow] = make_float2(m, lt);
+        }
+      }
+      if (tid == 0 && rank == 0) {
+        int2* sp2 = a.span + static_cast<size_t>(it.v) * a.row_tiles + it.rt;
+        if (seg_first_tile == 0) sp2->x = slot;
+        if (it.tile + 1 == it.nt) sp2->y = pair;
+      }
+      tc_fence_before();
+    }
+    it.next(a);
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
+    cache_mla_kernel(const __grid_constant__ CUtensorMap qmap, const MlaArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Misc* mi = reinterpret_cast<Misc*>(smem + kOffMisc);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  if (tid == 0) {
+    mbar_init(smem_u32(&mi->q_full), 1);
+    mbar_init(smem_u32(&mi->q_ready), 2);
+    mbar_init(smem_u32(&mi->q_free), 1);
+    mbar_init(smem_u32(&mi->k_full), 2 * kWidenWarps);
+    mbar_init(smem_u32(&mi->v_full), 2 * kWidenWarps);
+    mbar_init(smem_u32(&mi->p_full), 2 * kSoftWarps);
+    mbar_init(smem_u32(&mi->qk_done[0]), 1);
+    mbar_init(smem_u32(&mi->qk_done[1]), 1);
+    mbar_init(smem_u32(&mi->pv_done), 1);
+    mi->abort = 0;
+    fence_mbar_init();
+  }
+  pdl_wait_previous();
+  // this pair's share of all tiles: a scan of the entries' tile counts, a
+  // run of neighbouring entries per thread
+  const int per = (a.entries + kMlaThreads - 1) / kMlaThreads;
+  const int v0 = min(a.entries, tid * per), v1 = min(a.entries, v0 + per);
+  long long mine = 0;
+  for (int v = v0; v < v1; ++v)
+    mine += static_cast<long long>((entry_len(a, v) + kMt - 1) / kMt) * a.row_tiles;
+  long long before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
+  if (lane == 31) mi->scan[warp] = before;
+  __syncthreads();
+  long long total = 0;
+  before -= mine;
+  for (int w = 0; w < kMlaThreads / 32; ++w) {
+    if (w < warp) before += mi->scan[w];
+    total += mi->scan[w];
+  }
+  // neighbouring pairs share a request, so none between two may be idle
+  const long long busy = total < pairs ? total : pairs;
+  if (pair >= busy) return;   // both CTAs of the pair
+  const long long lo = total * pair / busy, hi = total * (pair + 1) / busy;
+  if (lo >= before && lo < before + mine) {
+    long long off = lo - before;
+    int v = v0;
+    for (;; ++v) {
+      const long long n = static_cast<long long>((entry_len(a, v) + kMt - 1) / kMt) * a.row_tiles;
+      if (off < n) break;
+      off -= n;
+    }
+    mi->start_v = v;
+    mi->start_off = off;
+    mi->lo = lo;
+    mi->hi = hi;
+  }
+  if (warp == kMmaWarp) {
+    if (lane == 0) tma_prefetch_desc(&qmap);
+    __syncwarp();
+    tmem_alloc_pair(smem_u32(&mi->tmem), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the peer's barriers are set up
+  tc_fence_after();
+  const uint32_t tmem = mi->tmem;
+
+  if (warp < kSoftWarps) {
+    softmax_role(a, smem, mi, rank, tmem, pair);
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) mma_role(a, &qmap, smem, mi, rank, tmem);
+    __syncwarp();
+  } else {
+    widen_role(a, smem, mi, rank);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // no barrier of the peer is arrived on after this
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc_pair(tmem, 512);
+}
+
+// One CTA per query row joins the partials of a row that several pairs share,
+// and writes the rows of requests without a token.
+__global__ void __launch_bounds__(128) cache_mla_join_kernel(const MlaArgs a) {
+  pdl_wait_previous();
+  const int x = blockIdx.x;                      // (b, m, h)
+  const int h = x % a.heads, bm = x / a.heads, b = bm / a.ways, m = bm % a.ways;
+  const int t = threadIdx.x;
+  const int T = a.T[b];
+  if (h == 0 && m == 0 && t == 0 &&
+      (T < 0 || T > static_cast<long long>(a.max_pages) * a.page))
+    set_status(a.status, ESS_ERR_DEVICE_CHECK);
+  const int v = a.tokens ? bm : b;
+  const int row = a.tokens ? h : m * a.heads + h;
+  uint2* out = reinterpret_cast<uint2*>(a.out + static_cast<size_t>(x) * kLatent) + t;
+  if (entry_len(a, v) == 0) {
+    *out = make_uint2(0u, 0u);
+    if (t == 0 && a.lse) a.lse[x] = -INFINITY;
+    return;
+  }
+  const int2 sp = a.span[static_cast<size_t>(v) * a.row_tiles + row / kPairRows];
+  const int p0 = sp.x >> 1;
+  if (p0 == sp.y) return;
+  const int pr = row % kPairRows;
   float mx = -INFINITY, l = 0.0f;
-  for (int t0 = 0; t0 < n; t0 += kTile) {
-    __syncthreads();
-    for (int r = warp; r < kTile; r += kHeadsPerCta) {
-      const int e = t0 + r;
-      long long row = -1;
-      if (e < n) {
-        const int t = list ? list[e] : e;
-        if (t >= 0) {
-          if (t < Tb) {
-            const int pg = a.page_table[static_cast<size_t>(b) * a.max_pages + t / a.page];
-            row = static_cast<long long>(pg) * a.page + t % a.page;
-          }
-          if (row < 0 || row >= a.n_rows) {
-            if (lane == 0) set_status(a.status, ESS_ERR_DEVICE_CHECK);
-            row = -1;
-          }
-        }
-      }
-      if (lane == 0) live[r] = row >= 0;
-      float* d = tile + r * kRowDim;
-      if (row >= 0) {
-        const uint8_t* s = a.rows + row * kQ4RowBytes;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint4 w = widen8_e2m1(reinterpret_cast<const uint32_t*>(s)[32 * half + lane],
-                                      s[256 + 8 * half + (lane >> 2)]);
-          unpack8(w, d + 256 * half + 8 * lane);
-        }
-        const uint32_t w = reinterpret_cast<const uint32_t*>(s + 272)[lane];
-        d[512 + 2 * lane] = bf16_lo(w);
-        d[513 + 2 * lane] = bf16_hi(w);
-      }
-    }
-    __syncthreads();
-    for (int r = 0; r < kTile; ++r) {
-      if (!live[r]) continue;
-      const float* d = tile + r * kRowDim;
-      float s = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 18; ++j) s = fmaf(q[j], d[32 * j + lane], s);
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      s *= a.c2;
-      const float m2 = fmaxf(mx, s);
-      const float base = m2 == -INFINITY ? 0.0f : m2;
-      const float f = exp2f(mx - base), p = exp2f(s - base);
-      mx = m2;
-      l = fmaf(l, f, p);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) o[j] = fmaf(o[j], f, p * d[32 * j + lane]);
-    }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = p0; p <= sp.y; ++p) {
+    const size_t i = static_cast<size_t>(p == p0 ? sp.x : 2 * p) * kPairRows + pr;
+    const float2 ml = a.part_ml[i];
+    const float4 o = reinterpret_cast<const float4*>(a.part_o + i * kLatent)[t];
+    const float m2 = fmaxf(mx, ml.x);
+    const float base = m2 == -INFINITY ? 0.0f : m2;
+    const float f = exp2f(mx - base), w = exp2f(ml.x - base);
+    // a part without a token has l = 0 and O = 0; its weight is 0 beside others
+    l = fmaf(l, f, w * ml.y);
+    acc.x = fmaf(acc.x, f, w * o.x);
+    acc.y = fmaf(acc.y, f, w * o.y);
+    acc.z = fmaf(acc.z, f, w * o.z);
+    acc.w = fmaf(acc.w, f, w * o.w);
+    mx = m2;
   }
-  if (h >= a.heads) return;
-  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    a.out[qrow * kLatent + 32 * j + lane] = static_cast<uint16_t>(bf16_bits(o[j] * inv));
-  if (a.lse && lane == 0)
-    a.lse[qrow] = l > 0.0f || l != l ? (mx + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  const bool some = l > 0.0f || l != l;
+  const float inv = some ? 1.0f / l : 0.0f;
+  *out = make_uint2(bf16x2_bits(acc.x * inv, acc.y * inv), bf16x2_bits(acc.z * inv, acc.w * inv));
+  if (t == 0 && a.lse)
+    a.lse[x] = some ? (mx + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -125,6 +745,23 @@ ess_status check_shape(int batch, int ways, int heads) {
   if (batch < 1 || ways < 1 || heads < 1) return ESS_ERR_INVALID_ARG;
   if (ways > kMaxCacheWays || heads > kMaxCacheHeads || batch > 65535) return ESS_ERR_UNSUPPORTED;
   return ESS_OK;
+}
+
+struct MlaLayout {
+  size_t span, part_o, part_ml, total;
+};
+MlaLayout mla_layout(int batch, int ways) {
+  MlaLayout L;
+  size_t o = 0;
+  // at most one row tile per (request, way), listed or not
+  L.span = o;
+  o += (static_cast<size_t>(batch) * ways * sizeof(int2) + 255) & ~static_cast<size_t>(255);
+  L.part_ml = o;
+  o += static_cast<size_t>(kMaxPairs) * 2 * kPairRows * sizeof(float2);
+  L.part_o = o;
+  o += static_cast<size_t>(kMaxPairs) * 2 * kPairRows * kLatent * sizeof(float);
+  L.total = o;
+  return L;
 }
 
 }  // namespace
@@ -138,7 +775,7 @@ ess_status ess_cache_mla_bytes(int32_t batch, int32_t ways, int32_t heads, size_
   if (!bytes) return ESS_ERR_INVALID_ARG;
   const ess_status s = check_shape(batch, ways, heads);
   if (s != ESS_OK) return s;
-  *bytes = 256;
+  *bytes = mla_layout(batch, ways).total;
   return ESS_OK;
 }
 
@@ -147,23 +784,31 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
                          const int32_t* T, int32_t batch, int32_t ways, int32_t heads,
                          const int32_t* tokens, int32_t k, float sm_scale, void* out, float* lse,
                          void* workspace, size_t ws_bytes, int32_t* status, ess_stream_t stream) {
-  size_t need = 0;
-  const ess_status s = ess_cache_mla_bytes(batch, ways, heads, &need);
+  const ess_status s = check_shape(batch, ways, heads);
   if (s != ESS_OK) return s;
   if (format < ESS_ROW_BF16 || format > ESS_ROW_Q4 || n_rows < 1 || max_pages < 1 || page < 1 ||
       (tokens && k < 1) || !(sm_scale > 0.0f) || !std::isfinite(sm_scale))
     return ESS_ERR_INVALID_ARG;
   if (format != ESS_ROW_Q4 || n_rows > 0x7fffffffLL ||
-      static_cast<long long>(max_pages) * page > 0x7fffffffLL)
+      static_cast<long long>(max_pages) * page > 0x7fffff00LL || k > 0x7fffff00)
     return ESS_ERR_UNSUPPORTED;
   if (!q || !rows || !page_table || !T || !out || !workspace || !aligned16(q) ||
       !aligned16(rows) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return ESS_ERR_INVALID_ARG;
-  if (ws_bytes < need) return ESS_ERR_OOM;
+  const MlaLayout L = mla_layout(batch, ways);
+  if (ws_bytes < L.total) return ESS_ERR_OOM;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return ESS_ERR_CUDA;
+  const long long all_rows = static_cast<long long>(batch) * ways * heads;
+  CUtensorMap qmap;
+  if (!encode_map_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, kRowDim, all_rows, kRowBytes, 64,
+                     kCtaRows))
+    return ESS_ERR_CUDA;
   MlaArgs a;
-  a.q = static_cast<const uint16_t*>(q);
   a.rows = static_cast<const uint8_t*>(rows);
-  a.n_rows = n_rows;
+  a.n_rows = static_cast<int>(n_rows);
   a.page_table = page_table;
   a.max_pages = max_pages;
   a.page = page;
@@ -173,17 +818,31 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
   a.heads = heads;
   a.tokens = tokens;
   a.k = k;
+  a.entries = tokens ? batch * ways : batch;
+  a.entry_rows = tokens ? heads : ways * heads;
+  a.row_tiles = (a.entry_rows + kPairRows - 1) / kPairRows;
   a.c2 = sm_scale * 1.4426950408889634f;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
+  char* ws = static_cast<char*>(workspace);
+  a.span = reinterpret_cast<int2*>(ws + L.span);
+  a.part_o = reinterpret_cast<float*>(ws + L.part_o);
+  a.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
   a.status = status;
-  const size_t smem = kTile * kRowDim * sizeof(float);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // no more pairs than tiles there can be
+  const long long most = static_cast<long long>(a.entries) * a.row_tiles *
+                         (((tokens ? std::min<long long>(k, static_cast<long long>(max_pages) * page)
+                                   : static_cast<long long>(max_pages) * page) +
+                           kMt - 1) /
+                          kMt);
+  const int pairs = static_cast<int>(std::min<long long>(most, std::min(kMaxPairs, sms / 2)));
   cudaError_t e = cudaFuncSetAttribute(cache_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+                                       static_cast<int>(kMlaSmem));
   if (e != cudaSuccess) return ESS_ERR_CUDA;
-  const dim3 grid((heads + kHeadsPerCta - 1) / kHeadsPerCta, ways, batch);
-  e = launch_pdl(cache_mla_kernel, grid, dim3(kHeadsPerCta * 32), smem,
-                 static_cast<cudaStream_t>(stream), a);
+  e = launch_pdl(cache_mla_kernel, dim3(2 * pairs), dim3(kMlaThreads), kMlaSmem, st, qmap, a);
+  if (e != cudaSuccess) return ESS_ERR_CUDA;
+  e = launch_pdl(cache_mla_join_kernel, dim3(static_cast<unsigned>(all_rows)), dim3(128), 0, st, a);
   return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
 }
 
