@@ -45,7 +45,9 @@ constexpr int kSoftWarps = 4;
 constexpr int kMmaWarp = 4;
 constexpr int kWidenWarp0 = 5;
 constexpr int kWidenWarps = 8;
-constexpr int kMlaThreads = (kWidenWarp0 + kWidenWarps) * 32;
+constexpr int kRowWarp = kWidenWarp0 + kWidenWarps;
+constexpr int kMlaThreads = (kRowWarp + 1) * 32;
+constexpr int kRing = 3;              // tiles whose rows are known ahead
 
 constexpr uint32_t kKBlk = 8192;      // [64 rows][64 dims], 128-byte swizzled
 constexpr uint32_t kVBlk = 16384;     // [128 tokens][64 dims]
@@ -61,14 +63,15 @@ constexpr float kGrow = 8.0f;         // log2 of the growth of a maximum that O 
 
 struct Misc {
   uint64_t q_full, q_ready, q_free, k_full, v_full, p_full, qk_done[2], pv_done;
+  uint64_t row_full[kRing], row_free[kRing];
   uint32_t tmem;
   int abort;
   int start_v;
   int pad;
   long long start_off, lo, hi;
   long long scan[16];
-  uint32_t mask[2][4];                // tokens of a tile that exist
-  int32_t row[2][kMt];                // cache rows of a tile's tokens, -1: none
+  uint32_t mask[kRing][4];            // tokens of a tile that exist
+  int32_t row[kRing][kMt];            // cache rows of a tile's tokens, -1: none
   float xch[2][kMt];                  // row statistics of a thread for its partner
 };
 constexpr uint32_t kMlaSmem = 232448;
@@ -79,6 +82,7 @@ struct MlaArgs {
   int n_rows;
   const int32_t* page_table;
   int max_pages, page;
+  int page_shift;          // log2(page), or -1
   const int32_t* T;
   int batch, ways, heads;
   const int32_t* tokens;
@@ -167,24 +171,60 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Mi
   }
   return false;
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
-  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+// this lane's 16 consecutive columns times f, in place
+__device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// pairs of fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(const float2& x, const float2& y, const float2& z) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(const float2& x, const float2& y) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return d;
 }
 
 // The tiles of one pair, in order: entry v, row tile rt, token tile.
@@ -235,8 +275,9 @@ __device__ __forceinline__ int token_row(const MlaArgs& a, int v, int len, int e
       return -1;
     }
   }
-  const int pg = a.page_table[static_cast<size_t>(b) * a.max_pages + t / a.page];
-  const long long row = static_cast<long long>(pg) * a.page + t % a.page;
+  const int pi = a.page_shift >= 0 ? t >> a.page_shift : t / a.page;
+  const int pg = a.page_table[static_cast<size_t>(b) * a.max_pages + pi];
+  const long long row = static_cast<long long>(pg) * a.page + (t - pi * a.page);
   if (row < 0 || row >= a.n_rows) {
     set_status(a.status, ESS_ERR_DEVICE_CHECK);
     return -1;
@@ -278,137 +319,183 @@ __device__ __forceinline__ int byte_of(uint32_t w, int i) {
 }
 
 // ---------------------------------------------------------------- roles
+// One warp resolves the cache rows of the tiles to come, four tokens a lane,
+// up to kRing tiles ahead, so that the page table's latency meets nobody.
+__device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
+  const int lane = threadIdx.x & 31;
+  Tiles it(a, mi);
+  int slot = 0, turn = 0;
+  for (int g = 0; it.more(); ++g) {
+    int row[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      row[j] = token_row(a, it.v, it.len, it.tile * kMt + 32 * j + lane);
+    if (turn > 0) wait_or_abort(&mi->row_free[slot], (turn - 1) & 1, mi, a.status);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      mi->row[slot][32 * j + lane] = row[j];
+      const uint32_t m = __ballot_sync(0xffffffffu, row[j] >= 0);
+      if (lane == 0) mi->mask[slot][j] = m;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&mi->row_full[slot]));
+    if (++slot == kRing) {
+      slot = 0;
+      ++turn;
+    }
+    it.next(a);
+  }
+}
+
 // Eight warps: gather the rows of a tile and widen them, K of this CTA's 64
-// tokens, then V of its 256 dims of all 128 tokens.
+// tokens, and V of its 256 dims of all 128 tokens.  Eight neighbouring lanes
+// read 128 neighbouring bytes of one row.  Their 16-byte codes make four
+// 16-byte units each, in only two of the eight bank groups for a given unit
+// number, so a lane stores its units in an order turned by its place: then
+// eight lanes cover all bank groups at every store.
 __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc* mi,
                                            uint32_t rank) {
   const int wt = threadIdx.x - kWidenWarp0 * 32;   // 0..255
   const int w = wt >> 5, lane = wt & 31;
-  const int r8 = lane & 7, cq = lane >> 3;
   const uint32_t k_full = dsmem_addr(smem_u32(&mi->k_full), 0);
   const uint32_t v_full = dsmem_addr(smem_u32(&mi->v_full), 0);
   uint8_t* sk = smem + kOffK;
   uint8_t* sv = smem + kOffV;
-  Tiles it(a, mi);
-
-  auto publish = [&](int buf, int row) {   // 128 threads, one token each
-    mi->row[buf][wt] = row;
-    const uint32_t m = __ballot_sync(0xffffffffu, row >= 0);
-    if (lane == 0) mi->mask[buf][w] = m;
-  };
-  if (wt < kMt) publish(0, token_row(a, it.v, it.len, it.tile * kMt + wt));
-  named_sync(3, kWidenWarps * 32);
-
-  uint4 kc[4], ks, kr[2];     // raw K row: codes, exponents, RoPE units
-  uint4 vc[2][2];
-  uint2 vs[2];
-  const int krow = 8 * w + r8;
+  const int n = static_cast<int>(mi->hi - mi->lo);
+  // K: instruction j covers rows 8w + 2j and + 1, lane = (row, chunk of 16);
+  // V: tokens 16w + 4j .. + 3, lane = (token, chunk of 8 of this CTA's half)
+  const int kc_ = lane & 15, kr_ = 8 * w + (lane >> 4);
+  const int vc_ = lane & 7, vt_ = 16 * w + (lane >> 3);
+  const int turn = (lane >> 1) & 3;   // the same for both mappings
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  auto load_k = [&](int buf) {
-    const int row = mi->row[buf][rank * kCtaRows + krow];
-    const uint8_t* s = a.rows + static_cast<size_t>(max(row, 0)) * kQ4RowBytes;
+
+  uint4 kc[4], kr[2], vc[4];   // raw codes and RoPE units
+  int ke[4], ve[4];            // exponent bytes
+  auto load_k = [&](int slot) {
+    const int32_t* rows = mi->row[slot] + rank * kCtaRows;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = rows[kr_ + 2 * j];
+      const uint8_t* s = a.rows + static_cast<size_t>(max(row, 0)) * kQ4RowBytes;
+      kc[j] = row < 0 ? zero : reinterpret_cast<const uint4*>(s)[kc_];
+      ke[j] = row < 0 ? 127 : s[256 + kc_];
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = rows[8 * w + 4 * j + (lane >> 3)];
+      const uint8_t* s = a.rows + static_cast<size_t>(max(row, 0)) * kQ4RowBytes;
+      kr[j] = row < 0 ? zero : reinterpret_cast<const uint4*>(s + 272)[lane & 7];
+    }
+  };
+  auto load_v = [&](int slot) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = mi->row[slot][vt_ + 4 * j];
+      const uint8_t* s = a.rows + static_cast<size_t>(max(row, 0)) * kQ4RowBytes;
+      vc[j] = row < 0 ? zero : reinterpret_cast<const uint4*>(s + 128 * rank)[vc_];
+      ve[j] = row < 0 ? 127 : s[256 + 8 * rank + vc_];
+    }
+  };
+  // four units of one chunk, in the lane's order, to row r of a block
+  auto put = [&](uint8_t* blk, int r, int chunk, uint4 codes, int byte, bool to_bf16) {
+    uint4 c = codes;
+    if (turn & 1) c = make_uint4(c.y, c.z, c.w, c.x);
+    if (turn & 2) c = make_uint4(c.z, c.w, c.x, c.y);
+    uint4 unit[4];
+    widen_block(c, byte, to_bf16, unit);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint4*>(blk + sw128_off(r, (chunk & 1) * 4 + ((q + turn) & 3))) = unit[q];
+  };
+  auto store_k = [&]() {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      kc[j] = row < 0 ? zero : reinterpret_cast<const uint4*>(s)[4 * j + cq];
-    ks = row < 0 ? zero : reinterpret_cast<const uint4*>(s + 256)[0];
+      put(sk + (kc_ >> 1) * kKBlk, kr_ + 2 * j, kc_, kc[j], ke[j], true);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      kr[j] = row < 0 ? zero : reinterpret_cast<const uint4*>(s + 272)[4 * j + cq];
-  };
-  auto load_v = [&](int buf) {
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int row = mi->row[buf][16 * w + 8 * g + r8];
-      const uint8_t* s = a.rows + static_cast<size_t>(max(row, 0)) * kQ4RowBytes;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        vc[g][j] = row < 0 ? zero : reinterpret_cast<const uint4*>(s + 128 * rank)[4 * j + cq];
-      vs[g] = row < 0 ? make_uint2(0u, 0u)
-                      : reinterpret_cast<const uint2*>(s + 256 + 8 * rank)[0];
-    }
-  };
-  load_k(0);
-  for (int g = 0; it.more(); ++g) {
-    const int buf = g & 1;
-    load_v(buf);
-    // K: free once QK of the tile before is done
-    if (g > 0) wait_or_abort(&mi->qk_done[(g - 1) & 1], ((g - 1) >> 1) & 1, mi, a.status);
-    {
-      const uint32_t ew[4] = {ks.x, ks.y, ks.z, ks.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint4 unit[4];
-        widen_block(kc[j], byte_of(ew[j], cq), true, unit);
-        const int c = 4 * j + cq;
-        uint8_t* d = sk + (c >> 1) * kKBlk;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(d + sw128_off(krow, (c & 1) * 4 + q)) = unit[q];
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        *reinterpret_cast<uint4*>(sk + 8 * kKBlk + sw128_off(krow, 4 * j + cq)) = kr[j];
-    }
+      *reinterpret_cast<uint4*>(sk + 8 * kKBlk +
+                                sw128_off(8 * w + 4 * j + (lane >> 3), lane & 7)) = kr[j];
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive_remote(k_full);
-    // the next tile's rows (page table loads in flight while V is waited for)
-    it.next(a);
-    int nrow = -1;
-    const bool more = it.more();
-    if (more && wt < kMt) nrow = token_row(a, it.v, it.len, it.tile * kMt + wt);
-    // V: free once PV of the tile before is done, as are that tile's masks
-    if (g > 0) wait_or_abort(&mi->pv_done, (g - 1) & 1, mi, a.status);
-    if (more) {
-      if (wt < kMt) publish(buf ^ 1, nrow);
-      named_sync(3, kWidenWarps * 32);
-      load_k(buf ^ 1);
-    }
+  };
+  auto store_v = [&]() {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int tok = 16 * w + 8 * h + r8;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint4 unit[4];
-        widen_block(vc[h][j], byte_of(j ? vs[h].y : vs[h].x, cq), false, unit);
-        const int c = 4 * j + cq;
-        uint8_t* d = sv + (c >> 1) * kVBlk;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(d + sw128_off(tok, (c & 1) * 4 + q)) = unit[q];
-      }
-    }
+    for (int j = 0; j < 4; ++j)
+      put(sv + (vc_ >> 1) * kVBlk, vt_ + 4 * j, vc_, vc[j], ve[j], false);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive_remote(v_full);
+  };
+  // K runs one tile ahead of V: K of tile g + 1 is written beside PV of tile
+  // g - 1, V of tile g beside QK of tile g + 1.  Slot s of the rows holds tile
+  // g for the (g / kRing)th time.
+  wait_or_abort(&mi->row_full[0], 0, mi, a.status);
+  load_k(0);
+  load_v(0);
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&mi->row_free[0]));
+  store_k();
+  if (n > 1) {
+    wait_or_abort(&mi->row_full[1], 0, mi, a.status);
+    load_k(1);
+  }
+  int slot2 = 2, turn2 = 0;   // of tile g + 2
+  int slot1 = 1;              // of tile g + 1
+  for (int g = 0; g < n; ++g) {
+    if (g + 1 < n) {
+      wait_or_abort(&mi->qk_done[g & 1], (g >> 1) & 1, mi, a.status);
+      store_k();
+    }
+    if (g + 2 < n) {
+      wait_or_abort(&mi->row_full[slot2], turn2 & 1, mi, a.status);
+      load_k(slot2);
+    }
+    if (g > 0) wait_or_abort(&mi->pv_done, (g - 1) & 1, mi, a.status);
+    store_v();
+    if (g + 1 < n) {
+      load_v(slot1);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&mi->row_free[slot1]));
+    }
+    slot1 = slot2;
+    if (++slot2 == kRing) {
+      slot2 = 0;
+      ++turn2;
+    }
   }
 }
 
-// One thread per CTA loads the queries; that of the even CTA issues the MMAs.
+// One warp per CTA: it loads the queries, and in the even CTA issues the MMAs.
+// The whole warp walks the tiles and one elected lane issues: with uniform
+// control flow the descriptors stay in uniform registers, and an MMA is issued
+// every 32 cycles (N = 128) instead of every 110.
 __device__ __forceinline__ void mma_role(const MlaArgs& a, const CUtensorMap* qmap, uint8_t* smem,
                                          Misc* mi, uint32_t rank, uint32_t tmem) {
   const uint32_t q_ready = dsmem_addr(smem_u32(&mi->q_ready), 0);
-  const uint32_t sq = smem_u32(smem + kOffQ), sk = smem_u32(smem + kOffK);
-  const uint32_t sv = smem_u32(smem + kOffV), sp = smem_u32(smem + kOffP);
+  const uint32_t sq = smem_u32(smem + kOffQ);
+  const uint64_t dq = make_sdesc_sw128(sq, 16, 1024);
+  const uint64_t dk = make_sdesc_sw128(smem_u32(smem + kOffK), 16, 1024);
+  const uint64_t dv = make_sdesc_sw128(smem_u32(smem + kOffV), kVBlk, 1024);
+  const uint64_t dp = make_sdesc_sw128(smem_u32(smem + kOffP), 16, 1024);
   const uint32_t idesc_qk = make_idesc(kFmtBF16, kFmtBF16, 0, kMt, kPairRows);
   const uint32_t idesc_pv = make_idesc(kFmtF16, kFmtF16, 1, 256, kPairRows);
+  const bool lead = elect_one();
   bool ok = true;
   auto pv = [&](int g, bool accumulate) {
     ok = wait_or_abort(&mi->v_full, g & 1, mi, a.status) && ok;
     ok = wait_or_abort(&mi->p_full, g & 1, mi, a.status) && ok;
-    if (ok) {
-      tc_fence_after();
-#pragma unroll 1
-      for (int kt = 0; kt < 8; ++kt) {
-        const uint64_t ad = make_sdesc_sw128(sp + (kt >> 2) * kKBlk + (kt & 3) * 32, 16, 1024);
+    tc_fence_after();
+    if (ok && lead) {
+#pragma unroll
+      for (int kt = 0; kt < 8; ++kt)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          umma_f16_pair(tmem + kColO + j * 128, ad,
-                        make_sdesc_sw128(sv + j * 2 * kVBlk + kt * 2048, kVBlk, 1024), idesc_pv,
-                        accumulate || kt > 0);
-      }
+          umma_f16_pair(tmem + kColO + j * 128, dp + ((kt >> 2) * kKBlk + (kt & 3) * 32) / 16,
+                        dv + (j * 2 * kVBlk + kt * 2048) / 16, idesc_pv, accumulate || kt > 0);
       umma_commit_pair(smem_u32(&mi->pv_done));
     }
+    __syncwarp();
   };
   int seg = 0;
   bool acc = false;   // the tile before was not the first of its segment
@@ -417,31 +504,32 @@ __device__ __forceinline__ void mma_role(const MlaArgs& a, const CUtensorMap* qm
     const bool first = it.first(), last = it.last();
     if (first) {
       if (seg > 0) ok = wait_or_abort(&mi->q_free, (seg - 1) & 1, mi, a.status) && ok;
-      mbar_arrive_expect_tx(smem_u32(&mi->q_full), 9 * kKBlk);
-      const int y = it.v * a.entry_rows + it.rt * kPairRows + rank * kCtaRows;
-      for (int kb = 0; kb < 9; ++kb)
-        tma_load_2d(sq + kb * kKBlk, qmap, smem_u32(&mi->q_full), kb * 64, y);
+      if (lead) {
+        mbar_arrive_expect_tx(smem_u32(&mi->q_full), 9 * kKBlk);
+        const int y = it.v * a.entry_rows + it.rt * kPairRows + rank * kCtaRows;
+        for (int kb = 0; kb < 9; ++kb)
+          tma_load_2d(sq + kb * kKBlk, qmap, smem_u32(&mi->q_full), kb * 64, y);
+      }
+      __syncwarp();
       if (rank == 0 && g > 0) pv(g - 1, acc);
       ok = wait_or_abort(&mi->q_full, seg & 1, mi, a.status) && ok;
-      mbar_arrive_remote(q_ready);
+      if (lead) mbar_arrive_remote(q_ready);
+      __syncwarp();
       if (rank == 0) ok = wait_or_abort(&mi->q_ready, seg & 1, mi, a.status) && ok;
       ++seg;
     }
     if (rank == 0) {
       ok = wait_or_abort(&mi->k_full, g & 1, mi, a.status) && ok;
-      if (ok) {
-        tc_fence_after();
-#pragma unroll 1
-        for (int kb = 0; kb < 9; ++kb)
+      tc_fence_after();
+      if (ok && lead) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_f16_pair(tmem + kColS + (g & 1) * 64,
-                          make_sdesc_sw128(sq + kb * kKBlk + kk * 32, 16, 1024),
-                          make_sdesc_sw128(sk + kb * kKBlk + kk * 32, 16, 1024), idesc_qk,
-                          (kb | kk) != 0);
+        for (int k = 0; k < 36; ++k)
+          umma_f16_pair(tmem + kColS + (g & 1) * 64, dq + ((k >> 2) * kKBlk + (k & 3) * 32) / 16,
+                        dk + ((k >> 2) * kKBlk + (k & 3) * 32) / 16, idesc_qk, k != 0);
         umma_commit_pair(smem_u32(&mi->qk_done[g & 1]));
         if (last) umma_commit_pair(smem_u32(&mi->q_free));
       }
+      __syncwarp();
       if (!first) pv(g - 1, acc);
     }
     acc = !first;
@@ -463,7 +551,7 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
   uint8_t* sp = smem + kOffP + half * kKBlk;
   const int bar_id = 1 + (warp & 1);   // warps w and w + 2 hold the same rows
   float m = -INFINITY, l = 0.0f;
-  int limit = 0, seg_first_tile = 0;
+  int limit = 0, seg_first_tile = 0, buf = 0;
   long long seg_u = 0;
   Tiles it(a, mi);
   for (int g = 0; it.more(); ++g) {
@@ -480,25 +568,29 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
     bool ok = wait_or_abort(&mi->qk_done[g & 1], (g >> 1) & 1, mi, a.status);
     tc_fence_after();
     const uint32_t ts = tmem + lanes + kColS + (g & 1) * 64;
-    uint32_t live[2] = {mi->mask[g & 1][2 * half], mi->mask[g & 1][2 * half + 1]};
+    uint32_t live[2] = {mi->mask[buf][2 * half], mi->mask[buf][2 * half + 1]};
     const int nv = limit - it.tile * kMt - half * 64;   // tokens of this half before the limit
     if (nv < 64) {
       live[0] = nv <= 0 ? 0u : (nv < 32 ? live[0] & ((1u << nv) - 1u) : live[0]);
       live[1] = nv <= 32 ? 0u : live[1] & ((1u << (nv - 32)) - 1u);
     }
-    float mt = -INFINITY;
+    __syncwarp();
+    if ((tid & 31) == 0) mbar_arrive(smem_u32(&mi->row_free[buf]));
+    float s[64];
+    tmem_ld64(ts, s);
+    if ((live[0] & live[1]) != 0xffffffffu) {
 #pragma unroll
-    for (int c2 = 0; c2 < 2; ++c2) {
-      float s[32];
-      tmem_ld32(ts + 32 * c2, s);
-      if (live[c2] == 0xffffffffu) {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) mt = fmaxf(mt, s[c]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) mt = fmaxf(mt, (live[c2] >> c) & 1u ? s[c] : -INFINITY);
-      }
+      for (int c = 0; c < 64; ++c) s[c] = (live[c >> 5] >> (c & 31)) & 1u ? s[c] : -INFINITY;
     }
+    float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+    for (int c = 4; c < 64; c += 8) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        m4[e] = c + 4 + e < 64 ? fmaxf(fmaxf(m4[e], s[c + e]), s[(c + 4 + e) & 63])
+                               : fmaxf(m4[e], s[c + e]);
+    }
+    float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
     mi->xch[g & 1][tid] = mt;
     named_sync(bar_id, 64);
     mt = fmaxf(mt, mi->xch[g & 1][tid ^ 64]) * a.c2;
@@ -510,36 +602,26 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       m = mt;
     }
     const float base = m == -INFINITY ? 0.0f : m;
-    float sum = 0.0f;
+    const float2 c2v = make_float2(a.c2, a.c2), bv = make_float2(-base, -base);
+    float2 sum2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
     uint32_t p[32];
 #pragma unroll
-    for (int c2 = 0; c2 < 2; ++c2) {
-      float s[32];
-      tmem_ld32(ts + 32 * c2, s);
-      if (live[c2] != 0xffffffffu) {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) s[c] = (live[c2] >> c) & 1u ? s[c] : -INFINITY;
-      }
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float p0 = ex2_approx(fmaf(s[2 * c], a.c2, -base));
-        const float p1 = ex2_approx(fmaf(s[2 * c + 1], a.c2, -base));
-        sum += p0 + p1;
-        p[16 * c2 + c] = half2_bits(p0, p1);
-      }
+    for (int c = 0; c < 32; ++c) {
+      float2 z = fma2(make_float2(s[2 * c], s[2 * c + 1]), c2v, bv);
+      z.x = ex2_approx(z.x);
+      z.y = ex2_approx(z.y);
+      sum2[c & 1] = add2(sum2[c & 1], z);
+      p[c] = half2_bits(z.x, z.y);
     }
+    sum2[0] = add2(sum2[0], sum2[1]);
+    const float sum = sum2[0].x + sum2[0].y;
     l = fmaf(l, f, sum);
     // P and O are free once PV of the tile before is done
     if (g > 0) ok = wait_or_abort(&mi->pv_done, (g - 1) & 1, mi, a.status) && ok;
     if (!first && __any_sync(0xffffffffu, f != 1.0f)) {
       tc_fence_after();
-      for (int c = 0; c < 8; ++c) {
-        float o[32];
-        tmem_ld32(tmem + lanes + kColO + 32 * c, o);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] *= f;
-        tmem_st32(tmem + lanes + kColO + 32 * c, o);
-      }
+#pragma unroll 1
+      for (int c = 0; c < 16; ++c) tmem_scale16(tmem + lanes + kColO + 16 * c, f);
       tmem_wait_st();
     }
 #pragma unroll
@@ -566,6 +648,7 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       const size_t orow = static_cast<size_t>(it.v) * a.entry_rows + row;
       const float inv = !whole ? 1.0f : (lt > 0.0f || lt != lt ? 1.0f / lt : 0.0f);
       const int prow = static_cast<int>(rank) * kCtaRows + r;
+#pragma unroll 1
       for (int c = 0; c < 8; ++c) {
         float o[32];
         tmem_ld32(tmem + lanes + kColO + 32 * c, o);
@@ -603,6 +686,7 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       tc_fence_before();
     }
     it.next(a);
+    buf = buf == 2 ? 0 : buf + 1;
   }
 }
 
@@ -610,7 +694,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     cache_mla_kernel(const __grid_constant__ CUtensorMap qmap, const MlaArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc* mi = reinterpret_cast<Misc*>(smem + kOffMisc);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (tid == 0) {
@@ -623,6 +708,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     mbar_init(smem_u32(&mi->qk_done[0]), 1);
     mbar_init(smem_u32(&mi->qk_done[1]), 1);
     mbar_init(smem_u32(&mi->pv_done), 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(smem_u32(&mi->row_full[i]), 1);
+      mbar_init(smem_u32(&mi->row_free[i]), kWidenWarps + kSoftWarps);
+    }
     mi->abort = 0;
     fence_mbar_init();
   }
@@ -680,8 +769,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   if (warp < kSoftWarps) {
     softmax_role(a, smem, mi, rank, tmem, pair);
   } else if (warp == kMmaWarp) {
-    if (lane == 0) mma_role(a, &qmap, smem, mi, rank, tmem);
-    __syncwarp();
+    mma_role(a, &qmap, smem, mi, rank, tmem);
+  } else if (warp == kRowWarp) {
+    row_role(a, mi);
   } else {
     widen_role(a, smem, mi, rank);
   }
@@ -812,6 +902,9 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
   a.page_table = page_table;
   a.max_pages = max_pages;
   a.page = page;
+  a.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (page == 1 << i) a.page_shift = i;
   a.T = T;
   a.batch = batch;
   a.ways = ways;
