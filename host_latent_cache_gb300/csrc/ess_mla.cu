@@ -41,9 +41,9 @@ constexpr int kPairRows = 128;        // query rows per pair
 constexpr int kCtaRows = 64;          // of them per CTA
 constexpr int kMaxPairs = 76;         // one pair per two SMs
 
-constexpr int kSoftWarps = 4;
-constexpr int kMmaWarp = 4;
-constexpr int kWidenWarp0 = 5;
+constexpr int kSoftWarps = 8;
+constexpr int kMmaWarp = 8;
+constexpr int kWidenWarp0 = 9;
 constexpr int kWidenWarps = 8;
 constexpr int kRowWarp = kWidenWarp0 + kWidenWarps;
 constexpr int kMlaThreads = (kRowWarp + 1) * 32;
@@ -62,22 +62,22 @@ constexpr uint32_t kColS = 256;
 constexpr float kGrow = 8.0f;         // log2 of the growth of a maximum that O absorbs unscaled
 
 struct Misc {
-  uint64_t q_full, q_ready, q_free, k_full, v_full, p_full, qk_done[2], pv_done;
+  uint64_t q_ready, q_free, k_full, vp_full, qk_done[2], pv_done;
   uint64_t row_full[kRing], row_free[kRing];
   uint32_t tmem;
   int abort;
-  int start_v;
-  int pad;
-  long long start_off, lo, hi;
-  long long scan[16];
+  int start_v, tiles;
+  long long start_off;
   uint32_t mask[kRing][4];            // tokens of a tile that exist
   int32_t row[kRing][kMt];            // cache rows of a tile's tokens, -1: none
-  float xch[2][kMt];                  // row statistics of a thread for its partner
+  float xch[4][kCtaRows];             // a row's statistics from the four threads that share it
+  float qexp[kCtaRows];               // log2 of what a query row was divided by
 };
 constexpr uint32_t kMlaSmem = 232448;
 static_assert(kOffMisc + sizeof(Misc) <= kMlaSmem, "shared memory of one CTA");
 
 struct MlaArgs {
+  const uint16_t* q;
   const uint8_t* rows;
   int n_rows;
   const int32_t* page_table;
@@ -142,28 +142,17 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // Bounded wait.  When it gives up (or another warp has) the role goes on
 // without waiting, so that every block-wide barrier is still reached; the
 // results are garbage and status says so.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Misc* mi,
                                               int* status) {
   const uint32_t addr = smem_u32(bar);
-  if (mbar_try_wait_cluster(addr, parity)) return true;
+  if (mbar_try_wait(addr, parity)) return true;
   volatile int* stop = &mi->abort;
   const long long t0 = clock64();
   while (!*stop) {
-    if (mbar_try_wait_cluster(addr, parity)) return true;
+    if (mbar_try_wait(addr, parity)) return true;
     if (clock64() - t0 > kWaitLimitCycles) {
       set_status(status, ESS_ERR_TIMEOUT);
       *stop = 1;
@@ -203,6 +192,19 @@ __device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// Barrier over `threads` threads that says whether any of them has x.
+__device__ __forceinline__ bool named_any(int id, int threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -229,27 +231,30 @@ __device__ __forceinline__ float2 add2(const float2& x, const float2& y) {
 
 // The tiles of one pair, in order: entry v, row tile rt, token tile.
 struct Tiles {
-  long long u, lo, hi;
+  int left;   // tiles from this one on
   int v, rt, tile, nt, len;
+  bool begins;   // the pair's first tile
 
   __device__ __forceinline__ Tiles(const MlaArgs& a, const Misc* mi) {
-    lo = u = mi->lo;
-    hi = mi->hi;
+    left = mi->tiles;
     v = mi->start_v;
     load(a);
     rt = static_cast<int>(mi->start_off / nt);
     tile = static_cast<int>(mi->start_off % nt);
+    begins = true;
   }
   __device__ __forceinline__ void load(const MlaArgs& a) {
     len = entry_len(a, v);
     nt = (len + kMt - 1) / kMt;
   }
-  __device__ __forceinline__ bool more() const { return u < hi; }
-  __device__ __forceinline__ bool first() const { return u == lo || tile == 0; }
-  __device__ __forceinline__ bool last() const { return u + 1 == hi || tile + 1 == nt; }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  // of a segment: a run of tiles of one entry and row tile
+  __device__ __forceinline__ bool first() const { return begins || tile == 0; }
+  __device__ __forceinline__ bool last() const { return left == 1 || tile + 1 == nt; }
   __device__ __forceinline__ void next(const MlaArgs& a) {
-    ++u;
-    if (++tile == nt && u < hi) {
+    begins = false;
+    --left;
+    if (++tile == nt && left > 0) {
       tile = 0;
       if (++rt == a.row_tiles) {
         rt = 0;
@@ -285,37 +290,22 @@ __device__ __forceinline__ int token_row(const MlaArgs& a, int v, int len, int e
   return static_cast<int>(row);
 }
 
-// 32 codes (one block) -> four 16-byte units of bf16 (K) or fp16 (V)
-__device__ __forceinline__ void widen_block(const uint4& codes, int byte, bool to_bf16,
-                                            uint4* unit) {
+// 32 codes (one block) -> four 16-byte units of fp16
+__device__ __forceinline__ void widen_block(const uint4& codes, int byte, uint4* unit) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-  const int eb = q4_exp_byte(byte);
-  if (to_bf16) {
-    const uint32_t s2 = q4_bf16_scale(eb);
+  const __half2 s2 =
+      __float2half2_rn(__uint_as_float(static_cast<uint32_t>(q4_exp_byte(byte)) << 23));
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t h[4];
-      e2m1_to_f16x2(w[q], h);
-      unit[q] = make_uint4(q4_bf16x2(h[0], s2), q4_bf16x2(h[1], s2), q4_bf16x2(h[2], s2),
-                           q4_bf16x2(h[3], s2));
+  for (int q = 0; q < 4; ++q) {
+    uint32_t h[4];
+    e2m1_to_f16x2(w[q], h);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), s2);
+      h[e] = *reinterpret_cast<const uint32_t*>(&r);
     }
-  } else {
-    const __half2 s2 = __float2half2_rn(__uint_as_float(static_cast<uint32_t>(eb) << 23));
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t h[4];
-      e2m1_to_f16x2(w[q], h);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), s2);
-        h[e] = *reinterpret_cast<const uint32_t*>(&r);
-      }
-      unit[q] = make_uint4(h[0], h[1], h[2], h[3]);
-    }
+    unit[q] = make_uint4(h[0], h[1], h[2], h[3]);
   }
-}
-__device__ __forceinline__ int byte_of(uint32_t w, int i) {
-  return static_cast<int>((w >> (8 * i)) & 0xffu);
 }
 
 // ---------------------------------------------------------------- roles
@@ -357,11 +347,9 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
                                            uint32_t rank) {
   const int wt = threadIdx.x - kWidenWarp0 * 32;   // 0..255
   const int w = wt >> 5, lane = wt & 31;
-  const uint32_t k_full = dsmem_addr(smem_u32(&mi->k_full), 0);
-  const uint32_t v_full = dsmem_addr(smem_u32(&mi->v_full), 0);
   uint8_t* sk = smem + kOffK;
   uint8_t* sv = smem + kOffV;
-  const int n = static_cast<int>(mi->hi - mi->lo);
+  const int n = mi->tiles;
   // K: instruction j covers rows 8w + 2j and + 1, lane = (row, chunk of 16);
   // V: tokens 16w + 4j .. + 3, lane = (token, chunk of 8 of this CTA's half)
   const int kc_ = lane & 15, kr_ = 8 * w + (lane >> 4);
@@ -397,12 +385,12 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
     }
   };
   // four units of one chunk, in the lane's order, to row r of a block
-  auto put = [&](uint8_t* blk, int r, int chunk, uint4 codes, int byte, bool to_bf16) {
+  auto put = [&](uint8_t* blk, int r, int chunk, uint4 codes, int byte) {
     uint4 c = codes;
     if (turn & 1) c = make_uint4(c.y, c.z, c.w, c.x);
     if (turn & 2) c = make_uint4(c.z, c.w, c.x, c.y);
     uint4 unit[4];
-    widen_block(c, byte, to_bf16, unit);
+    widen_block(c, byte, unit);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       *reinterpret_cast<uint4*>(blk + sw128_off(r, (chunk & 1) * 4 + ((q + turn) & 3))) = unit[q];
@@ -410,22 +398,22 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
   auto store_k = [&]() {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      put(sk + (kc_ >> 1) * kKBlk, kr_ + 2 * j, kc_, kc[j], ke[j], true);
+      put(sk + (kc_ >> 1) * kKBlk, kr_ + 2 * j, kc_, kc[j], ke[j]);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       *reinterpret_cast<uint4*>(sk + 8 * kKBlk +
                                 sw128_off(8 * w + 4 * j + (lane >> 3), lane & 7)) = kr[j];
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive_remote(k_full);
+    if (lane == 0) mbar_arrive(smem_u32(&mi->k_full));
   };
   auto store_v = [&]() {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      put(sv + (vc_ >> 1) * kVBlk, vt_ + 4 * j, vc_, vc[j], ve[j], false);
+      put(sv + (vc_ >> 1) * kVBlk, vt_ + 4 * j, vc_, vc[j], ve[j]);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive_remote(v_full);
+    if (lane == 0) mbar_arrive(smem_u32(&mi->vp_full));
   };
   // K runs one tile ahead of V: K of tile g + 1 is written beside PV of tile
   // g - 1, V of tile g beside QK of tile g + 1.  Slot s of the rows holds tile
@@ -466,25 +454,41 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
   }
 }
 
-// One warp per CTA: it loads the queries, and in the even CTA issues the MMAs.
-// The whole warp walks the tiles and one elected lane issues: with uniform
+// The odd CTA's full buffers, told to the even CTA's MMA warp by one warp: an
+// arrival across CTAs waits for its warp's loads in flight, which the widening
+// warps have and this one has not.
+__device__ __forceinline__ void forward_role(const MlaArgs& a, Misc* mi, int lane) {
+  const uint32_t k_full = dsmem_addr(smem_u32(&mi->k_full), 0);
+  const uint32_t vp_full = dsmem_addr(smem_u32(&mi->vp_full), 0);
+  const int n = mi->tiles;
+  for (int g = 0; g <= n; ++g) {   // in the order in which they are waited for
+    if (g < n) {
+      wait_or_abort(&mi->k_full, g & 1, mi, a.status);
+      if (lane == 0) mbar_arrive_remote(k_full);
+    }
+    if (g > 0) {
+      wait_or_abort(&mi->vp_full, (g - 1) & 1, mi, a.status);
+      if (lane == 0) mbar_arrive_remote(vp_full);
+    }
+  }
+}
+
+// One warp of the even CTA issues the MMAs.  The whole warp walks the tiles and one elected lane issues: with uniform
 // control flow the descriptors stay in uniform registers, and an MMA is issued
 // every 32 cycles (N = 128) instead of every 110.
-__device__ __forceinline__ void mma_role(const MlaArgs& a, const CUtensorMap* qmap, uint8_t* smem,
-                                         Misc* mi, uint32_t rank, uint32_t tmem) {
-  const uint32_t q_ready = dsmem_addr(smem_u32(&mi->q_ready), 0);
-  const uint32_t sq = smem_u32(smem + kOffQ);
-  const uint64_t dq = make_sdesc_sw128(sq, 16, 1024);
+__device__ __forceinline__ void mma_role(const MlaArgs& a, uint8_t* smem, Misc* mi,
+                                         uint32_t tmem) {
+  const uint64_t dq = make_sdesc_sw128(smem_u32(smem + kOffQ), 16, 1024);
   const uint64_t dk = make_sdesc_sw128(smem_u32(smem + kOffK), 16, 1024);
   const uint64_t dv = make_sdesc_sw128(smem_u32(smem + kOffV), kVBlk, 1024);
   const uint64_t dp = make_sdesc_sw128(smem_u32(smem + kOffP), 16, 1024);
-  const uint32_t idesc_qk = make_idesc(kFmtBF16, kFmtBF16, 0, kMt, kPairRows);
+  const uint32_t idesc_qk = make_idesc(kFmtF16, kFmtF16, 0, kMt, kPairRows);
+  const uint32_t idesc_rope = make_idesc(kFmtBF16, kFmtBF16, 0, kMt, kPairRows);
   const uint32_t idesc_pv = make_idesc(kFmtF16, kFmtF16, 1, 256, kPairRows);
   const bool lead = elect_one();
   bool ok = true;
   auto pv = [&](int g, bool accumulate) {
-    ok = wait_or_abort(&mi->v_full, g & 1, mi, a.status) && ok;
-    ok = wait_or_abort(&mi->p_full, g & 1, mi, a.status) && ok;
+    ok = wait_or_abort(&mi->vp_full, g & 1, mi, a.status) && ok;
     tc_fence_after();
     if (ok && lead) {
 #pragma unroll
@@ -503,110 +507,157 @@ __device__ __forceinline__ void mma_role(const MlaArgs& a, const CUtensorMap* qm
   for (int g = 0; it.more(); ++g) {
     const bool first = it.first(), last = it.last();
     if (first) {
-      if (seg > 0) ok = wait_or_abort(&mi->q_free, (seg - 1) & 1, mi, a.status) && ok;
-      if (lead) {
-        mbar_arrive_expect_tx(smem_u32(&mi->q_full), 9 * kKBlk);
-        const int y = it.v * a.entry_rows + it.rt * kPairRows + rank * kCtaRows;
-        for (int kb = 0; kb < 9; ++kb)
-          tma_load_2d(sq + kb * kKBlk, qmap, smem_u32(&mi->q_full), kb * 64, y);
-      }
-      __syncwarp();
-      if (rank == 0 && g > 0) pv(g - 1, acc);
-      ok = wait_or_abort(&mi->q_full, seg & 1, mi, a.status) && ok;
-      if (lead) mbar_arrive_remote(q_ready);
-      __syncwarp();
-      if (rank == 0) ok = wait_or_abort(&mi->q_ready, seg & 1, mi, a.status) && ok;
+      if (g > 0) pv(g - 1, acc);
+      ok = wait_or_abort(&mi->q_ready, seg & 1, mi, a.status) && ok;
       ++seg;
     }
-    if (rank == 0) {
-      ok = wait_or_abort(&mi->k_full, g & 1, mi, a.status) && ok;
-      tc_fence_after();
-      if (ok && lead) {
+    ok = wait_or_abort(&mi->k_full, g & 1, mi, a.status) && ok;
+    tc_fence_after();
+    if (ok && lead) {
 #pragma unroll
-        for (int k = 0; k < 36; ++k)
-          umma_f16_pair(tmem + kColS + (g & 1) * 64, dq + ((k >> 2) * kKBlk + (k & 3) * 32) / 16,
-                        dk + ((k >> 2) * kKBlk + (k & 3) * 32) / 16, idesc_qk, k != 0);
-        umma_commit_pair(smem_u32(&mi->qk_done[g & 1]));
-        if (last) umma_commit_pair(smem_u32(&mi->q_free));
-      }
-      __syncwarp();
-      if (!first) pv(g - 1, acc);
+      for (int k = 0; k < 36; ++k)
+        umma_f16_pair(tmem + kColS + (g & 1) * 64, dq + ((k >> 2) * kKBlk + (k & 3) * 32) / 16,
+                      dk + ((k >> 2) * kKBlk + (k & 3) * 32) / 16, k < 32 ? idesc_qk : idesc_rope,
+                      k != 0);
+      umma_commit_pair(smem_u32(&mi->qk_done[g & 1]));
+      if (last) umma_commit_pair(smem_u32(&mi->q_free));
     }
+    __syncwarp();
+    if (!first) pv(g - 1, acc);
     acc = !first;
     it.next(a);
-    if (rank == 0 && !it.more()) pv(g, acc);
+    if (!it.more()) pv(g, acc);
   }
-  // the last arrival on this CTA's q_free, which nothing else waits for
-  wait_or_abort(&mi->q_free, (seg - 1) & 1, mi, a.status);
 }
 
-// Four warps: thread = one query row and half of a tile's tokens, or half of
-// the row's output dims.
+// Eight rows of queries per warp into shared memory: the latent part as fp16,
+// beside the fp16 latents, each row divided by the power of two that brings
+// its largest value to [2^14, 2^15) (exact down to 2^-31 of that value, with an
+// error below 2^-39 of it under that); the RoPE part, divided alike, as bf16.
+__device__ __forceinline__ void load_queries(const MlaArgs& a, uint8_t* smem, Misc* mi, int v,
+                                             int row0, int warp, int lane) {
+  constexpr int kFly = 2;   // rows in flight
+  uint8_t* sq = smem + kOffQ;
+#pragma unroll 1
+  for (int i0 = 0; i0 < 8; i0 += kFly) {
+    uint4 u[kFly][2];
+    uint32_t rope[kFly];
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+      const int row = row0 + warp * 8 + i0 + i;
+      u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      rope[i] = 0u;
+      if (row < a.entry_rows) {
+        const uint16_t* q = a.q + (static_cast<size_t>(v) * a.entry_rows + row) * kRowDim;
+        u[i][0] = reinterpret_cast<const uint4*>(q)[lane];
+        u[i][1] = reinterpret_cast<const uint4*>(q)[32 + lane];
+        rope[i] = reinterpret_cast<const uint32_t*>(q + kLatent)[lane];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+      const int r = warp * 8 + i0 + i;
+      float x[16];
+      unpack8(u[i][0], x);
+      unpack8(u[i][1], x + 8);
+      const float ra = bf16_lo(rope[i]), rb = bf16_hi(rope[i]);
+      const float mx = group_max<32>(
+          fmaxf(fmaxf(amax8(x), amax8(x + 8)), fmaxf(fabsf(ra), fabsf(rb))));
+      // 2^e <= mx < 2^(e + 1); rows of zeros, infinities and NaN as they are
+      const int e = mx > 0.0f && mx < INFINITY
+                        ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 - 14
+                        : 0;
+      const int ec = min(max(e, -126), 126);
+      const float inv = exp2i(-ec);
+      if (lane == 0) mi->qexp[r] = static_cast<float>(ec);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float* y = x + 8 * h;
+        // unit 32 h + lane of the row: 64-dim block 4 h + lane / 8
+        *reinterpret_cast<uint4*>(sq + (4 * h + (lane >> 3)) * kKBlk + sw128_off(r, lane & 7)) =
+            make_uint4(half2_bits(y[0] * inv, y[1] * inv), half2_bits(y[2] * inv, y[3] * inv),
+                       half2_bits(y[4] * inv, y[5] * inv), half2_bits(y[6] * inv, y[7] * inv));
+      }
+      *reinterpret_cast<uint32_t*>(sq + 8 * kKBlk + sw128_off(r, lane >> 2) + (lane & 3) * 4) =
+          bf16x2_bits(ra * inv, rb * inv);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive_remote(dsmem_addr(smem_u32(&mi->q_ready), 0));
+}
+
+// Eight warps.  Four threads share a query row: (half, sub) names 32 of a
+// tile's tokens, and 128 of the row's output dims.
 __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Misc* mi,
                                              uint32_t rank, uint32_t tmem, int pair) {
-  const int tid = threadIdx.x, warp = tid >> 5;
-  const int r = tid & 63, half = tid >> 6;
-  const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-  const uint32_t p_full = dsmem_addr(smem_u32(&mi->p_full), 0);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = (warp & 1) * 32 + lane, half = (warp >> 1) & 1, sub = warp >> 2;
+  const int part = 2 * half + sub;
+  const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t to = tmem + lanes + kColO + sub * 128;
   uint8_t* sp = smem + kOffP + half * kKBlk;
-  const int bar_id = 1 + (warp & 1);   // warps w and w + 2 hold the same rows
-  float m = -INFINITY, l = 0.0f;
-  int limit = 0, seg_first_tile = 0, buf = 0;
-  long long seg_u = 0;
+  const int bar_id = 1 + (warp & 1);   // the four warps that hold the same rows
+  float m = -INFINITY, l = 0.0f, c2 = 0.0f;
+  int limit = 0, seg_first_tile = 0, buf = 0, seg = 0;
   Tiles it(a, mi);
+  load_queries(a, smem, mi, it.v, it.rt * kPairRows + static_cast<int>(rank) * kCtaRows, warp,
+               lane);
   for (int g = 0; it.more(); ++g) {
     const bool first = it.first(), last = it.last();
     if (first) {
       const int row = it.rt * kPairRows + static_cast<int>(rank) * kCtaRows + r;
       limit = row >= a.entry_rows ? 0 : it.len;
       if (!a.tokens && limit) limit = it.len - (a.ways - 1) + row / a.heads;
+      named_sync(3, kSoftWarps * 32);   // the rows' scales
+      c2 = a.c2 * exp2f(mi->qexp[r]);
       m = -INFINITY;
       l = 0.0f;
       seg_first_tile = it.tile;
-      seg_u = it.u;
     }
     bool ok = wait_or_abort(&mi->qk_done[g & 1], (g >> 1) & 1, mi, a.status);
     tc_fence_after();
-    const uint32_t ts = tmem + lanes + kColS + (g & 1) * 64;
-    uint32_t live[2] = {mi->mask[buf][2 * half], mi->mask[buf][2 * half + 1]};
-    const int nv = limit - it.tile * kMt - half * 64;   // tokens of this half before the limit
-    if (nv < 64) {
-      live[0] = nv <= 0 ? 0u : (nv < 32 ? live[0] & ((1u << nv) - 1u) : live[0]);
-      live[1] = nv <= 32 ? 0u : live[1] & ((1u << (nv - 32)) - 1u);
-    }
+    uint32_t live = mi->mask[buf][part];
+    const int nv = limit - it.tile * kMt - part * 32;   // tokens of these 32 before the limit
+    if (nv < 32) live = nv <= 0 ? 0u : live & ((1u << nv) - 1u);
     __syncwarp();
-    if ((tid & 31) == 0) mbar_arrive(smem_u32(&mi->row_free[buf]));
-    float s[64];
-    tmem_ld64(ts, s);
-    if ((live[0] & live[1]) != 0xffffffffu) {
+    if (lane == 0) mbar_arrive(smem_u32(&mi->row_free[buf]));
+    float s[32];
+    tmem_ld32(tmem + lanes + kColS + (g & 1) * 64 + sub * 32, s);
+    if (live != 0xffffffffu) {
 #pragma unroll
-      for (int c = 0; c < 64; ++c) s[c] = (live[c >> 5] >> (c & 31)) & 1u ? s[c] : -INFINITY;
+      for (int c = 0; c < 32; ++c) s[c] = (live >> c) & 1u ? s[c] : -INFINITY;
     }
     float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-    for (int c = 4; c < 64; c += 8) {
+    for (int c = 4; c < 28; c += 8) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        m4[e] = c + 4 + e < 64 ? fmaxf(fmaxf(m4[e], s[c + e]), s[(c + 4 + e) & 63])
-                               : fmaxf(m4[e], s[c + e]);
+      for (int e = 0; e < 4; ++e) m4[e] = fmaxf(fmaxf(m4[e], s[c + e]), s[c + 4 + e]);
     }
-    float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-    mi->xch[g & 1][tid] = mt;
-    named_sync(bar_id, 64);
-    mt = fmaxf(mt, mi->xch[g & 1][tid ^ 64]) * a.c2;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], s[28 + e]);
+    float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
+    // The row's maximum is only looked up when one of its parts outgrew the
+    // one in use by more than 2^kGrow (or there is none yet).
     float f = 1.0f;
-    if (m == -INFINITY) {
-      m = mt;   // nothing summed yet: O's row is zero
-    } else if (mt > m + kGrow) {
-      f = ex2_approx(m - mt);
-      m = mt;
+    if (named_any(bar_id, kSoftWarps * 16, mt > m + kGrow || (m == -INFINITY && mt > m))) {
+      mi->xch[part][r] = mt;
+      named_sync(bar_id, kSoftWarps * 16);
+      mt = fmaxf(fmaxf(mi->xch[0][r], mi->xch[1][r]), fmaxf(mi->xch[2][r], mi->xch[3][r]));
+      named_sync(bar_id, kSoftWarps * 16);
+      if (m == -INFINITY) {
+        m = mt;   // nothing summed yet: O's row is zero
+      } else if (mt > m + kGrow) {
+        f = ex2_approx(m - mt);
+        m = mt;
+      }
     }
     const float base = m == -INFINITY ? 0.0f : m;
-    const float2 c2v = make_float2(a.c2, a.c2), bv = make_float2(-base, -base);
+    const float2 c2v = make_float2(c2, c2), bv = make_float2(-base, -base);
     float2 sum2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-    uint32_t p[32];
+    uint32_t p[16];
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
+    for (int c = 0; c < 16; ++c) {
       float2 z = fma2(make_float2(s[2 * c], s[2 * c + 1]), c2v, bv);
       z.x = ex2_approx(z.x);
       z.y = ex2_approx(z.y);
@@ -614,48 +665,58 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       p[c] = half2_bits(z.x, z.y);
     }
     sum2[0] = add2(sum2[0], sum2[1]);
-    const float sum = sum2[0].x + sum2[0].y;
-    l = fmaf(l, f, sum);
+    l = fmaf(l, f, sum2[0].x + sum2[0].y);
     // P and O are free once PV of the tile before is done
     if (g > 0) ok = wait_or_abort(&mi->pv_done, (g - 1) & 1, mi, a.status) && ok;
     if (!first && __any_sync(0xffffffffu, f != 1.0f)) {
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < 16; ++c) tmem_scale16(tmem + lanes + kColO + 16 * c, f);
+      for (int c = 0; c < 8; ++c) tmem_scale16(to + 16 * c, f);
       tmem_wait_st();
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      *reinterpret_cast<uint4*>(sp + sw128_off(r, u)) =
+    for (int u = 0; u < 4; ++u)
+      *reinterpret_cast<uint4*>(sp + sw128_off(r, 4 * sub + u)) =
           make_uint4(p[4 * u], p[4 * u + 1], p[4 * u + 2], p[4 * u + 3]);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncwarp();
-    if ((tid & 31) == 0) mbar_arrive_remote(p_full);
+    if (lane == 0) mbar_arrive(smem_u32(&mi->vp_full));
 
-    if (last) {
+    if (!last) {
+      it.next(a);
+    } else {
+      const int v = it.v, row0 = it.rt * kPairRows + static_cast<int>(rank) * kCtaRows;
+      const int span = it.v * a.row_tiles + it.rt;
+      const bool ends = it.tile + 1 == it.nt;
+      const bool whole = seg_first_tile == 0 && ends;
+      const int slot = pair * 2 + (seg == 0 ? 0 : 1);
+      it.next(a);
+      if (it.more()) {   // the next segment's queries, ahead of this one's output
+        wait_or_abort(&mi->q_free, seg & 1, mi, a.status);
+        load_queries(a, smem, mi, it.v, it.rt * kPairRows + static_cast<int>(rank) * kCtaRows,
+                     warp, lane);
+      }
+      ++seg;
       // the whole row's sum, then O out of TMEM: final, or a partial
-      mi->xch[(g & 1) ^ 1][tid] = l;
-      named_sync(bar_id, 64);
-      const float lt = l + mi->xch[(g & 1) ^ 1][tid ^ 64];
-      named_sync(bar_id, 64);
-      const bool whole = seg_first_tile == 0 && it.tile + 1 == it.nt;
-      const int slot = pair * 2 + (seg_u == it.lo ? 0 : 1);
+      mi->xch[part][r] = l;
+      named_sync(bar_id, kSoftWarps * 16);
+      const float lt = (mi->xch[0][r] + mi->xch[1][r]) + (mi->xch[2][r] + mi->xch[3][r]);
+      named_sync(bar_id, kSoftWarps * 16);
       ok = wait_or_abort(&mi->pv_done, g & 1, mi, a.status) && ok;
       tc_fence_after();
-      const int row = it.rt * kPairRows + static_cast<int>(rank) * kCtaRows + r;
-      const bool mine = row < a.entry_rows;
-      const size_t orow = static_cast<size_t>(it.v) * a.entry_rows + row;
+      const bool mine = row0 + r < a.entry_rows;
+      const size_t orow = static_cast<size_t>(v) * a.entry_rows + row0 + r;
       const float inv = !whole ? 1.0f : (lt > 0.0f || lt != lt ? 1.0f / lt : 0.0f);
       const int prow = static_cast<int>(rank) * kCtaRows + r;
+      const int d0 = half * 256 + sub * 128;
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 4; ++c) {
         float o[32];
-        tmem_ld32(tmem + lanes + kColO + 32 * c, o);
-        const int d0 = half * 256 + 32 * c;
+        tmem_ld32(to + 32 * c, o);
         if (whole) {
           if (mine) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * kLatent + d0);
+            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * kLatent + d0 + 32 * c);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] *= inv;
 #pragma unroll
@@ -663,13 +724,13 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
           }
         } else {
           float4* dst = reinterpret_cast<float4*>(
-              a.part_o + (static_cast<size_t>(slot) * kPairRows + prow) * kLatent + d0);
+              a.part_o + (static_cast<size_t>(slot) * kPairRows + prow) * kLatent + d0 + 32 * c);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
       }
-      if (half == 0) {
+      if (part == 0) {
         if (whole) {
           if (mine && a.lse)
             a.lse[orow] = lt > 0.0f || lt != lt ? (m + log2f(lt)) * 0.69314718055994531f
@@ -679,19 +740,19 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
         }
       }
       if (tid == 0 && rank == 0) {
-        int2* sp2 = a.span + static_cast<size_t>(it.v) * a.row_tiles + it.rt;
-        if (seg_first_tile == 0) sp2->x = slot;
-        if (it.tile + 1 == it.nt) sp2->y = pair;
+        if (seg_first_tile == 0) a.span[span].x = slot;
+        if (ends) a.span[span].y = pair;
       }
       tc_fence_before();
     }
-    it.next(a);
     buf = buf == 2 ? 0 : buf + 1;
   }
+  // the last arrival on this CTA's q_free, which nothing else waits for
+  wait_or_abort(&mi->q_free, (seg - 1) & 1, mi, a.status);
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
-    cache_mla_kernel(const __grid_constant__ CUtensorMap qmap, const MlaArgs a) {
+    cache_mla_kernel(const MlaArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc* mi = reinterpret_cast<Misc*>(smem + kOffMisc);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -699,12 +760,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (tid == 0) {
-    mbar_init(smem_u32(&mi->q_full), 1);
-    mbar_init(smem_u32(&mi->q_ready), 2);
+    mbar_init(smem_u32(&mi->q_ready), 2 * kSoftWarps);
     mbar_init(smem_u32(&mi->q_free), 1);
-    mbar_init(smem_u32(&mi->k_full), 2 * kWidenWarps);
-    mbar_init(smem_u32(&mi->v_full), 2 * kWidenWarps);
-    mbar_init(smem_u32(&mi->p_full), 2 * kSoftWarps);
+    // the even CTA's also count the odd CTA's, forwarded as one
+    mbar_init(smem_u32(&mi->k_full), kWidenWarps + (rank == 0 ? 1 : 0));
+    mbar_init(smem_u32(&mi->vp_full), kWidenWarps + kSoftWarps + (rank == 0 ? 1 : 0));
     mbar_init(smem_u32(&mi->qk_done[0]), 1);
     mbar_init(smem_u32(&mi->qk_done[1]), 1);
     mbar_init(smem_u32(&mi->pv_done), 1);
@@ -729,13 +789,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     const long long x = __shfl_up_sync(0xffffffffu, before, o);
     if (lane >= o) before += x;
   }
-  if (lane == 31) mi->scan[warp] = before;
+  long long* scan = reinterpret_cast<long long*>(mi->row);   // free until the roles start
+  if (lane == 31) scan[warp] = before;
   __syncthreads();
   long long total = 0;
   before -= mine;
   for (int w = 0; w < kMlaThreads / 32; ++w) {
-    if (w < warp) before += mi->scan[w];
-    total += mi->scan[w];
+    if (w < warp) before += scan[w];
+    total += scan[w];
   }
   // neighbouring pairs share a request, so none between two may be idle
   const long long busy = total < pairs ? total : pairs;
@@ -751,12 +812,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     }
     mi->start_v = v;
     mi->start_off = off;
-    mi->lo = lo;
-    mi->hi = hi;
+    mi->tiles = static_cast<int>(hi - lo);
   }
   if (warp == kMmaWarp) {
-    if (lane == 0) tma_prefetch_desc(&qmap);
-    __syncwarp();
     tmem_alloc_pair(smem_u32(&mi->tmem), 512);
     tmem_relinquish_pair();
   }
@@ -769,7 +827,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   if (warp < kSoftWarps) {
     softmax_role(a, smem, mi, rank, tmem, pair);
   } else if (warp == kMmaWarp) {
-    mma_role(a, &qmap, smem, mi, rank, tmem);
+    if (rank == 0) mma_role(a, smem, mi, tmem);
+    else forward_role(a, mi, lane);
   } else if (warp == kRowWarp) {
     row_role(a, mi);
   } else {
@@ -892,11 +951,8 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return ESS_ERR_CUDA;
   const long long all_rows = static_cast<long long>(batch) * ways * heads;
-  CUtensorMap qmap;
-  if (!encode_map_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, kRowDim, all_rows, kRowBytes, 64,
-                     kCtaRows))
-    return ESS_ERR_CUDA;
   MlaArgs a;
+  a.q = static_cast<const uint16_t*>(q);
   a.rows = static_cast<const uint8_t*>(rows);
   a.n_rows = static_cast<int>(n_rows);
   a.page_table = page_table;
@@ -933,7 +989,7 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
   cudaError_t e = cudaFuncSetAttribute(cache_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kMlaSmem));
   if (e != cudaSuccess) return ESS_ERR_CUDA;
-  e = launch_pdl(cache_mla_kernel, dim3(2 * pairs), dim3(kMlaThreads), kMlaSmem, st, qmap, a);
+  e = launch_pdl(cache_mla_kernel, dim3(2 * pairs), dim3(kMlaThreads), kMlaSmem, st, a);
   if (e != cudaSuccess) return ESS_ERR_CUDA;
   e = launch_pdl(cache_mla_join_kernel, dim3(static_cast<unsigned>(all_rows)), dim3(128), 0, st, a);
   return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
