@@ -69,7 +69,7 @@ struct Misc {
   int start_v, tiles;
   long long start_off;
   uint32_t mask[kRing][4];            // tokens of a tile that exist
-  int32_t row[kRing][kMt];            // cache rows of a tile's tokens, -1: none
+  int32_t row[kRing][kMt];            // cache rows of a tile's tokens (0 for one that is not)
   float xch[4][kCtaRows];             // a row's statistics from the four threads that share it
   float qexp[kCtaRows];               // log2 of what a query row was divided by
 };
@@ -172,25 +172,42 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// this lane's 16 consecutive columns times f, in place
-__device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f) {
-  uint32_t r[16];
+// two runs of 16 consecutive columns of this lane
+__device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, float* v) {
+  uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
       "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t0), "r"(t1)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// this lane's 8 consecutive columns times f, in place
+__device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
       : "r"(taddr)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+               "r"(r[7])
+               : "memory");
 }
 // Barrier over `threads` threads that says whether any of them has x.
 __device__ __forceinline__ bool named_any(int id, int threads, bool x) {
@@ -323,7 +340,7 @@ __device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
     if (turn > 0) wait_or_abort(&mi->row_free[slot], (turn - 1) & 1, mi, a.status);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      mi->row[slot][32 * j + lane] = row[j];
+      mi->row[slot][32 * j + lane] = max(row[j], 0);
       const uint32_t m = __ballot_sync(0xffffffffu, row[j] >= 0);
       if (lane == 0) mi->mask[slot][j] = m;
     }
@@ -339,81 +356,73 @@ __device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
 
 // Eight warps: gather the rows of a tile and widen them, K of this CTA's 64
 // tokens, and V of its 256 dims of all 128 tokens.  Eight neighbouring lanes
-// read 128 neighbouring bytes of one row.  Their 16-byte codes make four
-// 16-byte units each, in only two of the eight bank groups for a given unit
-// number, so a lane stores its units in an order turned by its place: then
-// eight lanes cover all bank groups at every store.
+// read 128 neighbouring bytes of one row, eight chunks of 32 codes; each chunk
+// makes four 16-byte units of 8 dims.  Unit q of chunk c goes to 64-dim block
+// q (of four), place c: at every store the eight lanes then fill all eight
+// bank groups of one swizzled row.  So the dims lie in the order
+// (half, q, c, 8 dims) for (half, c, q, 8 dims); Q is stored in the same
+// order, and O comes out in it.  A token that does not exist reads row 0: its
+// scores are masked, and its V, finite like all codes, meets P = 0.
 __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc* mi,
                                            uint32_t rank) {
   const int wt = threadIdx.x - kWidenWarp0 * 32;   // 0..255
   const int w = wt >> 5, lane = wt & 31;
-  uint8_t* sk = smem + kOffK;
-  uint8_t* sv = smem + kOffV;
   const int n = mi->tiles;
-  // K: instruction j covers rows 8w + 2j and + 1, lane = (row, chunk of 16);
+  // K: load j covers rows 8w + 2j and + 1, lane = (row, chunk of 16);
   // V: tokens 16w + 4j .. + 3, lane = (token, chunk of 8 of this CTA's half)
-  const int kc_ = lane & 15, kr_ = 8 * w + (lane >> 4);
-  const int vc_ = lane & 7, vt_ = 16 * w + (lane >> 3);
-  const int turn = (lane >> 1) & 3;   // the same for both mappings
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const int kch = lane & 15, krow = 8 * w + (lane >> 4);
+  const int c8 = lane & 7, vtok = 16 * w + (lane >> 3);
+  const uint8_t* kcode = a.rows + 16 * kch;
+  const uint8_t* kexp = a.rows + 256 + kch;
+  const uint8_t* krope = a.rows + 272 + 16 * c8;
+  const uint8_t* vcode = a.rows + 128 * rank + 16 * c8;
+  const uint8_t* vexp = a.rows + 256 + 8 * rank + c8;
+  uint8_t* sk = smem + kOffK + (kch >> 3) * 4 * kKBlk + krow * 128;
+  uint8_t* sv = smem + kOffV + vtok * 128;
 
   uint4 kc[4], kr[2], vc[4];   // raw codes and RoPE units
   int ke[4], ve[4];            // exponent bytes
+  auto at = [](int row) { return static_cast<size_t>(static_cast<uint32_t>(row)) * kQ4RowBytes; };
   auto load_k = [&](int slot) {
     const int32_t* rows = mi->row[slot] + rank * kCtaRows;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = rows[kr_ + 2 * j];
-      const uint8_t* s = a.rows + static_cast<size_t>(max(row, 0)) * kQ4RowBytes;
-      kc[j] = row < 0 ? zero : reinterpret_cast<const uint4*>(s)[kc_];
-      ke[j] = row < 0 ? 127 : s[256 + kc_];
+      const size_t off = at(rows[krow + 2 * j]);
+      kc[j] = *reinterpret_cast<const uint4*>(kcode + off);
+      ke[j] = kexp[off];
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int row = rows[8 * w + 4 * j + (lane >> 3)];
-      const uint8_t* s = a.rows + static_cast<size_t>(max(row, 0)) * kQ4RowBytes;
-      kr[j] = row < 0 ? zero : reinterpret_cast<const uint4*>(s + 272)[lane & 7];
-    }
+    for (int j = 0; j < 2; ++j)
+      kr[j] = *reinterpret_cast<const uint4*>(krope + at(rows[8 * w + 4 * j + (lane >> 3)]));
   };
   auto load_v = [&](int slot) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = mi->row[slot][vt_ + 4 * j];
-      const uint8_t* s = a.rows + static_cast<size_t>(max(row, 0)) * kQ4RowBytes;
-      vc[j] = row < 0 ? zero : reinterpret_cast<const uint4*>(s + 128 * rank)[vc_];
-      ve[j] = row < 0 ? 127 : s[256 + 8 * rank + vc_];
+      const size_t off = at(mi->row[slot][vtok + 4 * j]);
+      vc[j] = *reinterpret_cast<const uint4*>(vcode + off);
+      ve[j] = vexp[off];
     }
   };
-  // four units of one chunk, in the lane's order, to row r of a block
-  auto put = [&](uint8_t* blk, int r, int chunk, uint4 codes, int byte) {
-    uint4 c = codes;
-    if (turn & 1) c = make_uint4(c.y, c.z, c.w, c.x);
-    if (turn & 2) c = make_uint4(c.z, c.w, c.x, c.y);
+  auto put = [&](uint8_t* d, uint32_t block_bytes, const uint4& codes, int byte) {
     uint4 unit[4];
-    widen_block(c, byte, unit);
+    widen_block(codes, byte, unit);
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<uint4*>(blk + sw128_off(r, (chunk & 1) * 4 + ((q + turn) & 3))) = unit[q];
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(d + q * block_bytes) = unit[q];
   };
   auto store_k = [&]() {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      put(sk + (kc_ >> 1) * kKBlk, kr_ + 2 * j, kc_, kc[j], ke[j]);
+      put(sk + 256 * j + ((c8 ^ ((lane >> 4) + 2 * j)) << 4), kKBlk, kc[j], ke[j]);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      *reinterpret_cast<uint4*>(sk + 8 * kKBlk +
-                                sw128_off(8 * w + 4 * j + (lane >> 3), lane & 7)) = kr[j];
+      *reinterpret_cast<uint4*>(smem + kOffK + 8 * kKBlk +
+                                sw128_off(8 * w + 4 * j + (lane >> 3), c8)) = kr[j];
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&mi->k_full));
   };
-  auto store_v = [&]() {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      put(sv + (vc_ >> 1) * kVBlk, vt_ + 4 * j, vc_, vc[j], ve[j]);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&mi->vp_full));
+  auto put_v = [&](int j) {
+    put(sv + 512 * j + ((c8 ^ ((lane >> 3) + 4 * (j & 1))) << 4), kVBlk, vc[j], ve[j]);
   };
   // K runs one tile ahead of V: K of tile g + 1 is written beside PV of tile
   // g - 1, V of tile g beside QK of tile g + 1.  Slot s of the rows holds tile
@@ -435,12 +444,19 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
       wait_or_abort(&mi->qk_done[g & 1], (g >> 1) & 1, mi, a.status);
       store_k();
     }
-    if (g + 2 < n) {
-      wait_or_abort(&mi->row_full[slot2], turn2 & 1, mi, a.status);
-      load_k(slot2);
-    }
+    if (g + 2 < n) wait_or_abort(&mi->row_full[slot2], turn2 & 1, mi, a.status);
     if (g > 0) wait_or_abort(&mi->pv_done, (g - 1) & 1, mi, a.status);
-    store_v();
+    // the next loads start once this tile's V has arrived: a wait for a load
+    // also waits for later ones
+    put_v(0);
+    asm volatile("" ::: "memory");
+    if (g + 2 < n) load_k(slot2);
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int j = 1; j < 4; ++j) put_v(j);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&mi->vp_full));
     if (g + 1 < n) {
       load_v(slot1);
       __syncwarp();
@@ -573,8 +589,8 @@ __device__ __forceinline__ void load_queries(const MlaArgs& a, uint8_t* smem, Mi
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float* y = x + 8 * h;
-        // unit 32 h + lane of the row: 64-dim block 4 h + lane / 8
-        *reinterpret_cast<uint4*>(sq + (4 * h + (lane >> 3)) * kKBlk + sw128_off(r, lane & 7)) =
+        // unit 32 h + lane: chunk 8 h + lane / 4, its unit lane % 4
+        *reinterpret_cast<uint4*>(sq + (4 * h + (lane & 3)) * kKBlk + sw128_off(r, lane >> 2)) =
             make_uint4(half2_bits(y[0] * inv, y[1] * inv), half2_bits(y[2] * inv, y[3] * inv),
                        half2_bits(y[4] * inv, y[5] * inv), half2_bits(y[6] * inv, y[7] * inv));
       }
@@ -671,7 +687,7 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
     if (!first && __any_sync(0xffffffffu, f != 1.0f)) {
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) tmem_scale16(to + 16 * c, f);
+      for (int c = 0; c < 16; ++c) tmem_scale8(to + 8 * c, f);
       tmem_wait_st();
     }
 #pragma unroll
@@ -709,25 +725,32 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       const size_t orow = static_cast<size_t>(v) * a.entry_rows + row0 + r;
       const float inv = !whole ? 1.0f : (lt > 0.0f || lt != lt ? 1.0f / lt : 0.0f);
       const int prow = static_cast<int>(rank) * kCtaRows + r;
-      const int d0 = half * 256 + sub * 128;
+      // column 64 q + 8 c + e holds dim 256 half + 32 c + 8 q + e; q = 2 sub, 2 sub + 1
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        float o[32];
-        tmem_ld32(to + 32 * c, o);
+      for (int c = 0; c < 8; c += 2) {
+        float o[32];   // units (c, q), (c + 1, q), then the same of q + 1
+        tmem_ld16x2(to + 8 * c, to + 64 + 8 * c, o);
         if (whole) {
           if (mine) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * kLatent + d0 + 32 * c);
+            uint16_t* dst = a.out + orow * kLatent + half * 256 + sub * 16 + 32 * c;
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] *= inv;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) dst[q] = pack8_bf16(o + 8 * q);
+            for (int x = 0; x < 2; ++x) {
+              reinterpret_cast<uint4*>(dst + 32 * x)[0] = pack8_bf16(o + 8 * x);
+              reinterpret_cast<uint4*>(dst + 32 * x)[1] = pack8_bf16(o + 16 + 8 * x);
+            }
           }
-        } else {
-          float4* dst = reinterpret_cast<float4*>(
-              a.part_o + (static_cast<size_t>(slot) * kPairRows + prow) * kLatent + d0 + 32 * c);
+        } else {   // in the order of the columns
+          float* dst = a.part_o + (static_cast<size_t>(slot) * kPairRows + prow) * kLatent +
+                       half * 256 + sub * 128 + 8 * c;
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              reinterpret_cast<float4*>(dst + 64 * x)[y] =
+                  make_float4(o[16 * x + 4 * y], o[16 * x + 4 * y + 1], o[16 * x + 4 * y + 2],
+                              o[16 * x + 4 * y + 3]);
         }
       }
       if (part == 0) {
@@ -865,11 +888,13 @@ __global__ void __launch_bounds__(128) cache_mla_join_kernel(const MlaArgs a) {
   if (p0 == sp.y) return;
   const int pr = row % kPairRows;
   float mx = -INFINITY, l = 0.0f;
+  // dims 4t .. 4t + 3 in the partials' order of columns
+  const int col = (t & ~63) * 4 + ((t >> 1) & 3) * 64 + ((t >> 3) & 7) * 8 + (t & 1) * 4;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int p = p0; p <= sp.y; ++p) {
     const size_t i = static_cast<size_t>(p == p0 ? sp.x : 2 * p) * kPairRows + pr;
     const float2 ml = a.part_ml[i];
-    const float4 o = reinterpret_cast<const float4*>(a.part_o + i * kLatent)[t];
+    const float4 o = *reinterpret_cast<const float4*>(a.part_o + i * kLatent + col);
     const float m2 = fmaxf(mx, ml.x);
     const float base = m2 == -INFINITY ? 0.0f : m2;
     const float f = exp2f(mx - base), w = exp2f(ml.x - base);
