@@ -44,7 +44,7 @@ constexpr int kMaxPairs = 76;         // one pair per two SMs
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 8;
 constexpr int kWidenWarp0 = 9;
-constexpr int kWidenWarps = 8;
+constexpr int kWidenWarps = 16;
 constexpr int kRowWarp = kWidenWarp0 + kWidenWarps;
 constexpr int kMlaThreads = (kRowWarp + 1) * 32;
 constexpr int kRing = 3;              // tiles whose rows are known ahead
@@ -62,7 +62,7 @@ constexpr uint32_t kColS = 256;
 constexpr float kGrow = 8.0f;         // log2 of the growth of a maximum that O absorbs unscaled
 
 struct Misc {
-  uint64_t q_ready, q_free, k_full, vp_full, qk_done[2], pv_done;
+  uint64_t q_ready, q_free, k_full[2], vp_full[2], qk_half, qk_done[2], pv_half, pv_done;
   uint64_t row_full[kRing], row_free[kRing];
   uint32_t tmem;
   int abort;
@@ -138,9 +138,12 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
+// Arrive on a barrier of either CTA.  The default (CTA-scope) release is
+// enough: what it orders are writes to this CTA's own shared memory, which
+// fence.proxy.async has already put before the tensor core's reads of it.  A
+// cluster-scope release would wait for the warp's loads in flight.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // Bounded wait.  When it gives up (or another warp has) the role goes on
 // without waiting, so that every block-wide barrier is still reached; the
@@ -172,24 +175,20 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// two runs of 16 consecutive columns of this lane
-__device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, float* v) {
-  uint32_t r[32];
+// two runs of 8 consecutive columns of this lane
+__device__ __forceinline__ void tmem_ld8x2(uint32_t t0, uint32_t t1, float* v) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
       "tcgen05.wait::ld.sync.aligned;\n"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[14]), "=r"(r[15])
       : "r"(t0), "r"(t1)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // this lane's 8 consecutive columns times f, in place
@@ -354,7 +353,7 @@ __device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
   }
 }
 
-// Eight warps: gather the rows of a tile and widen them, K of this CTA's 64
+// Sixteen warps: gather the rows of a tile and widen them, K of this CTA's 64
 // tokens, and V of its 256 dims of all 128 tokens.  Eight neighbouring lanes
 // read 128 neighbouring bytes of one row, eight chunks of 32 codes; each chunk
 // makes four 16-byte units of 8 dims.  Unit q of chunk c goes to 64-dim block
@@ -363,44 +362,38 @@ __device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
 // (half, q, c, 8 dims) for (half, c, q, 8 dims); Q is stored in the same
 // order, and O comes out in it.  A token that does not exist reads row 0: its
 // scores are masked, and its V, finite like all codes, meets P = 0.
+//
+// K is written in two halves of its dims and V in two halves of the tokens,
+// each as soon as the MMAs that read the half before it are done.
 __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc* mi,
                                            uint32_t rank) {
-  const int wt = threadIdx.x - kWidenWarp0 * 32;   // 0..255
+  const int wt = threadIdx.x - kWidenWarp0 * 32;
   const int w = wt >> 5, lane = wt & 31;
   const int n = mi->tiles;
-  // K: load j covers rows 8w + 2j and + 1, lane = (row, chunk of 16);
-  // V: tokens 16w + 4j .. + 3, lane = (token, chunk of 8 of this CTA's half)
-  const int kch = lane & 15, krow = 8 * w + (lane >> 4);
-  const int c8 = lane & 7, vtok = 16 * w + (lane >> 3);
-  const uint8_t* kcode = a.rows + 16 * kch;
-  const uint8_t* kexp = a.rows + 256 + kch;
-  const uint8_t* krope = a.rows + 272 + 16 * c8;
-  const uint8_t* vcode = a.rows + 128 * rank + 16 * c8;
-  const uint8_t* vexp = a.rows + 256 + 8 * rank + c8;
-  uint8_t* sk = smem + kOffK + (kch >> 3) * 4 * kKBlk + krow * 128;
-  uint8_t* sv = smem + kOffV + vtok * 128;
+  const int c8 = lane & 7, r4 = 4 * w + (lane >> 3);   // K's row; V's tokens r4 and 64 + r4
+  const uint8_t* code = a.rows + 16 * c8;
+  const uint32_t place = static_cast<uint32_t>(r4 * 128 + ((c8 ^ (r4 & 7)) << 4));
+  uint8_t* sk = smem + kOffK + place;
+  uint8_t* sv = smem + kOffV + place;
 
-  uint4 kc[4], kr[2], vc[4];   // raw codes and RoPE units
-  int ke[4], ve[4];            // exponent bytes
+  uint4 kc[2], kr, vc[2];   // raw codes (K: halves of the dims, V: of the tokens), RoPE unit
+  int ke[2], ve[2];         // exponent bytes
   auto at = [](int row) { return static_cast<size_t>(static_cast<uint32_t>(row)) * kQ4RowBytes; };
   auto load_k = [&](int slot) {
-    const int32_t* rows = mi->row[slot] + rank * kCtaRows;
+    const uint8_t* s = code + at(mi->row[slot][rank * kCtaRows + r4]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const size_t off = at(rows[krow + 2 * j]);
-      kc[j] = *reinterpret_cast<const uint4*>(kcode + off);
-      ke[j] = kexp[off];
+    for (int h = 0; h < 2; ++h) {
+      kc[h] = *reinterpret_cast<const uint4*>(s + 128 * h);
+      ke[h] = s[256 + 8 * h - 15 * c8];
     }
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      kr[j] = *reinterpret_cast<const uint4*>(krope + at(rows[8 * w + 4 * j + (lane >> 3)]));
+    kr = *reinterpret_cast<const uint4*>(s + 272);
   };
   auto load_v = [&](int slot) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const size_t off = at(mi->row[slot][vtok + 4 * j]);
-      vc[j] = *reinterpret_cast<const uint4*>(vcode + off);
-      ve[j] = vexp[off];
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* s = code + 128 * rank + at(mi->row[slot][64 * h + r4]);
+      vc[h] = *reinterpret_cast<const uint4*>(s);
+      ve[h] = s[256 - 120 * static_cast<int>(rank) - 15 * c8];
     }
   };
   auto put = [&](uint8_t* d, uint32_t block_bytes, const uint4& codes, int byte) {
@@ -409,20 +402,19 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
 #pragma unroll
     for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(d + q * block_bytes) = unit[q];
   };
-  auto store_k = [&]() {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      put(sk + 256 * j + ((c8 ^ ((lane >> 4) + 2 * j)) << 4), kKBlk, kc[j], ke[j]);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      *reinterpret_cast<uint4*>(smem + kOffK + 8 * kKBlk +
-                                sw128_off(8 * w + 4 * j + (lane >> 3), c8)) = kr[j];
+  auto told = [&](uint64_t* bar) {
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&mi->k_full));
+    if (lane == 0) mbar_arrive_remote(dsmem_addr(smem_u32(bar), 0));
   };
-  auto put_v = [&](int j) {
-    put(sv + 512 * j + ((c8 ^ ((lane >> 3) + 4 * (j & 1))) << 4), kVBlk, vc[j], ve[j]);
+  auto store_k = [&](int h) {
+    put(sk + h * 4 * kKBlk, kKBlk, kc[h], ke[h]);
+    if (h == 1) *reinterpret_cast<uint4*>(sk + 8 * kKBlk) = kr;
+    told(&mi->k_full[h]);
+  };
+  auto store_v = [&](int h) {
+    put(sv + h * 64 * 128, kVBlk, vc[h], ve[h]);
+    told(&mi->vp_full[h]);
   };
   // K runs one tile ahead of V: K of tile g + 1 is written beside PV of tile
   // g - 1, V of tile g beside QK of tile g + 1.  Slot s of the rows holds tile
@@ -432,7 +424,8 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
   load_v(0);
   __syncwarp();
   if (lane == 0) mbar_arrive(smem_u32(&mi->row_free[0]));
-  store_k();
+  store_k(0);
+  store_k(1);
   if (n > 1) {
     wait_or_abort(&mi->row_full[1], 0, mi, a.status);
     load_k(1);
@@ -441,22 +434,17 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
   int slot1 = 1;              // of tile g + 1
   for (int g = 0; g < n; ++g) {
     if (g + 1 < n) {
+      wait_or_abort(&mi->qk_half, g & 1, mi, a.status);
+      store_k(0);
       wait_or_abort(&mi->qk_done[g & 1], (g >> 1) & 1, mi, a.status);
-      store_k();
+      store_k(1);
     }
     if (g + 2 < n) wait_or_abort(&mi->row_full[slot2], turn2 & 1, mi, a.status);
-    if (g > 0) wait_or_abort(&mi->pv_done, (g - 1) & 1, mi, a.status);
-    // the next loads start once this tile's V has arrived: a wait for a load
-    // also waits for later ones
-    put_v(0);
-    asm volatile("" ::: "memory");
+    if (g > 0) wait_or_abort(&mi->pv_half, (g - 1) & 1, mi, a.status);
+    store_v(0);
     if (g + 2 < n) load_k(slot2);
-    asm volatile("" ::: "memory");
-#pragma unroll
-    for (int j = 1; j < 4; ++j) put_v(j);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&mi->vp_full));
+    if (g > 0) wait_or_abort(&mi->pv_done, (g - 1) & 1, mi, a.status);
+    store_v(1);
     if (g + 1 < n) {
       load_v(slot1);
       __syncwarp();
@@ -466,25 +454,6 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
     if (++slot2 == kRing) {
       slot2 = 0;
       ++turn2;
-    }
-  }
-}
-
-// The odd CTA's full buffers, told to the even CTA's MMA warp by one warp: an
-// arrival across CTAs waits for its warp's loads in flight, which the widening
-// warps have and this one has not.
-__device__ __forceinline__ void forward_role(const MlaArgs& a, Misc* mi, int lane) {
-  const uint32_t k_full = dsmem_addr(smem_u32(&mi->k_full), 0);
-  const uint32_t vp_full = dsmem_addr(smem_u32(&mi->vp_full), 0);
-  const int n = mi->tiles;
-  for (int g = 0; g <= n; ++g) {   // in the order in which they are waited for
-    if (g < n) {
-      wait_or_abort(&mi->k_full, g & 1, mi, a.status);
-      if (lane == 0) mbar_arrive_remote(k_full);
-    }
-    if (g > 0) {
-      wait_or_abort(&mi->vp_full, (g - 1) & 1, mi, a.status);
-      if (lane == 0) mbar_arrive_remote(vp_full);
     }
   }
 }
@@ -504,18 +473,21 @@ __device__ __forceinline__ void mma_role(const MlaArgs& a, uint8_t* smem, Misc* 
   const bool lead = elect_one();
   bool ok = true;
   auto pv = [&](int g, bool accumulate) {
-    ok = wait_or_abort(&mi->vp_full, g & 1, mi, a.status) && ok;
-    tc_fence_after();
-    if (ok && lead) {
 #pragma unroll
-      for (int kt = 0; kt < 8; ++kt)
+    for (int h = 0; h < 2; ++h) {   // 64 tokens each
+      ok = wait_or_abort(&mi->vp_full[h], g & 1, mi, a.status) && ok;
+      tc_fence_after();
+      if (ok && lead) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          umma_f16_pair(tmem + kColO + j * 128, dp + ((kt >> 2) * kKBlk + (kt & 3) * 32) / 16,
-                        dv + (j * 2 * kVBlk + kt * 2048) / 16, idesc_pv, accumulate || kt > 0);
-      umma_commit_pair(smem_u32(&mi->pv_done));
+        for (int kt = 4 * h; kt < 4 * h + 4; ++kt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            umma_f16_pair(tmem + kColO + j * 128, dp + (h * kKBlk + (kt & 3) * 32) / 16,
+                          dv + (j * 2 * kVBlk + kt * 2048) / 16, idesc_pv, accumulate || kt > 0);
+        umma_commit_pair(smem_u32(h == 0 ? &mi->pv_half : &mi->pv_done));
+      }
+      __syncwarp();
     }
-    __syncwarp();
   };
   int seg = 0;
   bool acc = false;   // the tile before was not the first of its segment
@@ -527,18 +499,21 @@ __device__ __forceinline__ void mma_role(const MlaArgs& a, uint8_t* smem, Misc* 
       ok = wait_or_abort(&mi->q_ready, seg & 1, mi, a.status) && ok;
       ++seg;
     }
-    ok = wait_or_abort(&mi->k_full, g & 1, mi, a.status) && ok;
-    tc_fence_after();
-    if (ok && lead) {
 #pragma unroll
-      for (int k = 0; k < 36; ++k)
-        umma_f16_pair(tmem + kColS + (g & 1) * 64, dq + ((k >> 2) * kKBlk + (k & 3) * 32) / 16,
-                      dk + ((k >> 2) * kKBlk + (k & 3) * 32) / 16, k < 32 ? idesc_qk : idesc_rope,
-                      k != 0);
-      umma_commit_pair(smem_u32(&mi->qk_done[g & 1]));
-      if (last) umma_commit_pair(smem_u32(&mi->q_free));
+    for (int h = 0; h < 2; ++h) {   // 256 dims each, the RoPE dims with the second
+      ok = wait_or_abort(&mi->k_full[h], g & 1, mi, a.status) && ok;
+      tc_fence_after();
+      if (ok && lead) {
+#pragma unroll
+        for (int k = 16 * h; k < 16 + 20 * h; ++k)
+          umma_f16_pair(tmem + kColS + (g & 1) * 64, dq + ((k >> 2) * kKBlk + (k & 3) * 32) / 16,
+                        dk + ((k >> 2) * kKBlk + (k & 3) * 32) / 16,
+                        k < 32 ? idesc_qk : idesc_rope, k != 0);
+        umma_commit_pair(smem_u32(h == 0 ? &mi->qk_half : &mi->qk_done[g & 1]));
+        if (h == 1 && last) umma_commit_pair(smem_u32(&mi->q_free));
+      }
+      __syncwarp();
     }
-    __syncwarp();
     if (!first) pv(g - 1, acc);
     acc = !first;
     it.next(a);
@@ -697,7 +672,7 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
     fence_proxy_async_smem();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&mi->vp_full));
+    if (lane == 0) mbar_arrive_remote(dsmem_addr(smem_u32(&mi->vp_full[half]), 0));
 
     if (!last) {
       it.next(a);
@@ -727,19 +702,17 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       const int prow = static_cast<int>(rank) * kCtaRows + r;
       // column 64 q + 8 c + e holds dim 256 half + 32 c + 8 q + e; q = 2 sub, 2 sub + 1
 #pragma unroll 1
-      for (int c = 0; c < 8; c += 2) {
-        float o[32];   // units (c, q), (c + 1, q), then the same of q + 1
-        tmem_ld16x2(to + 8 * c, to + 64 + 8 * c, o);
+      for (int c = 0; c < 8; ++c) {
+        float o[16];   // units (c, q) and (c, q + 1)
+        tmem_ld8x2(to + 8 * c, to + 64 + 8 * c, o);
         if (whole) {
           if (mine) {
-            uint16_t* dst = a.out + orow * kLatent + half * 256 + sub * 16 + 32 * c;
+            uint4* dst =
+                reinterpret_cast<uint4*>(a.out + orow * kLatent + half * 256 + sub * 16 + 32 * c);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= inv;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              reinterpret_cast<uint4*>(dst + 32 * x)[0] = pack8_bf16(o + 8 * x);
-              reinterpret_cast<uint4*>(dst + 32 * x)[1] = pack8_bf16(o + 16 + 8 * x);
-            }
+            for (int e = 0; e < 16; ++e) o[e] *= inv;
+            dst[0] = pack8_bf16(o);
+            dst[1] = pack8_bf16(o + 8);
           }
         } else {   // in the order of the columns
           float* dst = a.part_o + (static_cast<size_t>(slot) * kPairRows + prow) * kLatent +
@@ -747,10 +720,10 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
 #pragma unroll
           for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
+            for (int y = 0; y < 2; ++y)
               reinterpret_cast<float4*>(dst + 64 * x)[y] =
-                  make_float4(o[16 * x + 4 * y], o[16 * x + 4 * y + 1], o[16 * x + 4 * y + 2],
-                              o[16 * x + 4 * y + 3]);
+                  make_float4(o[8 * x + 4 * y], o[8 * x + 4 * y + 1], o[8 * x + 4 * y + 2],
+                              o[8 * x + 4 * y + 3]);
         }
       }
       if (part == 0) {
@@ -785,9 +758,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   if (tid == 0) {
     mbar_init(smem_u32(&mi->q_ready), 2 * kSoftWarps);
     mbar_init(smem_u32(&mi->q_free), 1);
-    // the even CTA's also count the odd CTA's, forwarded as one
-    mbar_init(smem_u32(&mi->k_full), kWidenWarps + (rank == 0 ? 1 : 0));
-    mbar_init(smem_u32(&mi->vp_full), kWidenWarps + kSoftWarps + (rank == 0 ? 1 : 0));
+    // those of the even CTA count both CTAs' warps
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(smem_u32(&mi->k_full[h]), 2 * kWidenWarps);
+      mbar_init(smem_u32(&mi->vp_full[h]), 2 * kWidenWarps + kSoftWarps);
+    }
+    mbar_init(smem_u32(&mi->qk_half), 1);
+    mbar_init(smem_u32(&mi->pv_half), 1);
     mbar_init(smem_u32(&mi->qk_done[0]), 1);
     mbar_init(smem_u32(&mi->qk_done[1]), 1);
     mbar_init(smem_u32(&mi->pv_done), 1);
@@ -851,7 +828,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     softmax_role(a, smem, mi, rank, tmem, pair);
   } else if (warp == kMmaWarp) {
     if (rank == 0) mma_role(a, smem, mi, tmem);
-    else forward_role(a, mi, lane);
   } else if (warp == kRowWarp) {
     row_role(a, mi);
   } else {
