@@ -57,6 +57,8 @@ constexpr uint32_t kOffV = kOffK + 9 * kKBlk;
 constexpr uint32_t kOffP = kOffV + 4 * kVBlk;
 constexpr uint32_t kOffMisc = kOffP + 2 * kKBlk;
 
+constexpr int kJoinFly = 8;           // partials in flight per thread of the join
+
 constexpr uint32_t kColO = 0;         // TMEM columns: O, then two score buffers
 constexpr uint32_t kColS = 256;
 constexpr float kGrow = 8.0f;         // log2 of the growth of a maximum that O absorbs unscaled
@@ -66,8 +68,7 @@ struct Misc {
   uint64_t row_full[kRing], row_free[kRing];
   uint32_t tmem;
   int abort;
-  int start_v, tiles;
-  long long start_off;
+  int start_v, start_rt, start_tile, tiles;
   uint32_t mask[kRing][4];            // tokens of a tile that exist
   int32_t row[kRing][kMt];            // cache rows of a tile's tokens (0 for one that is not)
   float xch[4][kCtaRows];             // a row's statistics from the four threads that share it
@@ -121,14 +122,23 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                : "memory");
 }
+// REUSE: 0 reads A from shared memory, 1 does and keeps it in the collector
+// buffer, 2 takes it from there (the MMA before had the same A).
+template <int REUSE>
 __device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                               uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+#define ESS_UMMA_PAIR(collector)                                                              \
+  asm volatile(                                                                               \
+      "{\n\t.reg .pred p;\n\t"                                                                \
+      "setp.ne.b32 p, %4, 0;\n\t"                                                             \
+      "tcgen05.mma.cta_group::2.kind::f16" collector " [%0], %1, %2, %3, p;\n\t}\n" ::"r"(     \
+          d_tmem),                                                                            \
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)                                   \
+      : "memory")
+  if (REUSE == 1) ESS_UMMA_PAIR(".collector::a::fill");
+  else if (REUSE == 2) ESS_UMMA_PAIR(".collector::a::lastuse");
+  else ESS_UMMA_PAIR("");
+#undef ESS_UMMA_PAIR
 }
 // arrive on the barrier at this offset in both CTAs when all prior MMAs are done
 __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
@@ -175,20 +185,30 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// two runs of 8 consecutive columns of this lane
-__device__ __forceinline__ void tmem_ld8x2(uint32_t t0, uint32_t t1, float* v) {
-  uint32_t r[16];
+// four runs of 8 consecutive columns of this lane, 64 columns apart
+__device__ __forceinline__ void tmem_ld8x4(uint32_t t, float* v) {
+  uint32_t r[32];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%33];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%34];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24,%25,%26,%27,%28,%29,%30,%31}, [%35];\n\t"
       "tcgen05.wait::ld.sync.aligned;\n"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(t0), "r"(t1)
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t), "r"(t + 64), "r"(t + 128), "r"(t + 192)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 32 bytes, 32-byte aligned, in one store
+__device__ __forceinline__ void st_global_32(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 
 // this lane's 8 consecutive columns times f, in place
@@ -255,8 +275,8 @@ struct Tiles {
     left = mi->tiles;
     v = mi->start_v;
     load(a);
-    rt = static_cast<int>(mi->start_off / nt);
-    tile = static_cast<int>(mi->start_off % nt);
+    rt = mi->start_rt;
+    tile = mi->start_tile;
     begins = true;
   }
   __device__ __forceinline__ void load(const MlaArgs& a) {
@@ -479,11 +499,12 @@ __device__ __forceinline__ void mma_role(const MlaArgs& a, uint8_t* smem, Misc* 
       tc_fence_after();
       if (ok && lead) {
 #pragma unroll
-        for (int kt = 4 * h; kt < 4 * h + 4; ++kt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            umma_f16_pair(tmem + kColO + j * 128, dp + (h * kKBlk + (kt & 3) * 32) / 16,
-                          dv + (j * 2 * kVBlk + kt * 2048) / 16, idesc_pv, accumulate || kt > 0);
+        for (int kt = 4 * h; kt < 4 * h + 4; ++kt) {
+          const uint64_t ad = dp + (h * kKBlk + (kt & 3) * 32) / 16, bd = dv + kt * 2048 / 16;
+          const uint32_t more = accumulate || kt > 0;
+          umma_f16_pair<1>(tmem + kColO, ad, bd, idesc_pv, more);
+          umma_f16_pair<2>(tmem + kColO + 128, ad, bd + 2 * kVBlk / 16, idesc_pv, more);
+        }
         umma_commit_pair(smem_u32(h == 0 ? &mi->pv_half : &mi->pv_done));
       }
       __syncwarp();
@@ -506,7 +527,7 @@ __device__ __forceinline__ void mma_role(const MlaArgs& a, uint8_t* smem, Misc* 
       if (ok && lead) {
 #pragma unroll
         for (int k = 16 * h; k < 16 + 20 * h; ++k)
-          umma_f16_pair(tmem + kColS + (g & 1) * 64, dq + ((k >> 2) * kKBlk + (k & 3) * 32) / 16,
+          umma_f16_pair<0>(tmem + kColS + (g & 1) * 64, dq + ((k >> 2) * kKBlk + (k & 3) * 32) / 16,
                         dk + ((k >> 2) * kKBlk + (k & 3) * 32) / 16,
                         k < 32 ? idesc_qk : idesc_rope, k != 0);
         umma_commit_pair(smem_u32(h == 0 ? &mi->qk_half : &mi->qk_done[g & 1]));
@@ -700,30 +721,27 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       const size_t orow = static_cast<size_t>(v) * a.entry_rows + row0 + r;
       const float inv = !whole ? 1.0f : (lt > 0.0f || lt != lt ? 1.0f / lt : 0.0f);
       const int prow = static_cast<int>(rank) * kCtaRows + r;
-      // column 64 q + 8 c + e holds dim 256 half + 32 c + 8 q + e; q = 2 sub, 2 sub + 1
+      // column 64 q + 8 c + e holds dim 256 half + 32 c + 8 q + e: a thread
+      // takes four c, so it has 32 neighbouring dims at a time
+      const uint32_t tq = tmem + lanes + kColO + sub * 32;
+      const int d0 = half * 256 + sub * 128;
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        float o[16];   // units (c, q) and (c, q + 1)
-        tmem_ld8x2(to + 8 * c, to + 64 + 8 * c, o);
+      for (int c = 0; c < 4; ++c) {
+        float o[32];
+        tmem_ld8x4(tq + 8 * c, o);
+        if (!mine) continue;
         if (whole) {
-          if (mine) {
-            uint4* dst =
-                reinterpret_cast<uint4*>(a.out + orow * kLatent + half * 256 + sub * 16 + 32 * c);
+          uint16_t* dst = a.out + orow * kLatent + d0 + 32 * c;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= inv;
-            dst[0] = pack8_bf16(o);
-            dst[1] = pack8_bf16(o + 8);
-          }
-        } else {   // in the order of the columns
-          float* dst = a.part_o + (static_cast<size_t>(slot) * kPairRows + prow) * kLatent +
-                       half * 256 + sub * 128 + 8 * c;
+          for (int e = 0; e < 32; ++e) o[e] *= inv;
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
+          for (int x = 0; x < 4; ++x)
+            reinterpret_cast<uint4*>(dst)[x] = pack8_bf16(o + 8 * x);
+        } else {
+          float* dst =
+              a.part_o + (static_cast<size_t>(slot) * kPairRows + prow) * kLatent + d0 + 32 * c;
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
-              reinterpret_cast<float4*>(dst + 64 * x)[y] =
-                  make_float4(o[8 * x + 4 * y], o[8 * x + 4 * y + 1], o[8 * x + 4 * y + 2],
-                              o[8 * x + 4 * y + 3]);
+          for (int x = 0; x < 4; ++x) st_global_32(dst + 8 * x, o + 8 * x);
         }
       }
       if (part == 0) {
@@ -732,7 +750,7 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
             a.lse[orow] = lt > 0.0f || lt != lt ? (m + log2f(lt)) * 0.69314718055994531f
                                                 : -INFINITY;
         } else {
-          a.part_ml[static_cast<size_t>(slot) * kPairRows + prow] = make_float2(m, lt);
+          if (mine) a.part_ml[static_cast<size_t>(slot) * kPairRows + prow] = make_float2(m, lt);
         }
       }
       if (tid == 0 && rank == 0) {
@@ -798,21 +816,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     if (w < warp) before += scan[w];
     total += scan[w];
   }
-  // neighbouring pairs share a request, so none between two may be idle
-  const long long busy = total < pairs ? total : pairs;
+  // the first total % busy pairs take one tile more; neighbouring pairs share
+  // a request, so none between two may be idle
+  const int busy = total < pairs ? static_cast<int>(total) : pairs;
   if (pair >= busy) return;   // both CTAs of the pair
-  const long long lo = total * pair / busy, hi = total * (pair + 1) / busy;
+  const long long share = total < 0x7fffffffLL
+                              ? static_cast<unsigned>(total) / static_cast<unsigned>(busy)
+                              : total / busy;
+  const int extra = static_cast<int>(total - share * busy);
+  const long long lo = share * pair + min(pair, extra);
   if (lo >= before && lo < before + mine) {
     long long off = lo - before;
-    int v = v0;
+    int v = v0, nt;
     for (;; ++v) {
-      const long long n = static_cast<long long>((entry_len(a, v) + kMt - 1) / kMt) * a.row_tiles;
-      if (off < n) break;
-      off -= n;
+      nt = (entry_len(a, v) + kMt - 1) / kMt;
+      if (off < static_cast<long long>(nt) * a.row_tiles) break;
+      off -= static_cast<long long>(nt) * a.row_tiles;
     }
+    int rt = 0;   // at most kMaxCacheWays row tiles
+    for (; off >= nt; off -= nt) ++rt;
     mi->start_v = v;
-    mi->start_off = off;
-    mi->tiles = static_cast<int>(hi - lo);
+    mi->start_rt = rt;
+    mi->start_tile = static_cast<int>(off);
+    mi->tiles = static_cast<int>(share) + (pair < extra ? 1 : 0);
   }
   if (warp == kMmaWarp) {
     tmem_alloc_pair(smem_u32(&mi->tmem), 512);
@@ -864,22 +890,38 @@ __global__ void __launch_bounds__(128) cache_mla_join_kernel(const MlaArgs a) {
   if (p0 == sp.y) return;
   const int pr = row % kPairRows;
   float mx = -INFINITY, l = 0.0f;
-  // dims 4t .. 4t + 3 in the partials' order of columns
-  const int col = (t & ~63) * 4 + ((t >> 1) & 3) * 64 + ((t >> 3) & 7) * 8 + (t & 1) * 4;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = p0; p <= sp.y; ++p) {
-    const size_t i = static_cast<size_t>(p == p0 ? sp.x : 2 * p) * kPairRows + pr;
-    const float2 ml = a.part_ml[i];
-    const float4 o = *reinterpret_cast<const float4*>(a.part_o + i * kLatent + col);
-    const float m2 = fmaxf(mx, ml.x);
+  for (int pb = p0; pb <= sp.y; pb += kJoinFly) {
+    float2 ml[kJoinFly];
+    float4 o[kJoinFly];
+#pragma unroll
+    for (int q = 0; q < kJoinFly; ++q) {
+      const int p = pb + q;
+      const size_t i = static_cast<size_t>(p == p0 ? sp.x : 2 * p) * kPairRows + pr;
+      ml[q] = p <= sp.y ? a.part_ml[i] : make_float2(-INFINITY, 0.0f);
+      o[q] = p <= sp.y ? reinterpret_cast<const float4*>(a.part_o + i * kLatent)[t]
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float m2 = mx;
+#pragma unroll
+    for (int q = 0; q < kJoinFly; ++q) m2 = fmaxf(m2, ml[q].x);
     const float base = m2 == -INFINITY ? 0.0f : m2;
-    const float f = exp2f(mx - base), w = exp2f(ml.x - base);
-    // a part without a token has l = 0 and O = 0; its weight is 0 beside others
-    l = fmaf(l, f, w * ml.y);
-    acc.x = fmaf(acc.x, f, w * o.x);
-    acc.y = fmaf(acc.y, f, w * o.y);
-    acc.z = fmaf(acc.z, f, w * o.z);
-    acc.w = fmaf(acc.w, f, w * o.w);
+    const float f = exp2f(mx - base);
+    l *= f;
+    acc.x *= f;
+    acc.y *= f;
+    acc.z *= f;
+    acc.w *= f;
+#pragma unroll
+    for (int q = 0; q < kJoinFly; ++q) {
+      // a part without a token has l = 0 and O = 0; its weight is 0 beside others
+      const float w = exp2f(ml[q].x - base);
+      l = fmaf(w, ml[q].y, l);
+      acc.x = fmaf(w, o[q].x, acc.x);
+      acc.y = fmaf(w, o[q].y, acc.y);
+      acc.z = fmaf(w, o[q].z, acc.z);
+      acc.w = fmaf(w, o[q].w, acc.w);
+    }
     mx = m2;
   }
   const bool some = l > 0.0f || l != l;
