@@ -793,6 +793,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     mi->abort = 0;
     fence_mbar_init();
   }
+  if (warp == kMmaWarp) {
+    tmem_alloc_pair(smem_u32(&mi->tmem), 512);
+    tmem_relinquish_pair();
+  }
+  __syncwarp();
+  cluster_arrive();   // the peer may arrive on this CTA's barriers once it has waited
   pdl_wait_previous();
   // this pair's share of all tiles: a scan of the entries' tile counts, a
   // run of neighbouring entries per thread
@@ -818,13 +824,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   }
   // the first total % busy pairs take one tile more; neighbouring pairs share
   // a request, so none between two may be idle
-  const int busy = total < pairs ? static_cast<int>(total) : pairs;
-  if (pair >= busy) return;   // both CTAs of the pair
+  const int busy = total < pairs ? max(static_cast<int>(total), 1) : pairs;
   const long long share = total < 0x7fffffffLL
                               ? static_cast<unsigned>(total) / static_cast<unsigned>(busy)
                               : total / busy;
   const int extra = static_cast<int>(total - share * busy);
-  const long long lo = share * pair + min(pair, extra);
+  const long long lo = share * pair + min(pair, extra);   // total, for an idle pair
   if (lo >= before && lo < before + mine) {
     long long off = lo - before;
     int v = v0, nt;
@@ -840,17 +845,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     mi->start_tile = static_cast<int>(off);
     mi->tiles = static_cast<int>(share) + (pair < extra ? 1 : 0);
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc_pair(smem_u32(&mi->tmem), 512);
-    tmem_relinquish_pair();
-  }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();   // the peer's barriers are set up
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem = mi->tmem;
 
-  if (warp < kSoftWarps) {
+  if (pair >= total) {
+    // nothing to do: both CTAs of the pair
+  } else if (warp < kSoftWarps) {
     softmax_role(a, smem, mi, rank, tmem, pair);
   } else if (warp == kMmaWarp) {
     if (rank == 0) mma_role(a, smem, mi, tmem);
