@@ -27,6 +27,7 @@
 // the device, so captured calls follow them); a request cut by a boundary
 // leaves fp32 partials, which a second kernel joins.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "ess_rows.cuh"
@@ -39,7 +40,7 @@ constexpr int kMaxCacheHeads = 128;
 constexpr int kMt = 128;              // tokens per tile
 constexpr int kPairRows = 128;        // query rows per pair
 constexpr int kCtaRows = 64;          // of them per CTA
-constexpr int kMaxPairs = 76;         // one pair per two SMs
+constexpr int kMaxPairs = 76;         // one pair per two of the 152 SMs (any number is right)
 
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 8;
@@ -942,6 +943,17 @@ ess_status check_shape(int batch, int ways, int heads) {
   return ESS_OK;
 }
 
+// The kernel's shared memory, allowed once per device.
+cudaError_t allow_smem(int dev) {
+  static std::atomic<unsigned long long> done{0};
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(
+      cache_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMlaSmem));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 struct MlaLayout {
   size_t span, part_o, part_ml, total;
 };
@@ -992,10 +1004,8 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
     return ESS_ERR_INVALID_ARG;
   const MlaLayout L = mla_layout(batch, ways);
   if (ws_bytes < L.total) return ESS_ERR_OOM;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return ESS_ERR_CUDA;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ESS_ERR_CUDA;
   const long long all_rows = static_cast<long long>(batch) * ways * heads;
   MlaArgs a;
   a.q = static_cast<const uint16_t*>(q);
@@ -1031,13 +1041,12 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
                                    : static_cast<long long>(max_pages) * page) +
                            kMt - 1) /
                           kMt);
-  const int pairs = static_cast<int>(std::min<long long>(most, std::min(kMaxPairs, sms / 2)));
-  cudaError_t e = cudaFuncSetAttribute(cache_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kMlaSmem));
+  const int pairs = static_cast<int>(std::min<long long>(most, kMaxPairs));
+  cudaError_t e = allow_smem(dev);
   if (e != cudaSuccess) return ESS_ERR_CUDA;
-  e = launch_pdl(cache_mla_kernel, dim3(2 * pairs), dim3(kMlaThreads), kMlaSmem, st, a);
+  e = launch_pdl_once(cache_mla_kernel, dim3(2 * pairs), dim3(kMlaThreads), kMlaSmem, st, a);
   if (e != cudaSuccess) return ESS_ERR_CUDA;
-  e = launch_pdl(cache_mla_join_kernel, dim3(static_cast<unsigned>(all_rows)), dim3(128), 0, st, a);
+  e = launch_pdl_once(cache_mla_join_kernel, dim3(static_cast<unsigned>(all_rows)), dim3(128), 0, st, a);
   return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
 }
 

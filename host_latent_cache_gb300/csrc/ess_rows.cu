@@ -264,8 +264,8 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
   constexpr int kThreads = TPR > 256 ? TPR : 256;
   constexpr int kRows = kThreads / TPR;
   const dim3 grid(static_cast<unsigned>((a.n + kRows - 1) / kRows));
-  return a.res ? launch_pdl(norm_quant_kernel<TPR, UNITS, true>, grid, dim3(kThreads), 0, st, a)
-               : launch_pdl(norm_quant_kernel<TPR, UNITS, false>, grid, dim3(kThreads), 0, st, a);
+  return a.res ? launch_pdl_once(norm_quant_kernel<TPR, UNITS, true>, grid, dim3(kThreads), 0, st, a)
+               : launch_pdl_once(norm_quant_kernel<TPR, UNITS, false>, grid, dim3(kThreads), 0, st, a);
 }
 
 // rows of one launch: the grid's x extent is a 31-bit number of CTAs
@@ -298,10 +298,10 @@ ess_status ess_cache_write(const void* kv, int64_t kv_stride, int64_t n, const v
       if (!std::isfinite(inv_freq[i])) return ESS_ERR_INVALID_ARG;
       // radians -> turns in [0, 1) -> a 64-bit binary fraction
       const double turns = inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
-      const double part = turns - std::floor(turns);
-      const double hi = std::floor(std::ldexp(part, 32));
-      const double lo = std::ldexp(std::ldexp(part, 32) - hi, 32);
-      fr.f[i] = (static_cast<unsigned long long>(hi) << 32) + static_cast<unsigned long long>(lo);
+      const double hi = (turns - std::floor(turns)) * 4294967296.0;
+      const unsigned long long whole = static_cast<unsigned long long>(hi);
+      fr.f[i] = (whole << 32) +
+                static_cast<unsigned long long>((hi - static_cast<double>(whole)) * 4294967296.0);
     }
   }
   if (n == 0) return ESS_OK;
@@ -325,11 +325,11 @@ ess_status ess_cache_write(const void* kv, int64_t kv_stride, int64_t n, const v
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (format == ESS_ROW_BF16)
-    e = launch_pdl(cache_write_kernel<ESS_ROW_BF16>, grid, block, 0, st, a, fr);
+    e = launch_pdl_once(cache_write_kernel<ESS_ROW_BF16>, grid, block, 0, st, a, fr);
   else if (format == ESS_ROW_COMPACT)
-    e = launch_pdl(cache_write_kernel<ESS_ROW_COMPACT>, grid, block, 0, st, a, fr);
+    e = launch_pdl_once(cache_write_kernel<ESS_ROW_COMPACT>, grid, block, 0, st, a, fr);
   else
-    e = launch_pdl(cache_write_kernel<ESS_ROW_Q4>, grid, block, 0, st, a, fr);
+    e = launch_pdl_once(cache_write_kernel<ESS_ROW_Q4>, grid, block, 0, st, a, fr);
   return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
 }
 
@@ -346,13 +346,13 @@ ess_status ess_cache_read(const void* rows, int64_t n_rows, int32_t format, cons
   uint16_t* o = static_cast<uint16_t*>(out);
   cudaError_t e;
   if (format == ESS_ROW_BF16)
-    e = launch_pdl(cache_read_kernel<ESS_ROW_BF16>, grid, block, 0, st, r, n_rows, slots, n, o,
+    e = launch_pdl_once(cache_read_kernel<ESS_ROW_BF16>, grid, block, 0, st, r, n_rows, slots, n, o,
                    status);
   else if (format == ESS_ROW_COMPACT)
-    e = launch_pdl(cache_read_kernel<ESS_ROW_COMPACT>, grid, block, 0, st, r, n_rows, slots, n, o,
+    e = launch_pdl_once(cache_read_kernel<ESS_ROW_COMPACT>, grid, block, 0, st, r, n_rows, slots, n, o,
                    status);
   else
-    e = launch_pdl(cache_read_kernel<ESS_ROW_Q4>, grid, block, 0, st, r, n_rows, slots, n, o,
+    e = launch_pdl_once(cache_read_kernel<ESS_ROW_Q4>, grid, block, 0, st, r, n_rows, slots, n, o,
                    status);
   return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
 }

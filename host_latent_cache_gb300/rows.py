@@ -25,27 +25,69 @@ LATENT, ROPE, ROW = 512, 64, 576
 TILE = 128   # values per scale of norm_q8
 
 
+_BF16, _I32, _I64 = torch.bfloat16, torch.int32, torch.int64
+
+
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
 
 
-def _tensor(t, name: str, dtype, shape, device, rows_apart: bool = False) -> None:
-    """t is a tensor of this type, shape and device; contiguous, or (rows_apart)
-    with contiguous rows at any stride."""
-    _need(isinstance(t, torch.Tensor) and t.dtype == dtype, f"{name}: a {dtype} tensor is needed")
-    _need(t.device == device, f"{name} is on {t.device}, not on {device}")
-    _need(tuple(t.shape) == tuple(shape), f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if rows_apart:
-        _need(t.stride(-1) == 1 or t.shape[-1] <= 1 or t.numel() == 0,
-              f"{name}: the values of a row are next to one another")
-    else:
-        _need(t.is_contiguous(), f"{name} is not contiguous")
+def _is(t, dtype, shape, index: int) -> bool:
+    """t is a contiguous tensor of this type and shape on this CUDA device."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
+            and t.get_device() == index and t.is_contiguous())
 
 
-def _on(device):
-    """The call runs on this device's current stream, whatever the current device."""
-    return torch.cuda.device(device)
+def _is_rows(t, dtype, shape, index: int) -> bool:
+    """The same, with contiguous rows at any stride."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
+            and t.get_device() == index
+            and (t.is_contiguous() or t.stride(1) == 1 or shape[1] <= 1))
+
+
+def _refuse(t, name: str, dtype, shape, index: int) -> None:
+    what = (f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}"
+            if isinstance(t, torch.Tensor) else repr(type(t)))
+    raise ValueError(f"{name}: {dtype} {tuple(shape)} on cuda:{index} with contiguous "
+                     f"values is needed, not {what}")
+
+
+def _check(t, name: str, dtype, shape, index: int) -> None:
+    if not _is(t, dtype, shape, index):
+        _refuse(t, name, dtype, shape, index)
+
+
+def _check_rows(t, name: str, dtype, shape, index: int) -> None:
+    if not _is_rows(t, dtype, shape, index):
+        _refuse(t, name, dtype, shape, index)
+
+
+def _row_stride(t) -> int:
+    """Elements from row to row; of a single row, any that the kernels take."""
+    n, dim = t.shape
+    return t.stride(0) if n > 1 else -(-dim // 8) * 8
+
+
+class _OnDevice:
+    """Makes a device current for a call and puts the old one back; costs
+    nothing when it is current already.  Yields the device's current stream."""
+
+    __slots__ = ("index", "old")
+
+    def __init__(self, index: int):
+        self.index = index
+
+    def __enter__(self) -> int:
+        self.old = torch._C._cuda_getDevice()
+        if self.old != self.index:
+            torch.cuda.set_device(self.index)
+        return torch._C._cuda_getCurrentRawStream(self.index)
+
+    def __exit__(self, *exc):
+        if self.old != self.index:
+            torch.cuda.set_device(self.old)
+        return False
 
 
 class RowCache:
@@ -60,10 +102,12 @@ class RowCache:
         self._f = FORMATS[fmt]
         _need(isinstance(rows, torch.Tensor) and rows.is_cuda and rows.dim() == 2,
               "rows: a CUDA tensor [n_rows][row bytes] is needed")
-        _tensor(rows, "rows", torch.uint8, (rows.shape[0], ess.ess_row_bytes(self._f)), rows.device)
         self.rows = rows
         self.n_rows = rows.shape[0]
         self.device = rows.device
+        self._index = rows.get_device()
+        _check(rows, "rows", torch.uint8, (self.n_rows, ess.ess_row_bytes(self._f)), self._index)
+        self._on = _OnDevice(self._index)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._freq = (None, None)
         self._ws = {}
@@ -74,9 +118,7 @@ class RowCache:
         self.status.zero_()
         return code
 
-    def _freqs(self, inv_freq: Optional[Sequence[float]]):
-        if inv_freq is None:
-            return None
+    def _freqs(self, inv_freq: Sequence[float]):
         key = tuple(inv_freq)
         if self._freq[0] != key:
             _need(len(key) == ROPE // 2, f"inv_freq has {len(key)} entries, not {ROPE // 2}")
@@ -89,32 +131,36 @@ class RowCache:
         the rows `slots` int64 [n] (negative: not written): the first 512
         values normed when gamma bf16 [512] is given, the last 64 rotated by
         pos int32 [n] when inv_freq (32 radians per position) is given."""
-        dev = self.device
+        at = self._index
+        _need(isinstance(slots, torch.Tensor) and slots.dim() == 1, "slots: [n] is needed")
         n = slots.shape[0]
-        _tensor(kv, "kv", torch.bfloat16, (n, ROW), dev, rows_apart=True)
-        _tensor(slots, "slots", torch.int64, (n,), dev)
+        _check(slots, "slots", _I64, (n,), at)
+        _check_rows(kv, "kv", _BF16, (n, ROW), at)
         _need(pairs in PAIRS, f"pairs {pairs!r} is none of {', '.join(PAIRS)}")
         if gamma is not None:
-            _tensor(gamma, "gamma", torch.bfloat16, (LATENT,), dev)
-        freq = self._freqs(inv_freq)
-        if freq is not None:
-            _need(pos is not None, "a rotation needs pos")
-            _tensor(pos, "pos", torch.int32, (n,), dev)
-        stride = kv.stride(0) if n > 1 else max(ROW, kv.stride(0) // 8 * 8)
-        with _on(dev):
-            ess.ess_cache_write(kv, stride, n, gamma, eps, freq, pos if freq is not None else None,
-                                PAIRS[pairs], slots, self.rows, self.n_rows, self._f, self.status)
+            _check(gamma, "gamma", _BF16, (LATENT,), at)
+        freq = None
+        if inv_freq is None:
+            pos = None
+        else:
+            freq = self._freqs(inv_freq)
+            _check(pos, "pos", _I32, (n,), at)
+        with self._on as stream:
+            ess.ess_cache_write(kv, _row_stride(kv), n, gamma, eps, freq, pos, PAIRS[pairs], slots,
+                                self.rows, self.n_rows, self._f, self.status, stream)
 
     def read(self, slots, out=None):
         """The rows `slots` int64 [n] as bf16 [n][576]; zeros for a negative slot."""
+        at = self._index
+        _need(isinstance(slots, torch.Tensor) and slots.dim() == 1, "slots: [n] is needed")
         n = slots.shape[0]
-        _tensor(slots, "slots", torch.int64, (n,), self.device)
+        _check(slots, "slots", _I64, (n,), at)
         if out is None:
-            out = torch.empty((n, ROW), dtype=torch.bfloat16, device=self.device)
+            out = torch.empty((n, ROW), dtype=_BF16, device=self.device)
         else:
-            _tensor(out, "out", torch.bfloat16, (n, ROW), self.device)
-        with _on(self.device):
-            ess.ess_cache_read(self.rows, self.n_rows, self._f, slots, n, out, self.status)
+            _check(out, "out", _BF16, (n, ROW), at)
+        with self._on as stream:
+            ess.ess_cache_read(self.rows, self.n_rows, self._f, slots, n, out, self.status, stream)
         return out
 
     def workspace(self, batch: int, ways: int, heads: int) -> torch.Tensor:
@@ -132,31 +178,30 @@ class RowCache:
         [batch]), or over tokens int32 [batch][ways][k].  Returns (out bf16
         [batch][ways][heads][512], lse float32 [batch][ways][heads]).  Without
         `workspace` the cache keeps one for each current stream."""
-        dev = self.device
+        at = self._index
         _need(isinstance(q, torch.Tensor) and q.dim() == 4, "q: [batch][ways][heads][576] is needed")
         batch, ways, heads, _ = q.shape
-        _tensor(q, "q", torch.bfloat16, (batch, ways, heads, ROW), dev)
+        _check(q, "q", _BF16, (batch, ways, heads, ROW), at)
         _need(isinstance(page_table, torch.Tensor) and page_table.dim() == 2,
               "page_table: [batch][max_pages] is needed")
         max_pages = page_table.shape[1]
-        _tensor(page_table, "page_table", torch.int32, (batch, max_pages), dev)
-        _tensor(T, "T", torch.int32, (batch,), dev)
+        _check(page_table, "page_table", _I32, (batch, max_pages), at)
+        _check(T, "T", _I32, (batch,), at)
         k = 0
         if tokens is not None:
             _need(isinstance(tokens, torch.Tensor) and tokens.dim() == 3,
                   "tokens: [batch][ways][k] is needed")
             k = tokens.shape[2]
-            _tensor(tokens, "tokens", torch.int32, (batch, ways, k), dev)
+            _check(tokens, "tokens", _I32, (batch, ways, k), at)
         if out is None:
-            out = torch.empty((batch, ways, heads, LATENT), dtype=torch.bfloat16, device=dev)
+            out = torch.empty((batch, ways, heads, LATENT), dtype=_BF16, device=self.device)
         else:
-            _tensor(out, "out", torch.bfloat16, (batch, ways, heads, LATENT), dev)
+            _check(out, "out", _BF16, (batch, ways, heads, LATENT), at)
         if lse is None:
-            lse = torch.empty((batch, ways, heads), dtype=torch.float32, device=dev)
+            lse = torch.empty((batch, ways, heads), dtype=torch.float32, device=self.device)
         else:
-            _tensor(lse, "lse", torch.float32, (batch, ways, heads), dev)
-        with _on(dev):
-            stream = torch.cuda.current_stream().cuda_stream
+            _check(lse, "lse", torch.float32, (batch, ways, heads), at)
+        with self._on as stream:
             if workspace is None:
                 key = (stream, batch, ways, heads)
                 workspace = self._ws.get(key)
@@ -174,34 +219,36 @@ def norm_q8(x, gamma, eps: float = 1e-6, residual=None, residual_out=None, codes
     that is a multiple of 8, with e4m3 output: (codes float8_e4m3fn [n][dim],
     scales float32 [n][ceil(dim / 128)], x + residual as bf16 or None).
     residual_out may be x or residual."""
-    _need(isinstance(x, torch.Tensor) and x.dim() == 2 and x.is_cuda, "x: a CUDA tensor [n][dim] is needed")
+    _need(isinstance(x, torch.Tensor) and x.dim() == 2 and x.is_cuda,
+          "x: a CUDA tensor [n][dim] is needed")
     n, dim = x.shape
-    dev = x.device
-    _tensor(x, "x", torch.bfloat16, (n, dim), dev, rows_apart=True)
-    _tensor(gamma, "gamma", torch.bfloat16, (dim,), dev)
-    apart = lambda t: t.stride(0) if n > 1 else max(dim, t.stride(0) // 8 * 8)
+    at = x.get_device()
+    _check_rows(x, "x", _BF16, (n, dim), at)
+    _check(gamma, "gamma", _BF16, (dim,), at)
     r_stride = 0
     if residual is not None:
-        _tensor(residual, "residual", torch.bfloat16, (n, dim), dev, rows_apart=True)
-        r_stride = apart(residual)
+        _check_rows(residual, "residual", _BF16, (n, dim), at)
+        r_stride = _row_stride(residual)
         if residual_out is None:
-            residual_out = torch.empty_strided((n, dim), (r_stride, 1), dtype=torch.bfloat16,
-                                               device=dev)
+            residual_out = (torch.empty((n, dim), dtype=_BF16, device=x.device) if r_stride == dim else
+                            torch.empty_strided((n, dim), (r_stride, 1), dtype=_BF16,
+                                                device=x.device))
         else:
-            _tensor(residual_out, "residual_out", torch.bfloat16, (n, dim), dev, rows_apart=True)
-            _need(apart(residual_out) == r_stride, "residual_out and residual have one row stride")
+            _check_rows(residual_out, "residual_out", _BF16, (n, dim), at)
+            _need(_row_stride(residual_out) == r_stride,
+                  "residual_out and residual have one row stride")
     else:
         _need(residual_out is None, "residual_out without a residual")
     groups = -(-dim // TILE)
     if codes is None:
-        codes = torch.empty((n, dim), dtype=torch.float8_e4m3fn, device=dev)
+        codes = torch.empty((n, dim), dtype=torch.float8_e4m3fn, device=x.device)
     else:
-        _tensor(codes, "codes", torch.float8_e4m3fn, (n, dim), dev)
+        _check(codes, "codes", torch.float8_e4m3fn, (n, dim), at)
     if scales is None:
-        scales = torch.empty((n, groups), dtype=torch.float32, device=dev)
+        scales = torch.empty((n, groups), dtype=torch.float32, device=x.device)
     else:
-        _tensor(scales, "scales", torch.float32, (n, groups), dev)
-    with _on(dev):
-        ess.ess_norm_quant(x, apart(x), residual, r_stride, gamma, eps, n, dim, residual_out, codes,
-                           scales)
+        _check(scales, "scales", torch.float32, (n, groups), at)
+    with _OnDevice(at) as stream:
+        ess.ess_norm_quant(x, _row_stride(x), residual, r_stride, gamma, eps, n, dim, residual_out,
+                           codes, scales, stream)
     return codes, scales, residual_out
