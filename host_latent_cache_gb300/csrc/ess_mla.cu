@@ -246,26 +246,6 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// pairs of fp32 operations in one instruction
-__device__ __forceinline__ float2 fma2(const float2& x, const float2& y, const float2& z) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(const float2& x, const float2& y) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
-  return d;
-}
-
 // The tiles of one pair, in order: entry v, row tile rt, token tile.
 struct Tiles {
   int left;   // tiles from this one on
@@ -666,12 +646,12 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       }
     }
     const float base = m == -INFINITY ? 0.0f : m;
-    const float2 c2v = make_float2(c2, c2), bv = make_float2(-base, -base);
-    float2 sum2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+    const F2 c2v = both(c2), bv = both(-base);
+    F2 sum2[2] = {both(0.0f), both(0.0f)};
     uint32_t p[16];
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
-      float2 z = fma2(make_float2(s[2 * c], s[2 * c + 1]), c2v, bv);
+      F2 z = fma2(F2{s[2 * c], s[2 * c + 1]}, c2v, bv);
       z.x = ex2_approx(z.x);
       z.y = ex2_approx(z.y);
       sum2[c & 1] = add2(sum2[c & 1], z);

@@ -6,6 +6,7 @@
 // 512 latents (dims 8l .. 8l + 7 and 256 + 8l ..), so every load and store
 // instruction of a warp covers consecutive bytes whatever the format: 16, 8 or
 // 4 bytes a lane for bf16, e4m3 and e2m1.
+#include <algorithm>
 #include <cmath>
 
 #include "ess_rows.cuh"
@@ -14,6 +15,7 @@ namespace ess {
 namespace {
 
 constexpr int kRowWarps = 8;          // rows in flight per CTA
+constexpr int kWriteCtas = 152 * 3;   // writing CTAs at most: one wave
 
 struct RopeFreq {
   // turns per position as a binary fraction of 2^64: position * fraction
@@ -35,96 +37,127 @@ struct WriteArgs {
   int* status;
 };
 
+// A warp's raw row: the two units of its lane, its pair of k^R, where it goes.
+struct RawRow {
+  uint4 u0, u1;
+  uint32_t ra, rb;
+  int32_t pos;
+  long long slot;
+
+  __device__ __forceinline__ void load(const WriteArgs& a, long long i, int lane) {
+    const uint16_t* x = a.kv + i * a.stride;
+    slot = a.slots[i];
+    u0 = reinterpret_cast<const uint4*>(x)[lane];
+    u1 = reinterpret_cast<const uint4*>(x)[32 + lane];
+    if (a.halves) {
+      ra = x[kLatent + lane];
+      rb = x[kLatent + 32 + lane];
+    } else {
+      ra = *reinterpret_cast<const uint32_t*>(x + kLatent + 2 * lane);
+      rb = 0u;
+    }
+    pos = a.pos ? a.pos[i] : 0;
+  }
+};
+
+// Warps walk over the rows, the next row's loads in flight while one is
+// worked on, with gamma in registers.  The arithmetic (about 250 instructions
+// a row and warp, a third of them for the exact sum) weighs as much as the
+// bytes do.
 template <int FMT>
 __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
     const WriteArgs a, const __grid_constant__ RopeFreq fr) {
   pdl_wait_previous();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const long long i = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  const long long step = static_cast<long long>(gridDim.x) * kRowWarps;
+  long long i = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
   if (i >= a.n) return;
-  const long long slot = a.slots[i];
-  const uint16_t* x = a.kv + i * a.stride;
-  const uint4* xv = reinterpret_cast<const uint4*>(x);
-  const uint4 u0 = xv[lane], u1 = xv[32 + lane];
-  if (slot < 0) return;
-  if (slot >= a.n_rows) {
-    if (lane == 0) set_status(a.status, ESS_ERR_DEVICE_CHECK);
-    return;
-  }
-  // k^R: lane l turns pair l
-  uint32_t ra, rb;
-  if (a.halves) {
-    ra = x[kLatent + lane];
-    rb = x[kLatent + 32 + lane];
-  } else {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(x + kLatent + 2 * lane);
-    ra = w & 0xffffu;
-    rb = w >> 16;
-  }
-  float y[16];
-  unpack8(u0, y);
-  unpack8(u1, y + 8);
+  RawRow next;
+  next.load(a, i, lane);
+  float gm[16];
   if (a.gamma) {
-    SumSq s;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) s.add(y[e]);
-    s.warp_reduce<32>();
-    const float r = s.rsqrt_mean(kLatent, a.eps);
     const uint4* gv = reinterpret_cast<const uint4*>(a.gamma);
-    float g[16];
-    unpack8(gv[lane], g);
-    unpack8(gv[32 + lane], g + 8);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) y[e] = __fmul_rn(__fmul_rn(y[e], r), g[e]);
+    unpack8(gv[lane], gm);
+    unpack8(gv[32 + lane], gm + 8);
   }
-  if (a.pos) {
-    const unsigned long long turn =
-        static_cast<unsigned long long>(static_cast<long long>(a.pos[i])) * fr.f[lane];
-    // the top 32 bits as a signed fraction of a turn, in half turns
-    const float h = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
-    float sn, cs;
-    sincospif(h, &sn, &cs);
-    const float xa = bf16_lo(ra), xb = bf16_lo(rb);
-    ra = bf16_bits(xa * cs - xb * sn);
-    rb = bf16_bits(xa * sn + xb * cs);
-  }
-  uint8_t* row = a.rows + slot * row_bytes_of(FMT);
-  uint16_t* rope;
-  if (FMT == ESS_ROW_BF16) {
-    uint4* o = reinterpret_cast<uint4*>(row);
-    o[lane] = pack8_bf16(y);
-    o[32 + lane] = pack8_bf16(y + 8);
-    rope = reinterpret_cast<uint16_t*>(row + 1024);
-  } else if (FMT == ESS_ROW_COMPACT) {
-    // a tile of 128 dims is 16 lanes of one unit
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float m = group_max<16>(amax8(y + 8 * h));
-      const int e = scale_exp(m, 448.0f);
-      const float inv = exp2i(-e);
-      reinterpret_cast<uint2*>(row)[32 * h + lane] = pack8_e4m3(y + 8 * h, inv);
-      if ((lane & 15) == 0)
-        reinterpret_cast<float*>(row + 512)[2 * h + (lane >> 4)] = exp2i(e);
+  const unsigned long long freq = fr.f[lane];
+  for (; i < a.n; i += step) {
+    const RawRow row = next;
+    if (i + step < a.n) next.load(a, i + step, lane);
+    if (row.slot < 0) continue;
+    if (row.slot >= a.n_rows) {
+      if (lane == 0) set_status(a.status, ESS_ERR_DEVICE_CHECK);
+      continue;
     }
-    rope = reinterpret_cast<uint16_t*>(row + 528);
-  } else {
-    // a block of 32 dims is 4 lanes of one unit
+    float y[16];
+    unpack8(row.u0, y);
+    unpack8(row.u1, y + 8);
+    if (a.gamma) {
+      SumSq s;
+      s.sum<16, 32>(y);
+      const F2 r = both(s.rsqrt_mean(kLatent, a.eps));
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float m = group_max<4>(amax8(y + 8 * h));
-      const int e = min(max(scale_exp(m, 6.0f), kQ4MinExp), kQ4MaxExp);
-      const float inv = exp2i(-e);
-      reinterpret_cast<uint32_t*>(row)[32 * h + lane] = pack8_e2m1(y + 8 * h, inv);
-      if ((lane & 3) == 0) row[256 + 8 * h + (lane >> 2)] = static_cast<uint8_t>(e + 127);
+      for (int e = 0; e < 16; e += 2) {
+        const F2 v = mul2(mul2(F2{y[e], y[e + 1]}, r), F2{gm[e], gm[e + 1]});
+        y[e] = v.x;
+        y[e + 1] = v.y;
+      }
     }
-    rope = reinterpret_cast<uint16_t*>(row + 272);
-  }
-  if (a.halves) {
-    rope[lane] = static_cast<uint16_t>(ra);
-    rope[32 + lane] = static_cast<uint16_t>(rb);
-  } else {
-    reinterpret_cast<uint32_t*>(rope)[lane] = ra | (rb << 16);
+    // k^R: lane l turns pair l
+    uint32_t ra = row.ra, rb = row.rb;
+    if (!a.halves) {
+      rb = ra >> 16;
+      ra &= 0xffffu;
+    }
+    if (a.pos) {
+      const unsigned long long turn =
+          static_cast<unsigned long long>(static_cast<long long>(row.pos)) * freq;
+      // the top 32 bits as a signed fraction of a turn, in half turns
+      const float h = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+      float sn, cs;
+      sincospif(h, &sn, &cs);
+      const float xa = bf16_lo(ra), xb = bf16_lo(rb);
+      ra = bf16_bits(xa * cs - xb * sn);
+      rb = bf16_bits(xa * sn + xb * cs);
+    }
+    uint8_t* out = a.rows + row.slot * row_bytes_of(FMT);
+    uint16_t* rope;
+    if (FMT == ESS_ROW_BF16) {
+      uint4* o = reinterpret_cast<uint4*>(out);
+      o[lane] = pack8_bf16(y);
+      o[32 + lane] = pack8_bf16(y + 8);
+      rope = reinterpret_cast<uint16_t*>(out + 1024);
+    } else if (FMT == ESS_ROW_COMPACT) {
+      // a tile of 128 dims is 16 lanes of one unit
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float m = group_max<16>(amax8(y + 8 * h));
+        const int e = scale_exp(m, 448.0f);
+        const float inv = exp2i(-e);
+        reinterpret_cast<uint2*>(out)[32 * h + lane] = pack8_e4m3(y + 8 * h, inv);
+        if ((lane & 15) == 0)
+          reinterpret_cast<float*>(out + 512)[2 * h + (lane >> 4)] = exp2i(e);
+      }
+      rope = reinterpret_cast<uint16_t*>(out + 528);
+    } else {
+      // a block of 32 dims is 4 lanes of one unit
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float m = group_max<4>(amax8(y + 8 * h));
+        const int e = min(max(scale_exp(m, 6.0f), kQ4MinExp), kQ4MaxExp);
+        const float inv = exp2i(-e);
+        reinterpret_cast<uint32_t*>(out)[32 * h + lane] = pack8_e2m1(y + 8 * h, inv);
+        if ((lane & 3) == 0) out[256 + 8 * h + (lane >> 2)] = static_cast<uint8_t>(e + 127);
+      }
+      rope = reinterpret_cast<uint16_t*>(out + 272);
+    }
+    if (a.halves) {
+      rope[lane] = static_cast<uint16_t>(ra);
+      rope[32 + lane] = static_cast<uint16_t>(rb);
+    } else {
+      reinterpret_cast<uint32_t*>(rope)[lane] = ra | (rb << 16);
+    }
   }
 }
 
@@ -199,8 +232,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const
   const long long i = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / TPR;
   const bool live = i < a.n;
   const int units = a.dim >> 3;
-  float h[UNITS][8];
-  SumSq s;
+  float h[UNITS * 8];
 #pragma unroll
   for (int u = 0; u < UNITS; ++u) {
     const int c = u * TPR + t;
@@ -209,25 +241,24 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const
       v = reinterpret_cast<const uint4*>(a.x + i * a.x_stride)[c];
       if (RES) w = reinterpret_cast<const uint4*>(a.res + i * a.res_stride)[c];
     }
-    unpack8(v, h[u]);
+    unpack8(v, h + 8 * u);
     if (RES) {
       float r[8];
       unpack8(w, r);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[u][e] += r[e];
+      for (int e = 0; e < 8; ++e) h[8 * u + e] += r[e];
     }
   }
+  uint4 gm[UNITS];
 #pragma unroll
   for (int u = 0; u < UNITS; ++u) {
-    if (RES) {
-      const int c = u * TPR + t;
-      if (a.res_out && live && c < units)
-        reinterpret_cast<uint4*>(a.res_out + i * a.res_stride)[c] = pack8_bf16(h[u]);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s.add(h[u][e]);
+    const int c = u * TPR + t;
+    gm[u] = c < units ? reinterpret_cast<const uint4*>(a.gamma)[c] : make_uint4(0u, 0u, 0u, 0u);
+    if (RES && a.res_out && live && c < units)
+      reinterpret_cast<uint4*>(a.res_out + i * a.res_stride)[c] = pack8_bf16(h + 8 * u);
   }
-  s.template warp_reduce<(TPR < 32 ? TPR : 32)>();
+  SumSq s;
+  s.template sum<UNITS * 8, (TPR < 32 ? TPR : 32)>(h);
   if (TPR > 32) {
     __shared__ float2 part[kThreads / 32];
     const int w = threadIdx.x >> 5;
@@ -238,16 +269,19 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const
 #pragma unroll
     for (int q = 0; q < TPR / 32; ++q) s.merge(part[w0 + q].x, part[w0 + q].y);
   }
-  const float r = s.rsqrt_mean(a.dim, a.eps);
+  const F2 r = both(s.rsqrt_mean(a.dim, a.eps));
   const int groups = (a.dim + 127) >> 7;
 #pragma unroll
   for (int u = 0; u < UNITS; ++u) {
     const int c = u * TPR + t;
     float y[8], g[8];
-    unpack8(c < units ? reinterpret_cast<const uint4*>(a.gamma)[c] : make_uint4(0u, 0u, 0u, 0u),
-            g);
+    unpack8(gm[u], g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(__fmul_rn(h[u][e], r), g[e]);
+    for (int e = 0; e < 8; e += 2) {
+      const F2 v = mul2(mul2(F2{h[8 * u + e], h[8 * u + e + 1]}, r), F2{g[e], g[e + 1]});
+      y[e] = v.x;
+      y[e + 1] = v.y;
+    }
     const float m = group_max<16>(amax8(y));
     const int e = scale_exp(m, 448.0f);
     if (live && c < units) {
@@ -320,7 +354,8 @@ ess_status ess_cache_write(const void* kv, int64_t kv_stride, int64_t n, const v
   a.rows = static_cast<uint8_t*>(rows);
   a.n_rows = n_rows;
   a.status = status;
-  const dim3 grid(static_cast<unsigned>((n + kRowWarps - 1) / kRowWarps));
+  const dim3 grid(static_cast<unsigned>(
+      std::min<long long>((n + kRowWarps - 1) / kRowWarps, kWriteCtas)));
   const dim3 block(kRowWarps * 32);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;

@@ -149,16 +149,47 @@ __device__ __forceinline__ uint4 widen8_e4m3(const uint2& c, float scale) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// A sum of squares as an unevaluated pair hi + lo (about 48 bits): the codes
-// of values next to a rounding border, and a scale next to a power of two,
-// hang on the last bit of r, so the sum must not depend on its order.
+// ---------------------------------------------------------------- pairs
+// Two fp32 operations in one instruction.
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ F2 fma2(const F2& a, const F2& b, const F2& c) {
+  F2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ F2 add2(const F2& a, const F2& b) {
+  F2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ F2 mul2(const F2& a, const F2& b) {
+  F2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ F2 both(float v) { return F2{v, v}; }
+
+// ---------------------------------------------------------------- norms
+// A sum of squares as an unevaluated pair hi + lo: the codes of values next to
+// a rounding border, and a scale next to a power of two, hang on the last bit
+// of r, so the sum must not depend on its order.
 struct SumSq {
   float hi = 0.0f, lo = 0.0f;
 
-  __device__ __forceinline__ void add(float x) {
-    const float p = __fmul_rn(x, x);
-    merge(p, __fmaf_rn(x, x, -p));
-  }
   // (hi, lo) += (p, e): the exact sum of hi and p, its error into lo
   __device__ __forceinline__ void merge(float p, float e) {
     const float t = __fadd_rn(hi, p);
@@ -167,14 +198,46 @@ struct SumSq {
     hi = t;
     lo = __fadd_rn(lo, __fadd_rn(err, e));
   }
-  // over aligned groups of N lanes (all 32 lanes call it)
-  template <int N>
-  __device__ __forceinline__ void warp_reduce() {
+
+  // The squares of N values in each of G neighbouring lanes (all 32 lanes call
+  // it).  A power of two C above their sum, known from the largest value, is
+  // put under the running sum s: then every s + x^2 is rounded at one place,
+  // the rounding is t = (s + x^2) - s exactly, and x^2 - t, from one fma, is
+  // what was rounded off.  The parts kept are multiples of that place below C
+  // and add up exactly in any order; those rounded off are 2^-24 of C or less
+  // and are summed apart.  (Four operations a value, in pairs, where an exact
+  // addition without C takes eight.)
+  template <int N, int G>
+  __device__ __forceinline__ void sum(const float* x) {
+    float m[4] = {fabsf(x[0]), fabsf(x[1]), fabsf(x[2]), fabsf(x[3])};
 #pragma unroll
-    for (int o = 1; o < N; o <<= 1) {
-      const float p = __shfl_xor_sync(0xffffffffu, hi, o);
-      const float e = __shfl_xor_sync(0xffffffffu, lo, o);
-      merge(p, e);
+    for (int i = 4; i < N; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(x[i]));
+    float mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    if (G == 32)
+      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+    else
+      mx = group_max<G>(mx);
+    constexpr int kLog = N * G <= 64 ? 6 : N * G <= 128 ? 7 : N * G <= 256 ? 8 : N * G <= 512 ? 9 : 10;
+    static_assert(N * G <= 1024 && N % 2 == 0 && N >= 4, "values of one sum");
+    const int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;   // mx < 2^(e + 1)
+    const float c = exp2i(min(max(2 * e + 2 + kLog, -100), 126));
+    F2 s = both(0.5f * c), l = both(0.0f);   // two running sums, each below half of it
+    const F2 neg = both(-1.0f);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const F2 v{x[i], x[i + 1]};
+      const F2 u = fma2(v, v, s);
+      const F2 t = fma2(s, neg, u);
+      const F2 r = fma2(v, v, mul2(t, neg));
+      l = add2(l, r);
+      s = u;
+    }
+    hi = __fadd_rn(__fsub_rn(s.x, 0.5f * c), __fsub_rn(s.y, 0.5f * c));
+    lo = __fadd_rn(l.x, l.y);
+#pragma unroll
+    for (int o = 1; o < G; o <<= 1) {
+      hi = __fadd_rn(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      lo = __fadd_rn(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     }
   }
   // 1 / sqrt((hi + lo) / n + eps): the hardware's reciprocal root, then one
@@ -182,9 +245,9 @@ struct SumSq {
   // the result is the rounded root up to a few in 2^20 cases.
   __device__ __forceinline__ float rsqrt_mean(int n, float eps) const {
     const float d = static_cast<float>(n);
-    const float q = __fdiv_rn(hi, d);
+    const float q = __fdividef(hi, d);           // near hi / d; the rest below makes up for it
     const float rem = __fadd_rn(__fmaf_rn(-q, d, hi), lo);
-    float ml = __fdiv_rn(rem, d);
+    float ml = __fdividef(rem, d);
     const float mh = __fadd_rn(q, eps);
     const float b = __fsub_rn(mh, q);
     ml = __fadd_rn(ml, __fadd_rn(__fsub_rn(q, __fsub_rn(mh, b)), __fsub_rn(eps, b)));
