@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
     if (a.gamma) {
       SumSq s;
       s.sum<16, 32>(y);
-      const F2 r = both(s.rsqrt_mean(kLatent, a.eps));
+      const F2 r = both(s.rsqrt_mean(make_float2(1.0f / kLatent, 0.0f), a.eps));
 #pragma unroll
       for (int e = 0; e < 16; e += 2) {
         const F2 v = mul2(mul2(F2{y[e], y[e + 1]}, r), F2{gm[e], gm[e + 1]});
@@ -113,10 +113,11 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
     if (a.pos) {
       const unsigned long long turn =
           static_cast<unsigned long long>(static_cast<long long>(row.pos)) * freq;
-      // the top 32 bits as a signed fraction of a turn, in half turns
-      const float h = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
-      float sn, cs;
-      sincospif(h, &sn, &cs);
+      // the top 32 bits as a signed fraction of a turn, in radians within
+      // +-pi, where the hardware's sine and cosine are off by at most 2^-21:
+      // far below half a step of the bf16 result
+      const float h = static_cast<float>(static_cast<int32_t>(turn >> 32)) * (3.14159265358979f * 0x1p-31f);
+      const float sn = __sinf(h), cs = __cosf(h);
       const float xa = bf16_lo(ra), xb = bf16_lo(rb);
       ra = bf16_bits(xa * cs - xb * sn);
       rb = bf16_bits(xa * sn + xb * cs);
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float m = group_max<16>(amax8(y + 8 * h));
-        const int e = scale_exp(m, 448.0f);
+        const int e = scale_exp<448>(m);
         const float inv = exp2i(-e);
         reinterpret_cast<uint2*>(out)[32 * h + lane] = pack8_e4m3(y + 8 * h, inv);
         if ((lane & 15) == 0)
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float m = group_max<4>(amax8(y + 8 * h));
-        const int e = min(max(scale_exp(m, 6.0f), kQ4MinExp), kQ4MaxExp);
+        const int e = min(max(scale_exp<6>(m), kQ4MinExp), kQ4MaxExp);
         const float inv = exp2i(-e);
         reinterpret_cast<uint32_t*>(out)[32 * h + lane] = pack8_e2m1(y + 8 * h, inv);
         if ((lane & 3) == 0) out[256 + 8 * h + (lane >> 2)] = static_cast<uint8_t>(e + 127);
@@ -215,6 +216,7 @@ struct NormArgs {
   float eps;
   long long n;
   int dim;
+  float2 inv_dim;      // 1 / dim as a sum of two floats
   uint16_t* res_out;
   uint8_t* codes;
   float* scales;
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const
 #pragma unroll
     for (int q = 0; q < TPR / 32; ++q) s.merge(part[w0 + q].x, part[w0 + q].y);
   }
-  const F2 r = both(s.rsqrt_mean(a.dim, a.eps));
+  const F2 r = both(s.rsqrt_mean(a.inv_dim, a.eps));
   const int groups = (a.dim + 127) >> 7;
 #pragma unroll
   for (int u = 0; u < UNITS; ++u) {
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const
       y[e + 1] = v.y;
     }
     const float m = group_max<16>(amax8(y));
-    const int e = scale_exp(m, 448.0f);
+    const int e = scale_exp<448>(m);
     if (live && c < units) {
       reinterpret_cast<uint2*>(a.codes + i * a.dim)[c] = pack8_e4m3(y, exp2i(-e));
       if ((c & 15) == 0) a.scales[i * groups + (c >> 4)] = exp2i(e);
@@ -415,6 +417,8 @@ ess_status ess_norm_quant(const void* x, int64_t x_stride, const void* residual,
   a.eps = eps;
   a.n = n;
   a.dim = dim;
+  a.inv_dim.x = static_cast<float>(1.0 / dim);
+  a.inv_dim.y = static_cast<float>(1.0 / dim - a.inv_dim.x);
   a.res_out = static_cast<uint16_t*>(residual_out);
   a.codes = static_cast<uint8_t*>(codes);
   a.scales = scales;

@@ -61,38 +61,19 @@ __device__ __forceinline__ float group_max(float v) {
 __device__ __forceinline__ float exp2i(int e) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
-// Exponent of the smallest power of two at or above fl32(amax / top), kept
-// within -126..126; 0 for amax = 0 (and for an infinite or NaN one, whose
-// codes saturate).
-__device__ __forceinline__ int scale_exp(float amax, float top) {
-  if (!(amax > 0.0f) || amax > 3.402823466e38f) return 0;
-  const uint32_t q = __float_as_uint(__fdiv_rn(amax, top));
-  const int e = static_cast<int>(q >> 23) - 127 + ((q & 0x7fffffu) ? 1 : 0);
-  return min(max(e, -126), 126);
-}
-
-// e4m3(f * inv), nearest even, saturating at +-448
-__device__ __forceinline__ uint2 pack8_e4m3(const float* f, float inv) {
-  uint32_t w[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    w[q] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * q] * inv, f[2 * q + 1] * inv),
-                                    __NV_SATFINITE, __NV_E4M3);
-  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-}
-// e2m1(f * inv), nearest even, saturating at +-6; value 2i in the low half of byte i
-__device__ __forceinline__ uint32_t pack8_e2m1(const float* f, float inv) {
-  uint32_t out;
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
-      "mov.b32 %0, {b0, b1, b2, b3};\n\t}\n"
-      : "=r"(out)
-      : "f"(f[0] * inv), "f"(f[1] * inv), "f"(f[2] * inv), "f"(f[3] * inv), "f"(f[4] * inv),
-        "f"(f[5] * inv), "f"(f[6] * inv), "f"(f[7] * inv));
-  return out;
+// Exponent e of the smallest power of two at or above fl32(amax / TOP), TOP = 6
+// or 448; 0 for amax = 0 (and for an infinite or NaN one, whose codes
+// saturate).  With TOP = c 2^t and amax = m 2^k, 1 <= c, m < 2, that is k - t
+// for m <= c and one more above it: the next float after c 2^k is far enough
+// away (a third of its ulp at least) for fl32 not to round it down to 2^(k - t).
+template <int TOP>
+__device__ __forceinline__ int scale_exp(float amax) {
+  static_assert(TOP == 6 || TOP == 448, "1.5 * 2^2 or 1.75 * 2^8");
+  constexpr uint32_t kMant = TOP == 6 ? 0x400000u : 0x600000u;
+  constexpr int kExp = TOP == 6 ? 2 : 8;
+  const uint32_t b = __float_as_uint(amax);
+  const int e = static_cast<int>((b + (0x7fffffu - kMant)) >> 23) - 127 - kExp;
+  return b - 1u < 0x7f7fffffu ? max(e, -126) : 0;   // 0 < amax < infinity
 }
 
 // eight e2m1 codes as four pairs of fp16 values (exact)
@@ -183,6 +164,34 @@ __device__ __forceinline__ F2 mul2(const F2& a, const F2& b) {
 }
 __device__ __forceinline__ F2 both(float v) { return F2{v, v}; }
 
+// e4m3(f * inv), nearest even, saturating at +-448
+__device__ __forceinline__ uint2 pack8_e4m3(const float* f, float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const F2 v = mul2(F2{f[2 * q], f[2 * q + 1]}, both(inv));
+    w[q] = __nv_cvt_float2_to_fp8x2(make_float2(v.x, v.y), __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+// e2m1(f * inv), nearest even, saturating at +-6; value 2i in the low half of byte i
+__device__ __forceinline__ uint32_t pack8_e2m1(const float* f, float inv) {
+  F2 v[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = mul2(F2{f[2 * q], f[2 * q + 1]}, both(inv));
+  uint32_t out;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}\n"
+      : "=r"(out)
+      : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x),
+        "f"(v[3].y));
+  return out;
+}
+
 // ---------------------------------------------------------------- norms
 // A sum of squares as an unevaluated pair hi + lo: the codes of values next to
 // a rounding border, and a scale next to a power of two, hang on the last bit
@@ -240,18 +249,18 @@ struct SumSq {
       lo = __fadd_rn(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     }
   }
-  // 1 / sqrt((hi + lo) / n + eps): the hardware's reciprocal root, then one
-  // Newton step whose residual 1 - m r^2 is formed from exact products, so
-  // the result is the rounded root up to a few in 2^20 cases.
-  __device__ __forceinline__ float rsqrt_mean(int n, float eps) const {
-    const float d = static_cast<float>(n);
-    const float q = __fdividef(hi, d);           // near hi / d; the rest below makes up for it
-    const float rem = __fadd_rn(__fmaf_rn(-q, d, hi), lo);
-    float ml = __fdividef(rem, d);
+  // 1 / sqrt((hi + lo) / n + eps), 1 / n given as a pair too: the hardware's
+  // reciprocal root, then one Newton step whose residual 1 - m r^2 is formed
+  // from exact products, so the result is the rounded root but for a few of
+  // 2^20 cases.
+  __device__ __forceinline__ float rsqrt_mean(float2 inv_n, float eps) const {
+    const float q = __fmul_rn(hi, inv_n.x);
+    float ml = __fmaf_rn(lo, inv_n.x, __fmaf_rn(hi, inv_n.y, __fmaf_rn(hi, inv_n.x, -q)));
     const float mh = __fadd_rn(q, eps);
     const float b = __fsub_rn(mh, q);
     ml = __fadd_rn(ml, __fadd_rn(__fsub_rn(q, __fsub_rn(mh, b)), __fsub_rn(eps, b)));
-    const float r0 = rsqrtf(mh);
+    float r0;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(mh));
     const float r2 = __fmul_rn(r0, r0);
     const float r2e = __fmaf_rn(r0, r0, -r2);
     const float t = __fmul_rn(mh, r2);
@@ -260,7 +269,7 @@ struct SumSq {
                                 __fmul_rn(ml, r2));
     const float r = __fmaf_rn(__fmul_rn(0.5f, r0), res, r0);
     // a mean of zero (or one past fp32's range) has no residual: 1 / 0 and 1 / inf as they are
-    return (mh > 0.0f && mh < 3.0e38f) ? r : r0;
+    return (mh > 1.2e-38f && mh < 3.0e38f) ? r : r0;
   }
 };
 
