@@ -223,7 +223,12 @@ struct NormArgs {
 };
 
 // TPR threads hold one row, UNITS 16-byte units (8 values) each: unit u of the
-// row sits in thread u % TPR, so 16 neighbouring lanes hold one group of 128.
+// row sits in thread u % TPR, so 16 neighbouring lanes hold one group of 128;
+// with TPR = 8 (an indexer key) both units of eight lanes do.  A warp so takes
+// four keys at once, and what is done once a row (the root, the joining of
+// sums), which bounds rows this short, is shared by them: 131072 keys in 11.6
+// us, where sixteen lanes a key took 16.0.  Two units a thread is the best for
+// long rows too (16384 x 4096 with a residual: 88 us, four units 90 us).
 template <int TPR, int UNITS, bool RES>
 __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const NormArgs a) {
   constexpr int kThreads = TPR > 256 ? TPR : 256;
@@ -275,20 +280,31 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const
   const int groups = (a.dim + 127) >> 7;
 #pragma unroll
   for (int u = 0; u < UNITS; ++u) {
-    const int c = u * TPR + t;
-    float y[8], g[8];
+    float g[8];
     unpack8(gm[u], g);
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
       const F2 v = mul2(mul2(F2{h[8 * u + e], h[8 * u + e + 1]}, r), F2{g[e], g[e + 1]});
-      y[e] = v.x;
-      y[e + 1] = v.y;
+      h[8 * u + e] = v.x;
+      h[8 * u + e + 1] = v.y;
     }
-    const float m = group_max<16>(amax8(y));
+  }
+  constexpr int kPer = TPR < 16 ? UNITS : 1;   // units of a thread in one group
+#pragma unroll
+  for (int u0 = 0; u0 < UNITS; u0 += kPer) {
+    float m = 0.0f;
+#pragma unroll
+    for (int u = u0; u < u0 + kPer; ++u) m = fmaxf(m, amax8(h + 8 * u));
+    m = group_max<(TPR < 16 ? TPR : 16)>(m);
     const int e = scale_exp<448>(m);
-    if (live && c < units) {
-      reinterpret_cast<uint2*>(a.codes + i * a.dim)[c] = pack8_e4m3(y, exp2i(-e));
-      if ((c & 15) == 0) a.scales[i * groups + (c >> 4)] = exp2i(e);
+    const float inv = exp2i(-e);
+#pragma unroll
+    for (int u = u0; u < u0 + kPer; ++u) {
+      const int c = u * TPR + t;
+      if (live && c < units) {
+        reinterpret_cast<uint2*>(a.codes + i * a.dim)[c] = pack8_e4m3(h + 8 * u, inv);
+        if ((c & 15) == 0) a.scales[i * groups + (c >> 4)] = exp2i(e);
+      }
     }
   }
 }
@@ -424,10 +440,10 @@ ess_status ess_norm_quant(const void* x, int64_t x_stride, const void* residual,
   a.scales = scales;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (dim <= 128) e = launch_norm<16, 1>(a, st);
-  else if (dim <= 256) e = launch_norm<32, 1>(a, st);
-  else if (dim <= 512) e = launch_norm<64, 1>(a, st);
-  else if (dim <= 1024) e = launch_norm<128, 1>(a, st);
+  if (dim <= 128) e = launch_norm<8, 2>(a, st);
+  else if (dim <= 256) e = launch_norm<16, 2>(a, st);
+  else if (dim <= 512) e = launch_norm<32, 2>(a, st);
+  else if (dim <= 1024) e = launch_norm<64, 2>(a, st);
   else if (dim <= 2048) e = launch_norm<128, 2>(a, st);
   else if (dim <= 4096) e = launch_norm<256, 2>(a, st);
   else if (dim <= 8192) e = launch_norm<512, 2>(a, st);
