@@ -284,27 +284,37 @@ struct Tiles {
   }
 };
 
-// The cache row of token e of the tile's entry, or -1.
-__device__ __forceinline__ int token_row(const MlaArgs& a, int v, int len, int e) {
-  if (e >= len) return -1;
-  int b = v, t = e;
-  if (a.tokens) {
-    b = v / a.ways;
-    t = a.tokens[static_cast<size_t>(v) * a.k + e];
-    if (t < 0) return -1;
-    if (t >= request_len(a, b)) {
-      set_status(a.status, ESS_ERR_DEVICE_CHECK);
-      return -1;
-    }
+// The cache rows of a lane's four tokens e, e + 32, .. of an entry, -1 for one
+// that is not.  The four list entries are loaded together, then the four page
+// table entries, so that a tile costs one latency of each.
+__device__ __forceinline__ void token_rows(const MlaArgs& a, int v, int len, int e, int* row) {
+  int t[4], pg[4];
+  const int b = a.tokens ? v / a.ways : v;
+  const int T = a.tokens ? request_len(a, b) : len;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int x = e + 32 * j;
+    t[j] = x;
+    if (a.tokens) t[j] = x < len ? a.tokens[static_cast<size_t>(v) * a.k + x] : -1;
+    else if (x >= len) t[j] = -1;
   }
-  const int pi = a.page_shift >= 0 ? t >> a.page_shift : t / a.page;
-  const int pg = a.page_table[static_cast<size_t>(b) * a.max_pages + pi];
-  const long long row = static_cast<long long>(pg) * a.page + (t - pi * a.page);
-  if (row < 0 || row >= a.n_rows) {
-    set_status(a.status, ESS_ERR_DEVICE_CHECK);
-    return -1;
+  const int32_t* table = a.page_table + static_cast<size_t>(b) * a.max_pages;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int u = t[j] >= 0 && t[j] < T ? t[j] : 0;
+    pg[j] = a.page_shift >= 0 ? u >> a.page_shift : u / a.page;
+    row[j] = u - pg[j] * a.page;
+    pg[j] = t[j] >= 0 && t[j] < T ? table[pg[j]] : -1;
   }
-  return static_cast<int>(row);
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const long long r = static_cast<long long>(pg[j]) * a.page + row[j];
+    const bool ok = pg[j] >= 0 && r < a.n_rows;
+    bad |= !ok && t[j] >= 0;
+    row[j] = ok ? static_cast<int>(r) : -1;
+  }
+  if (bad) set_status(a.status, ESS_ERR_DEVICE_CHECK);
 }
 
 // 32 codes (one block) -> four 16-byte units of fp16
@@ -334,9 +344,7 @@ __device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
   int slot = 0, turn = 0;
   for (int g = 0; it.more(); ++g) {
     int row[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      row[j] = token_row(a, it.v, it.len, it.tile * kMt + 32 * j + lane);
+    token_rows(a, it.v, it.len, it.tile * kMt + lane, row);
     if (turn > 0) wait_or_abort(&mi->row_free[slot], (turn - 1) & 1, mi, a.status);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -527,9 +535,9 @@ __device__ __forceinline__ void mma_role(const MlaArgs& a, uint8_t* smem, Misc* 
 // beside the fp16 latents, each row divided by the power of two that brings
 // its largest value to [2^14, 2^15) (exact down to 2^-31 of that value, with an
 // error below 2^-39 of it under that); the RoPE part, divided alike, as bf16.
+template <int kFly>   // rows in flight
 __device__ __forceinline__ void load_queries(const MlaArgs& a, uint8_t* smem, Misc* mi, int v,
                                              int row0, int warp, int lane) {
-  constexpr int kFly = 2;   // rows in flight
   uint8_t* sq = smem + kOffQ;
 #pragma unroll 1
   for (int i0 = 0; i0 < 8; i0 += kFly) {
@@ -594,7 +602,7 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
   float m = -INFINITY, l = 0.0f, c2 = 0.0f;
   int limit = 0, seg_first_tile = 0, buf = 0, seg = 0;
   Tiles it(a, mi);
-  load_queries(a, smem, mi, it.v, it.rt * kPairRows + static_cast<int>(rank) * kCtaRows, warp,
+  load_queries<4>(a, smem, mi, it.v, it.rt * kPairRows + static_cast<int>(rank) * kCtaRows, warp,
                lane);
   for (int g = 0; it.more(); ++g) {
     const bool first = it.first(), last = it.last();
@@ -687,7 +695,7 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       it.next(a);
       if (it.more()) {   // the next segment's queries, ahead of this one's output
         wait_or_abort(&mi->q_free, seg & 1, mi, a.status);
-        load_queries(a, smem, mi, it.v, it.rt * kPairRows + static_cast<int>(rank) * kCtaRows,
+        load_queries<2>(a, smem, mi, it.v, it.rt * kPairRows + static_cast<int>(rank) * kCtaRows,
                      warp, lane);
       }
       ++seg;
@@ -797,12 +805,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   long long* scan = reinterpret_cast<long long*>(mi->row);   // free until the roles start
   if (lane == 31) scan[warp] = before;
   __syncthreads();
-  long long total = 0;
-  before -= mine;
-  for (int w = 0; w < kMlaThreads / 32; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
+  long long sums = lane < kMlaThreads / 32 ? scan[lane] : 0;   // of the warps
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, sums, o);
+    if (lane >= o) sums += x;
   }
+  const long long total = __shfl_sync(0xffffffffu, sums, 31);
+  before += __shfl_sync(0xffffffffu, sums, max(warp - 1, 0)) * (warp > 0 ? 1 : 0) - mine;
   // the first total % busy pairs take one tile more; neighbouring pairs share
   // a request, so none between two may be idle
   const int busy = total < pairs ? max(static_cast<int>(total), 1) : pairs;
@@ -857,19 +867,19 @@ __global__ void __launch_bounds__(128) cache_mla_join_kernel(const MlaArgs a) {
   const int x = blockIdx.x;                      // (b, m, h)
   const int h = x % a.heads, bm = x / a.heads, b = bm / a.ways, m = bm % a.ways;
   const int t = threadIdx.x;
+  const int v = a.tokens ? bm : b;
+  const int row = a.tokens ? h : m * a.heads + h;
   const int T = a.T[b];
+  const int2 sp = a.span[static_cast<size_t>(v) * a.row_tiles + row / kPairRows];
   if (h == 0 && m == 0 && t == 0 &&
       (T < 0 || T > static_cast<long long>(a.max_pages) * a.page))
     set_status(a.status, ESS_ERR_DEVICE_CHECK);
-  const int v = a.tokens ? bm : b;
-  const int row = a.tokens ? h : m * a.heads + h;
   uint2* out = reinterpret_cast<uint2*>(a.out + static_cast<size_t>(x) * kLatent) + t;
   if (entry_len(a, v) == 0) {
     *out = make_uint2(0u, 0u);
     if (t == 0 && a.lse) a.lse[x] = -INFINITY;
     return;
   }
-  const int2 sp = a.span[static_cast<size_t>(v) * a.row_tiles + row / kPairRows];
   const int p0 = sp.x >> 1;
   if (p0 == sp.y) return;
   const int pr = row % kPairRows;
