@@ -58,8 +58,6 @@ constexpr uint32_t kOffV = kOffK + 9 * kKBlk;
 constexpr uint32_t kOffP = kOffV + 4 * kVBlk;
 constexpr uint32_t kOffMisc = kOffP + 2 * kKBlk;
 
-constexpr int kJoinFly = 8;           // partials in flight per thread of the join
-
 constexpr uint32_t kColO = 0;         // TMEM columns: O, then two score buffers
 constexpr uint32_t kColS = 256;
 constexpr float kGrow = 8.0f;         // log2 of the growth of a maximum that O absorbs unscaled
@@ -562,8 +560,9 @@ __device__ __forceinline__ void load_queries(const MlaArgs& a, uint8_t* smem, Mi
       unpack8(u[i][0], x);
       unpack8(u[i][1], x + 8);
       const float ra = bf16_lo(rope[i]), rb = bf16_hi(rope[i]);
-      const float mx = group_max<32>(
-          fmaxf(fmaxf(amax8(x), amax8(x + 8)), fmaxf(fabsf(ra), fabsf(rb))));
+      const float mx = __uint_as_float(__reduce_max_sync(
+          0xffffffffu, __float_as_uint(fmaxf(fmaxf(amax8(x), amax8(x + 8)),
+                                             fmaxf(fabsf(ra), fabsf(rb))))));
       // 2^e <= mx < 2^(e + 1); rows of zeros, infinities and NaN as they are
       const int e = mx > 0.0f && mx < INFINITY
                         ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 - 14
@@ -860,13 +859,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc_pair(tmem, 512);
 }
 
-// One CTA per query row joins the partials of a row that several pairs share,
-// and writes the rows of requests without a token.
-__global__ void __launch_bounds__(128) cache_mla_join_kernel(const MlaArgs a) {
+// Joins the partials of a query row that several pairs share, and writes the
+// rows of requests without a token.  A group of 64 threads takes every GROUPS-th
+// partial of a row, FLY of them in flight, and a CTA's four groups belong to one
+// row (few rows cut into many parts: one request over 32 pairs took 17.8 us a
+// call with one group of FLY = 8 a row) or to four (many rows with two or three
+// parts each).
+constexpr int kJoinThreads = 64;
+constexpr int kJoinGroups = 4;
+
+template <int FLY, int GROUPS>
+__global__ void __launch_bounds__(kJoinThreads* kJoinGroups) cache_mla_join_kernel(
+    const MlaArgs a, int all_rows) {
+  __shared__ float shared[GROUPS > 1 ? (GROUPS - 1) * kJoinThreads * 10 : 1];
   pdl_wait_previous();
-  const int x = blockIdx.x;                      // (b, m, h)
+  const int group = threadIdx.x / kJoinThreads;
+  const int x = GROUPS > 1 ? blockIdx.x : blockIdx.x * kJoinGroups + group;   // (b, m, h)
+  const int g = GROUPS > 1 ? group : 0;
+  if (x >= all_rows) return;
   const int h = x % a.heads, bm = x / a.heads, b = bm / a.ways, m = bm % a.ways;
-  const int t = threadIdx.x;
+  const int t = threadIdx.x % kJoinThreads;   // dims 4t .. and 256 + 4t ..
   const int v = a.tokens ? bm : b;
   const int row = a.tokens ? h : m * a.heads + h;
   const int T = a.T[b];
@@ -875,52 +887,89 @@ __global__ void __launch_bounds__(128) cache_mla_join_kernel(const MlaArgs a) {
       (T < 0 || T > static_cast<long long>(a.max_pages) * a.page))
     set_status(a.status, ESS_ERR_DEVICE_CHECK);
   uint2* out = reinterpret_cast<uint2*>(a.out + static_cast<size_t>(x) * kLatent) + t;
-  if (entry_len(a, v) == 0) {
-    *out = make_uint2(0u, 0u);
+  if (entry_len(a, v) == 0) {   // (the conditions that leave are the same for a CTA's one row)
+    out[0] = out[kJoinThreads] = make_uint2(0u, 0u);
     if (t == 0 && a.lse) a.lse[x] = -INFINITY;
     return;
   }
   const int p0 = sp.x >> 1;
   if (p0 == sp.y) return;
   const int pr = row % kPairRows;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   float mx = -INFINITY, l = 0.0f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int pb = p0; pb <= sp.y; pb += kJoinFly) {
-    float2 ml[kJoinFly];
-    float4 o[kJoinFly];
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int pb = p0 + g; pb <= sp.y; pb += FLY * GROUPS) {
+    float2 ml[FLY];
+    float4 o[FLY][2];
 #pragma unroll
-    for (int q = 0; q < kJoinFly; ++q) {
-      const int p = pb + q;
+    for (int q = 0; q < FLY; ++q) {
+      const int p = pb + q * GROUPS;
       const size_t i = static_cast<size_t>(p == p0 ? sp.x : 2 * p) * kPairRows + pr;
-      ml[q] = p <= sp.y ? a.part_ml[i] : make_float2(-INFINITY, 0.0f);
-      o[q] = p <= sp.y ? reinterpret_cast<const float4*>(a.part_o + i * kLatent)[t]
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4* po = reinterpret_cast<const float4*>(a.part_o + i * kLatent) + t;
+      const bool in = p <= sp.y;
+      ml[q] = in ? a.part_ml[i] : make_float2(-INFINITY, 0.0f);
+      o[q][0] = in ? po[0] : zero;
+      o[q][1] = in ? po[kJoinThreads] : zero;
     }
     float m2 = mx;
 #pragma unroll
-    for (int q = 0; q < kJoinFly; ++q) m2 = fmaxf(m2, ml[q].x);
+    for (int q = 0; q < FLY; ++q) m2 = fmaxf(m2, ml[q].x);
     const float base = m2 == -INFINITY ? 0.0f : m2;
     const float f = exp2f(mx - base);
     l *= f;
-    acc.x *= f;
-    acc.y *= f;
-    acc.z *= f;
-    acc.w *= f;
 #pragma unroll
-    for (int q = 0; q < kJoinFly; ++q) {
+    for (int e = 0; e < 8; ++e) acc[e] *= f;
+#pragma unroll
+    for (int q = 0; q < FLY; ++q) {
       // a part without a token has l = 0 and O = 0; its weight is 0 beside others
       const float w = exp2f(ml[q].x - base);
       l = fmaf(w, ml[q].y, l);
-      acc.x = fmaf(w, o[q].x, acc.x);
-      acc.y = fmaf(w, o[q].y, acc.y);
-      acc.z = fmaf(w, o[q].z, acc.z);
-      acc.w = fmaf(w, o[q].w, acc.w);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        acc[4 * e] = fmaf(w, o[q][e].x, acc[4 * e]);
+        acc[4 * e + 1] = fmaf(w, o[q][e].y, acc[4 * e + 1]);
+        acc[4 * e + 2] = fmaf(w, o[q][e].z, acc[4 * e + 2]);
+        acc[4 * e + 3] = fmaf(w, o[q][e].w, acc[4 * e + 3]);
+      }
+    }
+    mx = m2;
+  }
+  if (GROUPS > 1) {   // the groups' sums to the first one
+    if (g > 0) {
+      float* to = shared + (g - 1) * kJoinThreads * 10 + t;
+      to[0] = mx;
+      to[kJoinThreads] = l;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) to[(2 + e) * kJoinThreads] = acc[e];
+    }
+    __syncthreads();
+    if (g > 0) return;
+    float m2 = mx;
+#pragma unroll
+    for (int q = 0; q < GROUPS - 1; ++q)
+      m2 = fmaxf(m2, shared[q * kJoinThreads * 10 + t]);
+    const float base = m2 == -INFINITY ? 0.0f : m2;
+    const float f = exp2f(mx - base);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= f;
+#pragma unroll
+    for (int q = 0; q < GROUPS - 1; ++q) {
+      const float* from = shared + q * kJoinThreads * 10 + t;
+      const float w = exp2f(from[0] - base);
+      l = fmaf(w, from[kJoinThreads], l);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, from[(2 + e) * kJoinThreads], acc[e]);
     }
     mx = m2;
   }
   const bool some = l > 0.0f || l != l;
   const float inv = some ? 1.0f / l : 0.0f;
-  *out = make_uint2(bf16x2_bits(acc.x * inv, acc.y * inv), bf16x2_bits(acc.z * inv, acc.w * inv));
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    out[e * kJoinThreads] =
+        make_uint2(bf16x2_bits(acc[4 * e] * inv, acc[4 * e + 1] * inv),
+                   bf16x2_bits(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
   if (t == 0 && a.lse)
     a.lse[x] = some ? (mx + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
@@ -1036,7 +1085,14 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
   if (e != cudaSuccess) return ESS_ERR_CUDA;
   e = launch_pdl_once(cache_mla_kernel, dim3(2 * pairs), dim3(kMlaThreads), kMlaSmem, st, a);
   if (e != cudaSuccess) return ESS_ERR_CUDA;
-  e = launch_pdl_once(cache_mla_join_kernel, dim3(static_cast<unsigned>(all_rows)), dim3(128), 0, st, a);
+  const dim3 jblock(kJoinThreads * kJoinGroups);
+  if (all_rows >= 2048)   // more rows than CTAs that run at once
+    e = launch_pdl_once(cache_mla_join_kernel<4, 1>,
+                        dim3(static_cast<unsigned>((all_rows + kJoinGroups - 1) / kJoinGroups)),
+                        jblock, 0, st, a, static_cast<int>(all_rows));
+  else
+    e = launch_pdl_once(cache_mla_join_kernel<4, kJoinGroups>, dim3(static_cast<unsigned>(all_rows)),
+                        jblock, 0, st, a, static_cast<int>(all_rows));
   return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
 }
 
