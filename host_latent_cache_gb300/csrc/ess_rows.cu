@@ -81,7 +81,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
     unpack8(gv[lane], gm);
     unpack8(gv[32 + lane], gm + 8);
   }
-  const unsigned long long freq = fr.f[lane];
+  // kept in a register: an indexed constant is read lane by lane
+  unsigned long long freq = fr.f[lane];
+  asm volatile("" : "+l"(freq));
   for (; i < a.n; i += step) {
     const RawRow row = next;
     if (i + step < a.n) next.load(a, i + step, lane);
