@@ -60,7 +60,13 @@ constexpr uint32_t kOffMisc = kOffP + 2 * kKBlk;
 
 constexpr uint32_t kColO = 0;         // TMEM columns: O, then two score buffers
 constexpr uint32_t kColS = 256;
-constexpr float kGrow = 8.0f;         // log2 of the growth of a maximum that O absorbs unscaled
+// P is 2^((s - m) c2 + kLift) for a reference m that follows the row's maximum
+// score once that is 2^kGrow past it: at most 2^15, inside fp16's range, with
+// all 11 bits down to 2^-21 of the largest and steps of 2^-31 of it below that.
+// m stays in the scores' own units, where differences are exact, and the
+// rounding of m c2 is put back, so scores of any size keep their weights.
+constexpr float kGrow = 8.0f;
+constexpr float kLift = 7.0f;
 
 struct Misc {
   uint64_t q_ready, q_free, k_full[2], vp_full[2], qk_half, qk_done[2], pv_half, pv_done;
@@ -95,7 +101,7 @@ struct MlaArgs {
   float* lse;
   int2* span;              // [entries][row_tiles]: first pair * 2 + slot, last pair
   float* part_o;           // [pairs][2][128][512]
-  float2* part_ml;         // [pairs][2][128]
+  float4* part_ml;         // [pairs][2][128]: reference, sum, c2 of the row
   int* status;
 };
 
@@ -242,6 +248,11 @@ __device__ __forceinline__ bool named_any(int id, int threads, bool x) {
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Natural logarithm of a row's softmax sum from its reference and scaled sum.
+__device__ __forceinline__ float row_lse(float m, float c2, float l) {
+  return l > 0.0f || l != l ? (fmaf(m, c2, -kLift) + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 // The tiles of one pair, in order: entry v, row tile rt, token tile.
@@ -636,29 +647,30 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], s[28 + e]);
-    float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
+    float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
     // The row's maximum is only looked up when one of its parts outgrew the
-    // one in use by more than 2^kGrow (or there is none yet).
+    // one in use (or there is none yet: a difference of infinity).
     float f = 1.0f;
-    if (named_any(bar_id, kSoftWarps * 16, mt > m + kGrow || (m == -INFINITY && mt > m))) {
+    if (named_any(bar_id, kSoftWarps * 16, (mt - m) * c2 > kGrow)) {
       mi->xch[part][r] = mt;
       named_sync(bar_id, kSoftWarps * 16);
       mt = fmaxf(fmaxf(mi->xch[0][r], mi->xch[1][r]), fmaxf(mi->xch[2][r], mi->xch[3][r]));
       named_sync(bar_id, kSoftWarps * 16);
       if (m == -INFINITY) {
         m = mt;   // nothing summed yet: O's row is zero
-      } else if (mt > m + kGrow) {
-        f = ex2_approx(m - mt);
+      } else if ((mt - m) * c2 > kGrow) {
+        f = ex2_approx((m - mt) * c2);
         m = mt;
       }
     }
-    const float base = m == -INFINITY ? 0.0f : m;
-    const F2 c2v = both(c2), bv = both(-base);
+    const float hi = m == -INFINITY ? 0.0f : m * c2;
+    const float lo = m == -INFINITY ? 0.0f : fmaf(m, c2, -hi);
+    const F2 c2v = both(c2), hv = both(-hi), lv = both(kLift - lo);
     F2 sum2[2] = {both(0.0f), both(0.0f)};
     uint32_t p[16];
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
-      F2 z = fma2(F2{s[2 * c], s[2 * c + 1]}, c2v, bv);
+      F2 z = add2(fma2(F2{s[2 * c], s[2 * c + 1]}, c2v, hv), lv);
       z.x = ex2_approx(z.x);
       z.y = ex2_approx(z.y);
       sum2[c & 1] = add2(sum2[c & 1], z);
@@ -735,10 +747,9 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       if (part == 0) {
         if (whole) {
           if (mine && a.lse)
-            a.lse[orow] = lt > 0.0f || lt != lt ? (m + log2f(lt)) * 0.69314718055994531f
-                                                : -INFINITY;
+            a.lse[orow] = row_lse(m, c2, lt);
         } else {
-          if (mine) a.part_ml[static_cast<size_t>(slot) * kPairRows + prow] = make_float2(m, lt);
+          if (mine) a.part_ml[static_cast<size_t>(slot) * kPairRows + prow] = make_float4(m, lt, c2, 0.0f);
         }
       }
       if (tid == 0 && rank == 0) {
@@ -896,6 +907,7 @@ __global__ void __launch_bounds__(kJoinThreads* kJoinGroups) cache_mla_join_kern
   if (p0 == sp.y) return;
   const int pr = row % kPairRows;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float c2 = a.part_ml[static_cast<size_t>(sp.x) * kPairRows + pr].z;   // of every part
   float mx = -INFINITY, l = 0.0f;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int pb = p0 + g; pb <= sp.y; pb += FLY * GROUPS) {
@@ -907,7 +919,7 @@ __global__ void __launch_bounds__(kJoinThreads* kJoinGroups) cache_mla_join_kern
       const size_t i = static_cast<size_t>(p == p0 ? sp.x : 2 * p) * kPairRows + pr;
       const float4* po = reinterpret_cast<const float4*>(a.part_o + i * kLatent) + t;
       const bool in = p <= sp.y;
-      ml[q] = in ? a.part_ml[i] : make_float2(-INFINITY, 0.0f);
+      ml[q] = in ? *reinterpret_cast<const float2*>(a.part_ml + i) : make_float2(-INFINITY, 0.0f);
       o[q][0] = in ? po[0] : zero;
       o[q][1] = in ? po[kJoinThreads] : zero;
     }
@@ -915,14 +927,14 @@ __global__ void __launch_bounds__(kJoinThreads* kJoinGroups) cache_mla_join_kern
 #pragma unroll
     for (int q = 0; q < FLY; ++q) m2 = fmaxf(m2, ml[q].x);
     const float base = m2 == -INFINITY ? 0.0f : m2;
-    const float f = exp2f(mx - base);
+    const float f = exp2f((mx - base) * c2);
     l *= f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] *= f;
 #pragma unroll
     for (int q = 0; q < FLY; ++q) {
       // a part without a token has l = 0 and O = 0; its weight is 0 beside others
-      const float w = exp2f(ml[q].x - base);
+      const float w = exp2f((ml[q].x - base) * c2);
       l = fmaf(w, ml[q].y, l);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -949,14 +961,14 @@ __global__ void __launch_bounds__(kJoinThreads* kJoinGroups) cache_mla_join_kern
     for (int q = 0; q < GROUPS - 1; ++q)
       m2 = fmaxf(m2, shared[q * kJoinThreads * 10 + t]);
     const float base = m2 == -INFINITY ? 0.0f : m2;
-    const float f = exp2f(mx - base);
+    const float f = exp2f((mx - base) * c2);
     l *= f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] *= f;
 #pragma unroll
     for (int q = 0; q < GROUPS - 1; ++q) {
       const float* from = shared + q * kJoinThreads * 10 + t;
-      const float w = exp2f(from[0] - base);
+      const float w = exp2f((from[0] - base) * c2);
       l = fmaf(w, from[kJoinThreads], l);
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, from[(2 + e) * kJoinThreads], acc[e]);
@@ -971,7 +983,7 @@ __global__ void __launch_bounds__(kJoinThreads* kJoinGroups) cache_mla_join_kern
         make_uint2(bf16x2_bits(acc[4 * e] * inv, acc[4 * e + 1] * inv),
                    bf16x2_bits(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
   if (t == 0 && a.lse)
-    a.lse[x] = some ? (mx + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    a.lse[x] = row_lse(mx, c2, l);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -1003,7 +1015,7 @@ MlaLayout mla_layout(int batch, int ways) {
   L.span = o;
   o += (static_cast<size_t>(batch) * ways * sizeof(int2) + 255) & ~static_cast<size_t>(255);
   L.part_ml = o;
-  o += static_cast<size_t>(kMaxPairs) * 2 * kPairRows * sizeof(float2);
+  o += static_cast<size_t>(kMaxPairs) * 2 * kPairRows * sizeof(float4);
   L.part_o = o;
   o += static_cast<size_t>(kMaxPairs) * 2 * kPairRows * kLatent * sizeof(float);
   L.total = o;
@@ -1071,7 +1083,7 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
   char* ws = static_cast<char*>(workspace);
   a.span = reinterpret_cast<int2*>(ws + L.span);
   a.part_o = reinterpret_cast<float*>(ws + L.part_o);
-  a.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
+  a.part_ml = reinterpret_cast<float4*>(ws + L.part_ml);
   a.status = status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // no more pairs than tiles there can be

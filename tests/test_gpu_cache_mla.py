@@ -3,10 +3,12 @@
 The tolerance follows from the kernel's roundings.  A score is an fp32 sum of
 576 exact products: off by at most 576 * 2^-24 of the sum of their magnitudes
 (dz, after the scale, in nats), so a weight is off by dz relative, the weights'
-sum too, and the fp16 numerator by 2^-11 more (values under 2^-14 of the row's
-largest by 2^-25 of it).  With A = sum p |v| / sum p an output is off by at most
-(2 dz + 2^-11 + 2^-18) A, and its bf16 rounding by 2^-8 of itself.  The 2^-18
-covers the exponential's own error and fp32 sums.
+sum too, and the fp16 numerator by 2^-11 more.  The numerators are scaled so that
+the largest is 2^7 or more, and fp16's steps below 2^-14 are 2^-24: small ones are
+off by up to 2^-25 / 2^7 of the largest, which is at most the sum.  With
+A = sum p |v| / sum p an output is off by at most
+(2 dz + 2^-11 + 2^-18) A + 2^-32 sum |v|, and its bf16 rounding by 2^-8 of itself.
+The 2^-18 covers the exponential's own error and fp32 sums.
 """
 import numpy as np
 import pytest
@@ -75,7 +77,8 @@ class Case:
                 k = self.rows_of(b, t)
                 want, wl, size = R.attention(q[b, m], k, self.scale, np.ones((self.heads, t.size), bool))
                 dz = (576 * 2.0 ** -24) * (np.abs(q[b, m]) @ np.abs(k).T).max(axis=1) * self.scale
-                tol = (2 * dz[:, None] + 2.0 ** -11 + 2.0 ** -18) * size + 2.0 ** -8 * np.abs(want)
+                tol = (2 * dz[:, None] + 2.0 ** -11 + 2.0 ** -18) * size + 2.0 ** -8 * np.abs(want) \
+                    + 2.0 ** -32 * np.abs(k[:, :512]).sum(axis=0)
                 err = np.abs(got - want)
                 assert (err <= tol).all(), (b, m, float((err / tol).max()))
                 assert (np.abs(gl - wl) <= dz + 2.0 ** -20 * (1 + np.abs(wl))).all(), (b, m)
@@ -217,6 +220,61 @@ def test_captured_calls_follow_the_lengths():
         torch.cuda.synchronize()
         c.check(out, lse)
     assert c.cache.poll() == ess.ESS_OK
+
+
+def test_many_short_requests():
+    """More requests than threads that scan their lengths, runs of empty ones
+    among them, and more than fit the pairs evenly."""
+    lens = [(7 * i * i) % 150 if i % 5 else 0 for i in range(1700)]
+    lens[100:200] = [0] * 100
+    c = Case(18, lens, 1, 8, page=16)
+    out, lse = c.attend()
+    assert c.cache.poll() == ess.ESS_OK
+    c.check(out, lse)
+    lens = [0] * 40 + [1000] + [0] * 900
+    c = Case(19, lens, 2, 100)
+    out, lse = c.attend()
+    c.check(out, lse)
+
+
+def test_no_request_has_a_token():
+    c = Case(20, [1, 1, 1], 1, 128)
+    c.lens = [0, 0, 0]
+    c.T.zero_()
+    out, lse = c.attend()
+    c.check(out, lse)
+    assert c.cache.poll() == ess.ESS_OK
+
+
+def test_rows_past_32_bits_of_offset():
+    from host_latent_cache_gb300.rows import RowCache
+    n_rows = (5 << 30) // 400 // 64 * 64            # a cache of 5 GiB
+    rows = torch.zeros(n_rows, 400, dtype=torch.uint8, device="cuda")
+    c = Case(21, [300, 70], 1, 128)
+    last = n_rows // 64 - 1
+    table = torch.tensor([[last, 3, last - 7, last // 2, 0], [last - 1, 5, 6, 7, 8]],
+                         dtype=torch.int32, device="cuda")
+    for b in range(2):
+        for p in range(5):
+            at, frm = int(table[b, p]) * 64, int(c.table[b, p]) * 64
+            rows[at:at + 64] = c.cache.rows[frm:frm + 64]
+    cache = RowCache(rows, "q4")
+    out, lse = cache.attend(c.q, table, c.T, c.scale)
+    assert cache.poll() == ess.ESS_OK
+    c.check(out, lse)
+
+
+def test_queries_of_any_scale():
+    """Each query row is brought to fp16's range by its own power of two."""
+    c = Case(22, [400], 1, 64)
+    q = c.q.float()
+    for h in range(64):
+        q[0, 0, h] *= 2.0 ** (h - 30)               # 2^-30 .. 2^33
+    q[0, 0, 40:, 512:] *= 2.0 ** -20                # and a RoPE part far below the rest
+    q[0, 0, 3] = 0
+    c.q = q.to(torch.bfloat16)
+    out, lse = c.attend()
+    c.check(out, lse)
 
 
 def test_two_streams_beside_one_another():
