@@ -5,23 +5,37 @@
 // maximum and sum.
 //
 // With 128 heads a cached token costs 278 kflop and 400 bytes, so the tensor
-// cores bound it.  A pair of CTAs (cta_group::2) shares one tile of 128 tokens
-// and 128 query rows, 64 rows a CTA: the pair form with M = 128 keeps each
-// CTA's O[64][512] in 256 TMEM columns (lanes 64..127 hold the second half of
-// the columns), which leaves room for two score buffers, where one CTA with
-// 128 rows would fill TMEM with O alone.  Both products run at the full rate
-// of N = 256 (PV) and 70 % of it at N = 128 (QK), as measured.
+// cores are the floor (0.149 ns a token at 1868 TFLOP/s against 0.059 ns at
+// 6.78 TB/s).  A pair of CTAs (cta_group::2) shares one tile of 128 tokens and
+// 128 query rows, 64 rows a CTA: the pair form with M = 128 runs at the full
+// rate (32 cycles for N = 128, 64 for N = 256, as measured) and keeps each
+// CTA's O[64][512] in 256 TMEM columns, lanes 64..127 holding the second half
+// of the columns.  That leaves room for two score buffers, where one CTA with
+// 128 rows would fill TMEM with O alone.
 //
-//   S[128 rows][128 tokens] = Q K^T   bf16: each CTA widens its 64 tokens of K
-//   O[128 rows][512]       += P V     fp16: each CTA widens its 256 dims of V
+//   S[128 rows][128 tokens] = Q K^T   each CTA widens its 64 tokens of K
+//   O[128 rows][512]       += P V     each CTA widens its 256 dims of V
 //
-// The rows' 4-bit codes are widened exactly: to bf16 beside the bf16 queries,
-// to fp16 beside P, which so keeps 11 bits.  Eight warps gather and widen
-// (raw rows of the next phase are in registers before this phase's buffer is
-// free), four run the softmax (thread = row and half of the tile's tokens),
-// one thread of the even CTA issues the MMAs: QK of tile i + 1, then PV of
-// tile i, so the softmax of a tile and the widening of the next run beside
+// The rows' 4-bit codes are widened to fp16, exactly, by one conversion and one
+// multiplication a pair.  Queries become fp16 under a power of two of their
+// row, P keeps 11 bits, and the 64 RoPE dims stay bf16 in MMAs of their own.
+// Sixteen warps gather and widen, eight run the softmax, one resolves the
+// tokens' rows, one of the even CTA issues the MMAs: QK of tile i + 1, then PV
+// of tile i, so the softmax of a tile and the widening of the next run beside
 // them.  O is rescaled only when a row's maximum grows by more than 2^8.
+//
+// What bounds it: the shared-memory and L1 data path.  A tile writes 147 KB of
+// widened operands and P, reads 35 KB of raw rows through L1 (rows of 400 bytes
+// straddle its lines: 51 KB) and the MMAs read 245 KB of operands, beside 2200
+// cycles of tensor work.  All tokens of eight 128K contexts with 128 heads: 199
+// us, 1.01 PFLOP/s or 54 % of the measured tensor rate, 4200 cycles a tile.
+// Measured on the way there (same case): one thread issuing in divergent code
+// 526 us (110 cycles an MMA); V before K of the next tile 447; four softmax
+// warps, rows resolved by the widening warps 346; lanes across rows (32 lines a
+// load) 300; cluster-scope arrivals, which wait for loads in flight, 235; whole
+// tiles handed over instead of halves, eight widening warps 211; L2 prefetches
+// by the row warp +7 %; loads that skip L1 +14 %; warps of their own for K and
+// for V +1 %, and for even and odd tiles +17 %.
 //
 // All tiles of all requests are dealt evenly to the pairs (lengths are read on
 // the device, so captured calls follow them); a request cut by a boundary
@@ -48,7 +62,7 @@ constexpr int kWidenWarp0 = 9;
 constexpr int kWidenWarps = 16;
 constexpr int kRowWarp = kWidenWarp0 + kWidenWarps;
 constexpr int kMlaThreads = (kRowWarp + 1) * 32;
-constexpr int kRing = 3;              // tiles whose rows are known ahead
+constexpr int kRing = 3;              // tiles whose rows are known ahead of their use
 
 constexpr uint32_t kKBlk = 8192;      // [64 rows][64 dims], 128-byte swizzled
 constexpr uint32_t kVBlk = 16384;     // [128 tokens][64 dims]
@@ -476,9 +490,10 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
   }
 }
 
-// One warp of the even CTA issues the MMAs.  The whole warp walks the tiles and one elected lane issues: with uniform
-// control flow the descriptors stay in uniform registers, and an MMA is issued
-// every 32 cycles (N = 128) instead of every 110.
+// One warp of the even CTA issues the MMAs.  The whole warp walks the tiles and
+// one elected lane issues: with uniform control flow the descriptors stay in
+// uniform registers, and an MMA is issued every 32 cycles (N = 128).  The two
+// MMAs of PV that share a slice of P read it from shared memory once.
 __device__ __forceinline__ void mma_role(const MlaArgs& a, uint8_t* smem, Misc* mi,
                                          uint32_t tmem) {
   const uint64_t dq = make_sdesc_sw128(smem_u32(smem + kOffQ), 16, 1024);

@@ -1,11 +1,18 @@
 // Device row cache: writing raw token rows into a paged cache (norm, rotation,
 // encoding), reading cache rows back as bf16, and the 8-bit norm that makes
-// indexer keys.  All three stream rows once: they are bound by HBM.
+// indexer keys.  All three stream rows once, so HBM is their floor; the writes
+// and short norms are bound by their arithmetic.
 //
 // One warp per cache row.  Lane l holds the 16-byte units l and 32 + l of the
 // 512 latents (dims 8l .. 8l + 7 and 256 + 8l ..), so every load and store
 // instruction of a warp covers consecutive bytes whatever the format: 16, 8 or
 // 4 bytes a lane for bf16, e4m3 and e2m1.
+//
+// Measured (bytes that the call cannot do without / time): 131072 q4 rows read
+// 34.2 us (5.97 TB/s, 88 % of the measured copy rate); 65536 q4 rows written
+// 26.7 us (3.84 TB/s), without norm and rotation 21.4, as bf16 rows 29.3 (a
+// plain copy of the same bytes takes 23.9); the norm of 16384 x 4096 with a
+// residual 88 us (5.34 TB/s), of 131072 keys 11.6 us (4.4 TB/s).
 #include <algorithm>
 #include <cmath>
 
@@ -61,9 +68,10 @@ struct RawRow {
 };
 
 // Warps walk over the rows, the next row's loads in flight while one is
-// worked on, with gamma in registers.  The arithmetic (about 250 instructions
-// a row and warp, a third of them for the exact sum) weighs as much as the
-// bytes do.
+// worked on, with gamma in registers.  About 300 instructions a row and warp
+// bound it (two thirds of the issue slots).  65536 q4 rows written and read
+// back take 41.8 us this way, 42.4 with two rows a warp of sixteen lanes each
+// (fewer instructions, but 122 registers), 46.2 with two rows in flight a warp.
 template <int FMT>
 __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
     const WriteArgs a, const __grid_constant__ RopeFreq fr) {
