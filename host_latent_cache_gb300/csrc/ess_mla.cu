@@ -28,7 +28,7 @@
 // widened operands and P, reads 35 KB of raw rows through L1 (rows of 400 bytes
 // straddle its lines: 51 KB) and the MMAs read 245 KB of operands, beside 2200
 // cycles of tensor work.  All tokens of eight 128K contexts with 128 heads: 199
-// us, 1.01 PFLOP/s or 54 % of the measured tensor rate, 4200 cycles a tile.
+// us, 1.16 PFLOP/s or 62 % of the measured tensor rate, 4200 cycles a tile.
 // Measured on the way there (same case): one thread issuing in divergent code
 // 526 us (110 cycles an MMA); V before K of the next tile 447; four softmax
 // warps, rows resolved by the widening warps 346; lanes across rows (32 lines a
