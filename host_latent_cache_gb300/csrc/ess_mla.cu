@@ -637,6 +637,7 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       if (!a.tokens && limit) limit = it.len - (a.ways - 1) + row / a.heads;
       named_sync(3, kSoftWarps * 32);   // the rows' scales
       c2 = a.c2 * exp2f(mi->qexp[r]);
+      named_sync(3, kSoftWarps * 32);   // read, before the next segment's take their place
       m = -INFINITY;
       l = 0.0f;
       seg_first_tile = it.tile;

@@ -277,6 +277,18 @@ def test_queries_of_any_scale():
     c.check(out, lse)
 
 
+def test_short_requests_with_queries_of_many_scales():
+    """Requests of one tile each, several to a pair: each one's row scales
+    follow those of the one before at once."""
+    lens = [1 + (11 * i) % 128 for i in range(400)]
+    c = Case(23, lens, 1, 64, page=16)
+    q = c.q.float() * 2.0 ** ((torch.arange(400 * 64, device="cuda") * 13) % 41 - 30).view(400, 1, 64, 1)
+    c.q = q.to(torch.bfloat16)
+    out, lse = c.attend()
+    assert c.cache.poll() == ess.ESS_OK
+    c.check(out, lse)
+
+
 def test_two_streams_beside_one_another():
     a, b = Case(14, [6000] * 3, 1, 128), Case(15, [4000] * 4, 2, 64)
     want = a.attend(), b.attend()
