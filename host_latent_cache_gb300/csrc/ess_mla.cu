@@ -43,6 +43,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <cstddef>
 
 #include "ess_rows.cuh"
 
@@ -95,6 +96,9 @@ struct Misc {
 };
 constexpr uint32_t kMlaSmem = 232448;
 static_assert(kOffMisc + sizeof(Misc) <= kMlaSmem, "shared memory of one CTA");
+static_assert(offsetof(Misc, xch) % 8 == 0 && kMlaThreads / 32 * 8 <= sizeof(Misc::xch) &&
+                  kRing * kMt <= kMlaThreads,
+              "the scan's scratch, and the rows' first values");
 
 struct MlaArgs {
   const uint16_t* q;
@@ -488,6 +492,9 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
       ++turn2;
     }
   }
+  // the last arrivals on these two, which nothing else waits for
+  wait_or_abort(&mi->qk_half, (n - 1) & 1, mi, a.status);
+  wait_or_abort(&mi->pv_half, (n - 1) & 1, mi, a.status);
 }
 
 // One warp of the even CTA issues the MMAs.  The whole warp walks the tiles and
@@ -808,6 +815,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     mi->abort = 0;
     fence_mbar_init();
   }
+  // a role that gives up a wait goes on with the rows it finds: always some that exist
+  if (tid < kRing * kMt) mi->row[tid / kMt][tid % kMt] = 0;
   if (warp == kMmaWarp) {
     tmem_alloc_pair(smem_u32(&mi->tmem), 512);
     tmem_relinquish_pair();
@@ -828,7 +837,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     const long long x = __shfl_up_sync(0xffffffffu, before, o);
     if (lane >= o) before += x;
   }
-  long long* scan = reinterpret_cast<long long*>(mi->row);   // free until the roles start
+  long long* scan = reinterpret_cast<long long*>(mi->xch);   // free until the roles start
   if (lane == 31) scan[warp] = before;
   __syncthreads();
   long long sums = lane < kMlaThreads / 32 ? scan[lane] : 0;   // of the warps
