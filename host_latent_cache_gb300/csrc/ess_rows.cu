@@ -425,7 +425,8 @@ ess_status ess_norm_quant(const void* x, int64_t x_stride, const void* residual,
                           int32_t dim, void* residual_out, void* codes, float* scales,
                           ess_stream_t stream) {
   if (n < 0 || n > kMaxRows || dim < 1 || !(eps >= 0.0f) || x_stride < dim ||
-      (residual && residual_stride < dim) || (residual_out && !residual))
+      (residual && residual_stride < dim) || (residual_out && !residual) ||
+      (residual_out && residual_out == x && x_stride != residual_stride))
     return ESS_ERR_INVALID_ARG;
   if (dim % 8 != 0 || dim > 16384) return ESS_ERR_UNSUPPORTED;
   if (x_stride % 8 != 0 || (residual && residual_stride % 8 != 0)) return ESS_ERR_INVALID_ARG;

@@ -622,7 +622,8 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
  *   residual      device bf16, n rows, residual_stride apart, or NULL
  *   gamma         device bf16 [dim]
  *   residual_out  device bf16, residual_stride apart: bf16(x + residual); it
- *                 may be x or residual itself.  NULL: not stored
+ *                 may be residual itself, or x when both have one stride.
+ *                 NULL: not stored
  *   codes         device [n][dim] e4m3
  *   scales        device float [n][ceil(dim / 128)]
  * h = x + residual in fp32; y = h * r * gamma with r = 1 / sqrt(mean(h^2) +

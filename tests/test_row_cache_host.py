@@ -171,6 +171,14 @@ NORM = dict(x=A16, xs=128, res=A16, rs=128, gamma=A16, eps=1e-6, n=4, dim=128, o
             scales=A16)
 
 
+def test_norm_output_over_x_needs_one_stride(lib):
+    """Over x the sums may go only where x's own rows lie."""
+    a = {**NORM, "xs": 256, "out": A16, "res": P(1 << 24)}
+    got = lib.ess_norm_quant(a["x"], a["xs"], a["res"], a["rs"], a["gamma"], a["eps"], a["n"],
+                             a["dim"], a["out"], a["codes"], a["scales"], None)
+    assert got == ess.ESS_ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("change,code", [
     (dict(x=None), 1), (dict(x=BAD), 1), (dict(xs=120), 1), (dict(xs=129), 1), (dict(rs=120), 1),
     (dict(rs=130), 1), (dict(res=BAD), 1), (dict(gamma=None), 1), (dict(gamma=BAD), 1),
