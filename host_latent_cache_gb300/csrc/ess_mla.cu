@@ -1011,8 +1011,6 @@ __global__ void __launch_bounds__(kJoinThreads* kJoinGroups) cache_mla_join_kern
     a.lse[x] = row_lse(mx, c2, l);
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 ess_status check_shape(int batch, int ways, int heads) {
   if (batch < 1 || ways < 1 || heads < 1) return ESS_ERR_INVALID_ARG;
   if (ways > kMaxCacheWays || heads > kMaxCacheHeads || batch > 65535) return ESS_ERR_UNSUPPORTED;
@@ -1076,7 +1074,9 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
       static_cast<long long>(max_pages) * page > 0x7fffff00LL || k > 0x7fffff00)
     return ESS_ERR_UNSUPPORTED;
   if (!q || !rows || !page_table || !T || !out || !workspace || !aligned16(q) ||
-      !aligned16(rows) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+      !aligned16(rows) || !aligned16(out) || !aligned_to(workspace, 256) ||
+      !aligned_to(page_table, 4) || !aligned_to(T, 4) || !aligned_to(tokens, 4) ||
+      !aligned_to(lse, 4) || !aligned_to(status, 4))
     return ESS_ERR_INVALID_ARG;
   const MlaLayout L = mla_layout(batch, ways);
   if (ws_bytes < L.total) return ESS_ERR_OOM;

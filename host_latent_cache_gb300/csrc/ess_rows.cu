@@ -319,8 +319,6 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const
   }
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 template <int TPR, int UNITS>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
   constexpr int kThreads = TPR > 256 ? TPR : 256;
@@ -368,7 +366,8 @@ ess_status ess_cache_write(const void* kv, int64_t kv_stride, int64_t n, const v
   }
   if (n == 0) return ESS_OK;
   if (!kv || !slots || !rows || (inv_freq && !pos) || !aligned16(kv) || !aligned16(rows) ||
-      (gamma && !aligned16(gamma)))
+      (gamma && !aligned16(gamma)) || !aligned_to(slots, 8) || !aligned_to(status, 4) ||
+      (inv_freq && !aligned_to(pos, 4)))
     return ESS_ERR_INVALID_ARG;
   WriteArgs a;
   a.kv = static_cast<const uint16_t*>(kv);
@@ -401,7 +400,9 @@ ess_status ess_cache_read(const void* rows, int64_t n_rows, int32_t format, cons
   if (format < ESS_ROW_BF16 || format > ESS_ROW_Q4 || n < 0 || n > kMaxRows || n_rows < 0)
     return ESS_ERR_INVALID_ARG;
   if (n == 0) return ESS_OK;
-  if (!rows || !slots || !out || !aligned16(rows) || !aligned16(out)) return ESS_ERR_INVALID_ARG;
+  if (!rows || !slots || !out || !aligned16(rows) || !aligned16(out) || !aligned_to(slots, 8) ||
+      !aligned_to(status, 4))
+    return ESS_ERR_INVALID_ARG;
   const dim3 grid(static_cast<unsigned>((n + kRowWarps - 1) / kRowWarps));
   const dim3 block(kRowWarps * 32);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -432,7 +433,7 @@ ess_status ess_norm_quant(const void* x, int64_t x_stride, const void* residual,
   if (x_stride % 8 != 0 || (residual && residual_stride % 8 != 0)) return ESS_ERR_INVALID_ARG;
   if (n == 0) return ESS_OK;
   if (!x || !gamma || !codes || !scales || !aligned16(x) || !aligned16(gamma) ||
-      !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u) ||
+      !aligned16(codes) || !aligned_to(scales, 4) ||
       (residual && !aligned16(residual)) || (residual_out && !aligned16(residual_out)))
     return ESS_ERR_INVALID_ARG;
   NormArgs a;

@@ -12,6 +12,11 @@ constexpr int kQ4MinExp = -23;
 constexpr int kQ4MaxExp = 13;
 constexpr int kQ4RowBytes = 400;
 
+inline bool aligned_to(const void* p, uintptr_t n) {
+  return reinterpret_cast<uintptr_t>(p) % n == 0;
+}
+inline bool aligned16(const void* p) { return aligned_to(p, 16); }
+
 __host__ __device__ constexpr int row_bytes_of(int format) {
   return format == ESS_ROW_BF16 ? kRowBytes : format == ESS_ROW_COMPACT ? 656 : kQ4RowBytes;
 }

@@ -529,7 +529,8 @@ ess_status ess_prefill_run(int32_t n_layers, const int32_t* onload_layer_map, in
  *                   of the two.
  *
  * status is a device int32, or NULL: the first device-side error of the calls
- * that share it is put there when it holds ESS_OK; the caller clears it. */
+ * that share it is put there when it holds ESS_OK; the caller clears it.
+ * Pointers whose alignment is not given have that of their type. */
 enum { ESS_ROW_BF16 = 0, ESS_ROW_COMPACT = 1, ESS_ROW_Q4 = 2 };
 
 /* Bytes of one row of a format (a multiple of 16).

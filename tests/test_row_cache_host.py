@@ -167,6 +167,31 @@ def test_attention_workspace_sizes(lib):
     assert lib.ess_cache_mla_bytes(1, 1, 129, ctypes.byref(n)) == ess.ESS_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("name", ["table", "T", "tokens", "lse", "status"])
+def test_attention_refuses_odd_addresses(lib, name):
+    odd = P((1 << 20) + 2)
+    a = {**MLA, "k": 4, "lse": None, "status": None, name: odd}
+    got = lib.ess_cache_mla(a["q"], a["rows"], a["n_rows"], a["fmt"], a["table"], a["max_pages"],
+                            a["page"], a["T"], a["batch"], a["ways"], a["heads"], a["tokens"],
+                            a["k"], a["scale"], a["out"], a["lse"], a["ws"], a["ws_bytes"],
+                            a["status"], None)
+    assert got == ess.ESS_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name,at", [("slots", 4), ("pos", 2), ("status", 2)])
+def test_row_calls_refuse_odd_addresses(lib, name, at):
+    a = {**WRITE, "status": None, name: P((1 << 20) + at)}
+    got = lib.ess_cache_write(a["kv"], a["stride"], a["n"], a["gamma"], a["eps"], a["freq"],
+                              a["pos"], a["pairs"], a["slots"], a["rows"], a["n_rows"], a["fmt"],
+                              a["status"], None)
+    assert got == ess.ESS_ERR_INVALID_ARG
+    if name != "pos":
+        a = {**READ, "status": None, name: P((1 << 20) + at)}
+        got = lib.ess_cache_read(a["rows"], a["n_rows"], a["fmt"], a["slots"], a["n"], a["out"],
+                                 a["status"], None)
+        assert got == ess.ESS_ERR_INVALID_ARG
+
+
 NORM = dict(x=A16, xs=128, res=A16, rs=128, gamma=A16, eps=1e-6, n=4, dim=128, out=A16, codes=A16,
             scales=A16)
 
