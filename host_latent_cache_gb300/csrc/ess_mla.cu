@@ -643,7 +643,9 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       limit = row >= a.entry_rows ? 0 : it.len;
       if (!a.tokens && limit) limit = it.len - (a.ways - 1) + row / a.heads;
       named_sync(3, kSoftWarps * 32);   // the rows' scales
-      c2 = a.c2 * exp2f(mi->qexp[r]);
+      // at least 2^-126: |s| < 2^41 then still weighs less than half a step of
+      // 1 apart, and 0 * infinity does not arise
+      c2 = fmaxf(a.c2 * exp2f(mi->qexp[r]), 0x1p-126f);
       named_sync(3, kSoftWarps * 32);   // read, before the next segment's take their place
       m = -INFINITY;
       l = 0.0f;

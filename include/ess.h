@@ -604,14 +604,18 @@ ess_status ess_cache_mla_bytes(int32_t batch, int32_t ways, int32_t heads, size_
  *   workspace  device, 256-byte aligned, at least ess_cache_mla_bytes; calls
  *              that share one are ordered by the caller
  * A query that attends to nothing gets zeros and lse = -infinity.  Scores,
- * softmax and sums are fp32; the softmax numerators go into the second product
- * as fp16 (11 bits), beside the latents, which fp16 holds exactly.
+ * softmax and sums are fp32.  A query row's latent part goes into the first
+ * product as fp16 after division by a power of two that brings the row's largest
+ * value to [2^14, 2^15): exact for values down to 2^-31 of that one, off by less
+ * than 2^-39 of it below.  The softmax numerators go into the second product as
+ * fp16 (11 bits), beside the latents, which fp16 holds exactly.
  * A length outside its range, a token at or past T_b and a page outside the
  * cache report ESS_ERR_DEVICE_CHECK in status; such a token is left out.
  * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or non-positive
- * argument; ESS_ERR_UNSUPPORTED for more than 4 ways or 128 heads, another
- * format, or more than 2^31 - 1 rows or tokens of a request; ESS_ERR_OOM for
- * a workspace that is too small. */
+ * argument or a scale that is not finite; ESS_ERR_UNSUPPORTED for more than 4
+ * ways, 128 heads or 65535 requests, another format, more than 2^31 - 1 rows, or
+ * max_pages * page or k above 2^31 - 256; ESS_ERR_OOM for a workspace that is too
+ * small. */
 ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_t format,
                          const int32_t* page_table, int32_t max_pages, int32_t page,
                          const int32_t* T, int32_t batch, int32_t ways, int32_t heads,

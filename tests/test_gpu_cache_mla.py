@@ -277,6 +277,16 @@ def test_queries_of_any_scale():
     c.check(out, lse)
 
 
+def test_scales_far_below_one():
+    """A scale whose product with a row's power of two is below fp32's range:
+    every token weighs the same."""
+    c = Case(24, [300, 3], 2, 16)
+    c.q = (c.q.float() * 2.0 ** -115).to(torch.bfloat16)
+    c.scale = 2.0 ** -60
+    out, lse = c.attend()
+    c.check(out, lse)
+
+
 def test_short_requests_with_queries_of_many_scales():
     """Requests of one tile each, several to a pair: each one's row scales
     follow those of the one before at once."""
