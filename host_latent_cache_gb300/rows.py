@@ -119,11 +119,13 @@ class RowCache:
         return code
 
     def _freqs(self, inv_freq: Sequence[float]):
-        key = tuple(inv_freq)
-        if self._freq[0] != key:
+        key = tuple(map(float, inv_freq))   # numbers: a tensor's entries may change later
+        old, freq = self._freq
+        if old != key:
             _need(len(key) == ROPE // 2, f"inv_freq has {len(key)} entries, not {ROPE // 2}")
-            self._freq = (key, (ctypes.c_double * len(key))(*key))
-        return self._freq[1]
+            freq = (ctypes.c_double * len(key))(*key)
+            self._freq = (key, freq)
+        return freq
 
     def write(self, kv, slots, gamma=None, eps: float = 1e-6, pos=None, inv_freq=None,
               pairs: str = "adjacent") -> None:

@@ -127,6 +127,21 @@ def test_write(fmt, n, stride, norm, rope):
     assert (got[rest] == 0xA5).all(), "a row that no token names was changed"
 
 
+def test_frequencies_that_change_in_place():
+    rows = rows_mod()
+    g = torch.Generator(device="cuda").manual_seed(31)
+    kv, slots = make_rows(4, g), torch.arange(4, device="cuda")
+    pos = torch.arange(1, 5, dtype=torch.int32, device="cuda")
+    freq = torch.tensor(FREQ, dtype=torch.float64)
+    cache = rows.RowCache(torch.zeros(4, 1152, dtype=torch.uint8, device="cuda"), "bf16")
+    cache.write(kv, slots, pos=pos, inv_freq=freq)
+    freq *= 0.5
+    cache.write(kv, slots, pos=pos, inv_freq=freq)
+    got = cache.rows.clone()
+    cache.write(kv, slots, pos=pos, inv_freq=[f * 0.5 for f in FREQ])
+    assert torch.equal(got, cache.rows)
+
+
 def test_compact_rows_are_those_of_the_host_encoder():
     rows = rows_mod()
     g = torch.Generator(device="cuda").manual_seed(5)
