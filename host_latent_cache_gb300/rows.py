@@ -203,6 +203,10 @@ class RowCache:
             lse = torch.empty((batch, ways, heads), dtype=torch.float32, device=self.device)
         else:
             _check(lse, "lse", torch.float32, (batch, ways, heads), at)
+        if workspace is not None:
+            _need(_is(workspace, torch.uint8, (workspace.numel(),), at)
+                  if isinstance(workspace, torch.Tensor) else False,
+                  f"workspace: contiguous uint8 [bytes] on cuda:{at} is needed")
         with self._on as stream:
             if workspace is None:
                 key = (stream, batch, ways, heads)

@@ -332,6 +332,18 @@ def test_arguments_are_refused():
         RowCache(torch.zeros(64, 656, dtype=torch.uint8, device="cuda"), "compact").attend(**ok)
 
 
+def test_workspaces_are_refused():
+    c = Case(25, [50], 1, 4)
+    ws = c.cache.workspace(1, 1, 4)
+    for bad in (ws.cpu(), ws.numel(), ws[: 1 << 20].view(torch.float32), ws.view(1, -1),
+                torch.empty(2 * ws.numel(), dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            c.attend(workspace=bad)
+    with pytest.raises(ess.EssError):
+        c.attend(workspace=ws[16:])                  # not 256-byte aligned
+    c.check(*c.attend(workspace=ws))
+
+
 def test_written_rows_are_attended_and_read():
     """Prompt rows and then a decode step's rows into the cache, attention over
     all of them, and the rows read back: as a server runs them."""
