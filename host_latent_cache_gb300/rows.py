@@ -13,6 +13,7 @@ ValueError; nothing is copied or converted on the way.
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import Optional, Sequence
 
 import torch
@@ -107,10 +108,11 @@ class RowCache:
         self.device = rows.device
         self._index = rows.get_device()
         _check(rows, "rows", torch.uint8, (self.n_rows, ess.ess_row_bytes(self._f)), self._index)
-        self._on = _OnDevice(self._index)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._freq = (None, None)
-        self._ws = {}
+        self._ws = {}       # by stream: the largest workspace a call on it needed
+        self._bytes = {}    # by shape
+        self._lock = threading.Lock()
 
     def poll(self) -> int:
         """The first device-side error since the last poll (synchronous), cleared."""
@@ -147,7 +149,7 @@ class RowCache:
         else:
             freq = self._freqs(inv_freq)
             _check(pos, "pos", _I32, (n,), at)
-        with self._on as stream:
+        with _OnDevice(self._index) as stream:
             ess.ess_cache_write(kv, _row_stride(kv), n, gamma, eps, freq, pos, PAIRS[pairs], slots,
                                 self.rows, self.n_rows, self._f, self.status, stream)
 
@@ -161,7 +163,7 @@ class RowCache:
             out = torch.empty((n, ROW), dtype=_BF16, device=self.device)
         else:
             _check(out, "out", _BF16, (n, ROW), at)
-        with self._on as stream:
+        with _OnDevice(self._index) as stream:
             ess.ess_cache_read(self.rows, self.n_rows, self._f, slots, n, out, self.status, stream)
         return out
 
@@ -179,7 +181,10 @@ class RowCache:
         of each request (page_table int32 [batch][max_pages], T int32
         [batch]), or over tokens int32 [batch][ways][k].  Returns (out bf16
         [batch][ways][heads][512], lse float32 [batch][ways][heads]).  Without
-        `workspace` the cache keeps one for each current stream."""
+        `workspace` the cache keeps one for each current stream, and a captured
+        call takes one from its graph's memory.  Threads may call it at once
+        without `workspace`; calls that are given one are ordered by the
+        caller."""
         at = self._index
         _need(isinstance(q, torch.Tensor) and q.dim() == 4, "q: [batch][ways][heads][576] is needed")
         batch, ways, heads, _ = q.shape
@@ -207,16 +212,34 @@ class RowCache:
             _need(_is(workspace, torch.uint8, (workspace.numel(),), at)
                   if isinstance(workspace, torch.Tensor) else False,
                   f"workspace: contiguous uint8 [bytes] on cuda:{at} is needed")
-        with self._on as stream:
+        with _OnDevice(at) as stream:
             if workspace is None:
-                key = (stream, batch, ways, heads)
-                workspace = self._ws.get(key)
-                if workspace is None:
-                    workspace = self._ws[key] = self.workspace(batch, ways, heads)
-            ess.ess_cache_mla(q, self.rows, self.n_rows, self._f, page_table, max_pages, self.page,
-                              T, batch, ways, heads, tokens, k, sm_scale, out, lse, workspace,
-                              workspace.numel(), self.status, stream)
+                if torch._C._cuda_isCurrentStreamCapturing():
+                    workspace = self.workspace(batch, ways, heads)
+                else:
+                    # one call's two launches stay together on the stream
+                    with self._lock:
+                        self._attend(q, page_table, max_pages, T, batch, ways, heads, tokens, k,
+                                     sm_scale, out, lse, self._kept(stream, batch, ways, heads), stream)
+                    return out, lse
+            self._attend(q, page_table, max_pages, T, batch, ways, heads, tokens, k, sm_scale, out,
+                         lse, workspace, stream)
         return out, lse
+
+    def _kept(self, stream: int, batch: int, ways: int, heads: int) -> torch.Tensor:
+        need = self._bytes.get((batch, ways, heads))
+        if need is None:
+            need = self._bytes[batch, ways, heads] = ess.ess_cache_mla_bytes(batch, ways, heads)
+        ws = self._ws.get(stream)
+        if ws is None or ws.numel() < need:
+            ws = self._ws[stream] = self.workspace(batch, ways, heads)
+        return ws
+
+    def _attend(self, q, page_table, max_pages, T, batch, ways, heads, tokens, k, sm_scale, out,
+                lse, workspace, stream) -> None:
+        ess.ess_cache_mla(q, self.rows, self.n_rows, self._f, page_table, max_pages, self.page, T,
+                          batch, ways, heads, tokens, k, sm_scale, out, lse, workspace,
+                          workspace.numel(), self.status, stream)
 
 
 def norm_q8(x, gamma, eps: float = 1e-6, residual=None, residual_out=None, codes=None,

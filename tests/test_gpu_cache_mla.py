@@ -332,6 +332,60 @@ def test_arguments_are_refused():
         RowCache(torch.zeros(64, 656, dtype=torch.uint8, device="cuda"), "compact").attend(**ok)
 
 
+def test_threads_at_once():
+    """Threads that share the cache and its stream, each with its own request."""
+    import threading
+    c = Case(26, [5000, 900], 1, 128)
+    qs = [c.q.roll(i, 2) for i in range(4)]
+    want = [c.cache.attend(q, c.dev_table, c.T, c.scale) for q in qs]
+    got = [[] for _ in qs]
+
+    def run(i):
+        for _ in range(30):
+            got[i].append(c.cache.attend(qs[i], c.dev_table, c.T, c.scale))
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert len(g) == 30
+        for o, l in g:
+            assert torch.equal(o, w[0]) and torch.equal(l, w[1])
+
+
+def test_two_captured_graphs_beside_one_another():
+    """Without a workspace of the caller's each graph has one of its own."""
+    a, b = Case(27, [6000] * 3, 1, 128), Case(28, [4000] * 4, 2, 64)
+    q2 = a.q.roll(1, 2)
+    want = [a.attend(), a.cache.attend(q2, a.dev_table, a.T, a.scale), b.attend()]
+    graphs, got = [], []
+    for x, q in ((a, a.q), (a, q2), (b, b.q)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(x.cache.attend(q, x.dev_table, x.T, x.scale))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = a.attend()
+    torch.cuda.synchronize()
+    for g, w in zip(got + [eager], want + [want[0]]):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+def test_one_workspace_serves_every_batch():
+    c = Case(29, [70] * 6, 1, 16)
+    for n in (1, 6, 3, 2):
+        c.lens = [70] * n
+        c.check(*c.cache.attend(c.q[:n], c.dev_table[:n], c.T[:n], c.scale))
+    assert len(c.cache._ws) == 1
+
+
 def test_workspaces_are_refused():
     c = Case(25, [50], 1, 4)
     ws = c.cache.workspace(1, 1, 4)
