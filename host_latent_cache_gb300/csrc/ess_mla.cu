@@ -84,7 +84,7 @@ constexpr float kGrow = 8.0f;
 constexpr float kLift = 7.0f;
 
 struct Misc {
-  uint64_t q_ready, q_free, k_full[2], vp_full[2], qk_half, qk_done[2], pv_half, pv_done;
+  uint64_t q_ready, q_here[2], q_free, k_full[2], vp_full[2], qk_half, qk_done[2], pv_half, pv_done;
   uint64_t row_full[kRing], row_free[kRing];
   uint32_t tmem;
   int abort;
@@ -92,7 +92,8 @@ struct Misc {
   uint32_t mask[kRing][4];            // tokens of a tile that exist
   int32_t row[kRing][kMt];            // cache rows of a tile's tokens (0 for one that is not)
   float xch[4][kCtaRows];             // a row's statistics from the four threads that share it
-  float qexp[kCtaRows];               // log2 of what a query row was divided by
+  int2 seg[kRing];                    // entry and row tile of a segment that a tile begins, or -1
+  int8_t qexp[2][kCtaRows];           // log2 of what a query row was divided by, of two segments
 };
 constexpr uint32_t kMlaSmem = 232448;
 static_assert(kOffMisc + sizeof(Misc) <= kMlaSmem, "shared memory of one CTA");
@@ -118,7 +119,7 @@ struct MlaArgs {
   uint16_t* out;
   float* lse;
   int2* span;              // [entries][row_tiles]: first pair * 2 + slot, last pair
-  float* part_o;           // [pairs][2][128][512]
+  float* part_o;           // [pairs][2][512 / 8][128][8]: a lane's 32 bytes beside its neighbours'
   float4* part_ml;         // [pairs][2][128]: reference, sum, c2 of the row
   int* status;
 };
@@ -379,6 +380,15 @@ __device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
       const uint32_t m = __ballot_sync(0xffffffffu, row[j] >= 0);
       if (lane == 0) mi->mask[slot][j] = m;
     }
+    if (it.first() && g > 0) {   // the segment's queries into L2
+      const int row0 = it.rt * kPairRows + static_cast<int>(cluster_ctarank()) * kCtaRows;
+      const char* q = reinterpret_cast<const char*>(
+          a.q + (static_cast<size_t>(it.v) * a.entry_rows + row0) * kRowDim);
+      const int bytes = min(kCtaRows, a.entry_rows - row0) * kRowDim * 2;
+      for (int x = lane * 128; x < bytes; x += 32 * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(q + x));
+    }
+    if (lane == 0) mi->seg[slot] = make_int2(it.first() ? it.v : -1, it.rt);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&mi->row_full[slot]));
     if (++slot == kRing) {
@@ -386,6 +396,71 @@ __device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
       ++turn;
     }
     it.next(a);
+  }
+}
+
+// Four rows of queries per widening warp into shared memory, kFly of them in
+// flight: the latent part as fp16, beside the fp16 latents, each row divided by
+// the power of two that brings its largest value to [2^14, 2^15) (exact down to
+// 2^-31 of that value, with an error below 2^-39 of it under that); the RoPE
+// part, divided alike, as bf16.  A lane takes unit 32 h + 4 (lane % 8) + lane / 8:
+// chunk 8 h + lane % 8, its unit lane / 8; eight lanes then fill the places of one
+// swizzled row.
+template <int kFly>
+__device__ __forceinline__ void load_queries(const MlaArgs& a, uint8_t* smem, Misc* mi, int v,
+                                             int row0, int warp, int lane, int seg) {
+  constexpr int kRows = kCtaRows / kWidenWarps;
+  uint8_t* sq = smem + kOffQ;
+  const int un = 4 * (lane & 7) + (lane >> 3);
+#pragma unroll 1
+  for (int i0 = 0; i0 < kRows; i0 += kFly) {
+    uint4 u[kFly][2];
+    uint32_t rope[kFly];
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+      const int row = row0 + warp * kRows + i0 + i;
+      u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      rope[i] = 0u;
+      if (row < a.entry_rows) {
+        const uint16_t* q = a.q + (static_cast<size_t>(v) * a.entry_rows + row) * kRowDim;
+        u[i][0] = reinterpret_cast<const uint4*>(q)[un];
+        u[i][1] = reinterpret_cast<const uint4*>(q)[32 + un];
+        rope[i] = reinterpret_cast<const uint32_t*>(q + kLatent)[lane];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+      const int r = warp * kRows + i0 + i;
+      float x[16];
+      unpack8(u[i][0], x);
+      unpack8(u[i][1], x + 8);
+      const float ra = bf16_lo(rope[i]), rb = bf16_hi(rope[i]);
+      const float mx = __uint_as_float(__reduce_max_sync(
+          0xffffffffu, __float_as_uint(fmaxf(fmaxf(amax8(x), amax8(x + 8)),
+                                             fmaxf(fabsf(ra), fabsf(rb))))));
+      // 2^e <= mx < 2^(e + 1); rows of zeros, infinities and NaN as they are
+      const int e = mx > 0.0f && mx < INFINITY
+                        ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 - 14
+                        : 0;
+      const int ec = min(max(e, -126), 126);
+      const float inv = exp2i(-ec);
+      if (lane == 0) mi->qexp[seg & 1][r] = static_cast<int8_t>(ec);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float* y = x + 8 * h;
+        *reinterpret_cast<uint4*>(sq + (4 * h + (lane >> 3)) * kKBlk + sw128_off(r, lane & 7)) =
+            make_uint4(half2_bits(y[0] * inv, y[1] * inv), half2_bits(y[2] * inv, y[3] * inv),
+                       half2_bits(y[4] * inv, y[5] * inv), half2_bits(y[6] * inv, y[7] * inv));
+      }
+      *reinterpret_cast<uint32_t*>(sq + 8 * kKBlk + sw128_off(r, lane >> 2) + (lane & 3) * 4) =
+          bf16x2_bits(ra * inv, rb * inv);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    mbar_arrive(smem_u32(&mi->q_here[seg & 1]));   // this CTA's softmax reads the powers
+    mbar_arrive_remote(dsmem_addr(smem_u32(&mi->q_ready), 0));
   }
 }
 
@@ -455,6 +530,9 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
   // K runs one tile ahead of V: K of tile g + 1 is written beside PV of tile
   // g - 1, V of tile g beside QK of tile g + 1.  Slot s of the rows holds tile
   // g for the (g / kRing)th time.
+  const int q0 = static_cast<int>(rank) * kCtaRows;
+  load_queries<4>(a, smem, mi, mi->start_v, mi->start_rt * kPairRows + q0, w, lane, 0);
+  int seg = 0;
   wait_or_abort(&mi->row_full[0], 0, mi, a.status);
   load_k(0);
   load_v(0);
@@ -482,6 +560,14 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
     if (g > 0) wait_or_abort(&mi->pv_done, (g - 1) & 1, mi, a.status);
     store_v(1);
     if (g + 1 < n) {
+      const int2 next = mi->seg[slot1];
+      // The next tile begins a segment: its queries, beside this one's softmax and
+      // output.  (Before V they would be there sooner, but with V's codes in
+      // registers too the tile loop spills, or with two rows in flight costs 2 %.)
+      if (next.x >= 0) {
+        wait_or_abort(&mi->q_free, seg & 1, mi, a.status);
+        load_queries<2>(a, smem, mi, next.x, next.y * kPairRows + q0, w, lane, ++seg);
+      }
       load_v(slot1);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&mi->row_free[slot1]));
@@ -562,64 +648,6 @@ __device__ __forceinline__ void mma_role(const MlaArgs& a, uint8_t* smem, Misc* 
   }
 }
 
-// Eight rows of queries per warp into shared memory: the latent part as fp16,
-// beside the fp16 latents, each row divided by the power of two that brings
-// its largest value to [2^14, 2^15) (exact down to 2^-31 of that value, with an
-// error below 2^-39 of it under that); the RoPE part, divided alike, as bf16.
-template <int kFly>   // rows in flight
-__device__ __forceinline__ void load_queries(const MlaArgs& a, uint8_t* smem, Misc* mi, int v,
-                                             int row0, int warp, int lane) {
-  uint8_t* sq = smem + kOffQ;
-#pragma unroll 1
-  for (int i0 = 0; i0 < 8; i0 += kFly) {
-    uint4 u[kFly][2];
-    uint32_t rope[kFly];
-#pragma unroll
-    for (int i = 0; i < kFly; ++i) {
-      const int row = row0 + warp * 8 + i0 + i;
-      u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      rope[i] = 0u;
-      if (row < a.entry_rows) {
-        const uint16_t* q = a.q + (static_cast<size_t>(v) * a.entry_rows + row) * kRowDim;
-        u[i][0] = reinterpret_cast<const uint4*>(q)[lane];
-        u[i][1] = reinterpret_cast<const uint4*>(q)[32 + lane];
-        rope[i] = reinterpret_cast<const uint32_t*>(q + kLatent)[lane];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kFly; ++i) {
-      const int r = warp * 8 + i0 + i;
-      float x[16];
-      unpack8(u[i][0], x);
-      unpack8(u[i][1], x + 8);
-      const float ra = bf16_lo(rope[i]), rb = bf16_hi(rope[i]);
-      const float mx = __uint_as_float(__reduce_max_sync(
-          0xffffffffu, __float_as_uint(fmaxf(fmaxf(amax8(x), amax8(x + 8)),
-                                             fmaxf(fabsf(ra), fabsf(rb))))));
-      // 2^e <= mx < 2^(e + 1); rows of zeros, infinities and NaN as they are
-      const int e = mx > 0.0f && mx < INFINITY
-                        ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 - 14
-                        : 0;
-      const int ec = min(max(e, -126), 126);
-      const float inv = exp2i(-ec);
-      if (lane == 0) mi->qexp[r] = static_cast<float>(ec);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float* y = x + 8 * h;
-        // unit 32 h + lane: chunk 8 h + lane / 4, its unit lane % 4
-        *reinterpret_cast<uint4*>(sq + (4 * h + (lane & 3)) * kKBlk + sw128_off(r, lane >> 2)) =
-            make_uint4(half2_bits(y[0] * inv, y[1] * inv), half2_bits(y[2] * inv, y[3] * inv),
-                       half2_bits(y[4] * inv, y[5] * inv), half2_bits(y[6] * inv, y[7] * inv));
-      }
-      *reinterpret_cast<uint32_t*>(sq + 8 * kKBlk + sw128_off(r, lane >> 2) + (lane & 3) * 4) =
-          bf16x2_bits(ra * inv, rb * inv);
-    }
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) mbar_arrive_remote(dsmem_addr(smem_u32(&mi->q_ready), 0));
-}
-
 // Eight warps.  Four threads share a query row: (half, sub) names 32 of a
 // tile's tokens, and 128 of the row's output dims.
 __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Misc* mi,
@@ -634,19 +662,18 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
   float m = -INFINITY, l = 0.0f, c2 = 0.0f;
   int limit = 0, seg_first_tile = 0, buf = 0, seg = 0;
   Tiles it(a, mi);
-  load_queries<4>(a, smem, mi, it.v, it.rt * kPairRows + static_cast<int>(rank) * kCtaRows, warp,
-               lane);
   for (int g = 0; it.more(); ++g) {
     const bool first = it.first(), last = it.last();
     if (first) {
       const int row = it.rt * kPairRows + static_cast<int>(rank) * kCtaRows + r;
       limit = row >= a.entry_rows ? 0 : it.len;
       if (!a.tokens && limit) limit = it.len - (a.ways - 1) + row / a.heads;
-      named_sync(3, kSoftWarps * 32);   // the rows' scales
+      // The rows' powers of two.  Those of the segment after the next wait for
+      // this one's P, so two places and two barriers are enough.
+      wait_or_abort(&mi->q_here[seg & 1], (seg >> 1) & 1, mi, a.status);
       // at least 2^-126: |s| < 2^41 then still weighs less than half a step of
       // 1 apart, and 0 * infinity does not arise
-      c2 = fmaxf(a.c2 * exp2f(mi->qexp[r]), 0x1p-126f);
-      named_sync(3, kSoftWarps * 32);   // read, before the next segment's take their place
+      c2 = fmaxf(a.c2 * exp2i(mi->qexp[seg & 1][r]), 0x1p-126f);
       m = -INFINITY;
       l = 0.0f;
       seg_first_tile = it.tile;
@@ -729,11 +756,6 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       const bool whole = seg_first_tile == 0 && ends;
       const int slot = pair * 2 + (seg == 0 ? 0 : 1);
       it.next(a);
-      if (it.more()) {   // the next segment's queries, ahead of this one's output
-        wait_or_abort(&mi->q_free, seg & 1, mi, a.status);
-        load_queries<2>(a, smem, mi, it.v, it.rt * kPairRows + static_cast<int>(rank) * kCtaRows,
-                     warp, lane);
-      }
       ++seg;
       // the whole row's sum, then O out of TMEM: final, or a partial
       mi->xch[part][r] = l;
@@ -763,10 +785,10 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
           for (int x = 0; x < 4; ++x)
             reinterpret_cast<uint4*>(dst)[x] = pack8_bf16(o + 8 * x);
         } else {
-          float* dst =
-              a.part_o + (static_cast<size_t>(slot) * kPairRows + prow) * kLatent + d0 + 32 * c;
+          float* dst = a.part_o + static_cast<size_t>(slot) * kPairRows * kLatent +
+                       ((d0 + 32 * c) / 8 * kPairRows + prow) * 8;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) st_global_32(dst + 8 * x, o + 8 * x);
+          for (int x = 0; x < 4; ++x) st_global_32(dst + x * kPairRows * 8, o + 8 * x);
         }
       }
       if (part == 0) {
@@ -798,7 +820,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (tid == 0) {
-    mbar_init(smem_u32(&mi->q_ready), 2 * kSoftWarps);
+    mbar_init(smem_u32(&mi->q_ready), 2 * kWidenWarps);
+    mbar_init(smem_u32(&mi->q_here[0]), kWidenWarps);
+    mbar_init(smem_u32(&mi->q_here[1]), kWidenWarps);
     mbar_init(smem_u32(&mi->q_free), 1);
     // those of the even CTA count both CTAs' warps
     for (int h = 0; h < 2; ++h) {
@@ -817,8 +841,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     mi->abort = 0;
     fence_mbar_init();
   }
-  // a role that gives up a wait goes on with the rows it finds: always some that exist
+  // a role that gives up a wait goes on with what it finds: always rows that exist
   if (tid < kRing * kMt) mi->row[tid / kMt][tid % kMt] = 0;
+  if (tid < kRing) mi->seg[tid] = make_int2(-1, 0);
   if (warp == kMmaWarp) {
     tmem_alloc_pair(smem_u32(&mi->tmem), 512);
     tmem_relinquish_pair();
@@ -898,57 +923,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
 }
 
 // Joins the partials of a query row that several pairs share, and writes the
-// rows of requests without a token.  A group of 64 threads takes every GROUPS-th
-// partial of a row, FLY of them in flight, and a CTA's four groups belong to one
-// row (few rows cut into many parts: one request over 32 pairs took 17.8 us a
-// call with one group of FLY = 8 a row) or to four (many rows with two or three
-// parts each).
+// rows of requests without a token.  A CTA takes SLICE of the 64 parts (8 dims) of
+// ROWS neighbouring rows, one thread a part, in GROUPS groups; a group takes
+// every GROUPS-th partial of its rows, FLY of them in flight.  Partials lie with
+// 8 dims of all 128 rows side by side, so that a warp of the attention, a row a
+// lane, writes 1 KB at a time (with rows of 2 KB its stores met 32 lines each
+// and O took 4.0 us to leave a CTA; 2.2 now), and four rows here fill a line.
 constexpr int kJoinThreads = 64;
-constexpr int kJoinGroups = 4;
 
-template <int FLY, int GROUPS>
-__global__ void __launch_bounds__(kJoinThreads* kJoinGroups) cache_mla_join_kernel(
+template <int ROWS, int SLICE, int GROUPS, int FLY>
+__global__ void __launch_bounds__(SLICE* ROWS* GROUPS) cache_mla_join_kernel(
     const MlaArgs a, int all_rows) {
-  __shared__ float shared[GROUPS > 1 ? (GROUPS - 1) * kJoinThreads * 10 : 1];
+  constexpr int kSlices = kJoinThreads / SLICE;
+  constexpr int kSpan = SLICE * ROWS;   // threads of one group
+  __shared__ float shared[GROUPS > 1 ? (GROUPS - 1) * kSpan * 10 : 1];
   pdl_wait_previous();
-  const int group = threadIdx.x / kJoinThreads;
-  const int x = GROUPS > 1 ? blockIdx.x : blockIdx.x * kJoinGroups + group;   // (b, m, h)
-  const int g = GROUPS > 1 ? group : 0;
-  if (x >= all_rows) return;
-  const int h = x % a.heads, bm = x / a.heads, b = bm / a.ways, m = bm % a.ways;
-  const int t = threadIdx.x % kJoinThreads;   // dims 4t .. and 256 + 4t ..
+  // neighbouring threads: the halves of 32 bytes of one row, then the next row
+  const int at = threadIdx.x % kSpan, g = threadIdx.x / kSpan;
+  const int t = static_cast<int>(blockIdx.x % kSlices) * SLICE + 2 * (at / (2 * ROWS)) +
+                (at & 1);                               // dims 4t .. and 256 + 4t ..
+  const int x = static_cast<int>(blockIdx.x / kSlices) * ROWS + (at >> 1) % ROWS;   // (b, m, h)
+  const bool real = x < all_rows;
+  const int xr = real ? x : 0;
+  const int h = xr % a.heads, bm = xr / a.heads, b = bm / a.ways, m = bm % a.ways;
   const int v = a.tokens ? bm : b;
   const int row = a.tokens ? h : m * a.heads + h;
   const int T = a.T[b];
   const int2 sp = a.span[static_cast<size_t>(v) * a.row_tiles + row / kPairRows];
-  if (h == 0 && m == 0 && t == 0 &&
+  if (real && h == 0 && m == 0 && t == 0 &&
       (T < 0 || T > static_cast<long long>(a.max_pages) * a.page))
     set_status(a.status, ESS_ERR_DEVICE_CHECK);
+  const bool empty = entry_len(a, v) == 0;   // then nothing wrote its span
+  const bool join = real && !empty && sp.x >> 1 != sp.y;   // else one pair wrote the row
+  const int p0 = join ? sp.x >> 1 : 0;
   uint2* out = reinterpret_cast<uint2*>(a.out + static_cast<size_t>(x) * kLatent) + t;
-  if (entry_len(a, v) == 0) {   // (the conditions that leave are the same for a CTA's one row)
+  if (real && empty && g == 0) {
     out[0] = out[kJoinThreads] = make_uint2(0u, 0u);
     if (t == 0 && a.lse) a.lse[x] = -INFINITY;
-    return;
   }
-  const int p0 = sp.x >> 1;
-  if (p0 == sp.y) return;
-  const int pr = row % kPairRows;
+  if (GROUPS == 1 && !join) return;
+  const int pr = row % kPairRows, last = join ? sp.y : -1;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float c2 = a.part_ml[static_cast<size_t>(sp.x) * kPairRows + pr].z;   // of every part
+  // of every part
+  const float c2 = join ? a.part_ml[static_cast<size_t>(sp.x) * kPairRows + pr].z : 0.0f;
   float mx = -INFINITY, l = 0.0f;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int pb = p0 + g; pb <= sp.y; pb += FLY * GROUPS) {
+  for (int pb = p0 + g; pb <= last; pb += FLY * GROUPS) {
     float2 ml[FLY];
     float4 o[FLY][2];
 #pragma unroll
     for (int q = 0; q < FLY; ++q) {
       const int p = pb + q * GROUPS;
-      const size_t i = static_cast<size_t>(p == p0 ? sp.x : 2 * p) * kPairRows + pr;
-      const float4* po = reinterpret_cast<const float4*>(a.part_o + i * kLatent) + t;
-      const bool in = p <= sp.y;
-      ml[q] = in ? *reinterpret_cast<const float2*>(a.part_ml + i) : make_float2(-INFINITY, 0.0f);
+      const size_t i = p == p0 ? sp.x : 2 * p;
+      const float4* po = reinterpret_cast<const float4*>(a.part_o + i * kPairRows * kLatent) +
+                         ((t >> 1) * kPairRows + pr) * 2 + (t & 1);
+      const bool in = p <= last;
+      ml[q] = in ? *reinterpret_cast<const float2*>(a.part_ml + i * kPairRows + pr)
+                 : make_float2(-INFINITY, 0.0f);
       o[q][0] = in ? po[0] : zero;
-      o[q][1] = in ? po[kJoinThreads] : zero;
+      o[q][1] = in ? po[256 / 8 * kPairRows * 2] : zero;
     }
     float m2 = mx;
 #pragma unroll
@@ -975,18 +1008,17 @@ __global__ void __launch_bounds__(kJoinThreads* kJoinGroups) cache_mla_join_kern
   }
   if (GROUPS > 1) {   // the groups' sums to the first one
     if (g > 0) {
-      float* to = shared + (g - 1) * kJoinThreads * 10 + t;
+      float* to = shared + (g - 1) * kSpan * 10 + at;
       to[0] = mx;
-      to[kJoinThreads] = l;
+      to[kSpan] = l;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) to[(2 + e) * kJoinThreads] = acc[e];
+      for (int e = 0; e < 8; ++e) to[(2 + e) * kSpan] = acc[e];
     }
     __syncthreads();
-    if (g > 0) return;
+    if (g > 0 || !join) return;
     float m2 = mx;
 #pragma unroll
-    for (int q = 0; q < GROUPS - 1; ++q)
-      m2 = fmaxf(m2, shared[q * kJoinThreads * 10 + t]);
+    for (int q = 0; q < GROUPS - 1; ++q) m2 = fmaxf(m2, shared[q * kSpan * 10 + at]);
     const float base = m2 == -INFINITY ? 0.0f : m2;
     const float f = exp2f((mx - base) * c2);
     l *= f;
@@ -994,11 +1026,11 @@ __global__ void __launch_bounds__(kJoinThreads* kJoinGroups) cache_mla_join_kern
     for (int e = 0; e < 8; ++e) acc[e] *= f;
 #pragma unroll
     for (int q = 0; q < GROUPS - 1; ++q) {
-      const float* from = shared + q * kJoinThreads * 10 + t;
+      const float* from = shared + q * kSpan * 10 + at;
       const float w = exp2f((from[0] - base) * c2);
-      l = fmaf(w, from[kJoinThreads], l);
+      l = fmaf(w, from[kSpan], l);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, from[(2 + e) * kJoinThreads], acc[e]);
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, from[(2 + e) * kSpan], acc[e]);
     }
     mx = m2;
   }
@@ -1011,6 +1043,14 @@ __global__ void __launch_bounds__(kJoinThreads* kJoinGroups) cache_mla_join_kern
                    bf16x2_bits(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
   if (t == 0 && a.lse)
     a.lse[x] = row_lse(mx, c2, l);
+}
+
+template <int ROWS, int SLICE, int GROUPS, int FLY>
+cudaError_t launch_join(const MlaArgs& a, long long all_rows, cudaStream_t st) {
+  const long long ctas = (all_rows + ROWS - 1) / ROWS * (kJoinThreads / SLICE);
+  return launch_pdl_once(cache_mla_join_kernel<ROWS, SLICE, GROUPS, FLY>,
+                         dim3(static_cast<unsigned>(ctas)), dim3(SLICE * ROWS * GROUPS), 0, st, a,
+                         static_cast<int>(all_rows));
 }
 
 ess_status check_shape(int batch, int ways, int heads) {
@@ -1124,14 +1164,14 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
   if (e != cudaSuccess) return ESS_ERR_CUDA;
   e = launch_pdl_once(cache_mla_kernel, dim3(2 * pairs), dim3(kMlaThreads), kMlaSmem, st, a);
   if (e != cudaSuccess) return ESS_ERR_CUDA;
-  const dim3 jblock(kJoinThreads * kJoinGroups);
-  if (all_rows >= 2048)   // more rows than CTAs that run at once
-    e = launch_pdl_once(cache_mla_join_kernel<4, 1>,
-                        dim3(static_cast<unsigned>((all_rows + kJoinGroups - 1) / kJoinGroups)),
-                        jblock, 0, st, a, static_cast<int>(all_rows));
-  else
-    e = launch_pdl_once(cache_mla_join_kernel<4, kJoinGroups>, dim3(static_cast<unsigned>(all_rows)),
-                        jblock, 0, st, a, static_cast<int>(all_rows));
+  // Few rows with many parts (a 4096-token request: 32) are cut into many small
+  // slices: 12.1 us a call, where whole rows took 14.4.  Many rows (2048 and more
+  // fill the GPU) have two or three parts each: one group is enough, and four
+  // parts in flight cost 1.5 us of 97 more than two.  Between, two groups: 2048 listed
+  // tokens of eight requests 19.3 us, four groups 21.7, slices of 16 19.7.
+  if (all_rows <= 608) e = launch_join<4, 8, 16, 2>(a, all_rows, st);
+  else if (all_rows < 2048) e = launch_join<4, 64, 2, 4>(a, all_rows, st);
+  else e = launch_join<4, 64, 1, 2>(a, all_rows, st);
   return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
 }
 

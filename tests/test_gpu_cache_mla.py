@@ -246,6 +246,19 @@ def test_no_request_has_a_token():
     assert c.cache.poll() == ess.ESS_OK
 
 
+@pytest.mark.parametrize("fill", [0xFF, 0x7F])
+@pytest.mark.parametrize("heads,ways", [(128, 1), (7, 2), (128, 4)])
+def test_empty_requests_over_a_dirty_workspace(fill, heads, ways):
+    """Nothing of an empty request is in the workspace, whatever it held."""
+    c = Case(30, [1] * 9, ways, heads)
+    c.lens = [0, 0, 1, 0, 0, 1, 0, 0, 0]
+    c.T.copy_(torch.tensor(c.lens, dtype=torch.int32))
+    ws = c.cache.workspace(9, ways, heads)
+    ws.fill_(fill)
+    out, lse = c.attend(workspace=ws)
+    c.check(out, lse)
+
+
 def test_rows_past_32_bits_of_offset():
     from host_latent_cache_gb300.rows import RowCache
     n_rows = (5 << 30) // 400 // 64 * 64            # a cache of 5 GiB
