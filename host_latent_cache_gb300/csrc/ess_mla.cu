@@ -37,9 +37,10 @@
 // by the row warp +7 %; loads that skip L1 +14 %; warps of their own for K and
 // for V +1 %, and for even and odd tiles +17 %.
 //
-// All tiles of all requests are dealt evenly to the pairs (lengths are read on
-// the device, so captured calls follow them); a request cut by a boundary
-// leaves fp32 partials, which a second kernel joins.
+// All tiles of all requests are dealt evenly to the pairs, a segment's queries and
+// output counted too (lengths are read on the device, so captured calls follow
+// them); a request cut by a boundary leaves fp32 partials, which a second kernel
+// joins.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -63,6 +64,9 @@ constexpr int kWidenWarp0 = 9;
 constexpr int kWidenWarps = 16;
 constexpr int kRowWarp = kWidenWarp0 + kWidenWarps;
 constexpr int kMlaThreads = (kRowWarp + 1) * 32;
+// What a segment costs beside its tiles, in tiles, when they are dealt: ragged
+// requests to 8192 took 97.3 us with 0, 94.1 with 1, 91.9 with 2, 92.3 with 3.
+constexpr int kSegmentCost = 2;
 constexpr int kRing = 3;              // tiles whose rows are known ahead of their use
 
 constexpr uint32_t kKBlk = 8192;      // [64 rows][64 dims], 128-byte swizzled
@@ -88,7 +92,8 @@ struct Misc {
   uint64_t row_full[kRing], row_free[kRing];
   uint32_t tmem;
   int abort;
-  int start_v, start_rt, start_tile, tiles;
+  int start_v, start_rt, start_tile;
+  long long first_tile, end_tile;     // of all tiles of all requests
   uint32_t mask[kRing][4];            // tokens of a tile that exist
   int32_t row[kRing][kMt];            // cache rows of a tile's tokens (0 for one that is not)
   float xch[4][kCtaRows];             // a row's statistics from the four threads that share it
@@ -281,7 +286,7 @@ struct Tiles {
   bool begins;   // the pair's first tile
 
   __device__ __forceinline__ Tiles(const MlaArgs& a, const Misc* mi) {
-    left = mi->tiles;
+    left = static_cast<int>(mi->end_tile - mi->first_tile);
     v = mi->start_v;
     load(a);
     rt = mi->start_rt;
@@ -480,7 +485,7 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
                                            uint32_t rank) {
   const int wt = threadIdx.x - kWidenWarp0 * 32;
   const int w = wt >> 5, lane = wt & 31;
-  const int n = mi->tiles;
+  const int n = static_cast<int>(mi->end_tile - mi->first_tile);
   const int c8 = lane & 7, r4 = 4 * w + (lane >> 3);   // K's row; V's tokens r4 and 64 + r4
   const uint8_t* code = a.rows + 16 * c8;
   const uint32_t place = static_cast<uint32_t>(r4 * 128 + ((c8 ^ (r4 & 7)) << 4));
@@ -851,13 +856,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   __syncwarp();
   cluster_arrive();   // the peer may arrive on this CTA's barriers once it has waited
   pdl_wait_previous();
-  // this pair's share of all tiles: a scan of the entries' tile counts, a
-  // run of neighbouring entries per thread
+  // This pair's share.  A segment (one entry and row tile) costs its tiles and
+  // kSegmentCost more (its queries, its output), so positions are dealt in which
+  // each segment has that many in front of its tiles: a scan of the entries'
+  // tiles and segments, a run of neighbouring entries per thread.  With few
+  // tiles those positions are left out, as a pair with none but them would lie
+  // between two that share a request.  (Few entries are scanned by every warp,
+  // without the block: 0.3 us of a small call.)
+  constexpr int kSegShift = 43;   // tiles below, segments above
   const int per = (a.entries + kMlaThreads - 1) / kMlaThreads;
-  const int v0 = min(a.entries, tid * per), v1 = min(a.entries, v0 + per);
+  const bool few = a.entries <= 32;   // then each warp scans them
+  const int v0 = min(a.entries, few ? lane : tid * per), v1 = min(a.entries, v0 + per);
   long long mine = 0;
-  for (int v = v0; v < v1; ++v)
-    mine += static_cast<long long>((entry_len(a, v) + kMt - 1) / kMt) * a.row_tiles;
+  int nt0 = 0;
+  for (int v = v0; v < v1; ++v) {
+    const int nt = (entry_len(a, v) + kMt - 1) / kMt;
+    if (v == v0) nt0 = nt;
+    if (nt > 0) mine += (static_cast<long long>(nt) + (1LL << kSegShift)) * a.row_tiles;
+  }
   long long before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -865,38 +881,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     if (lane >= o) before += x;
   }
   long long* scan = reinterpret_cast<long long*>(mi->xch);   // free until the roles start
-  if (lane == 31) scan[warp] = before;
-  __syncthreads();
-  long long sums = lane < kMlaThreads / 32 ? scan[lane] : 0;   // of the warps
+  long long total = __shfl_sync(0xffffffffu, before, 31);
+  before -= mine;
+  if (!few) {
+    if (lane == 31) scan[warp] = total;
+    __syncthreads();
+    long long sums = lane < kMlaThreads / 32 ? scan[lane] : 0;   // of the warps
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, sums, o);
-    if (lane >= o) sums += x;
-  }
-  const long long total = __shfl_sync(0xffffffffu, sums, 31);
-  before += __shfl_sync(0xffffffffu, sums, max(warp - 1, 0)) * (warp > 0 ? 1 : 0) - mine;
-  // the first total % busy pairs take one tile more; neighbouring pairs share
-  // a request, so none between two may be idle
-  const int busy = total < pairs ? max(static_cast<int>(total), 1) : pairs;
-  const long long share = total < 0x7fffffffLL
-                              ? static_cast<unsigned>(total) / static_cast<unsigned>(busy)
-                              : total / busy;
-  const int extra = static_cast<int>(total - share * busy);
-  const long long lo = share * pair + min(pair, extra);   // total, for an idle pair
-  if (lo >= before && lo < before + mine) {
-    long long off = lo - before;
-    int v = v0, nt;
-    for (;; ++v) {
-      nt = (entry_len(a, v) + kMt - 1) / kMt;
-      if (off < static_cast<long long>(nt) * a.row_tiles) break;
-      off -= static_cast<long long>(nt) * a.row_tiles;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, sums, o);
+      if (lane >= o) sums += x;
     }
-    int rt = 0;   // at most kMaxCacheWays row tiles
-    for (; off >= nt; off -= nt) ++rt;
-    mi->start_v = v;
-    mi->start_rt = rt;
-    mi->start_tile = static_cast<int>(off);
-    mi->tiles = static_cast<int>(share) + (pair < extra ? 1 : 0);
+    total = __shfl_sync(0xffffffffu, sums, 31);
+    before += warp > 0 ? __shfl_sync(0xffffffffu, sums, warp - 1) : 0;
+  }
+  constexpr long long kTileMask = (1LL << kSegShift) - 1;
+  const long long tiles = total & kTileMask;
+  const int cost = tiles >= static_cast<long long>(kSegmentCost + 1) * pairs ? kSegmentCost : 0;
+  const long long tiles_before = before & kTileMask;
+  const long long pos0 = tiles_before + cost * (before >> kSegShift);
+  const long long pos1 = pos0 + (mine & kTileMask) + cost * (mine >> kSegShift);
+  const long long all = tiles + cost * (total >> kSegShift);
+  // the first all % busy pairs take one position more
+  const int busy = tiles < pairs ? max(static_cast<int>(tiles), 1) : pairs;
+  const long long share = all < 0x7fffffffLL
+                              ? static_cast<unsigned>(all) / static_cast<unsigned>(busy)
+                              : all / busy;
+  const int extra = static_cast<int>(all - share * busy);
+  const bool deals = !few || warp == 0;
+#pragma unroll 1
+  for (int end = 0; deals && end < 2; ++end) {
+    const long long at = share * (pair + end) + min(pair + end, extra);
+    if (at == all && tid == 0) mi->end_tile = tiles;   // of the last pair (and idle ones)
+    if (at < pos0 || at >= pos1) continue;
+    long long off = at - pos0, t = tiles_before;
+    int v = v0, nt, rt = 0;
+    for (;; ++v) {
+      nt = v == v0 ? nt0 : (entry_len(a, v) + kMt - 1) / kMt;
+      const long long w = nt > 0 ? static_cast<long long>(nt + cost) * a.row_tiles : 0;
+      if (off < w) break;
+      off -= w;
+      t += static_cast<long long>(nt) * a.row_tiles;
+    }
+    for (; off >= nt + cost; off -= nt + cost) ++rt;   // at most kMaxCacheWays row tiles
+    const int tile = max(static_cast<int>(off) - cost, 0);
+    t += static_cast<long long>(rt) * nt + tile;
+    if (end) {
+      mi->end_tile = t;
+    } else {
+      mi->start_v = v;
+      mi->start_rt = rt;
+      mi->start_tile = tile;
+      mi->first_tile = t;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -904,7 +941,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   tc_fence_after();
   const uint32_t tmem = mi->tmem;
 
-  if (pair >= total) {
+  if (pair >= tiles) {
     // nothing to do: both CTAs of the pair
   } else if (warp < kSoftWarps) {
     softmax_role(a, smem, mi, rank, tmem, pair);
