@@ -368,6 +368,10 @@ __device__ __forceinline__ void widen_block(const uint4& codes, int byte, uint4*
   }
 }
 
+__device__ __forceinline__ uint4 pick4(bool p, const uint4& a, const uint4& b) {
+  return make_uint4(p ? a.x : b.x, p ? a.y : b.y, p ? a.z : b.z, p ? a.w : b.w);
+}
+
 // ---------------------------------------------------------------- roles
 // One warp resolves the cache rows of the tiles to come, four tokens a lane,
 // up to kRing tiles ahead, so that the page table's latency meets nobody.
@@ -492,8 +496,11 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
   uint8_t* sk = smem + kOffK + place;
   uint8_t* sv = smem + kOffV + place;
 
-  uint4 kc[2], kr, vc[2];   // raw codes (K: halves of the dims, V: of the tokens), RoPE unit
-  int ke[2], ve[2];         // exponent bytes
+  // Raw codes and exponent bytes: K's two halves of the dims and its RoPE unit,
+  // and this CTA's dims of two tokens of V: one that is K's row too, kept from K
+  // (loaded again it cost 1.6 % of the long attention), and one of the other CTA's.
+  uint4 kc[2], kr, own, other;
+  int ke[2], own_e, other_e;
   auto at = [](int row) { return static_cast<size_t>(static_cast<uint32_t>(row)) * kQ4RowBytes; };
   auto load_k = [&](int slot) {
     const uint8_t* s = code + at(mi->row[slot][rank * kCtaRows + r4]);
@@ -505,12 +512,9 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
     kr = *reinterpret_cast<const uint4*>(s + 272);
   };
   auto load_v = [&](int slot) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint8_t* s = code + 128 * rank + at(mi->row[slot][64 * h + r4]);
-      vc[h] = *reinterpret_cast<const uint4*>(s);
-      ve[h] = s[256 - 120 * static_cast<int>(rank) - 15 * c8];
-    }
+    const uint8_t* s = code + 128 * rank + at(mi->row[slot][64 * (rank ^ 1) + r4]);
+    other = *reinterpret_cast<const uint4*>(s);
+    other_e = s[256 - 120 * static_cast<int>(rank) - 15 * c8];
   };
   auto put = [&](uint8_t* d, uint32_t block_bytes, const uint4& codes, int byte) {
     uint4 unit[4];
@@ -528,8 +532,8 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
     if (h == 1) *reinterpret_cast<uint4*>(sk + 8 * kKBlk) = kr;
     told(&mi->k_full[h]);
   };
-  auto store_v = [&](int h) {
-    put(sv + h * 64 * 128, kVBlk, vc[h], ve[h]);
+  auto store_v = [&](int h, const uint4& codes, int byte) {
+    put(sv + h * 64 * 128, kVBlk, codes, byte);
     told(&mi->vp_full[h]);
   };
   // K runs one tile ahead of V: K of tile g + 1 is written beside PV of tile
@@ -545,6 +549,8 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
   if (lane == 0) mbar_arrive(smem_u32(&mi->row_free[0]));
   store_k(0);
   store_k(1);
+  own = pick4(rank, kc[1], kc[0]);
+  own_e = rank ? ke[1] : ke[0];
   if (n > 1) {
     wait_or_abort(&mi->row_full[1], 0, mi, a.status);
     load_k(1);
@@ -560,10 +566,14 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
     }
     if (g + 2 < n) wait_or_abort(&mi->row_full[slot2], turn2 & 1, mi, a.status);
     if (g > 0) wait_or_abort(&mi->pv_half, (g - 1) & 1, mi, a.status);
-    store_v(0);
+    const uint4 c0 = pick4(rank, other, own), c1 = pick4(rank, own, other);
+    const int e0 = rank ? other_e : own_e, e1 = rank ? own_e : other_e;
+    store_v(0, c0, e0);
+    own = pick4(rank, kc[1], kc[0]);   // of tile g + 1
+    own_e = rank ? ke[1] : ke[0];
     if (g + 2 < n) load_k(slot2);
     if (g > 0) wait_or_abort(&mi->pv_done, (g - 1) & 1, mi, a.status);
-    store_v(1);
+    store_v(1, c1, e1);
     if (g + 1 < n) {
       const int2 next = mi->seg[slot1];
       // The next tile begins a segment: its queries, beside this one's softmax and
