@@ -565,13 +565,13 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
       store_k(1);
     }
     if (g + 2 < n) wait_or_abort(&mi->row_full[slot2], turn2 & 1, mi, a.status);
-    if (g > 0) wait_or_abort(&mi->pv_half, (g - 1) & 1, mi, a.status);
     const uint4 c0 = pick4(rank, other, own), c1 = pick4(rank, own, other);
     const int e0 = rank ? other_e : own_e, e1 = rank ? own_e : other_e;
-    store_v(0, c0, e0);
     own = pick4(rank, kc[1], kc[0]);   // of tile g + 1
     own_e = rank ? ke[1] : ke[0];
     if (g + 2 < n) load_k(slot2);
+    if (g > 0) wait_or_abort(&mi->pv_half, (g - 1) & 1, mi, a.status);
+    store_v(0, c0, e0);
     if (g > 0) wait_or_abort(&mi->pv_done, (g - 1) & 1, mi, a.status);
     store_v(1, c1, e1);
     if (g + 1 < n) {
