@@ -19,23 +19,29 @@
 // The rows' 4-bit codes are widened to fp16, exactly, by one conversion and one
 // multiplication a pair.  Queries become fp16 under a power of two of their
 // row, P keeps 11 bits, and the 64 RoPE dims stay bf16 in MMAs of their own.
-// Sixteen warps gather and widen, eight run the softmax, one resolves the
-// tokens' rows, one of the even CTA issues the MMAs: QK of tile i + 1, then PV
-// of tile i, so the softmax of a tile and the widening of the next run beside
-// them.  O is rescaled only when a row's maximum grows by more than 2^8.
+// Sixteen warps gather and widen (and bring in a segment's queries), eight run the
+// softmax, one resolves the tokens' rows, one of the even CTA issues the MMAs: QK
+// of tile i + 1, then PV of tile i, so the softmax of a tile and the widening of
+// the next run beside them.  O is rescaled only when a row's maximum grows by
+// more than 2^8.
 //
 // What bounds it: the shared-memory and L1 data path.  A tile writes 147 KB of
-// widened operands and P, reads 35 KB of raw rows through L1 (rows of 400 bytes
-// straddle its lines: 51 KB) and the MMAs read 245 KB of operands, beside 2200
-// cycles of tensor work.  All tokens of eight 128K contexts with 128 heads: 199
-// us, 1.16 PFLOP/s or 62 % of the measured tensor rate, 4200 cycles a tile.
+// widened operands and P, reads 34 KB of raw rows through L1, in pieces of 128
+// bytes that straddle its lines, and the MMAs read 245 KB of operands, beside
+// 2200 cycles of tensor work.  All tokens of eight 128K contexts with 128 heads:
+// 188 us, 1.23 PFLOP/s or 65 % of the measured tensor rate, 3900 cycles a tile.
+// A segment costs about 5 us beside its tiles: its queries (1.2 us of conversions
+// and stores), O's way out (2.2 us) and the pipeline's start.
 // Measured on the way there (same case): one thread issuing in divergent code
 // 526 us (110 cycles an MMA); V before K of the next tile 447; four softmax
 // warps, rows resolved by the widening warps 346; lanes across rows (32 lines a
 // load) 300; cluster-scope arrivals, which wait for loads in flight, 235; whole
-// tiles handed over instead of halves, eight widening warps 211; L2 prefetches
-// by the row warp +7 %; loads that skip L1 +14 %; warps of their own for K and
-// for V +1 %, and for even and odd tiles +17 %.
+// tiles handed over instead of halves, eight widening warps 211; queries by the
+// softmax warps, V loaded whole 197; K's loads after V's first half 190; L2
+// prefetches of rows by the row warp +7 %; loads that skip L1 +14 %; warps of
+// their own for K and for V +1 %, and for even and odd tiles +17 %; V's loads a
+// step earlier, or K's in two halves, +9 to 11 % (more loads in flight than the
+// data path takes); any spill of registers in the tile loop 10 to 25 %.
 //
 // All tiles of all requests are dealt evenly to the pairs, a segment's queries and
 // output counted too (lengths are read on the device, so captured calls follow
