@@ -246,21 +246,19 @@ __device__ __forceinline__ void st_global_32(float* p, const float* v) {
                : "memory");
 }
 
-// this lane's 8 consecutive columns times f, in place
-__device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f) {
-  uint32_t r[8];
+// this lane's 4 consecutive columns times f, in place
+__device__ __forceinline__ void tmem_scale4(uint32_t taddr, float f) {
+  uint32_t r[4];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\t"
       "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
       : "r"(taddr)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-               "r"(r[7])
+  for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
                : "memory");
 }
 // Barrier over `threads` threads that says whether any of them has x.
@@ -681,7 +679,7 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
   uint8_t* sp = smem + kOffP + half * kKBlk;
   const int bar_id = 1 + (warp & 1);   // the four warps that hold the same rows
   float m = -INFINITY, l = 0.0f, c2 = 0.0f;
-  int limit = 0, seg_first_tile = 0, buf = 0, seg = 0;
+  int limit = 0, seg_first_tile = 0, seg = 0;
   Tiles it(a, mi);
   for (int g = 0; it.more(); ++g) {
     const bool first = it.first(), last = it.last();
@@ -701,11 +699,11 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
     }
     bool ok = wait_or_abort(&mi->qk_done[g & 1], (g >> 1) & 1, mi, a.status);
     tc_fence_after();
-    uint32_t live = mi->mask[buf][part];
+    uint32_t live = mi->mask[g % kRing][part];
     const int nv = limit - it.tile * kMt - part * 32;   // tokens of these 32 before the limit
     if (nv < 32) live = nv <= 0 ? 0u : live & ((1u << nv) - 1u);
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&mi->row_free[buf]));
+    if (lane == 0) mbar_arrive(smem_u32(&mi->row_free[g % kRing]));
     float s[32];
     tmem_ld32(tmem + lanes + kColS + (g & 1) * 64 + sub * 32, s);
     if (live != 0xffffffffu) {
@@ -724,7 +722,8 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
     // The row's maximum is only looked up when one of its parts outgrew the
     // one in use (or there is none yet: a difference of infinity).
     float f = 1.0f;
-    if (named_any(bar_id, kSoftWarps * 16, (mt - m) * c2 > kGrow)) {
+    const bool grown = named_any(bar_id, kSoftWarps * 16, (mt - m) * c2 > kGrow);
+    if (grown) {
       mi->xch[part][r] = mt;
       named_sync(bar_id, kSoftWarps * 16);
       mt = fmaxf(fmaxf(mi->xch[0][r], mi->xch[1][r]), fmaxf(mi->xch[2][r], mi->xch[3][r]));
@@ -753,11 +752,16 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
     l = fmaf(l, f, sum2[0].x + sum2[0].y);
     // P and O are free once PV of the tile before is done
     if (g > 0) ok = wait_or_abort(&mi->pv_done, (g - 1) & 1, mi, a.status) && ok;
-    if (!first && __any_sync(0xffffffffu, f != 1.0f)) {
+    if (!first && grown) {
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < 16; ++c) tmem_scale8(to + 8 * c, f);
+      for (int c = 0; c < 32; ++c) tmem_scale4(to + 4 * c, f);
       tmem_wait_st();
+      // Each half of PV adds to all of O's columns, so these rows are scaled in both
+      // halves before any of the four warps lets its own half start.  (grown is the
+      // barrier's answer: all four come here or none.)
+      tc_fence_before();
+      named_sync(bar_id, kSoftWarps * 16);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
@@ -826,7 +830,6 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       }
       tc_fence_before();
     }
-    buf = buf == 2 ? 0 : buf + 1;
   }
   // the last arrival on this CTA's q_free, which nothing else waits for
   wait_or_abort(&mi->q_free, (seg - 1) & 1, mi, a.status);

@@ -143,6 +143,63 @@ def test_peaked_and_rising_scores():
         c.check(out, lse, t)
 
 
+class Rising(Case):
+    """A Case whose scores rise by `step` nats with every tile of 128 tokens, in
+    a saw-tooth of `period` tiles, for the heads that `rises` picks: the first RoPE
+    value of token t is the tile's number in its period, the queries' is
+    step / scale (both exact in bf16)."""
+
+    def __init__(self, seed, lens, ways, heads, step=6, period=60, rises=lambda h: True):
+        from host_latent_cache_gb300 import rows
+        super().__init__(seed, lens, ways, heads)
+        for b, T in enumerate(self.lens):
+            t = np.arange(T)
+            at = self.table[b, t // 64].astype(np.int64) * 64 + t % 64
+            tooth = torch.from_numpy((t // 128 % period).astype(np.float32)).to(torch.bfloat16)
+            self.raw[at, 272:274] = tooth.view(torch.uint8).numpy().reshape(-1, 2)
+        self.cache = rows.RowCache(torch.from_numpy(self.raw).cuda(), "q4")
+        for h in range(heads):
+            self.q[:, :, h, 512] = step / self.scale if rises(h) else 0.0
+
+
+@pytest.mark.parametrize("lens,ways,heads,rises", [
+    ([800] * 76, 1, 128, lambda h: True), ([800] * 76, 1, 128, lambda h: h % 3 == 0),
+    ([1500] * 40, 2, 64, lambda h: h != 17), ([3000, 40, 9000, 1], 1, 20, lambda h: True),
+], ids=["all", "some", "two-ways", "few-heads"])
+def test_maxima_that_grow_from_tile_to_tile(lens, ways, heads, rises):
+    """Pairs hold several tiles of a segment and rescale O at nearly each; every
+    one of a pair's rows, and both halves of the dims, follow."""
+    c = Rising(40 + len(lens), lens, ways, heads, rises=rises)
+    out, lse = c.attend()
+    assert c.cache.poll() == ess.ESS_OK
+    c.check(out, lse)
+    for _ in range(20):
+        again = c.attend()
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+def test_a_long_request_whose_maxima_grow():
+    c = Rising(45, [60000], 1, 128, period=25)       # six tiles a pair
+    out, lse = c.attend()
+    c.check(out, lse)
+    for _ in range(20):
+        again = c.attend()
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+def test_listed_tokens_whose_maxima_grow():
+    c = Rising(46, [7000] * 8, 1, 128)
+    tok = np.stack([np.sort(c.rng.permutation(7000)[:6000]) for _ in range(8)]).astype(np.int32)[:, None]
+    out, lse = c.attend(tok)                         # five tiles a pair
+    assert c.cache.poll() == ess.ESS_OK
+    c.check(out, lse, tok)
+    down = np.ascontiguousarray(tok[:, :, ::-1])     # and maxima that never grow
+    c.check(*c.attend(down), down)
+    for _ in range(20):
+        again = c.attend(tok)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
 def test_what_lies_behind_the_last_token_does_not_matter():
     c = Case(9, [70, 129], 2, 16, max_pages=5)
     want = c.attend()
