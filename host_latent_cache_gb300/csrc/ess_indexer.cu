@@ -53,7 +53,7 @@ struct IdxArgs {
   int B, M, HI, NP, T, total_tiles, A;
   int S;                     // key-ring stages (chunks)
   int U;                     // tiles per chunk, the unit of the barrier rounds
-  int early;                 // 1: no append since the last indexer launch on this layer
+  int early;                 // 1: no append or key norm since the last indexer launch on this layer
 };
 
 constexpr uint32_t kTileBytes = kIdxTile * kKeyRowBytes;  // 16 KB
@@ -195,8 +195,9 @@ __global__ void __launch_bounds__(kIdxThreads, 1)
                   b * a.T + (j0 + u) * kIdxTile);
   };
   // Early mode: no append kernel has run on this layer since its last indexer,
-  // so the tile prefix and the key rows of the first chunks are
-  // final already; the first ring's worth is requested before the wait.
+  // nor a norm that may have written its keys, so the tile prefix and the key
+  // rows of the first chunks are final already; the first ring's worth is
+  // requested before the wait.
   int n_early = 0;
   if (warp == 0 && a.early) {
     if (lane == 0) {
@@ -548,7 +549,8 @@ cudaError_t launch_indexer(const ess_pool& p, int layer, const void* q_idx, cons
   const int HB = with_hist ? c.mtp * (kHistBins + kFineBins) : 0;
   indexer_shape(a.NP, HB, &a.U, &a.S);
   a.A = 512 / (a.U * a.NP) < kMaxAcc ? 512 / (a.U * a.NP) : kMaxAcc;
-  a.early = L.append_pending ? 0 : 1;
+  const unsigned long long norms = key_norms().load();
+  a.early = L.append_pending || norms != L.norms_seen ? 0 : 1;
   CUtensorMap qmap;
   if (!encode_map_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, q_idx, kKeyRowBytes,
                      static_cast<uint64_t>(c.batch) * c.mtp * c.idx_heads, kKeyRowBytes,
@@ -569,8 +571,9 @@ cudaError_t launch_indexer(const ess_pool& p, int layer, const void* q_idx, cons
   e = launch_pdl(kern, dim3(grid), dim3(kIdxThreads), smem, st, L.kmap, qmap, a);
   if (e == cudaSuccess) {
     count_launch(p);
-    // this launch waits for any append before it, so the next one may load early
+    // this launch waits for any append or norm before it, so the next one may load early
     p.layers[layer].append_pending = false;
+    p.layers[layer].norms_seen = norms;
   }
   return e;
 }

@@ -6,6 +6,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <vector>
 
 #include "ess.h"
@@ -73,6 +74,9 @@ struct Layer {
   // an append kernel was launched after the last indexer launch: the next
   // indexer must wait for it before reading tile prefixes or key rows
   mutable bool append_pending = false;
+  // key_norms() at the last indexer launch: a norm launched since then may have
+  // written key rows, for which the next indexer waits in the same way
+  mutable unsigned long long norms_seen = 0;
   CUtensorMap kmap;               // keys as [B*T rows][128 B], 128x128 boxes, 128B swizzle
   // state
   int32_t* cache_slots = nullptr; // [B][T]
@@ -144,6 +148,13 @@ struct ess_pool {
 };
 
 namespace ess {
+
+// Norms of rows that can be indexer keys launched by this process so far.  They
+// belong to no pool, so each layer compares the count with its own last one.
+inline std::atomic<unsigned long long>& key_norms() {
+  static std::atomic<unsigned long long> n{0};
+  return n;
+}
 
 inline void count_launch(const ess_pool& p) {
   if (p.n_launch) ++*p.n_launch;

@@ -244,7 +244,9 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const
   constexpr int kThreads = TPR > 256 ? TPR : 256;
   constexpr int kRows = kThreads / TPR;
   pdl_wait_previous();
-  pdl_launch_dependents();
+  // Rows of up to 128 values may be bound indexer keys, and an indexer loads its
+  // first keys ahead of its own wait: nothing is launched before they are written.
+  if (TPR > 8) pdl_launch_dependents();
   const int t = threadIdx.x % TPR;
   const long long i = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / TPR;
   const bool live = i < a.n;
@@ -452,6 +454,7 @@ ess_status ess_norm_quant(const void* x, int64_t x_stride, const void* residual,
   a.scales = scales;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
+  if (dim <= 128) ++key_norms();   // the next indexer of each layer waits
   if (dim <= 128) e = launch_norm<8, 2>(a, st);
   else if (dim <= 256) e = launch_norm<16, 2>(a, st);
   else if (dim <= 512) e = launch_norm<32, 2>(a, st);

@@ -637,7 +637,8 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
  * above fl32(amax / 448) (1 for zeros, at least 2^-126), and the codes
  * e4m3(y / scale).  With dim = 128 a row is an indexer key with its key scale:
  * codes and scales are ess_append's key_row and key_scale, or rows of the bound
- * idx_keys and idx_scale for a prompt.
+ * idx_keys and idx_scale for a prompt: indexer calls that follow on the stream
+ * wait for them.
  * n = 0 launches nothing.  Pointers and strides are 16-byte aligned (scales
  * 4-byte).  Errors: ESS_ERR_INVALID_ARG for a null, misaligned or negative
  * argument, a stride below dim, residual_out without residual, or eps < 0;

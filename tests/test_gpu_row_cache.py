@@ -343,6 +343,77 @@ def test_misaligned_rows_are_refused():
         cache.write(odd, torch.zeros(2, dtype=torch.int64, device="cuda"))
 
 
+@pytest.mark.parametrize("how", ["eager", "one graph", "graph of the norm", "host step"])
+def test_an_indexer_right_behind_the_norm_that_makes_its_keys(how):
+    """A prompt's keys normed straight into the bound keys, and the indexer next on
+    the stream: it scores those keys, as one that starts after everything is done."""
+    from host_latent_cache_gb300.session import Session
+    rows = rows_mod()
+    cfg = W.v32_32k().replace(batch=2, T=32768, k=512, C=2048, mtp=1, mla_heads=16, layers=1)
+    ld = W.gen_layer(cfg)
+    sess = Session(cfg, [ld])
+    keys = sess.keys[0].view(torch.uint8).view(torch.float8_e4m3fn).view(-1, 128)
+    scale = sess.scale[0].view(-1, 1)
+    n = keys.shape[0]
+    gamma = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(21)
+    raws = [torch.randn(n, 128, generator=g, device="cuda").to(torch.bfloat16) for _ in range(4)]
+    raw = torch.empty_like(raws[0])
+    q, enc, qm = W.QueryStream(cfg).next()
+    w = W.head_weights(cfg, ld.w)
+    qd, wd, qmd = sess.device_inputs(enc, w, qm)
+    norm = lambda: rows.norm_q8(raw, gamma, codes=keys, scales=scale)
+
+    def done():                     # the scores, or the output of a step
+        torch.cuda.synchronize()
+        return (out if how == "host step" else sess.scores).clone()
+    if how == "host step":
+        host = [ess.HostBuffer(a.shape, a.dtype) for a in (enc.view(np.uint8), w, qm)]
+        for h, a in zip(host, (enc.view(np.uint8), w, qm)):
+            h.array[...] = a
+        out_host = ess.HostBuffer((2, 1, 16, 512), np.float32)
+        out = None
+
+        def index():
+            nonlocal out
+            ess.ess_pool_reset(sess.pool, 0)
+            torch.cuda.synchronize()
+            norm()
+            ess.ess_step_host(sess.pool, 0, *host, out_host)
+            torch.cuda.synchronize()
+            out = torch.from_numpy(out_host.array.copy())
+    else:
+        index = lambda: sess.scores_only(0, qd, wd)
+
+    want = []
+    for r in raws:
+        raw.copy_(r)
+        norm()
+        torch.cuda.synchronize()
+        index()
+        want.append(done())
+    assert not torch.equal(want[0], want[1])
+    graph = torch.cuda.CUDAGraph()
+    if how in ("one graph", "graph of the norm"):
+        with torch.cuda.graph(graph):
+            norm()
+            if how == "one graph":
+                sess.scores_only(0, qd, wd, torch.cuda.current_stream())
+        index()                     # the count of norms is seen again
+    for i in range(24):
+        raw.copy_(raws[i % 4])
+        torch.cuda.synchronize()
+        if how == "eager":
+            norm()
+        elif how != "host step":
+            graph.replay()
+        if how != "one graph":
+            index()
+        assert torch.equal(done(), want[i % 4]), i
+    assert sess.poll() == ess.ESS_OK
+    sess.close()
+
+
 def test_raw_rows_through_the_norms_into_a_decode_step():
     """The producers beside the step that eats them: norm_q8 makes the indexer
     key and its scale, a bf16 cache write the latent row, ess_append takes
