@@ -172,10 +172,13 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
   }
 }
 
+// rows and slots are plain pointers: the kernel may be launched while the one that
+// writes them still runs, so they are not read-only for its whole life, which is
+// what loads through __restrict__ pointers may take for granted.
 template <int FMT>
 __global__ void __launch_bounds__(kRowWarps * 32) cache_read_kernel(
-    const uint8_t* __restrict__ rows, long long n_rows, const int64_t* __restrict__ slots,
-    long long n, uint16_t* __restrict__ out, int* status) {
+    const uint8_t* rows, long long n_rows, const int64_t* slots, long long n, uint16_t* out,
+    int* status) {
   pdl_wait_previous();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;

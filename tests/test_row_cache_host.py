@@ -1,6 +1,8 @@
 """The row cache's oracle is pinned to the formats' definitions, and the C ABI
 refuses what its kernels do not take, all without a GPU."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -82,6 +84,18 @@ def test_rotation_oracle_at_far_positions():
     out = R.rotate(k, np.array([1, 1000003]), f, False)
     assert np.allclose(out[:, 0], [np.cos(1.0), np.cos(1000003.0)], atol=1e-9)
     assert np.allclose(out[:, 1], [np.sin(1.0), np.sin(1000003.0)], atol=1e-9)
+
+
+# ------------------------------------------------------------------ the sources
+
+def test_kernels_that_start_early_take_no_read_only_pointers():
+    """The row cache's kernels start while the kernel before them may still write
+    what they read; a load through a __restrict__ const pointer (or __ldg) may be
+    moved ahead of the wait for it."""
+    for name in ("ess_rows.cu", "ess_rows.cuh", "ess_mla.cu"):
+        with open(os.path.join(B.CSRC, name)) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        assert not re.search(r"__restrict__|__ldg|ld\.global\.nc", code), name
 
 
 # ------------------------------------------------------------------ refusals
