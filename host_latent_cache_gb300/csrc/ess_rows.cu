@@ -106,7 +106,11 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
     if (a.gamma) {
       SumSq s;
       s.sum<16, 32>(y);
-      const F2 r = both(s.rsqrt_mean(make_float2(1.0f / kLatent, 0.0f), a.eps));
+      float m;
+      float root = s.rsqrt_mean(make_float2(1.0f / kLatent, 0.0f), a.eps, &m);
+      if (__builtin_expect(!__all_sync(0xffffffffu, SumSq::near(m)), 0))
+        root = far_root<16, 32>(y, make_float2(1.0f / kLatent, 0.0f), a.eps, nullptr);
+      const F2 r = both(root);
 #pragma unroll
       for (int e = 0; e < 16; e += 2) {
         const F2 v = mul2(mul2(F2{y[e], y[e + 1]}, r), F2{gm[e], gm[e + 1]});
@@ -241,9 +245,12 @@ struct NormArgs {
 // four keys at once, and what is done once a row (the root, the joining of
 // sums), which bounds rows this short, is shared by them: 131072 keys in 11.6
 // us, where sixteen lanes a key took 16.0.  Two units a thread is the best for
-// long rows too (16384 x 4096 with a residual: 88 us, four units 90 us).
+// long rows too (16384 x 4096 with a residual: 88 us, four units 90 us).  The
+// resident CTAs asked for are those that fit without far_root, which is off the
+// usual path and must not cost them registers.
 template <int TPR, int UNITS, bool RES>
-__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256, TPR <= 32 ? 6 : TPR <= 256 ? 5 : 2)
+    norm_quant_kernel(const NormArgs a) {
   constexpr int kThreads = TPR > 256 ? TPR : 256;
   constexpr int kRows = kThreads / TPR;
   pdl_wait_previous();
@@ -281,8 +288,8 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const
   }
   SumSq s;
   s.template sum<UNITS * 8, (TPR < 32 ? TPR : 32)>(h);
+  __shared__ float2 part[kThreads / 32];
   if (TPR > 32) {
-    __shared__ float2 part[kThreads / 32];
     const int w = threadIdx.x >> 5;
     if ((threadIdx.x & 31) == 0) part[w] = make_float2(s.hi, s.lo);
     __syncthreads();
@@ -291,7 +298,11 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const
 #pragma unroll
     for (int q = 0; q < TPR / 32; ++q) s.merge(part[w0 + q].x, part[w0 + q].y);
   }
-  const F2 r = both(s.rsqrt_mean(a.inv_dim, a.eps));
+  float m;
+  float root = s.rsqrt_mean(a.inv_dim, a.eps, &m);
+  if (__builtin_expect(!__all_sync(0xffffffffu, SumSq::near(m)), 0))
+    root = far_root<UNITS * 8, TPR>(h, a.inv_dim, a.eps, part);
+  const F2 r = both(root);
   const int groups = (a.dim + 127) >> 7;
 #pragma unroll
   for (int u = 0; u < UNITS; ++u) {

@@ -223,14 +223,21 @@ struct SumSq {
   // addition without C takes eight.)
   template <int N, int G>
   __device__ __forceinline__ void sum(const float* x) {
+    sum_below<N, G>(x, largest<N, G>(x), 1.0f);
+  }
+  // the largest magnitude of them
+  template <int N, int G>
+  __device__ static __forceinline__ float largest(const float* x) {
     float m[4] = {fabsf(x[0]), fabsf(x[1]), fabsf(x[2]), fabsf(x[3])};
 #pragma unroll
     for (int i = 4; i < N; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(x[i]));
-    float mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-    if (G == 32)
-      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
-    else
-      mx = group_max<G>(mx);
+    const float mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    if (G == 32) return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+    return group_max<G>(mx);
+  }
+  // sum() of the values times f, none of whose products is above mx
+  template <int N, int G>
+  __device__ __forceinline__ void sum_below(const float* x, float mx, float f) {
     constexpr int kLog = N * G <= 64 ? 6 : N * G <= 128 ? 7 : N * G <= 256 ? 8 : N * G <= 512 ? 9 : 10;
     static_assert(N * G <= 1024 && N % 2 == 0 && N >= 4, "values of one sum");
     const int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;   // mx < 2^(e + 1)
@@ -239,7 +246,7 @@ struct SumSq {
     const F2 neg = both(-1.0f);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      const F2 v{x[i], x[i + 1]};
+      const F2 v{x[i] * f, x[i + 1] * f};
       const F2 u = fma2(v, v, s);
       const F2 t = fma2(s, neg, u);
       const F2 r = fma2(v, v, mul2(t, neg));
@@ -257,8 +264,10 @@ struct SumSq {
   // 1 / sqrt((hi + lo) / n + eps), 1 / n given as a pair too: the hardware's
   // reciprocal root, then one Newton step whose residual 1 - m r^2 is formed
   // from exact products, so the result is the rounded root but for a few of
-  // 2^20 cases.
-  __device__ __forceinline__ float rsqrt_mean(float2 inv_n, float eps) const {
+  // 2^20 cases.  m is mean + eps: between 2^-60 and 2^100 (near) that holds for
+  // sum()'s result, as no square came near fp32's end and none that counts was
+  // rounded as a subnormal.  Other rows take far_root.
+  __device__ __forceinline__ float rsqrt_mean(float2 inv_n, float eps, float* m) const {
     const float q = __fmul_rn(hi, inv_n.x);
     float ml = __fmaf_rn(lo, inv_n.x, __fmaf_rn(hi, inv_n.y, __fmaf_rn(hi, inv_n.x, -q)));
     const float mh = __fadd_rn(q, eps);
@@ -272,10 +281,56 @@ struct SumSq {
     const float te = __fmaf_rn(mh, r2, -t);
     const float res = __fsub_rn(__fsub_rn(__fsub_rn(__fsub_rn(1.0f, t), te), __fmul_rn(mh, r2e)),
                                 __fmul_rn(ml, r2));
-    const float r = __fmaf_rn(__fmul_rn(0.5f, r0), res, r0);
-    // a mean of zero (or one past fp32's range) has no residual: 1 / 0 and 1 / inf as they are
-    return (mh > 1.2e-38f && mh < 3.0e38f) ? r : r0;
+    *m = mh;
+    return __fmaf_rn(__fmul_rn(0.5f, r0), res, r0);
   }
+  __device__ static __forceinline__ bool near(float m) { return m >= 0x1p-60f && m < 0x1p100f; }
 };
+
+// r of rows whose mean of squares is far from 1 (or of a warp with such a row), the
+// long way: the sum is of 2^-80 or 2^80 times the values where the row's largest is
+// outside 2^+-40, so it stays below 2^111, and its mean above 2^-121.  Values of a
+// small row are multiplied themselves, as their r may be past fp32's range.  A row
+// with an infinity has r = 0, one with a NaN r = NaN.  TPR threads share a row; above
+// a warp they all come here, or none, and part is one place a warp of the block.
+template <int N, int TPR>
+__device__ __forceinline__ float far_root(float* x, float2 inv_n, float eps, float2* part) {
+  constexpr int kWarps = TPR / 32;
+  const int w = threadIdx.x >> 5, row = threadIdx.x / TPR;
+  // (barriers by number: one named by a register takes all sixteen of a CTA, and
+  // 32768 x 1024 then 28.8 us instead of 26.6)
+  auto meet = [&] {
+    if (TPR > 128 || (TPR > 32 && row == 0)) asm volatile("bar.sync 1, %0;" ::"n"(TPR) : "memory");
+    else if (TPR > 64 || (TPR > 32 && row == 1)) asm volatile("bar.sync 2, %0;" ::"n"(TPR) : "memory");
+    else if (TPR > 32 && row == 2) asm volatile("bar.sync 3, %0;" ::"n"(TPR) : "memory");
+    else if (TPR > 32) asm volatile("bar.sync 4, %0;" ::"n"(TPR) : "memory");
+  };
+  float mx = SumSq::largest<N, (TPR < 32 ? TPR : 32)>(x);
+  if (TPR > 32) {
+    meet();
+    part[w].x = mx;
+    meet();
+    for (int q = 0; q < kWarps; ++q) mx = fmaxf(mx, part[row * kWarps + q].x);
+    meet();
+  }
+  const int pow2 = mx >= 0x1p41f ? -80 : mx < 0x1p-40f && eps < 0x1p-60f ? 80 : 0;
+  const float f = exp2i(pow2);
+  if (pow2 > 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] *= f;
+  }
+  SumSq s;
+  s.sum_below<N, (TPR < 32 ? TPR : 32)>(x, mx * f, pow2 > 0 ? 1.0f : f);
+  if (TPR > 32) {
+    part[w] = make_float2(s.hi, s.lo);
+    meet();
+    s = SumSq();
+    for (int q = 0; q < kWarps; ++q) s.merge(part[row * kWarps + q].x, part[row * kWarps + q].y);
+  }
+  float m;
+  float r = s.rsqrt_mean(inv_n, eps * f * f, &m);
+  if (m == 0.0f || m == INFINITY) r = rsqrtf(m);   // 1 / 0 and 1 / inf have no residual
+  return pow2 < 0 ? r * f : r;
+}
 
 }  // namespace ess

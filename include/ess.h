@@ -557,8 +557,9 @@ enum { ESS_ROPE_ADJACENT = 0, ESS_ROPE_HALVES = 1 };
  *   rows      device [n_rows][row bytes of format], 16-byte aligned
  * Rows that no token names are left as they were.  The slots of one call are
  * distinct; of a row named twice the bytes of either token may stay.  y and
- * the rotated k^R are formed in fp32 (the mean to about 48 bits) and rounded
- * once, to the row's format.  A slot at or past n_rows writes nothing and
+ * the rotated k^R are formed in fp32 (the mean to about 48 bits, whatever the
+ * size of the values) and rounded once, to the row's format.  The mean of a row
+ * with an infinity is infinite: its finite values become 0 and the infinity NaN.  A slot at or past n_rows writes nothing and
  * reports ESS_ERR_DEVICE_CHECK in status.  n = 0 launches nothing.
  * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or negative argument, an
  * unknown format or pairs, a frequency that is not finite, or eps < 0. */
@@ -632,7 +633,7 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
  *   codes         device [n][dim] e4m3
  *   scales        device float [n][ceil(dim / 128)]
  * h = x + residual in fp32; y = h * r * gamma with r = 1 / sqrt(mean(h^2) +
- * eps), the mean to about 48 bits; each 128 values (the last group may be
+ * eps), the mean as in ess_cache_write; each 128 values (the last group may be
  * shorter) get the scale of ess_compact_rows, the smallest power of two at or
  * above fl32(amax / 448) (1 for zeros, at least 2^-126), and the codes
  * e4m3(y / scale).  With dim = 128 a row is an indexer key with its key scale:

@@ -267,6 +267,77 @@ def test_norm(dim, n, res):
         assert out is None
 
 
+def far_rows(dim, g):
+    """Rows of every size that bf16 has, and rows in which a few values are far
+    larger than all the others."""
+    power = torch.cat([torch.arange(-120, 121, device="cuda"), torch.tensor([-30, -50, -50, 20, -60], device="cuda")])
+    x = torch.randn(len(power), dim, generator=g, device="cuda", dtype=torch.float64)
+    x = (x + 0.25 * x.sign()) * torch.exp2(power.double())[:, None]   # no value far below its row's
+    x[-5, dim // 2] = 2.0 ** 60
+    x[-4, dim - 1] = 2.0 ** 30
+    x[-3, 0] = 2.0 ** 41
+    x[-2, dim - 8:] *= 2.0 ** 90
+    x[-1, dim // 2:] *= 2.0 ** 15
+    return x.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "compact", "q4"])
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-25])
+def test_written_rows_of_any_size(fmt, eps):
+    """As test_write: r and y are within their tolerance at every size."""
+    rows = rows_mod()
+    g = torch.Generator(device="cuda").manual_seed(41)
+    x = far_rows(512, g)
+    n = x.shape[0]
+    kv = torch.zeros(n, 576, dtype=torch.bfloat16, device="cuda")
+    kv[:, :512] = x
+    gamma = (0.5 + torch.rand(512, generator=g, device="cuda")).to(torch.bfloat16)
+    buf = torch.zeros(n, R.ROW_BYTES[fmt], dtype=torch.uint8, device="cuda")
+    rows.RowCache(buf, fmt).write(kv, torch.arange(n, device="cuda"), gamma=gamma, eps=eps)
+    zero = np.zeros((n, 64))
+    check_rows(buf.cpu().numpy(), fmt, R.rms_norm(f64(x), f64(gamma), eps), zero, zero)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256, 1000, 1024, 4096, 16384])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_norms_of_any_size(dim, eps):
+    rows = rows_mod()
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    x = far_rows(dim, g)
+    gamma = (0.5 + torch.rand(dim, generator=g, device="cuda")).to(torch.bfloat16)
+    codes, scales, _ = rows.norm_q8(x, gamma, eps)
+    y, _ = R.norm_quant(f64(x), f64(gamma), eps)
+    s = f64(scales)
+    check_scales(np.log2(s).astype(np.int64), y, 128, 448.0)
+    wide = np.repeat(s, 128, axis=1)[:, :dim]
+    check_codes(f64(codes) * wide, wide, y, R.E4M3)
+
+
+def test_an_infinity_and_a_nan_stay_in_their_row():
+    rows = rows_mod()
+    for dim in (128, 512, 4096):
+        x = torch.ones(6, dim, dtype=torch.bfloat16, device="cuda")
+        x[1, 5], x[2, dim - 1] = float("inf"), float("-inf")
+        x[3, 7] = float("nan")
+        x[4, 3], x[4, dim - 2] = float("inf"), float("nan")
+        gamma = torch.ones(dim, dtype=torch.bfloat16, device="cuda")
+        codes = rows.norm_q8(x, gamma)[0].float()
+        assert (codes[[0, 5]] == codes[0, 0]).all() and codes[0, 0] > 0
+        for i, at in ((1, 5), (2, dim - 1)):
+            bad = torch.zeros(dim, dtype=torch.bool, device="cuda")
+            bad[at] = True
+            assert torch.isnan(codes[i][bad]).all() and (codes[i][~bad] == 0).all()
+        assert torch.isnan(codes[3:5]).all()
+    kv = torch.ones(3, 576, dtype=torch.bfloat16, device="cuda")
+    kv[1, 100] = float("inf")
+    buf = torch.zeros(3, 1152, dtype=torch.uint8, device="cuda")
+    cache = rows.RowCache(buf, "bf16")
+    cache.write(kv, torch.arange(3, device="cuda"), gamma=torch.ones(512, dtype=torch.bfloat16, device="cuda"))
+    out = cache.read(torch.arange(3, device="cuda"))
+    assert torch.isnan(out[1, 100]) and out[1].isnan().sum() == 1 and out[1, :512].nan_to_num(0).eq(0).all()
+    assert out[0].eq(out[2]).all() and not out[0].isnan().any()
+
+
 def test_norm_in_place_and_rows_apart():
     rows = rows_mod()
     g = torch.Generator(device="cuda").manual_seed(9)
