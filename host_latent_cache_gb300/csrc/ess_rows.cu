@@ -26,9 +26,25 @@ constexpr int kWriteCtas = 152 * 3;   // writing CTAs at most: one wave
 
 struct RopeFreq {
   // turns per position as a binary fraction of 2^64: position * fraction
-  // modulo 2^64 is the angle, exact at any position, with no range reduction
+  // modulo 2^64 is the angle, off by the fraction's own error times the
+  // position (2^-33 of a turn at 2^31), with no range reduction
   unsigned long long f[32];
 };
+
+// x modulo 1 as a binary fraction of 2^64
+unsigned long long binary_fraction(double x) {
+  const double a = std::fabs(x);
+  const unsigned long long u =
+      static_cast<unsigned long long>(std::rint((a - std::floor(a)) * 18446744073709551616.0));
+  return x < 0 ? 0 - u : u;
+}
+// The turns of an angle in radians, modulo 1, to 2^-64 (up to 2^40 radians): 1 / (2 pi)
+// and the product are sums of two doubles.
+unsigned long long turns_of(double radians) {
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+  const double p = radians * kHi;
+  return binary_fraction(p) + binary_fraction(std::fma(radians, kHi, -p) + radians * kLo);
+}
 
 struct WriteArgs {
   const uint16_t* kv;
@@ -372,12 +388,7 @@ ess_status ess_cache_write(const void* kv, int64_t kv_stride, int64_t n, const v
   if (inv_freq) {
     for (int i = 0; i < 32; ++i) {
       if (!std::isfinite(inv_freq[i])) return ESS_ERR_INVALID_ARG;
-      // radians -> turns in [0, 1) -> a 64-bit binary fraction
-      const double turns = inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
-      const double hi = (turns - std::floor(turns)) * 4294967296.0;
-      const unsigned long long whole = static_cast<unsigned long long>(hi);
-      fr.f[i] = (whole << 32) +
-                static_cast<unsigned long long>((hi - static_cast<double>(whole)) * 4294967296.0);
+      fr.f[i] = turns_of(inv_freq[i]);
     }
   }
   if (n == 0) return ESS_OK;

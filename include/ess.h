@@ -548,8 +548,9 @@ enum { ESS_ROPE_ADJACENT = 0, ESS_ROPE_HALVES = 1 };
  *             r = 1 / sqrt(mean(x^2) + eps) over the 512; NULL: y = x
  *   inv_freq  host double [32], radians per position of each of the 32
  *             pairs, read before the call returns: pair i turns by
- *             pos * inv_freq[i] (kept to 2^-32 of a turn at any position);
- *             NULL: k^R as it is (pos is then ignored and may be NULL)
+ *             pos * inv_freq[i], kept to 2^-31 of a turn at any position for
+ *             frequencies up to 2^40; NULL: k^R as it is (pos is then
+ *             ignored and may be NULL)
  *   pos       device int32 [n]
  *   pairs     ESS_ROPE_ADJACENT or ESS_ROPE_HALVES
  *   slots     device int64 [n]: the cache row of each token (page * page size
@@ -558,9 +559,11 @@ enum { ESS_ROPE_ADJACENT = 0, ESS_ROPE_HALVES = 1 };
  * Rows that no token names are left as they were.  The slots of one call are
  * distinct; of a row named twice the bytes of either token may stay.  y and
  * the rotated k^R are formed in fp32 (the mean to about 48 bits, whatever the
- * size of the values) and rounded once, to the row's format.  The mean of a row
- * with an infinity is infinite: its finite values become 0 and the infinity NaN.  A slot at or past n_rows writes nothing and
- * reports ESS_ERR_DEVICE_CHECK in status.  n = 0 launches nothing.
+ * size of the values) and rounded once, to the row's format; the sine and
+ * cosine move either value of a pair (a, b) by at most 2^-20 (|a| + |b|) before
+ * that.  The mean of a row with an infinity is infinite: its finite values become
+ * 0 and the infinity NaN.  A slot at or past n_rows writes nothing and reports
+ * ESS_ERR_DEVICE_CHECK in status.  n = 0 launches nothing.
  * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or negative argument, an
  * unknown format or pairs, a frequency that is not finite, or eps < 0. */
 ess_status ess_cache_write(const void* kv, int64_t kv_stride, int64_t n, const void* gamma,

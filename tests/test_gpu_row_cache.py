@@ -142,6 +142,38 @@ def test_frequencies_that_change_in_place():
     assert torch.equal(got, cache.rows)
 
 
+@pytest.mark.parametrize("pairs", ["adjacent", "halves"])
+def test_angles_of_far_positions(pairs):
+    """Positions up to 2^31 under frequencies up to 1000 and below 0, against angles
+    reduced in 70 decimal digits.  Angles near a quarter turn make values near 0,
+    where only the rotation's own error is left."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 70
+    turn = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+    rows = rows_mod()
+    g = torch.Generator(device="cuda").manual_seed(51)
+    freq = [1000.0 ** (1 - i / 12) * (-1) ** (i % 3) for i in range(32)]
+    pos = torch.cat([2 ** 31 - 1 - torch.randint(0, 1 << 20, (200,), generator=g, device="cuda"),
+                     torch.randint(-2 ** 31, 2 ** 31, (200,), generator=g, device="cuda")]).int()
+    kv = make_rows(400, g)
+    kv[::2, 512:] = 0                    # pairs (1, 0)
+    one = slice(512, 576, 2) if pairs == "adjacent" else slice(512, 544)
+    kv[::2, one] = 1
+    buf = torch.zeros(400, 1152, dtype=torch.uint8, device="cuda")
+    rows.RowCache(buf, "bf16").write(kv, torch.arange(400, device="cuda"), pos=pos, inv_freq=freq, pairs=pairs)
+    f = [Decimal(x) for x in freq]
+    angle = np.array([[float((int(p) * x) % turn) for x in f] for p in pos.cpu().tolist()])
+    z = np.cos(angle) + 1j * np.sin(angle)
+    k = f64(kv)[:, 512:]
+    a, b = (k[:, 0::2], k[:, 1::2]) if pairs == "adjacent" else (k[:, :32], k[:, 32:])
+    out = (a + 1j * b) * z
+    got = R.row_values(buf.cpu().numpy(), "bf16")[:, 512:]
+    ga, gb = (got[:, 0::2], got[:, 1::2]) if pairs == "adjacent" else (got[:, :32], got[:, 32:])
+    slack = 2.0 ** -20 * (np.abs(a) + np.abs(b))
+    assert (np.abs(ga - out.real) <= BF16_HALF * np.abs(out.real) + slack).all()
+    assert (np.abs(gb - out.imag) <= BF16_HALF * np.abs(out.imag) + slack).all()
+
+
 def test_compact_rows_are_those_of_the_host_encoder():
     rows = rows_mod()
     g = torch.Generator(device="cuda").manual_seed(5)
