@@ -109,6 +109,9 @@ class RowCache:
         self._index = rows.get_device()
         _check(rows, "rows", torch.uint8, (self.n_rows, ess.ess_row_bytes(self._f)), self._index)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        with _OnDevice(self._index):
+            if not torch._C._cuda_isCurrentStreamCapturing():
+                torch.cuda.current_stream().synchronize()   # any stream may use it from here on
         self._freq = (None, None)
         self._ws = {}       # by stream: the largest workspace a call on it needed
         self._bytes = {}    # by shape

@@ -255,6 +255,27 @@ def test_slots_past_the_cache_are_reported_and_skipped():
     assert not out.any()
 
 
+def test_a_new_cache_may_be_used_on_any_stream():
+    """The status word is clear before the constructor returns, whatever the
+    stream it ran on still has to do."""
+    rows = rows_mod()
+    kv = torch.ones(1, 576, dtype=torch.bfloat16, device="cuda")
+    slots = torch.tensor([99], device="cuda")
+    buf = torch.zeros(10, 400, dtype=torch.uint8, device="cuda")
+    big = torch.ones(8192, 8192, dtype=torch.bfloat16, device="cuda")
+    out = big @ big
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        torch.mm(big, big, out=out)
+    cache = rows.RowCache(buf, "q4")
+    with torch.cuda.stream(side):
+        cache.write(kv, slots)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert cache.poll() == ess.ESS_ERR_DEVICE_CHECK
+
+
 def test_offsets_past_32_bits():
     rows = rows_mod()
     n_rows = (5 << 30) // 400        # a cache of 5 GiB
