@@ -240,6 +240,11 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_read_kernel(
   if (lane < 8) o[64 + lane] = rope;
 }
 
+__global__ void status_take_kernel(int* status, int* taken) {
+  pdl_wait_previous();
+  *taken = atomicExch(status, ESS_OK);
+}
+
 struct NormArgs {
   const uint16_t* x;
   long long x_stride;
@@ -374,6 +379,15 @@ ess_status ess_row_bytes(int32_t format, int32_t* bytes) {
   if (!bytes || format < ESS_ROW_BF16 || format > ESS_ROW_Q4) return ESS_ERR_INVALID_ARG;
   *bytes = row_bytes_of(format);
   return ESS_OK;
+}
+
+ess_status ess_status_take(int32_t* status, int32_t* taken, ess_stream_t stream) {
+  if (!status || !taken || !aligned_to(status, 4) || !aligned_to(taken, 4))
+    return ESS_ERR_INVALID_ARG;
+  return launch_pdl_once(status_take_kernel, dim3(1), dim3(1), 0,
+                         static_cast<cudaStream_t>(stream), status, taken) == cudaSuccess
+             ? ESS_OK
+             : ESS_ERR_CUDA;
 }
 
 ess_status ess_cache_write(const void* kv, int64_t kv_stride, int64_t n, const void* gamma,

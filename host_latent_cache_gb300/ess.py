@@ -44,7 +44,8 @@ EXPORTS = (
     "ess_pipeline_step", "ess_pool_get_state", "ess_pool_set_state", "ess_pool_get_rows",
     "ess_pool_read_stats", "ess_pool_poll", "ess_pool_kernel_launches", "ess_prefill_plan",
     "ess_compact_rows", "ess_replay_misses", "ess_host_gather", "ess_pool_set_eviction",
-    "ess_pool_bind_layer_compact", "ess_prefill_run", "ess_row_bytes", "ess_cache_write",
+    "ess_pool_bind_layer_compact", "ess_prefill_run", "ess_row_bytes", "ess_status_take",
+    "ess_cache_write",
     "ess_cache_read", "ess_cache_mla_bytes", "ess_cache_mla", "ess_norm_quant",
 )
 
@@ -128,6 +129,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "ess_prefill_run": [I, P, I, I, P, ctypes.c_size_t, ctypes.c_size_t, ctypes.c_size_t, P,
                             PREFILL_COMPUTE_FN, P, P, P, P],
         "ess_row_bytes": [I, ctypes.POINTER(ctypes.c_int32)],
+        "ess_status_take": [P, P, P],
         "ess_cache_write": [P, L, L, P, F, P, P, I, P, P, L, I, P, P],
         "ess_cache_read": [P, L, I, P, L, P, P, P],
         "ess_cache_mla_bytes": [I, I, I, ctypes.POINTER(ctypes.c_size_t)],
@@ -428,6 +430,10 @@ def ess_row_bytes(fmt: int) -> int:
     n = ctypes.c_int32(0)
     check(load().ess_row_bytes(int(fmt), ctypes.byref(n)), "ess_row_bytes")
     return n.value
+
+
+def ess_status_take(status, taken, stream=None) -> None:
+    check(load().ess_status_take(_p(status), _p(taken), _stream(stream)), "ess_status_take")
 
 
 def ess_cache_write(kv, kv_stride: int, n: int, gamma, eps: float, inv_freq, pos, pairs: int,

@@ -118,10 +118,13 @@ class RowCache:
         self._lock = threading.Lock()
 
     def poll(self) -> int:
-        """The first device-side error since the last poll (synchronous), cleared."""
-        code = int(self.status.item())
-        self.status.zero_()
-        return code
+        """The first device-side error that is there, cleared.  Waits for the calls on
+        the current stream; what a call that still runs on another stream reports
+        is kept for a later poll."""
+        with _OnDevice(self._index) as stream:
+            taken = torch.empty(1, dtype=torch.int32, device=self.device)
+            ess.ess_status_take(self.status, taken, stream)
+            return int(taken.item())
 
     def _freqs(self, inv_freq: Sequence[float]):
         key = tuple(map(float, inv_freq))   # numbers: a tensor's entries may change later

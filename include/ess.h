@@ -524,18 +524,26 @@ ess_status ess_prefill_run(int32_t n_layers, const int32_t* onload_layer_map, in
  *                   every value is exact in fp16 as in bf16; a value's code
  *                   is e2m1(x / scale), nearest with ties to the even code,
  *                   saturating at +-6.  The format has no infinity and no
- *                   NaN: an infinity saturates and a NaN becomes 6 * scale.
+ *                   NaN: an infinity saturates, in a block of scale 1, and a
+ *                   NaN becomes 6 * scale.
  *                   Exponent bytes outside 104..140 are read as the nearest
  *                   of the two.
  *
  * status is a device int32, or NULL: the first device-side error of the calls
- * that share it is put there when it holds ESS_OK; the caller clears it.
+ * that share it is put there when it holds ESS_OK; the caller clears it before
+ * their first use, and with ess_status_take afterwards.
  * Pointers whose alignment is not given have that of their type. */
 enum { ESS_ROW_BF16 = 0, ESS_ROW_COMPACT = 1, ESS_ROW_Q4 = 2 };
 
 /* Bytes of one row of a format (a multiple of 16).
  * Errors: ESS_ERR_INVALID_ARG for an unknown format. */
 ess_status ess_row_bytes(int32_t format, int32_t* bytes);
+
+/* Move the error in status to *taken (device int32) and put ESS_OK in its place, in one
+ * exchange: an error that a call on another stream reports meanwhile is either
+ * taken or stays.  Asynchronous on stream: the calls before it on stream are done.
+ * Errors: ESS_ERR_INVALID_ARG for a null or misaligned argument. */
+ess_status ess_status_take(int32_t* status, int32_t* taken, ess_stream_t stream);
 
 /* Which of the 64 RoPE values turn together: (2i, 2i + 1) or (i, i + 32). */
 enum { ESS_ROPE_ADJACENT = 0, ESS_ROPE_HALVES = 1 };

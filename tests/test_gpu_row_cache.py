@@ -255,6 +255,29 @@ def test_slots_past_the_cache_are_reported_and_skipped():
     assert not out.any()
 
 
+def test_errors_on_another_stream_are_kept():
+    """An error that lands while a poll on another stream runs is that poll's or the
+    next one's."""
+    rows = rows_mod()
+    cache = rows.RowCache(torch.zeros(10, 400, dtype=torch.uint8, device="cuda"), "q4")
+    kv = torch.ones(1, 576, dtype=torch.bfloat16, device="cuda")
+    slots = torch.tensor([99], device="cuda")
+    side = torch.cuda.Stream()
+    busy = torch.ones(4000, 4000, dtype=torch.bfloat16, device="cuda")
+    out = busy @ busy
+    torch.cuda.synchronize()
+    for i in range(600):
+        n = 520 + 168 * (i % 20)                    # 3 to 60 us ahead of the write
+        with torch.cuda.stream(side):
+            torch.mm(busy[:n, :n], busy[:n, :n], out=out[:n, :n])
+            cache.write(kv, slots)
+        first = cache.poll()
+        side.synchronize()
+        second = cache.poll()
+        assert ess.ESS_ERR_DEVICE_CHECK in (first, second), i
+        assert cache.poll() == ess.ESS_OK
+
+
 def test_a_new_cache_may_be_used_on_any_stream():
     """The status word is clear before the constructor returns, whatever the
     stream it ran on still has to do."""

@@ -112,6 +112,12 @@ def test_row_bytes(lib):
     assert lib.ess_row_bytes(0, None) == ess.ESS_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("status,taken", [(None, A16), (A16, None), (P((1 << 20) + 2), A16),
+                                          (A16, P((1 << 20) + 2))])
+def test_status_take_refusals(lib, status, taken):
+    assert lib.ess_status_take(status, taken, None) == ess.ESS_ERR_INVALID_ARG
+
+
 WRITE = dict(kv=A16, stride=576, n=4, gamma=A16, eps=1e-6, freq=FREQ, pos=A16, pairs=0, slots=A16,
              rows=A16, n_rows=64, fmt=2)
 
