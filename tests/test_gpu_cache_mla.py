@@ -384,6 +384,31 @@ def test_two_streams_beside_one_another():
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
 
 
+def test_one_cache_on_two_streams():
+    """Calls on one cache beside one another, with other queries and lengths, both
+    long enough that their outputs go through the workspace."""
+    c = Case(31, [6000, 5000, 7000], 1, 128)
+    q2, T2 = c.q.roll(1, 2), c.T.flip(0).contiguous()
+    table2 = c.dev_table.flip(0).contiguous()
+    calls = [lambda: c.cache.attend(c.q, c.dev_table, c.T, c.scale),
+             lambda: c.cache.attend(q2, table2, T2, c.scale)]
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    assert not torch.equal(want[0][0], want[1][0])
+    before = len(c.cache._ws)
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[], []]
+    for _ in range(40):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(calls[i]())
+    torch.cuda.synchronize()
+    assert len(c.cache._ws) == before + 2
+    for w, results in zip(want, got):
+        for out, lse in results:
+            assert torch.equal(out, w[0]) and torch.equal(lse, w[1])
+
+
 def test_arguments_are_refused():
     c = Case(16, [50], 1, 4)
     ok = dict(q=c.q, page_table=c.dev_table, T=c.T, sm_scale=c.scale)
