@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import threading
+import weakref
 from typing import Optional, Sequence
 
 import torch
@@ -91,6 +92,32 @@ class _OnDevice:
         return False
 
 
+class _Workspace:
+    """What the eager calls on one stream of a device share, whichever cache makes
+    them: the largest workspace any of them needed, and a lock that keeps a call's
+    two launches together on the stream."""
+
+    __slots__ = ("buf", "lock", "__weakref__")
+
+    def __init__(self):
+        self.buf = None
+        self.lock = threading.Lock()
+
+
+_workspaces = weakref.WeakValueDictionary()   # (device index, stream): as long as a cache uses it
+_workspaces_lock = threading.Lock()
+
+
+def release_workspaces() -> None:
+    """Give up the workspaces that caches keep for their streams; the next call on
+    a stream takes a new one."""
+    with _workspaces_lock:
+        kept = list(_workspaces.values())
+    for ws in kept:
+        with ws.lock:
+            ws.buf = None
+
+
 class RowCache:
     """A caller's tensor of cache rows, uint8 [n_rows][row bytes], with the
     calls on it.  `status` is a device int32 that keeps the first device-side
@@ -113,9 +140,8 @@ class RowCache:
             if not torch._C._cuda_isCurrentStreamCapturing():
                 torch.cuda.current_stream().synchronize()   # any stream may use it from here on
         self._freq = (None, None)
-        self._ws = {}       # by stream: the largest workspace a call on it needed
+        self._ws = {}       # by stream, shared with the other caches that run on it
         self._bytes = {}    # by shape
-        self._lock = threading.Lock()
 
     def poll(self) -> int:
         """The first device-side error that is there, cleared.  Waits for the calls on
@@ -187,10 +213,10 @@ class RowCache:
         of each request (page_table int32 [batch][max_pages], T int32
         [batch]), or over tokens int32 [batch][ways][k].  Returns (out bf16
         [batch][ways][heads][512], lse float32 [batch][ways][heads]).  Without
-        `workspace` the cache keeps one for each current stream, and a captured
-        call takes one from its graph's memory.  Threads may call it at once
-        without `workspace`; calls that are given one are ordered by the
-        caller."""
+        `workspace` all caches keep one for each current stream (see
+        `release_workspaces`), and a captured call takes one from its graph's
+        memory.  Threads may call it at once without `workspace`; calls that are
+        given one are ordered by the caller."""
         at = self._index
         _need(isinstance(q, torch.Tensor) and q.dim() == 4, "q: [batch][ways][heads][576] is needed")
         batch, ways, heads, _ = q.shape
@@ -223,23 +249,31 @@ class RowCache:
                 if torch._C._cuda_isCurrentStreamCapturing():
                     workspace = self.workspace(batch, ways, heads)
                 else:
-                    # one call's two launches stay together on the stream
-                    with self._lock:
+                    kept = self._ws.get(stream) or self._share(stream)
+                    with kept.lock:
                         self._attend(q, page_table, max_pages, T, batch, ways, heads, tokens, k,
-                                     sm_scale, out, lse, self._kept(stream, batch, ways, heads), stream)
+                                     sm_scale, out, lse, self._enough(kept, batch, ways, heads),
+                                     stream)
                     return out, lse
             self._attend(q, page_table, max_pages, T, batch, ways, heads, tokens, k, sm_scale, out,
                          lse, workspace, stream)
         return out, lse
 
-    def _kept(self, stream: int, batch: int, ways: int, heads: int) -> torch.Tensor:
+    def _share(self, stream: int) -> _Workspace:
+        with _workspaces_lock:
+            kept = _workspaces.get((self._index, stream))
+            if kept is None:
+                kept = _workspaces[self._index, stream] = _Workspace()
+            self._ws[stream] = kept
+        return kept
+
+    def _enough(self, kept: _Workspace, batch: int, ways: int, heads: int) -> torch.Tensor:
         need = self._bytes.get((batch, ways, heads))
         if need is None:
             need = self._bytes[batch, ways, heads] = ess.ess_cache_mla_bytes(batch, ways, heads)
-        ws = self._ws.get(stream)
-        if ws is None or ws.numel() < need:
-            ws = self._ws[stream] = self.workspace(batch, ways, heads)
-        return ws
+        if kept.buf is None or kept.buf.numel() < need:
+            kept.buf = self.workspace(batch, ways, heads)
+        return kept.buf
 
     def _attend(self, q, page_table, max_pages, T, batch, ways, heads, tokens, k, sm_scale, out,
                 lse, workspace, stream) -> None:

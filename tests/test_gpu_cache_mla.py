@@ -481,6 +481,58 @@ def test_one_workspace_serves_every_batch():
     assert len(c.cache._ws) == 1
 
 
+def test_caches_on_one_stream_share_a_workspace():
+    """A model's layers hold one workspace between them, and give it up together."""
+    import gc
+    from host_latent_cache_gb300 import rows
+    from host_latent_cache_gb300.rows import RowCache
+    gc.collect()
+    rows.release_workspaces()
+    cases = [Case(60 + i, [5000 - 900 * i, 300], 1, 128) for i in range(3)]
+    want = [c.attend(workspace=c.cache.workspace(2, 1, 128)) for c in cases]
+    size = cases[0].cache.workspace(2, 1, 128).numel()
+    layers = [(c, RowCache(c.cache.rows, "q4")) for c in cases for _ in range(8)]
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    got = [layer.attend(c.q, c.dev_table, c.T, c.scale) for c, layer in layers]
+    outs = sum(o.untyped_storage().nbytes() + l.untyped_storage().nbytes() for o, l in got)
+    used = torch.cuda.memory_allocated() - before
+    assert size <= used < outs + 2 * size
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, want[i // 8][0]) and torch.equal(lse, want[i // 8][1])
+    rows.release_workspaces()
+    assert torch.cuda.memory_allocated() - before <= used - size
+    again = layers[0][1].attend(cases[0].q, cases[0].dev_table, cases[0].T, cases[0].scale)
+    assert torch.equal(again[0], want[0][0])
+    del got, again
+    del layers
+    gc.collect()
+    assert torch.cuda.memory_allocated() < before + size     # it goes with the last cache
+
+
+def test_threads_with_a_cache_each():
+    """Threads on one stream, each with a cache of its own, share that stream's
+    workspace and not one another's partials."""
+    import threading
+    cases = [Case(70 + i, [5000 - 1000 * i, 900], 1, 128) for i in range(3)]
+    want = [c.attend() for c in cases]
+    got = [[] for _ in cases]
+
+    def run(i):
+        for _ in range(30):
+            got[i].append(cases[i].attend())
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert len(g) == 30
+        for out, lse in g:
+            assert torch.equal(out, w[0]) and torch.equal(lse, w[1])
+
+
 def test_workspaces_are_refused():
     c = Case(25, [50], 1, 4)
     ws = c.cache.workspace(1, 1, 4)
