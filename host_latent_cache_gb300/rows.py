@@ -216,7 +216,8 @@ class RowCache:
         `workspace` all caches keep one for each current stream (see
         `release_workspaces`), and a captured call takes one from its graph's
         memory.  Threads may call it at once without `workspace`; calls that are
-        given one are ordered by the caller."""
+        given one are ordered by the caller.  An empty batch, list (k = 0) or page
+        table is taken: queries without a token get zeros and lse = -infinity."""
         at = self._index
         _need(isinstance(q, torch.Tensor) and q.dim() == 4, "q: [batch][ways][heads][576] is needed")
         batch, ways, heads, _ = q.shape
@@ -244,6 +245,15 @@ class RowCache:
             _need(_is(workspace, torch.uint8, (workspace.numel(),), at)
                   if isinstance(workspace, torch.Tensor) else False,
                   f"workspace: contiguous uint8 [bytes] on cuda:{at} is needed")
+        if batch == 0:
+            return out, lse
+        page = self.page
+        if k == 0 and tokens is not None:      # as a list that holds nothing
+            k = 1
+            tokens = torch.full((batch, ways, 1), -1, dtype=_I32, device=self.device)
+        if max_pages == 0:                     # as one page that is not there
+            max_pages = page = 1
+            page_table = torch.full((batch, 1), -1, dtype=_I32, device=self.device)
         with _OnDevice(at) as stream:
             if workspace is None:
                 if torch._C._cuda_isCurrentStreamCapturing():
@@ -251,12 +261,12 @@ class RowCache:
                 else:
                     kept = self._ws.get(stream) or self._share(stream)
                     with kept.lock:
-                        self._attend(q, page_table, max_pages, T, batch, ways, heads, tokens, k,
-                                     sm_scale, out, lse, self._enough(kept, batch, ways, heads),
-                                     stream)
+                        self._attend(q, page_table, max_pages, page, T, batch, ways, heads,
+                                     tokens, k, sm_scale, out, lse,
+                                     self._enough(kept, batch, ways, heads), stream)
                     return out, lse
-            self._attend(q, page_table, max_pages, T, batch, ways, heads, tokens, k, sm_scale, out,
-                         lse, workspace, stream)
+            self._attend(q, page_table, max_pages, page, T, batch, ways, heads, tokens, k, sm_scale,
+                         out, lse, workspace, stream)
         return out, lse
 
     def _share(self, stream: int) -> _Workspace:
@@ -275,9 +285,9 @@ class RowCache:
             kept.buf = self.workspace(batch, ways, heads)
         return kept.buf
 
-    def _attend(self, q, page_table, max_pages, T, batch, ways, heads, tokens, k, sm_scale, out,
-                lse, workspace, stream) -> None:
-        ess.ess_cache_mla(q, self.rows, self.n_rows, self._f, page_table, max_pages, self.page, T,
+    def _attend(self, q, page_table, max_pages, page, T, batch, ways, heads, tokens, k, sm_scale,
+                out, lse, workspace, stream) -> None:
+        ess.ess_cache_mla(q, self.rows, self.n_rows, self._f, page_table, max_pages, page, T,
                           batch, ways, heads, tokens, k, sm_scale, out, lse, workspace,
                           workspace.numel(), self.status, stream)
 

@@ -427,6 +427,25 @@ def test_arguments_are_refused():
         RowCache(torch.zeros(64, 656, dtype=torch.uint8, device="cuda"), "compact").attend(**ok)
 
 
+def test_empty_batches_lists_and_tables():
+    c = Case(32, [70, 3], 2, 16)
+    out, lse = c.cache.attend(c.q[:0], c.dev_table[:0], c.T[:0], c.scale)
+    assert out.shape == (0, 2, 16, 512) and lse.shape == (0, 2, 16)
+    empty = torch.empty(0, 2, 7, dtype=torch.int32, device="cuda")
+    assert c.cache.attend(c.q[:0], c.dev_table[:0], c.T[:0], c.scale, tokens=empty)[0].numel() == 0
+    none = np.zeros((2, 2, 0), dtype=np.int32)
+    c.check(*c.attend(none), none)
+    got = torch.full_like(c.q[..., :512], 7).contiguous()
+    c.lens = [0, 0]
+    c.T.zero_()
+    c.check(*c.cache.attend(c.q, c.dev_table[:, :0].contiguous(), c.T, c.scale, out=got))
+    assert not got.any() and c.cache.poll() == ess.ESS_OK
+    c.T[1] = 5                                      # a token, and no page for it
+    out, lse = c.cache.attend(c.q, c.dev_table[:, :0].contiguous(), c.T, c.scale)
+    assert c.cache.poll() == ess.ESS_ERR_DEVICE_CHECK
+    assert not out.any() and (lse == -float("inf")).all()
+
+
 def test_threads_at_once():
     """Threads that share the cache and its stream, each with its own request."""
     import threading
