@@ -25,6 +25,7 @@ FORMATS = {"bf16": ess.ESS_ROW_BF16, "compact": ess.ESS_ROW_COMPACT, "q4": ess.E
 PAIRS = {"adjacent": ess.ESS_ROPE_ADJACENT, "halves": ess.ESS_ROPE_HALVES}
 LATENT, ROPE, ROW = 512, 64, 576
 TILE = 128   # values per scale of norm_q8
+MOST = (1 << 31) - 1   # of a size that the C calls take as int32
 
 
 _BF16, _I32, _I64 = torch.bfloat16, torch.int32, torch.int64
@@ -125,7 +126,7 @@ class RowCache:
 
     def __init__(self, rows: torch.Tensor, fmt: str, page: int = 64):
         _need(fmt in FORMATS, f"format {fmt!r} is none of {', '.join(FORMATS)}")
-        _need(page >= 1, "a page has at least one row")
+        _need(1 <= page <= MOST, "a page has at least one row, and no more than 2^31 - 1")
         self.fmt, self.page = fmt, int(page)
         self._f = FORMATS[fmt]
         _need(isinstance(rows, torch.Tensor) and rows.is_cuda and rows.dim() == 2,
@@ -233,6 +234,7 @@ class RowCache:
                   "tokens: [batch][ways][k] is needed")
             k = tokens.shape[2]
             _check(tokens, "tokens", _I32, (batch, ways, k), at)
+        _need(max_pages <= MOST and k <= MOST, "more than 2^31 - 1 pages or listed tokens")
         if out is None:
             out = torch.empty((batch, ways, heads, LATENT), dtype=_BF16, device=self.device)
         else:
@@ -302,6 +304,7 @@ def norm_q8(x, gamma, eps: float = 1e-6, residual=None, residual_out=None, codes
           "x: a CUDA tensor [n][dim] is needed")
     n, dim = x.shape
     at = x.get_device()
+    _need(dim <= MOST, "more than 2^31 - 1 values a row")
     _check_rows(x, "x", _BF16, (n, dim), at)
     _check(gamma, "gamma", _BF16, (dim,), at)
     r_stride = 0

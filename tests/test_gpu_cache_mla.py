@@ -446,6 +446,20 @@ def test_empty_batches_lists_and_tables():
     assert not out.any() and (lse == -float("inf")).all()
 
 
+def test_sizes_past_32_bits_are_refused():
+    """Not taken modulo 2^32: a list of 2^32 + 5 entries is not one of five."""
+    from host_latent_cache_gb300 import rows
+    c = Case(33, [50], 1, 4)
+    tok = torch.empty(1, 1, (1 << 32) + 5, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        c.cache.attend(c.q, c.dev_table, c.T, c.scale, tokens=tok)
+    with pytest.raises(ValueError):
+        c.cache.attend(c.q, tok[0], c.T, c.scale)
+    wide = tok.view(torch.bfloat16)[0, :, :(1 << 32) + 128]
+    with pytest.raises(ValueError):
+        rows.norm_q8(wide, wide[0])
+
+
 def test_threads_at_once():
     """Threads that share the cache and its stream, each with its own request."""
     import threading

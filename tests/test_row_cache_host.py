@@ -118,6 +118,13 @@ def test_status_take_refusals(lib, status, taken):
     assert lib.ess_status_take(status, taken, None) == ess.ESS_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("page", [0, -1, 1 << 31, (1 << 32) + 64])
+def test_pages_past_32_bits_are_refused(page):
+    from host_latent_cache_gb300 import rows
+    with pytest.raises(ValueError, match="a page has"):
+        rows.RowCache(None, "q4", page=page)
+
+
 WRITE = dict(kv=A16, stride=576, n=4, gamma=A16, eps=1e-6, freq=FREQ, pos=A16, pairs=0, slots=A16,
              rows=A16, n_rows=64, fmt=2)
 
