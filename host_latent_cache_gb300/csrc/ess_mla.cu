@@ -49,6 +49,7 @@
 // joins.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstddef>
 
@@ -691,8 +692,8 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       // this one's P, so two places and two barriers are enough.
       wait_or_abort(&mi->q_here[seg & 1], (seg >> 1) & 1, mi, a.status);
       // at least 2^-126: |s| < 2^41 then still weighs less than half a step of
-      // 1 apart, and 0 * infinity does not arise
-      c2 = fmaxf(a.c2 * exp2i(mi->qexp[seg & 1][r]), 0x1p-126f);
+      // 1 apart, and 0 * infinity does not arise; finite, for the same reason
+      c2 = fminf(fmaxf(a.c2 * exp2i(mi->qexp[seg & 1][r]), 0x1p-126f), FLT_MAX);
       m = -INFINITY;
       l = 0.0f;
       seg_first_tile = it.tile;
@@ -1200,7 +1201,7 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
   a.entries = tokens ? batch * ways : batch;
   a.entry_rows = tokens ? heads : ways * heads;
   a.row_tiles = (a.entry_rows + kPairRows - 1) / kPairRows;
-  a.c2 = sm_scale * 1.4426950408889634f;
+  a.c2 = std::min(sm_scale * 1.4426950408889634f, FLT_MAX);
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   char* ws = static_cast<char*>(workspace);

@@ -616,7 +616,7 @@ ess_status ess_cache_mla_bytes(int32_t batch, int32_t ways, int32_t heads, size_
  *   workspace  device, 256-byte aligned, at least ess_cache_mla_bytes; calls
  *              that share one are ordered by the caller
  * A query that attends to nothing gets zeros and lse = -infinity.  Scores,
- * softmax and sums are fp32.  A query row's latent part goes into the first
+ * softmax and sums are fp32: a query whose scores pass its range gets NaN.  A query row's latent part goes into the first
  * product as fp16 after division by a power of two that brings the row's largest
  * value to [2^14, 2^15): exact for values down to 2^-31 of that one, off by less
  * than 2^-39 of it below.  The softmax numerators go into the second product as

@@ -357,6 +357,28 @@ def test_scales_far_below_one():
     c.check(out, lse)
 
 
+def test_scales_far_above_one():
+    """A scale near fp32's end, alone or with a row's power of two: scores of 0 still
+    weigh every token the same."""
+    c = Case(34, [300, 3], 2, 16)
+    c.q[:, :, ::2] = 0
+    for scale, q in ((3e38, None), (2.0 ** 100, 2.0 ** 60)):
+        if q:                                       # c2 past the range; rows orthogonal to the tokens
+            c.q.zero_()
+            c.q[:, :, ::2, 575] = q
+            c.raw[:, 398:400] = 0
+            c.cache.rows.copy_(torch.from_numpy(c.raw))
+        out, lse = c.cache.attend(c.q, c.dev_table, c.T, scale)
+        for b, T in enumerate(c.lens):
+            for m in range(2):
+                n = T - 1 + m
+                v = torch.from_numpy(c.rows_of(b, np.arange(n))[:, :512])
+                want, size = v.mean(0), v.abs().mean(0)
+                got = out[b, m, ::2].double().cpu()
+                assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -18) * size).all()
+                assert ((lse[b, m, ::2].double().cpu() - np.log(n)).abs() <= 2.0 ** -20 * (1 + np.log(n))).all()
+
+
 def test_short_requests_with_queries_of_many_scales():
     """Requests of one tile each, several to a pair: each one's row scales
     follow those of the one before at once."""
