@@ -634,3 +634,52 @@ def test_written_rows_are_attended_and_read():
             assert ((out[b, 0].double() - want).abs() <= tol).all()
             assert ((lse[b, 0].double() - torch.logsumexp(z, 1)).abs() <= dz[:, 0] + 2.0 ** -16).all()
     assert cache.poll() == ess.ESS_OK
+
+
+@pytest.mark.parametrize("mtp,lens", [(1, [3000, 130, 2048]), (2, [700, 2, 2900])])
+def test_attention_over_the_indexers_list(mtp, lens):
+    """The indexer's selection straight into the attention over a 4-bit copy of the
+    same context, as a layer runs them, step after step on one stream."""
+    from host_latent_cache_gb300 import workloads as W
+    from host_latent_cache_gb300.rows import RowCache
+    from host_latent_cache_gb300.session import Session
+    cfg = W.v32_32k().replace(batch=3, T=3200, k=512, C=2048, mtp=mtp, mla_heads=32, layers=1,
+                              T_per_req=lens)
+    ld = W.gen_layer(cfg)
+    sess = Session(cfg, [ld])
+    n, page = ld.latent.shape[1], cfg.page
+    per = n // page
+    table = ld.page_table + per * np.arange(3, dtype=np.int32)[:, None]
+    t = np.arange(n)
+    slots = table[:, t // page].astype(np.int64) * page + t % page
+    cache = RowCache(torch.zeros(3 * n, 400, dtype=torch.uint8, device="cuda"), "q4", page=page)
+    kv = torch.from_numpy(ld.latent.view(np.int16)).cuda().view(torch.bfloat16)
+    for b in range(3):
+        cache.write(kv[b], torch.from_numpy(slots[b]).cuda())
+    raw = cache.rows.cpu().numpy()
+    T = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    dev_table = torch.from_numpy(table).cuda()
+    qs = W.QueryStream(cfg)
+    for _ in range(3):
+        _, enc, qm = qs.next()
+        qd, wd, qmd = sess.device_inputs(enc, W.head_weights(cfg, ld.w), qm)
+        q = qmd.view(torch.bfloat16).view(3, mtp, 32, 576)
+        sess.indexer_topk(0, qd, wd)
+        out, lse = cache.attend(q, dev_table, T, cfg.sm_scale, tokens=sess.topk_idx)
+        torch.cuda.synchronize()
+        assert sess.poll() == ess.ESS_OK and cache.poll() == ess.ESS_OK
+        top = sess.topk_idx.cpu().numpy()
+        qf = q.double().cpu().numpy()
+        for b in range(3):
+            for m in range(mtp):
+                at = top[b, m, :min(512, lens[b])].astype(np.int64)
+                assert len(set(at.tolist())) == len(at) and at.max() < lens[b]
+                k = R.row_values(raw[slots[b, at]], "q4")
+                want, wl, size = R.attention(qf[b, m], k, cfg.sm_scale, np.ones((32, len(at)), bool))
+                dz = 576 * 2.0 ** -24 * (np.abs(qf[b, m]) @ np.abs(k).T).max(axis=1) * cfg.sm_scale
+                tol = (2 * dz[:, None] + 2.0 ** -11 + 2.0 ** -18) * size + 2.0 ** -8 * np.abs(want) \
+                    + 2.0 ** -32 * np.abs(k[:, :512]).sum(axis=0)
+                assert (np.abs(out[b, m].double().cpu().numpy() - want) <= tol).all()
+                gl = lse[b, m].double().cpu().numpy()
+                assert (np.abs(gl - wl) <= dz + 2.0 ** -20 * (1 + np.abs(wl))).all()
+    sess.close()

@@ -490,7 +490,8 @@ def test_misaligned_rows_are_refused():
         cache.write(odd, torch.zeros(2, dtype=torch.int64, device="cuda"))
 
 
-@pytest.mark.parametrize("how", ["eager", "one graph", "graph of the norm", "host step"])
+@pytest.mark.parametrize("how", ["eager", "one graph", "graph of the norm", "graph of the indexer",
+                                 "host step"])
 def test_an_indexer_right_behind_the_norm_that_makes_its_keys(how):
     """A prompt's keys normed straight into the bound keys, and the indexer next on
     the stream: it scores those keys, as one that starts after everything is done."""
@@ -541,20 +542,22 @@ def test_an_indexer_right_behind_the_norm_that_makes_its_keys(how):
         want.append(done())
     assert not torch.equal(want[0], want[1])
     graph = torch.cuda.CUDAGraph()
-    if how in ("one graph", "graph of the norm"):
+    if "graph" in how:
+        index()                     # one after the last norm: the next need not wait
         with torch.cuda.graph(graph):
-            norm()
-            if how == "one graph":
+            if how != "graph of the indexer":
+                norm()
+            if how != "graph of the norm":
                 sess.scores_only(0, qd, wd, torch.cuda.current_stream())
-        index()                     # the count of norms is seen again
+        index()
     for i in range(24):
         raw.copy_(raws[i % 4])
         torch.cuda.synchronize()
-        if how == "eager":
+        if how in ("eager", "graph of the indexer"):
             norm()
-        elif how != "host step":
+        if "graph" in how:
             graph.replay()
-        if how != "one graph":
+        if how in ("eager", "graph of the norm", "host step"):
             index()
         assert torch.equal(done(), want[i % 4]), i
     assert sess.poll() == ess.ESS_OK
