@@ -23,15 +23,21 @@
 // softmax, one resolves the tokens' rows, one of the even CTA issues the MMAs: QK
 // of tile i + 1, then PV of tile i, so the softmax of a tile and the widening of
 // the next run beside them.  O is rescaled only when a row's maximum grows by
-// more than 2^8.
+// more than 2^8: 76 requests of 800 tokens take 28.7 us where it grows at every
+// tile, 27.1 where it does not.
 //
-// What bounds it: the shared-memory and L1 data path.  A tile writes 147 KB of
-// widened operands and P, reads 34 KB of raw rows through L1, in pieces of 128
-// bytes that straddle its lines, and the MMAs read 245 KB of operands, beside
-// 2200 cycles of tensor work.  All tokens of eight 128K contexts with 128 heads:
-// 188 us, 1.23 PFLOP/s or 65 % of the measured tensor rate, 3900 cycles a tile.
-// A segment costs about 5 us beside its tiles: its queries (1.2 us of conversions
-// and stores), O's way out (2.2 us) and the pipeline's start.
+// What it spends its time on: no unit is saturated.  The data path of shared
+// memory and L1 is the busiest (63 % over a ragged launch, the tensor pipe 46 %,
+// DRAM 12 %, 0.45 issues a cycle and scheduler), and between its bursts the roles
+// wait for loads and for one another.  A tile writes 147 KB of widened operands
+// and P, reads 34 KB of raw rows through L1, in pieces of 128 bytes that straddle
+// its lines, and the MMAs read 245 KB of operands, beside 2200 cycles of tensor
+// work.  All tokens of eight 128K contexts with 128 heads: 188 us, 1.23 PFLOP/s or
+// 65 % of the measured tensor rate, 3900 cycles a tile.  Fewer heads cost as much,
+// as a tile has 128 query rows whether they are there or not: 182 us with 16 heads,
+// 3.7 times what their bytes take.  A segment costs about 5 us beside its tiles: its
+// queries (1.2 us of conversions and stores), O's way out (2.2 us) and the
+// pipeline's start.
 // Measured on the way there (same case): one thread issuing in divergent code
 // 526 us (110 cycles an MMA); V before K of the next tile 447; four softmax
 // warps, rows resolved by the widening warps 346; lanes across rows (32 lines a
@@ -1223,9 +1229,12 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
   if (e != cudaSuccess) return ESS_ERR_CUDA;
   // Few rows with many parts (a 4096-token request: 32) are cut into many small
   // slices: 12.1 us a call, where whole rows took 14.4.  Many rows (2048 and more
-  // fill the GPU) have two or three parts each: one group is enough, and four
-  // parts in flight cost 1.5 us of 97 more than two.  Between, two groups: 2048 listed
-  // tokens of eight requests 19.3 us, four groups 21.7, slices of 16 19.7.
+  // fill the GPU) have two or three parts each where requests are alike: one group is
+  // enough, and four parts in flight cost 1.5 us of 97 more than two.  Between, two
+  // groups: 2048 listed tokens of eight requests 19.3 us, four groups 21.7, slices of 16
+  // 19.7.  Only rows are counted, as the parts of a row are known on the device: one
+  // 128K request among 31 of 512 tokens, with some 70 parts a row in one group, takes
+  // 69 us where it takes 42 alone.
   if (all_rows <= 608) e = launch_join<4, 8, 16, 2>(a, all_rows, st);
   else if (all_rows < 2048) e = launch_join<4, 64, 2, 4>(a, all_rows, st);
   else e = launch_join<4, 64, 1, 2>(a, all_rows, st);

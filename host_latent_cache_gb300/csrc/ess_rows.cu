@@ -9,10 +9,11 @@
 // 4 bytes a lane for bf16, e4m3 and e2m1.
 //
 // Measured (bytes that the call cannot do without / time): 131072 q4 rows read
-// 34.2 us (5.97 TB/s, 88 % of the measured copy rate); 65536 q4 rows written
-// 26.7 us (3.84 TB/s), without norm and rotation 21.4, as bf16 rows 29.3 (a
-// plain copy of the same bytes takes 23.9); the norm of 16384 x 4096 with a
-// residual 88 us (5.34 TB/s), of 131072 keys 11.6 us (4.4 TB/s).
+// 33.7 us (6.07 TB/s, 89 % of the measured copy rate); 65536 q4 rows written
+// 27.0 us (3.80 TB/s), without norm and rotation 21.3, as compact rows 28.1, as
+// bf16 rows 29.0 (a plain copy of the same bytes takes 23.9); the norm of
+// 16384 x 4096 with a residual 87.3 us (5.38 TB/s), of 131072 keys 12.6 us
+// (4.04 TB/s).
 #include <algorithm>
 #include <cmath>
 
@@ -84,10 +85,11 @@ struct RawRow {
 };
 
 // Warps walk over the rows, the next row's loads in flight while one is
-// worked on, with gamma in registers.  About 300 instructions a row and warp
-// bound it (two thirds of the issue slots).  65536 q4 rows written and read
-// back take 41.8 us this way, 42.4 with two rows a warp of sixteen lanes each
-// (fewer instructions, but 122 registers), 46.2 with two rows in flight a warp.
+// worked on, with gamma in registers.  It takes about 300 instructions a row and
+// warp, and two thirds of the issue slots.  65536 q4 rows written and read back
+// took 41.8 us this way, 42.4 with two rows a warp of sixteen lanes each (fewer
+// instructions, but 122 registers), 46.2 with two rows in flight a warp; 42.2
+// now, with the long way round for far rows beside the usual one.
 template <int FMT>
 __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
     const WriteArgs a, const __grid_constant__ RopeFreq fr) {
@@ -144,8 +146,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
       const unsigned long long turn =
           static_cast<unsigned long long>(static_cast<long long>(row.pos)) * freq;
       // the top 32 bits as a signed fraction of a turn, in radians within
-      // +-pi, where the hardware's sine and cosine are off by at most 2^-21:
-      // far below half a step of the bf16 result
+      // +-pi, where the hardware's sine and cosine are off by at most 2^-21: far
+      // below half a bf16 step of the pair's larger value (and of the result,
+      // unless the two products cancel)
       const float h = static_cast<float>(static_cast<int32_t>(turn >> 32)) * (3.14159265358979f * 0x1p-31f);
       const float sn = __sinf(h), cs = __cosf(h);
       const float xa = bf16_lo(ra), xb = bf16_lo(rb);
@@ -264,9 +267,10 @@ struct NormArgs {
 // row sits in thread u % TPR, so 16 neighbouring lanes hold one group of 128;
 // with TPR = 8 (an indexer key) both units of eight lanes do.  A warp so takes
 // four keys at once, and what is done once a row (the root, the joining of
-// sums), which bounds rows this short, is shared by them: 131072 keys in 11.6
-// us, where sixteen lanes a key took 16.0.  Two units a thread is the best for
-// long rows too (16384 x 4096 with a residual: 88 us, four units 90 us).  The
+// sums), which weighs most in rows this short, is shared by them: 131072 keys in
+// 11.6 us, where sixteen lanes a key took 16.0 (12.1 since nothing starts ahead
+// of a key norm's end, 12.6 with far_root beside it).  Two units a thread is the
+// best for long rows too (16384 x 4096 with a residual: 87 us, four units 90).  The
 // resident CTAs asked for are those that fit without far_root, which is off the
 // usual path and must not cost them registers.
 template <int TPR, int UNITS, bool RES>
