@@ -174,7 +174,8 @@ cudaError_t prefer_max_smem(void (*kernel)(KArgs...)) {
 // Launches a kernel as a programmatic dependent of the previous kernel on the
 // stream: its CTAs may be scheduled before that kernel has finished, so every
 // kernel of this library waits (griddepcontrol.wait) before it touches global
-// memory, and lets its own dependents launch once it is running.
+// memory, and lets its own dependents launch once it is running.  (The indexer
+// loads keys ahead of its wait where nothing can still write them; see key_norms.)
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t st, Args... args) {
