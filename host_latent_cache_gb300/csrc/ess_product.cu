@@ -1,0 +1,779 @@
+// 8-bit products: bf16 values quantised to e4m3 with a power-of-two scale for
+// 128 values of a row (activations) or for 128 x 128 values (weights), and
+//
+//   out[t][f] = sum_j xs[t][j] ws[f / 128][j] sum_{k in group j} x[t][k] w[f][k]
+//
+// over the groups j of 128 along K.  All scales are powers of two, so the tensor
+// core multiplies them in itself: kind::mxf8f6f4 takes one 8-bit exponent per
+// row and 32 values of K, from TMEM, at the full 8-bit rate, and no accumulator
+// is read before its sum is complete.
+//
+// The weight's rows are the MMA's M (128 a CTA), the tokens its N: a product with
+// few tokens, which is bound by reading the weight, then wastes no tensor width,
+// and a thread of the epilogue holds one output column, so a warp writes runs of
+// neighbouring columns.
+//
+//   warps 0-3  epilogue: accumulators out of TMEM, converted and stored
+//   warps 4-7  scales: fp32 scales -> exponent bytes -> TMEM.  The four bytes of a
+//              32-bit cell are four groups of K; row 32 c + l sits in column c of
+//              lane l, once for each quarter of the lanes
+//   warp 8     TMA: 128 bytes of K of both operands a stage, 128B swizzle
+//   warp 9     MMA
+//
+// Few tokens: one tile a CTA, two CTAs an SM; the CTAs of a cluster share a tile,
+// each with a part of K, and add their fp32 accumulators up through distributed
+// shared memory, in order.  Many tokens: pairs of CTAs (cta_group::2) compute 256 x
+// 256 tiles, walking over tiles, the epilogue of one beside the MMAs of the next.
+#include <algorithm>
+#include <atomic>
+#include <cstddef>
+
+#include "ess_rows.cuh"
+
+namespace ess {
+namespace {
+
+// ---------------------------------------------------------------- quantisation
+struct QuantArgs {
+  const uint16_t* x;
+  long long stride;
+  int n;
+  int dim;
+  int groups;              // ceil(dim / 128)
+  uint32_t mul;            // i / groups = umulhi(i, mul) >> shift for i < 2^31
+  int shift;
+  uint8_t* codes;
+  float* scales;
+};
+
+constexpr int kQuantThreads = 256;
+constexpr int kQuantItems = 4;     // groups in flight per 16 lanes
+
+// Sixteen lanes a group of 128 values, 16 bytes a lane.
+__global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const QuantArgs a) {
+  pdl_wait_previous();
+  // rows of 128 values may be bound indexer keys: nothing starts before they are written
+  if (a.dim > 128) pdl_launch_dependents();
+  const int lane = threadIdx.x & 15;
+  const uint32_t total = static_cast<uint32_t>(a.n) * static_cast<uint32_t>(a.groups);
+  const uint32_t first =
+      blockIdx.x * (kQuantThreads / 16 * kQuantItems) + (threadIdx.x >> 4);
+  uint4 v[kQuantItems];
+  int row[kQuantItems], g[kQuantItems];
+#pragma unroll
+  for (int q = 0; q < kQuantItems; ++q) {
+    const uint32_t i = first + q * (kQuantThreads / 16);
+    const uint32_t r = a.shift < 0 ? i : __umulhi(i, a.mul) >> a.shift;
+    row[q] = i < total ? static_cast<int>(r) : -1;
+    g[q] = static_cast<int>(i - r * static_cast<uint32_t>(a.groups));
+    v[q] = make_uint4(0u, 0u, 0u, 0u);
+    if (row[q] >= 0 && g[q] * 128 + lane * 8 < a.dim)
+      v[q] = reinterpret_cast<const uint4*>(a.x + row[q] * a.stride + g[q] * 128)[lane];
+  }
+#pragma unroll
+  for (int q = 0; q < kQuantItems; ++q) {
+    float f[8];
+    unpack8(v[q], f);
+    const int e = scale_exp<448>(group_max<16>(amax8(f)));
+    if (row[q] < 0) continue;
+    const int c = g[q] * 128 + lane * 8;
+    if (c < a.dim)
+      *reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(row[q]) * a.dim + c) =
+          pack8_e4m3(f, exp2i(-e));
+    if (lane == 0) a.scales[static_cast<size_t>(row[q]) * a.groups + g[q]] = exp2i(e);
+  }
+}
+
+// One CTA a block of 128 x 128: 16 lanes a row, 16 rows at a time.
+__global__ void __launch_bounds__(kQuantThreads) quant_square_kernel(const QuantArgs a) {
+  __shared__ float part[kQuantThreads / 32];
+  pdl_wait_previous();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 15, r0 = blockIdx.y * 128 + (threadIdx.x >> 4);
+  const int c = blockIdx.x * 128 + lane * 8;
+  uint4 v[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int r = r0 + 16 * q;
+    v[q] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < a.n && c < a.dim) v[q] = *reinterpret_cast<const uint4*>(a.x + r * a.stride + c);
+  }
+  float m = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    float f[8];
+    unpack8(v[q], f);
+    m = fmaxf(m, amax8(f));
+  }
+  m = group_max<32>(m);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kQuantThreads / 32; ++w) m = fmaxf(m, part[w]);
+  const int e = scale_exp<448>(m);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int r = r0 + 16 * q;
+    float f[8];
+    unpack8(v[q], f);
+    if (r < a.n && c < a.dim)
+      *reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(r) * a.dim + c) =
+          pack8_e4m3(f, exp2i(-e));
+  }
+  if (threadIdx.x == 0)
+    a.scales[static_cast<size_t>(blockIdx.y) * a.groups + blockIdx.x] = exp2i(e);
+}
+
+// ---------------------------------------------------------------- product
+constexpr int kEpiWarps = 4, kScaleWarps = 4;
+constexpr int kTmaWarp = kEpiWarps + kScaleWarps, kProdMmaWarp = kTmaWarp + 1;
+constexpr int kProdThreads = (kProdMmaWarp + 1) * 32;
+constexpr uint32_t kWTile = 128 * 128;   // bytes of the weight's part of a stage
+constexpr int kMaxStages = 6;
+constexpr int kOverlap = 32;             // columns that the two accumulators of a pair share
+
+// Groups of K that one accumulator adds up when results are fp32.  The tensor core
+// cuts off what an addition shifts out, so a sum drifts towards zero with each of
+// its additions: products of 4096 values were off by 2e-6 of their norm (2^-24 is
+// 6e-8).  Sums of 1024 are added up in registers, rounded, instead: 5e-7.  For bf16
+// results (2^-9) the whole of K is one sum.
+constexpr int kSumGroups = 8;
+
+constexpr int prod_stages(int bn, bool pair, bool sums) {
+  return pair ? 6 : bn <= 16 ? 6 : bn <= 32 ? 5 : bn <= 64 ? 4 : sums ? 6 : 3;
+}
+constexpr int prod_x_rows(int bn, bool pair) { return pair ? bn / 2 : bn; }   // of one CTA
+constexpr uint32_t prod_stage_bytes(int bn, bool pair) {
+  return kWTile + prod_x_rows(bn, pair) * 128;
+}
+
+struct ProdMisc {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t sf_full[2], sf_empty[2];
+  uint64_t acc_full[2], acc_free[2];
+  uint32_t tmem;
+  int abort;
+};
+constexpr uint32_t prod_smem(int bn, bool pair, bool sums) {
+  return prod_stages(bn, pair, sums) * prod_stage_bytes(bn, pair) + sizeof(ProdMisc) + 1024;
+}
+
+struct ProdArgs {
+  const float* xs;        // [n][groups]
+  const float* ws;        // [ceil(outs / 128)][groups]
+  int n, outs, groups;
+  int m_tiles, n_tiles;
+  void* out;
+  long long stride;
+  int* status;
+};
+
+// Bounded wait (see the cache attention): when it gives up, or another role has,
+// the role goes on without waiting, so that every barrier of the block is reached.
+__device__ __forceinline__ bool prod_wait(uint64_t* bar, uint32_t parity, ProdMisc* mi,
+                                          int* status) {
+  const uint32_t addr = smem_u32(bar);
+  if (mbar_try_wait(addr, parity)) return true;
+  volatile int* stop = &mi->abort;
+  const long long t0 = clock64();
+  while (!*stop) {
+    if (mbar_try_wait(addr, parity)) return true;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      set_status(status, ESS_ERR_TIMEOUT);
+      *stop = 1;
+    }
+  }
+  return false;
+}
+__device__ __forceinline__ bool prod_elect() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+// arrive on a barrier of either CTA of a pair, behind everything before it
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+// a load into this CTA that counts its bytes on the even CTA's barrier
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m,
+                                                 uint32_t cluster_bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+      ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(cluster_bar), "r"(x), "r"(y)
+      : "memory");
+}
+// D (+)= (A * scales) (B * scales)^T, e4m3, one exponent byte per row and 32 values
+template <bool PAIR>
+__device__ __forceinline__ void umma_mx8(uint32_t d, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor of the scaled kinds: bits 4-5 which byte of B's scale cells,
+// 17-22 N>>3, 23 scales are exponents, 27-28 M>>7, 29-30 which byte of A's.
+__device__ __forceinline__ uint32_t mx_idesc(uint32_t M, uint32_t N, uint32_t byte) {
+  return (byte << 4) | ((N >> 3) << 17) | (1u << 23) | ((M >> 7) << 27) | (byte << 29);
+}
+template <bool PAIR>
+__device__ __forceinline__ void prod_commit(uint32_t bar) {   // in both CTAs of a pair
+  if (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    umma_commit(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void prod_alloc(uint32_t dst, uint32_t cols) {
+  if (PAIR) {
+    asm volatile(
+        "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
+        "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(dst),
+        "r"(cols)
+        : "memory");
+  } else {
+    tmem_alloc(dst, cols);
+    tmem_relinquish();
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void prod_dealloc(uint32_t taddr, uint32_t cols) {
+  if (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols)
+                 : "memory");
+  else
+    tmem_dealloc(taddr, cols);
+}
+// N consecutive columns of this lane
+template <int N>
+__device__ __forceinline__ void tmem_put(uint32_t t, const uint32_t* r) {
+  static_assert(N == 1 || N == 2 || N == 4 || N == 8, "columns");
+  if (N == 1)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(t), "r"(r[0]) : "memory");
+  else if (N == 2)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(t), "r"(r[0]),
+                 "r"(r[N > 1 ? 1 : 0])
+                 : "memory");
+  else
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(t + i),
+                   "r"(r[i]), "r"(r[N > 2 ? i + 1 : 0]), "r"(r[N > 2 ? i + 2 : 0]),
+                   "r"(r[N > 2 ? i + 3 : 0])
+                   : "memory");
+}
+// 16 consecutive fp32 columns of this lane
+__device__ __forceinline__ void tmem_ld16(uint32_t t, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(t)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+
+// Exponent bytes of up to four scales; groups past the last count as 1.
+__device__ __forceinline__ uint32_t scale_word(const float* s, int left, bool* bad) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t b = j < left ? __float_as_uint(s[j]) : 0x3f800000u;
+    const uint32_t e = (b >> 23) & 0xffu;
+    *bad |= (b & 0x807fffffu) != 0u || e == 0u || e == 255u;
+    w |= min(max(e, 1u), 254u) << (8 * j);
+  }
+  return w;
+}
+
+// What a CTA works on: tiles first, first + step, ..., groups [g0, g1) of K.
+struct ProdShare {
+  int first, step, tiles, g0, g1;
+};
+
+template <int BN, bool PAIR, typename Out>
+__global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out) == 4) ? 1 : 2)
+    product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                   const ProdArgs a) {
+  constexpr bool kSums = sizeof(Out) == 4;   // short sums, added up in registers
+  static_assert(!(PAIR && kSums), "pairs have no registers for sums");
+  constexpr int kStages = prod_stages(BN, PAIR, kSums);
+  constexpr uint32_t kStage = prod_stage_bytes(BN, PAIR);
+  constexpr int kXRows = prod_x_rows(BN, PAIR);
+  constexpr int kAcc = BN < 32 ? 32 : BN;                   // columns of an accumulator
+  constexpr uint32_t kAcc2 = PAIR ? kAcc - kOverlap : kSums ? kAcc : 0;   // the second one
+  constexpr uint32_t kColSf = kAcc2 + kAcc;
+  constexpr int kXCols = BN < 32 ? 1 : BN / 32;             // scale columns of the tokens
+  constexpr uint32_t kSfBuf = 4 + (kXCols < 4 ? 4 : kXCols);
+  constexpr uint32_t kNeed = kColSf + 2 * kSfBuf;
+  constexpr uint32_t kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+  static_assert(kNeed <= kCols, "TMEM columns");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  ProdMisc* mi = reinterpret_cast<ProdMisc*>(smem + kStages * kStage);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t rank = cluster_ctarank();
+  uint32_t parts;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(parts));
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&mi->full[i]), 1);
+      mbar_init(smem_u32(&mi->empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&mi->sf_full[i]), kScaleWarps * (PAIR ? 2 : 1));
+      mbar_init(smem_u32(&mi->sf_empty[i]), 1);
+      mbar_init(smem_u32(&mi->acc_full[i]), 1);
+      mbar_init(smem_u32(&mi->acc_free[i]), kEpiWarps * (PAIR ? 2 : 1));
+    }
+    mi->abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&wmap);
+    tma_prefetch_desc(&xmap);
+  }
+  if (warp == kProdMmaWarp) prod_alloc<PAIR>(smem_u32(&mi->tmem), kCols);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (parts > 1) cluster_sync();   // the peers' barriers exist
+  tc_fence_after();
+  const uint32_t tmem = mi->tmem;
+  pdl_wait_previous();
+  pdl_launch_dependents();
+
+  ProdShare sh;
+  sh.tiles = a.m_tiles * a.n_tiles;
+  sh.first = static_cast<int>(blockIdx.x / parts);
+  sh.step = static_cast<int>(gridDim.x / parts);
+  sh.g0 = PAIR ? 0 : static_cast<int>(static_cast<long long>(a.groups) * rank / parts);
+  sh.g1 = PAIR ? a.groups : static_cast<int>(static_cast<long long>(a.groups) * (rank + 1) / parts);
+  // tile -> first weight row and first token of this CTA
+  auto m_of = [&](int t) { return (t % a.m_tiles) * (PAIR ? 256 : 128) + (PAIR ? static_cast<int>(rank) * 128 : 0); };
+  auto n_of = [&](int t) { return (t / a.m_tiles) * BN; };
+
+  if (warp == kTmaWarp) {
+    if (prod_elect()) {
+      int stage = 0, turn = 0;
+      for (int t = sh.first; t < sh.tiles; t += sh.step) {
+        const int m0 = m_of(t), x0 = n_of(t) + (PAIR ? static_cast<int>(rank) * kXRows : 0);
+        for (int g = sh.g0; g < sh.g1; ++g) {
+          if (turn > 0) prod_wait(&mi->empty[stage], (turn - 1) & 1, mi, a.status);
+          const uint32_t dst = smem_u32(smem + stage * kStage), bar = smem_u32(&mi->full[stage]);
+          if (PAIR) {
+            if (rank == 0) mbar_arrive_expect_tx(bar, 2 * kStage);
+            const uint32_t lead = dsmem_addr(bar, 0);
+            tma_load_2d_pair(dst, &wmap, lead, g * 128, m0);
+            tma_load_2d_pair(dst + kWTile, &xmap, lead, g * 128, x0);
+          } else {
+            mbar_arrive_expect_tx(bar, kStage);
+            tma_load_2d(dst, &wmap, bar, g * 128, m0);
+            tma_load_2d(dst + kWTile, &xmap, bar, g * 128, x0);
+          }
+          if (++stage == kStages) {
+            stage = 0;
+            ++turn;
+          }
+        }
+      }
+      // The last arrivals of every stage are waited for, so that none is on its way
+      // when the CTA ends.  After a wait that gave up, copies may be: the stages'
+      // last ones are waited for with a limit of their own.  (The odd CTA's bytes
+      // are counted by the even one, which stays until the cluster's last barrier.)
+      for (int i = 0; i < kStages; ++i) {
+        const int last = i < stage ? turn : turn - 1;   // the stage's last use
+        if (last < 0 || prod_wait(&mi->empty[i], last & 1, mi, a.status)) continue;
+        const long long t0 = clock64();
+        while ((!PAIR || rank == 0) && !mbar_try_wait(smem_u32(&mi->full[i]), last & 1) &&
+               clock64() - t0 < kWaitLimitCycles) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kProdMmaWarp) {
+    if (!PAIR || rank == 0) {
+      const bool lead = prod_elect();
+      int stage = 0, turn = 0, sb = 0, sturn = 0, i = 0;   // i counts sums
+      bool ok = true;
+      for (int t = sh.first; t < sh.tiles; t += sh.step) {
+        for (int g = sh.g0; g < sh.g1; ++g) {
+          const bool first = g == sh.g0 || (kSums && (g - sh.g0) % kSumGroups == 0);
+          const bool last = g + 1 == sh.g1 || (kSums && (g + 1 - sh.g0) % kSumGroups == 0);
+          if (first) {
+            // the accumulator is read out: of a pair's, the part that the sum before
+            // shares with it, and so all of the one before that
+            if (PAIR && i > 0) ok = prod_wait(&mi->acc_free[0], (i - 1) & 1, mi, a.status) && ok;
+            if (kSums && i > 1)
+              ok = prod_wait(&mi->acc_free[i & 1], ((i >> 1) - 1) & 1, mi, a.status) && ok;
+          }
+          if (g == sh.g0 || (g & 3) == 0)
+            ok = prod_wait(&mi->sf_full[sb], sturn & 1, mi, a.status) && ok;
+          ok = prod_wait(&mi->full[stage], turn & 1, mi, a.status) && ok;
+          tc_fence_after();
+          const bool cells = (g & 3) == 3 || g + 1 == sh.g1;   // done with a buffer of scales
+          if (ok && lead) {
+            const uint32_t at = smem_u32(smem + stage * kStage);
+            const uint64_t dw = make_sdesc_sw128(at, 16, 1024);
+            const uint64_t dx = make_sdesc_sw128(at + kWTile, 16, 1024);
+            const uint32_t idesc = mx_idesc(PAIR ? 256 : 128, BN, g & 3);
+            const uint32_t sf = tmem + kColSf + sb * kSfBuf, acc = tmem + (i & 1) * kAcc2;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_mx8<PAIR>(acc, dw + 2 * k, dx + 2 * k, idesc, sf, sf + 4, !first || k > 0);
+            prod_commit<PAIR>(smem_u32(&mi->empty[stage]));
+            if (cells) prod_commit<PAIR>(smem_u32(&mi->sf_empty[sb]));
+            if (last) prod_commit<PAIR>(smem_u32(&mi->acc_full[i & 1]));
+          }
+          __syncwarp();
+          if (last) ++i;
+          if (++stage == kStages) {
+            stage = 0;
+            ++turn;
+          }
+          if (cells && ++sb == 2) {
+            sb = 0;
+            ++sturn;
+          }
+        }
+      }
+    }
+  } else if (warp >= kEpiWarps) {
+    // scales
+    const int q = warp & 3;
+    const uint32_t ts = tmem + (static_cast<uint32_t>(q * 32) << 16) + kColSf;
+    int sb = 0, sturn = 0;
+    bool bad = false;
+    for (int t = sh.first; t < sh.tiles; t += sh.step) {
+      const int m0 = m_of(t), x0 = n_of(t);
+      const float* ws = a.ws + static_cast<size_t>(min(m0, a.outs - 1) >> 7) * a.groups;
+      for (int s = sh.g0 >> 2; s <= (sh.g1 - 1) >> 2; ++s) {
+        uint32_t w[4], x[kXCols];
+        w[0] = scale_word(ws + 4 * s, a.groups - 4 * s, &bad);
+        w[1] = w[2] = w[3] = w[0];
+#pragma unroll
+        for (int c = 0; c < kXCols; ++c) {
+          const int row = x0 + 32 * c + lane;
+          x[c] = 0x7f7f7f7fu;
+          if (row < a.n && 32 * c + lane < BN)
+            x[c] = scale_word(a.xs + static_cast<size_t>(row) * a.groups + 4 * s, a.groups - 4 * s,
+                              &bad);
+        }
+        if (sturn > 0) prod_wait(&mi->sf_empty[sb], (sturn - 1) & 1, mi, a.status);
+        tc_fence_after();
+        tmem_put<4>(ts + sb * kSfBuf, w);
+        tmem_put<kXCols>(ts + sb * kSfBuf + 4, x);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR) mbar_arrive_cluster(dsmem_addr(smem_u32(&mi->sf_full[sb]), 0));
+          else mbar_arrive(smem_u32(&mi->sf_full[sb]));
+        }
+        if (++sb == 2) {
+          sb = 0;
+          ++sturn;
+        }
+      }
+    }
+    for (int i = 0; i < 2; ++i) {   // the last arrivals, which nothing else waits for
+      const int last = i < sb ? sturn : sturn - 1;
+      if (last >= 0) prod_wait(&mi->sf_empty[i], last & 1, mi, a.status);
+    }
+    if (q == 0 && bad) set_status(a.status, ESS_ERR_DEVICE_CHECK);
+  } else {
+    // epilogue: lane l of warp q holds output column 32 q + l
+    constexpr int kBlocks = kAcc / 32, kLive = BN < 32 ? BN : 32;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    auto store = [&](int t, int b, const float* v) {
+      const int f = m_of(t) + warp * 32 + lane, x0 = n_of(t) + 32 * b;
+      const int left = min(a.n - x0, kLive);
+      if (f >= a.outs) return;
+      Out* o = static_cast<Out*>(a.out) + x0 * a.stride + f;
+#pragma unroll
+      for (int c = 0; c < kLive; ++c)
+        if (c < left) o[c * a.stride] = static_cast<Out>(v[c]);
+    };
+    // this part's sums of a block of tokens, to the CTAs that add them up
+    auto send = [&](int b, const float* v) {
+      constexpr int kLogBn = BN == 16 ? 4 : BN == 32 ? 5 : BN == 64 ? 6 : BN == 128 ? 7 : 8;
+      const int lg = 31 - __clz(static_cast<int>(parts)), share = BN >> lg;
+      const uint32_t to = smem_u32(smem) + (rank * share * 128 + warp * 32 + lane) * 4;
+#pragma unroll
+      for (int c = 0; c < kLive; ++c) {
+        const int tok = 32 * b + c;
+        st_cluster_f32(dsmem_addr(to + (tok & (share - 1)) * 512, tok >> (kLogBn - lg)), v[c]);
+      }
+    };
+    if (kSums) {
+      float sum[kAcc];
+      const int n = (sh.g1 - sh.g0 + kSumGroups - 1) / kSumGroups;
+#pragma unroll
+      for (int c = 0; c < kAcc; ++c) sum[c] = 0.0f;
+      for (int i = 0; i < n; ++i) {
+        prod_wait(&mi->acc_full[i & 1], (i >> 1) & 1, mi, a.status);
+        tc_fence_after();
+#pragma unroll
+        for (int b = 0; b < kAcc; b += 16) {
+          float v[16];
+          tmem_ld16(tmem + lanes + (i & 1) * kAcc2 + b, v);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) sum[b + c] += v[c];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&mi->acc_free[i & 1]));
+      }
+      if (parts > 1) cluster_sync();
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        if (parts > 1) send(b, sum + 32 * b);
+        else store(sh.first, b, sum + 32 * b);
+      }
+    } else {
+      int i = 0;
+      for (int t = sh.first; t < sh.tiles; t += sh.step, ++i) {
+        prod_wait(&mi->acc_full[i & 1], (i >> 1) & 1, mi, a.status);
+        tc_fence_after();
+        if (!PAIR && parts > 1) cluster_sync();   // one tile a CTA
+#pragma unroll 1
+        for (int j = 0; j < kBlocks; ++j) {
+          // the columns that the next tile's accumulator shares come first
+          const int b = PAIR && (i & 1) == 0 ? kBlocks - 1 - j : j;
+          float v[32];
+          tmem_ld32(tmem + lanes + (i & 1) * kAcc2 + 32 * b, v);
+          if (PAIR && j == 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&mi->acc_free[0]), 0));
+          }
+          if (!PAIR && parts > 1) send(b, v);
+          else store(t, b, v);
+        }
+      }
+    }
+  }
+
+  if (!PAIR && parts > 1) {
+    // The cluster's CTAs hold the same tile's sums over their parts of K: each adds
+    // up the tokens [BN rank / parts, BN (rank + 1) / parts), in the order of the
+    // parts, in the ring, which nothing uses any more once all have their sums.
+    __syncwarp();
+    if (warp >= kEpiWarps) cluster_sync();   // all have their sums (see the epilogue)
+    cluster_sync();                          // all have sent them
+    const int share = BN / static_cast<int>(parts);
+    const int f = m_of(sh.first) + (tid & 127);
+    const int x0 = n_of(sh.first) + static_cast<int>(rank) * share;
+    if (tid < 256 && f < a.outs) {
+      const float* in = reinterpret_cast<const float*>(smem) + (tid & 127);
+      for (int c = tid >> 7; c < share && x0 + c < a.n; c += 2) {
+        float s = in[c * 128];
+        for (uint32_t p = 1; p < parts; ++p) s += in[(p * share + c) * 128];
+        static_cast<Out*>(a.out)[(x0 + c) * a.stride + f] = static_cast<Out>(s);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (parts > 1) cluster_sync();
+  tc_fence_after();
+  if (warp == kProdMmaWarp) prod_dealloc<PAIR>(tmem, kCols);
+}
+
+template <int BN, bool PAIR, typename Out>
+cudaError_t launch_product(const CUtensorMap& w, const CUtensorMap& x, const ProdArgs& a, int parts,
+                           int ctas, int dev, cudaStream_t st) {
+  auto kernel = product_kernel<BN, PAIR, Out>;
+  constexpr uint32_t kSmem = prod_smem(BN, PAIR, sizeof(Out) == 4);
+  static std::atomic<unsigned long long> done{0};   // allowed once per device
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[3];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+  at[1].val.sharedMemCarveout = static_cast<int>(cudaSharedmemCarveoutMaxShared);
+  at[2].id = cudaLaunchAttributeClusterDimension;
+  at[2].val.clusterDim.x = PAIR ? 2 : parts;
+  at[2].val.clusterDim.y = at[2].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kProdThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 3;
+  return cudaLaunchKernelEx(&cfg, kernel, w, x, a);
+}
+
+template <int BN>
+cudaError_t launch_single(bool fp32, const CUtensorMap& w, const CUtensorMap& x, const ProdArgs& a,
+                          int parts, int ctas, int dev, cudaStream_t st) {
+  return fp32 ? launch_product<BN, false, float>(w, x, a, parts, ctas, dev, st)
+              : launch_product<BN, false, __nv_bfloat16>(w, x, a, parts, ctas, dev, st);
+}
+
+int sms_of(int dev) {
+  static std::atomic<int> known[64];
+  if (dev >= 0 && dev < 64) {
+    const int k = known[dev].load(std::memory_order_relaxed);
+    if (k > 0) return k;
+  }
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+}  // namespace
+}  // namespace ess
+
+using namespace ess;
+
+extern "C" {
+
+ess_status ess_quant(const void* x, int64_t x_stride, int64_t n, int32_t dim, int32_t square,
+                     void* codes, float* scales, ess_stream_t stream) {
+  if (n < 0 || n > 0x7fffffffLL || dim < 1 || x_stride < dim || x_stride % 8 != 0 ||
+      (square != 0 && square != 1))
+    return ESS_ERR_INVALID_ARG;
+  if (dim % 8 != 0) return ESS_ERR_UNSUPPORTED;
+  if (n == 0) return ESS_OK;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned_to(scales, 4))
+    return ESS_ERR_INVALID_ARG;
+  QuantArgs a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.stride = x_stride;
+  a.n = static_cast<int>(n);
+  a.dim = dim;
+  a.groups = (dim - 1) / 128 + 1;
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = scales;
+  a.mul = 0;
+  a.shift = -1;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (square) {
+    const long long high = (n + 127) / 128;
+    if (high > 65535) return ESS_ERR_UNSUPPORTED;
+    return launch_pdl_once(quant_square_kernel, dim3(a.groups, static_cast<unsigned>(high)),
+                           dim3(kQuantThreads), 0, st, a) == cudaSuccess
+               ? ESS_OK
+               : ESS_ERR_CUDA;
+  }
+  if (dim <= 128) ++key_norms();   // the next indexer of each layer waits
+  if (a.groups > 1) {
+    // i / groups for i < 2^31: ceil(2^(32 + shift) / groups) with 2^shift < groups <= 2^(shift + 1)
+    int s = 0;
+    while ((2 << s) < a.groups) ++s;
+    a.shift = s;
+    a.mul = static_cast<uint32_t>(((1ull << (32 + s)) + a.groups - 1) / a.groups);
+  }
+  // rows of one launch: below 2^30 groups
+  const int most = static_cast<int>(std::max(1LL, (1LL << 30) / a.groups));
+  for (long long r = 0; r < n; r += most) {
+    QuantArgs b = a;
+    b.n = static_cast<int>(std::min<long long>(most, n - r));
+    b.x += r * x_stride;
+    b.codes += r * dim;
+    b.scales += r * a.groups;
+    const long long items = static_cast<long long>(b.n) * a.groups;
+    constexpr int kPer = kQuantThreads / 16 * kQuantItems;
+    if (launch_pdl_once(quant_rows_kernel, dim3(static_cast<unsigned>((items + kPer - 1) / kPer)),
+                        dim3(kQuantThreads), 0, st, b) != cudaSuccess)
+      return ESS_ERR_CUDA;
+  }
+  return ESS_OK;
+}
+
+ess_status ess_product(const void* x, const float* x_scales, int64_t n, const void* w,
+                       const float* w_scales, int32_t outs, int32_t ins, void* out,
+                       int64_t out_stride, int32_t fp32, int32_t* status, ess_stream_t stream) {
+  if (n < 0 || outs < 1 || ins < 1 || out_stride < outs || (fp32 != 0 && fp32 != 1))
+    return ESS_ERR_INVALID_ARG;
+  if (ins % 16 != 0 || ins > 0x7fffff00 || outs > 0x7fffff00 || n > 0x7fffff00LL)
+    return ESS_ERR_UNSUPPORTED;
+  if (n == 0) return ESS_OK;
+  if (!x || !x_scales || !w || !w_scales || !out || !aligned16(x) || !aligned16(w) ||
+      !aligned_to(x_scales, 4) || !aligned_to(w_scales, 4) || !aligned_to(out, fp32 ? 4 : 2) ||
+      !aligned_to(status, 4))
+    return ESS_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ESS_ERR_CUDA;
+  const int sms = sms_of(dev);
+  if (sms < 2) return ESS_ERR_CUDA;
+  ProdArgs a;
+  a.xs = x_scales;
+  a.ws = w_scales;
+  a.n = static_cast<int>(n);
+  a.outs = outs;
+  a.groups = (ins - 1) / 128 + 1;
+  a.out = out;
+  a.stride = out_stride;
+  a.status = status;
+  auto cover = [](long long v, int by) { return static_cast<int>((v + by - 1) / by); };
+  const long long pair_tiles = static_cast<long long>(cover(outs, 256)) * cover(n, 256);
+  const bool pair = !fp32 && n > 128 && pair_tiles >= sms / 2;
+  const int bn = pair ? 256 : n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : 128;
+  a.m_tiles = cover(outs, pair ? 256 : 128);
+  a.n_tiles = cover(n, bn);
+  const long long tiles = static_cast<long long>(a.m_tiles) * a.n_tiles;
+  if (tiles > 0x3fffffffLL) return ESS_ERR_UNSUPPORTED;
+  int parts = 1, ctas;
+  if (pair) {
+    ctas = 2 * static_cast<int>(std::min<long long>(tiles, sms / 2));
+  } else {
+    const int slots = (bn == 128 && fp32 ? 1 : 2) * sms;   // CTAs that run at once
+    while (parts < 8 && tiles * parts * 2 <= slots && a.groups >= 4 * parts) parts *= 2;
+    ctas = static_cast<int>(tiles) * parts;
+  }
+  CUtensorMap wm, xm;
+  if (!encode_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, ins, outs, ins, 128, 128) ||
+      !encode_map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, ins, n, ins, 128, pair ? 128 : bn))
+    return ESS_ERR_CUDA;
+  if (!fp32 && outs <= 64) ++key_norms();   // rows of 64 bf16 values may be indexer keys too
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  const bool f = fp32 != 0;
+  if (pair) e = launch_product<256, true, __nv_bfloat16>(wm, xm, a, parts, ctas, dev, st);
+  else if (bn == 16) e = launch_single<16>(f, wm, xm, a, parts, ctas, dev, st);
+  else if (bn == 32) e = launch_single<32>(f, wm, xm, a, parts, ctas, dev, st);
+  else if (bn == 64) e = launch_single<64>(f, wm, xm, a, parts, ctas, dev, st);
+  else e = launch_single<128>(f, wm, xm, a, parts, ctas, dev, st);
+  return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
+}
+
+}  // extern "C"

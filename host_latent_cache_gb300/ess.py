@@ -47,6 +47,7 @@ EXPORTS = (
     "ess_pool_bind_layer_compact", "ess_prefill_run", "ess_row_bytes", "ess_status_take",
     "ess_cache_write",
     "ess_cache_read", "ess_cache_mla_bytes", "ess_cache_mla", "ess_norm_quant",
+    "ess_quant", "ess_product",
 )
 
 # void (*)(void* user, int32_t layer, void* buffer, void* stream)
@@ -136,6 +137,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "ess_cache_mla": [P, P, L, I, P, I, I, P, I, I, I, P, I, F, P, P, P, ctypes.c_size_t, P,
                           P],
         "ess_norm_quant": [P, L, P, L, P, F, L, I, P, P, P, P],
+        "ess_quant": [P, L, L, I, I, P, P, P],
+        "ess_product": [P, P, L, P, P, I, I, P, L, I, P, P],
     }
     for name, args in sigs.items():
         f = getattr(lib, name)
@@ -470,3 +473,14 @@ def ess_norm_quant(x, x_stride: int, residual, residual_stride: int, gamma, eps:
     check(load().ess_norm_quant(_p(x), x_stride, _p(residual), residual_stride, _p(gamma), eps, n,
                                 dim, _p(residual_out), _p(codes), _p(scales), _stream(stream)),
           "ess_norm_quant")
+
+
+def ess_quant(x, x_stride: int, n: int, dim: int, square: int, codes, scales, stream=None) -> None:
+    check(load().ess_quant(_p(x), x_stride, n, dim, square, _p(codes), _p(scales),
+                           _stream(stream)), "ess_quant")
+
+
+def ess_product(x, x_scales, n: int, w, w_scales, outs: int, ins: int, out, out_stride: int,
+                fp32: int, status=None, stream=None) -> None:
+    check(load().ess_product(_p(x), _p(x_scales), n, _p(w), _p(w_scales), outs, ins, _p(out),
+                             out_stride, fp32, _p(status), _stream(stream)), "ess_product")

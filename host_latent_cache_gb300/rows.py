@@ -93,6 +93,22 @@ class _OnDevice:
         return False
 
 
+def _new_status(index: int) -> torch.Tensor:
+    """A status word without an error, that any stream may use from here on."""
+    with _OnDevice(index):
+        status = torch.zeros(1, dtype=torch.int32, device=f"cuda:{index}")
+        if not torch._C._cuda_isCurrentStreamCapturing():
+            torch.cuda.current_stream().synchronize()
+    return status
+
+
+def _take_status(status: torch.Tensor, index: int) -> int:
+    with _OnDevice(index) as stream:
+        taken = torch.empty(1, dtype=torch.int32, device=status.device)
+        ess.ess_status_take(status, taken, stream)
+        return int(taken.item())
+
+
 class _Workspace:
     """What the eager calls on one stream of a device share, whichever cache makes
     them: the largest workspace any of them needed, and a lock that keeps a call's
@@ -136,10 +152,7 @@ class RowCache:
         self.device = rows.device
         self._index = rows.get_device()
         _check(rows, "rows", torch.uint8, (self.n_rows, ess.ess_row_bytes(self._f)), self._index)
-        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
-        with _OnDevice(self._index):
-            if not torch._C._cuda_isCurrentStreamCapturing():
-                torch.cuda.current_stream().synchronize()   # any stream may use it from here on
+        self.status = _new_status(self._index)
         self._freq = (None, None)
         self._ws = {}       # by stream, shared with the other caches that run on it
         self._bytes = {}    # by shape
@@ -148,10 +161,7 @@ class RowCache:
         """The first device-side error that is there, cleared.  Waits for the calls on
         the current stream; what a call that still runs on another stream reports
         is kept for a later poll."""
-        with _OnDevice(self._index) as stream:
-            taken = torch.empty(1, dtype=torch.int32, device=self.device)
-            ess.ess_status_take(self.status, taken, stream)
-            return int(taken.item())
+        return _take_status(self.status, self._index)
 
     def _freqs(self, inv_freq: Sequence[float]):
         key = tuple(map(float, inv_freq))   # numbers: a tensor's entries may change later

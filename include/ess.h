@@ -660,6 +660,42 @@ ess_status ess_norm_quant(const void* x, int64_t x_stride, const void* residual,
                           int32_t dim, void* residual_out, void* codes, float* scales,
                           ess_stream_t stream);
 
+/* Values to e4m3 with power-of-two scales: activations on their way into
+ * ess_product that no norm has quantised, or weights.
+ *   x        device bf16, n rows of dim values, x_stride elements apart, 16-byte
+ *            aligned rows
+ *   square   0: a scale for each 128 values of a row (the last group may be shorter);
+ *            1: a scale for each 128 rows x 128 values
+ *   codes    device [n][dim] e4m3, 16-byte aligned
+ *   scales   device float [n or ceil(n / 128)][ceil(dim / 128)]
+ * A scale is the smallest power of two at or above fl32(amax / 448) (1 for zeros, at
+ * least 2^-126), the codes are e4m3(x / scale), nearest with ties to the even code.
+ * An infinity saturates, in a block of scale 1; a NaN stays one.  With square = 0 and
+ * dim = 128 a row is an indexer key, as in ess_norm_quant.  n = 0 launches nothing.
+ * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or negative argument, a stride
+ * below dim or not a multiple of 8; ESS_ERR_UNSUPPORTED when dim is not a multiple of 8,
+ * or square and n is above 128 * 65535. */
+ess_status ess_quant(const void* x, int64_t x_stride, int64_t n, int32_t dim, int32_t square,
+                     void* codes, float* scales, ess_stream_t stream);
+
+/* Product of 8-bit activations with an 8-bit weight (transposed), on the tensor cores:
+ *   out[t][f] = sum_k x[t][k] x_scales[t][k / 128] w[f][k] w_scales[f / 128][k / 128]
+ *   x         device [n][ins] e4m3, 16-byte aligned: codes of ess_norm_quant or ess_quant
+ *   x_scales  device float [n][ceil(ins / 128)]
+ *   w         device [outs][ins] e4m3, 16-byte aligned
+ *   w_scales  device float [ceil(outs / 128)][ceil(ins / 128)]
+ *   out       device bf16, or float with fp32 = 1, n rows of outs values, out_stride
+ *             elements apart; other values of a row are left as they were
+ * Scales are powers of two from 2^-126 to 2^127; of any other the exponent alone is used,
+ * and ESS_ERR_DEVICE_CHECK is reported in status (see above; may be NULL).  Products and
+ * sums are fp32 and rounded once.  A NaN code makes the outputs it enters NaN, and no
+ * others.  One shape always adds in one order.  n = 0 launches nothing.
+ * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or non-positive argument or
+ * out_stride below outs; ESS_ERR_UNSUPPORTED when ins is not a multiple of 16. */
+ess_status ess_product(const void* x, const float* x_scales, int64_t n, const void* w,
+                       const float* w_scales, int32_t outs, int32_t ins, void* out,
+                       int64_t out_stride, int32_t fp32, int32_t* status, ess_stream_t stream);
+
 /* Synchronise stream, return the first device-side error since the last
  * poll (ESS_OK if none) and clear it. */
 ess_status ess_pool_poll(ess_pool* pool, ess_stream_t stream);
