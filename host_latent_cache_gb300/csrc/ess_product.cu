@@ -130,6 +130,7 @@ constexpr int kTmaWarp = kEpiWarps + kScaleWarps, kProdMmaWarp = kTmaWarp + 1;
 constexpr int kProdThreads = (kProdMmaWarp + 1) * 32;
 constexpr uint32_t kWTile = 128 * 128;   // bytes of the weight's part of a stage
 constexpr int kMaxStages = 6;
+constexpr int kOutBlk = 32 * 128;        // a block of a pair's results: 32 tokens, 128 columns
 constexpr int kOverlap = 32;             // columns that the two accumulators of a pair share
 
 // Groups of K that one accumulator adds up when results are fp32.  The tensor core
@@ -153,9 +154,11 @@ struct ProdMisc {
   uint64_t acc_full[2], acc_free[2];
   uint32_t tmem;
   int abort;
+  uint32_t cells[2][256];   // scale words on their way to all four scale warps
 };
 constexpr uint32_t prod_smem(int bn, bool pair, bool sums) {
-  return prod_stages(bn, pair, sums) * prod_stage_bytes(bn, pair) + sizeof(ProdMisc) + 1024;
+  return prod_stages(bn, pair, sums) * prod_stage_bytes(bn, pair) + (pair ? 4 * kOutBlk : 0) +
+         sizeof(ProdMisc) + 1024;
 }
 
 struct ProdArgs {
@@ -165,6 +168,8 @@ struct ProdArgs {
   int m_tiles, n_tiles;
   void* out;
   long long stride;
+  bool blocks;            // a pair's results go through omap
+  bool wide;              // rows of scales are multiples of 16 bytes, 16-byte aligned
   int* status;
 };
 
@@ -193,6 +198,14 @@ __device__ __forceinline__ bool prod_elect() {
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(p));
   return p != 0;
+}
+// a block of shared memory to global memory; what lies outside the tensor is left out
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(m)),
+      "r"(src), "r"(x), "r"(y)
+      : "memory");
 }
 // arrive on a barrier of either CTA of a pair, behind everything before it
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
@@ -302,12 +315,20 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
-// Exponent bytes of up to four scales; groups past the last count as 1.
-__device__ __forceinline__ uint32_t scale_word(const float* s, int left, bool* bad) {
+// Four scales; groups past the last count as 1.  wide: rows of scales are 16-byte aligned
+__device__ __forceinline__ uint4 load_scales(const float* s, int left, bool wide) {
+  if (wide) return *reinterpret_cast<const uint4*>(s);   // then left is at least 4
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(s);
+  return make_uint4(left > 0 ? u[0] : 0x3f800000u, left > 1 ? u[1] : 0x3f800000u,
+                    left > 2 ? u[2] : 0x3f800000u, left > 3 ? u[3] : 0x3f800000u);
+}
+// Their exponent bytes.
+__device__ __forceinline__ uint32_t scale_word(const uint4& s, bool* bad) {
+  const uint32_t v[4] = {s.x, s.y, s.z, s.w};
   uint32_t w = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t b = j < left ? __float_as_uint(s[j]) : 0x3f800000u;
+    const uint32_t b = v[j];
     const uint32_t e = (b >> 23) & 0xffu;
     *bad |= (b & 0x807fffffu) != 0u || e == 0u || e == 255u;
     w |= min(max(e, 1u), 254u) << (8 * j);
@@ -323,7 +344,7 @@ struct ProdShare {
 template <int BN, bool PAIR, typename Out>
 __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out) == 4) ? 1 : 2)
     product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                   const ProdArgs a) {
+                   const __grid_constant__ CUtensorMap omap, const ProdArgs a) {
   constexpr bool kSums = sizeof(Out) == 4;   // short sums, added up in registers
   static_assert(!(PAIR && kSums), "pairs have no registers for sums");
   constexpr int kStages = prod_stages(BN, PAIR, kSums);
@@ -340,7 +361,8 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  ProdMisc* mi = reinterpret_cast<ProdMisc*>(smem + kStages * kStage);
+  uint16_t* blocks = reinterpret_cast<uint16_t*>(smem + kStages * kStage);   // of a pair
+  ProdMisc* mi = reinterpret_cast<ProdMisc*>(smem + kStages * kStage + (PAIR ? 4 * kOutBlk : 0));
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t rank = cluster_ctarank();
@@ -361,6 +383,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
     fence_mbar_init();
     tma_prefetch_desc(&wmap);
     tma_prefetch_desc(&xmap);
+    if (PAIR && a.blocks) tma_prefetch_desc(&omap);
   }
   if (warp == kProdMmaWarp) prod_alloc<PAIR>(smem_u32(&mi->tmem), kCols);
   __syncwarp();
@@ -473,20 +496,39 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
     const uint32_t ts = tmem + (static_cast<uint32_t>(q * 32) << 16) + kColSf;
     int sb = 0, sturn = 0;
     bool bad = false;
-    for (int t = sh.first; t < sh.tiles; t += sh.step) {
-      const int m0 = m_of(t), x0 = n_of(t);
-      const float* ws = a.ws + static_cast<size_t>(min(m0, a.outs - 1) >> 7) * a.groups;
-      for (int s = sh.g0 >> 2; s <= (sh.g1 - 1) >> 2; ++s) {
-        uint32_t w[4], x[kXCols];
-        w[0] = scale_word(ws + 4 * s, a.groups - 4 * s, &bad);
-        w[1] = w[2] = w[3] = w[0];
+    // Up to 64 tokens every warp loads all rows' scales.  Of more, a warp loads a
+    // quarter, and the words meet in shared memory: a load touches 32 lines.
+    constexpr bool kMeet = kXCols >= 4;
+    constexpr int kMine = kMeet ? kXCols / 4 : kXCols;
+    const uint4 one = make_uint4(0x3f800000u, 0x3f800000u, 0x3f800000u, 0x3f800000u);
+    const int s0 = sh.g0 >> 2, s1 = ((sh.g1 - 1) >> 2) + 1;
+    uint4 nw = one, nx[kMine];   // of the next four groups
+    auto load = [&](int t, int s) {
+      const float* ws = a.ws + static_cast<size_t>(min(m_of(t), a.outs - 1) >> 7) * a.groups;
+      nw = load_scales(ws + 4 * s, a.groups - 4 * s, a.wide);
 #pragma unroll
-        for (int c = 0; c < kXCols; ++c) {
-          const int row = x0 + 32 * c + lane;
-          x[c] = 0x7f7f7f7fu;
-          if (row < a.n && 32 * c + lane < BN)
-            x[c] = scale_word(a.xs + static_cast<size_t>(row) * a.groups + 4 * s, a.groups - 4 * s,
-                              &bad);
+      for (int c = 0; c < kMine; ++c) {
+        const int at = 32 * (kMeet ? q * kMine + c : c) + lane, row = n_of(t) + at;
+        nx[c] = row < a.n && at < BN ? load_scales(a.xs + static_cast<size_t>(row) * a.groups + 4 * s,
+                                                   a.groups - 4 * s, a.wide)
+                                     : one;
+      }
+    };
+    if (sh.first < sh.tiles) load(sh.first, s0);
+    for (int t = sh.first; t < sh.tiles; t += sh.step) {
+      for (int s = s0; s < s1; ++s) {
+        uint32_t w[4], x[kXCols];
+        w[0] = w[1] = w[2] = w[3] = scale_word(nw, &bad);
+#pragma unroll
+        for (int c = 0; c < kMine; ++c) x[c] = scale_word(nx[c], &bad);
+        if (s + 1 < s1) load(t, s + 1);
+        else if (t + sh.step < sh.tiles) load(t + sh.step, s0);
+        if (kMeet) {
+#pragma unroll
+          for (int c = 0; c < kMine; ++c) mi->cells[sb][32 * (q * kMine + c) + lane] = x[c];
+          asm volatile("bar.sync 1, %0;" ::"n"(kScaleWarps * 32) : "memory");
+#pragma unroll
+          for (int c = 0; c < kXCols; ++c) x[c] = mi->cells[sb][32 * c + lane];
         }
         if (sturn > 0) prod_wait(&mi->sf_empty[sb], (sturn - 1) & 1, mi, a.status);
         tc_fence_after();
@@ -560,7 +602,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
         else store(sh.first, b, sum + 32 * b);
       }
     } else {
-      int i = 0;
+      int i = 0, turn = 0;
       for (int t = sh.first; t < sh.tiles; t += sh.step, ++i) {
         prod_wait(&mi->acc_full[i & 1], (i >> 1) & 1, mi, a.status);
         tc_fence_after();
@@ -576,10 +618,31 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&mi->acc_free[0]), 0));
           }
-          if (!PAIR && parts > 1) send(b, v);
-          else store(t, b, v);
+          if (!PAIR && parts > 1) {
+            send(b, v);
+          } else if (PAIR && a.blocks) {
+            // Through shared memory, so that a token's 128 columns leave together:
+            // stored from here, in runs of 64 bytes, a tile took 19500 cycles.
+            uint16_t* o = blocks + (turn & 1) * kOutBlk;
+            if (tid == 0) bulk_wait_read<1>();   // the block before the last one has left
+            asm volatile("bar.sync 2, %0;" ::"n"(kEpiWarps * 32) : "memory");
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              o[c * 128 + warp * 32 + lane] = static_cast<uint16_t>(bf16_bits(v[c]));
+            fence_proxy_async_smem();
+            asm volatile("bar.sync 2, %0;" ::"n"(kEpiWarps * 32) : "memory");
+            if (tid == 0) {
+              if (m_of(t) < a.outs && n_of(t) + 32 * b < a.n)
+                tma_store_2d(&omap, smem_u32(o), m_of(t), n_of(t) + 32 * b);
+              bulk_commit();
+            }
+            ++turn;
+          } else {
+            store(t, b, v);
+          }
         }
       }
+      if (PAIR && a.blocks && tid == 0) bulk_wait_all();
     }
   }
 
@@ -610,8 +673,8 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
 }
 
 template <int BN, bool PAIR, typename Out>
-cudaError_t launch_product(const CUtensorMap& w, const CUtensorMap& x, const ProdArgs& a, int parts,
-                           int ctas, int dev, cudaStream_t st) {
+cudaError_t launch_product(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& o,
+                           const ProdArgs& a, int parts, int ctas, int dev, cudaStream_t st) {
   auto kernel = product_kernel<BN, PAIR, Out>;
   constexpr uint32_t kSmem = prod_smem(BN, PAIR, sizeof(Out) == 4);
   static std::atomic<unsigned long long> done{0};   // allowed once per device
@@ -637,14 +700,14 @@ cudaError_t launch_product(const CUtensorMap& w, const CUtensorMap& x, const Pro
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 3;
-  return cudaLaunchKernelEx(&cfg, kernel, w, x, a);
+  return cudaLaunchKernelEx(&cfg, kernel, w, x, o, a);
 }
 
 template <int BN>
 cudaError_t launch_single(bool fp32, const CUtensorMap& w, const CUtensorMap& x, const ProdArgs& a,
                           int parts, int ctas, int dev, cudaStream_t st) {
-  return fp32 ? launch_product<BN, false, float>(w, x, a, parts, ctas, dev, st)
-              : launch_product<BN, false, __nv_bfloat16>(w, x, a, parts, ctas, dev, st);
+  return fp32 ? launch_product<BN, false, float>(w, x, w, a, parts, ctas, dev, st)
+              : launch_product<BN, false, __nv_bfloat16>(w, x, w, a, parts, ctas, dev, st);
 }
 
 int sms_of(int dev) {
@@ -743,6 +806,7 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   a.groups = (ins - 1) / 128 + 1;
   a.out = out;
   a.stride = out_stride;
+  a.wide = a.groups % 4 == 0 && aligned16(x_scales) && aligned16(w_scales);
   a.status = status;
   auto cover = [](long long v, int by) { return static_cast<int>((v + by - 1) / by); };
   const long long pair_tiles = static_cast<long long>(cover(outs, 256)) * cover(n, 256);
@@ -760,15 +824,20 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
     while (parts < 8 && tiles * parts * 2 <= slots && a.groups >= 4 * parts) parts *= 2;
     ctas = static_cast<int>(tiles) * parts;
   }
-  CUtensorMap wm, xm;
+  CUtensorMap wm, xm, om;
   if (!encode_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, ins, outs, ins, 128, 128) ||
       !encode_map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, ins, n, ins, 128, pair ? 128 : bn))
+    return ESS_ERR_CUDA;
+  a.blocks = pair && aligned16(out) && out_stride % 8 == 0;
+  if (a.blocks &&
+      !encode_map_2d(&om, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, outs, n,
+                     static_cast<uint64_t>(out_stride) * 2, 128, 32, false))
     return ESS_ERR_CUDA;
   if (!fp32 && outs <= 64) ++key_norms();   // rows of 64 bf16 values may be indexer keys too
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   const bool f = fp32 != 0;
-  if (pair) e = launch_product<256, true, __nv_bfloat16>(wm, xm, a, parts, ctas, dev, st);
+  if (pair) e = launch_product<256, true, __nv_bfloat16>(wm, xm, a.blocks ? om : wm, a, parts, ctas, dev, st);
   else if (bn == 16) e = launch_single<16>(f, wm, xm, a, parts, ctas, dev, st);
   else if (bn == 32) e = launch_single<32>(f, wm, xm, a, parts, ctas, dev, st);
   else if (bn == 64) e = launch_single<64>(f, wm, xm, a, parts, ctas, dev, st);
