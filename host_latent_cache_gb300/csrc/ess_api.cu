@@ -120,7 +120,7 @@ EncodeTiledFn get_encode_fn() {
 
 bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                    uint64_t inner_elems, uint64_t outer_rows, uint64_t row_stride_bytes,
-                   uint32_t box_inner, uint32_t box_rows, bool swizzle) {
+                   uint32_t box_inner, uint32_t box_rows) {
   EncodeTiledFn fn = get_encode_fn();
   if (!fn || !aligned16(base) || (row_stride_bytes & 15u)) return false;
   cuuint64_t dims[2] = {inner_elems, outer_rows};
@@ -128,7 +128,7 @@ bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base
   cuuint32_t box[2] = {box_inner, box_rows};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }

@@ -254,9 +254,9 @@ cudaError_t launch_refill(const ess_pool& p, int layer, cudaStream_t st);
 cudaError_t launch_append(const ess_pool& p, int layer, const void* latent, const void* key,
                           const float* key_scale, cudaStream_t st);
 
-// Encodes a 2-D tiled tensor map (128-byte swizzle or none); returns false on failure.
+// Encodes a 2-D tiled tensor map; returns false on failure.
 bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                    uint64_t inner_elems, uint64_t outer_rows, uint64_t row_stride_bytes,
-                   uint32_t box_inner, uint32_t box_rows, bool swizzle = true);
+                   uint32_t box_inner, uint32_t box_rows);
 
 }  // namespace ess

@@ -128,9 +128,8 @@ __global__ void __launch_bounds__(kQuantThreads) quant_square_kernel(const Quant
 constexpr int kEpiWarps = 4, kScaleWarps = 4;
 constexpr int kTmaWarp = kEpiWarps + kScaleWarps, kProdMmaWarp = kTmaWarp + 1;
 constexpr int kProdThreads = (kProdMmaWarp + 1) * 32;
-constexpr uint32_t kWTile = 128 * 128;   // bytes of the weight's part of a stage
+constexpr uint32_t kATile = 128 * 128;   // bytes of the first operand's part of a stage
 constexpr int kMaxStages = 6;
-constexpr int kOutBlk = 32 * 128;        // a block of a pair's results: 32 tokens, 128 columns
 constexpr int kOverlap = 32;             // columns that the two accumulators of a pair share
 
 // Groups of K that one accumulator adds up when results are fp32.  The tensor core
@@ -143,9 +142,9 @@ constexpr int kSumGroups = 8;
 constexpr int prod_stages(int bn, bool pair, bool sums) {
   return pair ? 6 : bn <= 16 ? 6 : bn <= 32 ? 5 : bn <= 64 ? 4 : sums ? 6 : 3;
 }
-constexpr int prod_x_rows(int bn, bool pair) { return pair ? bn / 2 : bn; }   // of one CTA
+constexpr int prod_b_rows(int bn, bool pair) { return pair ? bn / 2 : bn; }   // a CTA's part of B
 constexpr uint32_t prod_stage_bytes(int bn, bool pair) {
-  return kWTile + prod_x_rows(bn, pair) * 128;
+  return kATile + prod_b_rows(bn, pair) * 128;
 }
 
 struct ProdMisc {
@@ -154,11 +153,20 @@ struct ProdMisc {
   uint64_t acc_full[2], acc_free[2];
   uint32_t tmem;
   int abort;
-  uint32_t cells[2][256];   // scale words on their way to all four scale warps
 };
+// Scales on their way to TMEM.  A piece is the 16 bytes of four groups of K (a round); a
+// fetch brings prod_run neighbouring pieces of each of the CTA's tokens and of its one
+// or two blocks of the weight, as L2 serves a whole line for the price of a piece (with
+// single pieces 8192 x 4096 x 8192 took 212 us).
+constexpr int prod_run(bool pair) { return pair ? 8 : 2; }
+constexpr int prod_fetches(bool pair) { return pair ? 2 : 3; }   // in flight or in use
+constexpr int prod_tokens(int bn, bool pair) { return pair ? 128 : bn; }   // of one CTA
+constexpr uint32_t prod_fetch_bytes(int bn, bool pair) {
+  return (prod_tokens(bn, pair) + (pair ? 2 : 1)) * prod_run(pair) * 16;
+}
 constexpr uint32_t prod_smem(int bn, bool pair, bool sums) {
-  return prod_stages(bn, pair, sums) * prod_stage_bytes(bn, pair) + (pair ? 4 * kOutBlk : 0) +
-         sizeof(ProdMisc) + 1024;
+  return prod_stages(bn, pair, sums) * prod_stage_bytes(bn, pair) +
+         prod_fetches(pair) * prod_fetch_bytes(bn, pair) + sizeof(ProdMisc);
 }
 
 struct ProdArgs {
@@ -168,7 +176,7 @@ struct ProdArgs {
   int m_tiles, n_tiles;
   void* out;
   long long stride;
-  bool blocks;            // a pair's results go through omap
+  bool runs;              // rows of out are multiples of 32 bytes, 32-byte aligned
   bool wide;              // rows of scales are multiples of 16 bytes, 16-byte aligned
   int* status;
 };
@@ -198,14 +206,6 @@ __device__ __forceinline__ bool prod_elect() {
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(p));
   return p != 0;
-}
-// a block of shared memory to global memory; what lies outside the tensor is left out
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-          reinterpret_cast<uint64_t>(m)),
-      "r"(src), "r"(x), "r"(y)
-      : "memory");
 }
 // arrive on a barrier of either CTA of a pair, behind everything before it
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
@@ -311,16 +311,32 @@ __device__ __forceinline__ void tmem_ld16(uint32_t t, float* v) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+// 32 bytes, 32-byte aligned, in one store
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
-// Four scales; groups past the last count as 1.  wide: rows of scales are 16-byte aligned
-__device__ __forceinline__ uint4 load_scales(const float* s, int left, bool wide) {
-  if (wide) return *reinterpret_cast<const uint4*>(s);   // then left is at least 4
-  const uint32_t* u = reinterpret_cast<const uint32_t*>(s);
-  return make_uint4(left > 0 ? u[0] : 0x3f800000u, left > 1 ? u[1] : 0x3f800000u,
-                    left > 2 ? u[2] : 0x3f800000u, left > 3 ? u[3] : 0x3f800000u);
+// Four scales from global to shared memory; groups past the last count as 1.  wide:
+// rows of scales are 16-byte aligned (then there are four).
+__device__ __forceinline__ void fetch_scales(uint8_t* to, const float* s, int left, bool wide) {
+  if (wide) {
+    cp_async16(smem_u32(to), s);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j < left)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to) + 4 * j),
+                   "l"(s + j)
+                   : "memory");
+    else
+      reinterpret_cast<float*>(to)[j] = 1.0f;
+  }
 }
 // Their exponent bytes.
 __device__ __forceinline__ uint32_t scale_word(const uint4& s, bool* bad) {
@@ -343,26 +359,24 @@ struct ProdShare {
 
 template <int BN, bool PAIR, typename Out>
 __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out) == 4) ? 1 : 2)
-    product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                   const __grid_constant__ CUtensorMap omap, const ProdArgs a) {
+    product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                   const ProdArgs a) {
   constexpr bool kSums = sizeof(Out) == 4;   // short sums, added up in registers
   static_assert(!(PAIR && kSums), "pairs have no registers for sums");
   constexpr int kStages = prod_stages(BN, PAIR, kSums);
   constexpr uint32_t kStage = prod_stage_bytes(BN, PAIR);
-  constexpr int kXRows = prod_x_rows(BN, PAIR);
+  constexpr int kBRows = prod_b_rows(BN, PAIR);
   constexpr int kAcc = BN < 32 ? 32 : BN;                   // columns of an accumulator
   constexpr uint32_t kAcc2 = PAIR ? kAcc - kOverlap : kSums ? kAcc : 0;   // the second one
   constexpr uint32_t kColSf = kAcc2 + kAcc;
-  constexpr int kXCols = BN < 32 ? 1 : BN / 32;             // scale columns of the tokens
-  constexpr uint32_t kSfBuf = 4 + (kXCols < 4 ? 4 : kXCols);
+  constexpr uint32_t kSfBuf = 4 + (BN <= 128 ? 4 : 8);      // columns of scales: A's, B's
   constexpr uint32_t kNeed = kColSf + 2 * kSfBuf;
   constexpr uint32_t kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
   static_assert(kNeed <= kCols, "TMEM columns");
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  uint16_t* blocks = reinterpret_cast<uint16_t*>(smem + kStages * kStage);   // of a pair
-  ProdMisc* mi = reinterpret_cast<ProdMisc*>(smem + kStages * kStage + (PAIR ? 4 * kOutBlk : 0));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* ring = smem + kStages * kStage;
+  constexpr uint32_t kFetch = prod_fetch_bytes(BN, PAIR);
+  ProdMisc* mi = reinterpret_cast<ProdMisc*>(ring + prod_fetches(PAIR) * kFetch);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t rank = cluster_ctarank();
@@ -381,9 +395,8 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
     }
     mi->abort = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&wmap);
-    tma_prefetch_desc(&xmap);
-    if (PAIR && a.blocks) tma_prefetch_desc(&omap);
+    tma_prefetch_desc(&amap);
+    tma_prefetch_desc(&bmap);
   }
   if (warp == kProdMmaWarp) prod_alloc<PAIR>(smem_u32(&mi->tmem), kCols);
   __syncwarp();
@@ -401,27 +414,29 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
   sh.step = static_cast<int>(gridDim.x / parts);
   sh.g0 = PAIR ? 0 : static_cast<int>(static_cast<long long>(a.groups) * rank / parts);
   sh.g1 = PAIR ? a.groups : static_cast<int>(static_cast<long long>(a.groups) * (rank + 1) / parts);
-  // tile -> first weight row and first token of this CTA
-  auto m_of = [&](int t) { return (t % a.m_tiles) * (PAIR ? 256 : 128) + (PAIR ? static_cast<int>(rank) * 128 : 0); };
-  auto n_of = [&](int t) { return (t / a.m_tiles) * BN; };
+  // tile -> first row of this CTA's A, first row of B
+  auto m_of = [&](int t) {
+    return PAIR ? (t / a.n_tiles) * 256 + static_cast<int>(rank) * 128 : (t % a.m_tiles) * 128;
+  };
+  auto n_of = [&](int t) { return (PAIR ? t % a.n_tiles : t / a.m_tiles) * BN; };
 
   if (warp == kTmaWarp) {
     if (prod_elect()) {
       int stage = 0, turn = 0;
       for (int t = sh.first; t < sh.tiles; t += sh.step) {
-        const int m0 = m_of(t), x0 = n_of(t) + (PAIR ? static_cast<int>(rank) * kXRows : 0);
+        const int m0 = m_of(t), n0 = n_of(t) + (PAIR ? static_cast<int>(rank) * kBRows : 0);
         for (int g = sh.g0; g < sh.g1; ++g) {
           if (turn > 0) prod_wait(&mi->empty[stage], (turn - 1) & 1, mi, a.status);
           const uint32_t dst = smem_u32(smem + stage * kStage), bar = smem_u32(&mi->full[stage]);
           if (PAIR) {
             if (rank == 0) mbar_arrive_expect_tx(bar, 2 * kStage);
             const uint32_t lead = dsmem_addr(bar, 0);
-            tma_load_2d_pair(dst, &wmap, lead, g * 128, m0);
-            tma_load_2d_pair(dst + kWTile, &xmap, lead, g * 128, x0);
+            tma_load_2d_pair(dst, &amap, lead, g * 128, m0);
+            tma_load_2d_pair(dst + kATile, &bmap, lead, g * 128, n0);
           } else {
             mbar_arrive_expect_tx(bar, kStage);
-            tma_load_2d(dst, &wmap, bar, g * 128, m0);
-            tma_load_2d(dst + kWTile, &xmap, bar, g * 128, x0);
+            tma_load_2d(dst, &amap, bar, g * 128, m0);
+            tma_load_2d(dst + kATile, &bmap, bar, g * 128, n0);
           }
           if (++stage == kStages) {
             stage = 0;
@@ -467,7 +482,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
           if (ok && lead) {
             const uint32_t at = smem_u32(smem + stage * kStage);
             const uint64_t dw = make_sdesc_sw128(at, 16, 1024);
-            const uint64_t dx = make_sdesc_sw128(at + kWTile, 16, 1024);
+            const uint64_t dx = make_sdesc_sw128(at + kATile, 16, 1024);
             const uint32_t idesc = mx_idesc(PAIR ? 256 : 128, BN, g & 3);
             const uint32_t sf = tmem + kColSf + sb * kSfBuf, acc = tmem + (i & 1) * kAcc2;
 #pragma unroll
@@ -496,44 +511,67 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
     const uint32_t ts = tmem + (static_cast<uint32_t>(q * 32) << 16) + kColSf;
     int sb = 0, sturn = 0;
     bool bad = false;
-    // Up to 64 tokens every warp loads all rows' scales.  Of more, a warp loads a
-    // quarter, and the words meet in shared memory: a load touches 32 lines.
-    constexpr bool kMeet = kXCols >= 4;
-    constexpr int kMine = kMeet ? kXCols / 4 : kXCols;
-    const uint4 one = make_uint4(0x3f800000u, 0x3f800000u, 0x3f800000u, 0x3f800000u);
-    const int s0 = sh.g0 >> 2, s1 = ((sh.g1 - 1) >> 2) + 1;
-    uint4 nw = one, nx[kMine];   // of the next four groups
-    auto load = [&](int t, int s) {
-      const float* ws = a.ws + static_cast<size_t>(min(m_of(t), a.outs - 1) >> 7) * a.groups;
-      nw = load_scales(ws + 4 * s, a.groups - 4 * s, a.wide);
-#pragma unroll
-      for (int c = 0; c < kMine; ++c) {
-        const int at = 32 * (kMeet ? q * kMine + c : c) + lane, row = n_of(t) + at;
-        nx[c] = row < a.n && at < BN ? load_scales(a.xs + static_cast<size_t>(row) * a.groups + 4 * s,
-                                                   a.groups - 4 * s, a.wide)
-                                     : one;
+    constexpr int kTok = prod_tokens(BN, PAIR), kRun = prod_run(PAIR), kFetches = prod_fetches(PAIR);
+    constexpr int kBlocks = PAIR ? 2 : 1, kTokCols = kTok < 32 ? 1 : kTok / 32;
+    const int s0 = sh.g0 >> 2, s1 = ((sh.g1 - 1) >> 2) + 1;   // rounds
+    const int me = q * 32 + lane;
+    int lt = sh.first, ls = s0, lslot = 0;   // what is fetched next
+    // piece p of row r lies at place p ^ (r % kRun): a warp's reads then meet all banks
+    auto fetch = [&] {
+      if (lt < sh.tiles) {
+        uint8_t* to = ring + lslot * kFetch;
+        const int f0 = PAIR ? n_of(lt) : m_of(lt), x0 = PAIR ? m_of(lt) : n_of(lt);
+#pragma unroll 1
+        for (int i = me; i < (kTok + kBlocks) * kRun; i += kScaleWarps * 32) {
+          const int r = i / kRun, p = i % kRun, s = ls / kRun * kRun + p;
+          if (s >= s1) continue;
+          uint8_t* at = to + (r * kRun + (p ^ (r & (kRun - 1)))) * 16;
+          const bool token = r < kTok;
+          if (token && x0 + r >= a.n) {
+            *reinterpret_cast<float4*>(at) = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+          } else {
+            const int row = token ? x0 + r : min(f0 + 128 * (r - kTok), a.outs - 1) >> 7;
+            fetch_scales(at, (token ? a.xs : a.ws) + static_cast<size_t>(row) * a.groups + 4 * s,
+                         a.groups - 4 * s, a.wide);
+          }
+        }
+        ls = ls / kRun * kRun + kRun;
+        if (ls >= s1) {
+          ls = s0;
+          lt += sh.step;
+        }
       }
+      cp_async_commit();
+      if (++lslot == kFetches) lslot = 0;
     };
-    if (sh.first < sh.tiles) load(sh.first, s0);
+    int slot = kFetches - 1;
+#pragma unroll
+    for (int i = 0; i < kFetches - 1; ++i) fetch();
     for (int t = sh.first; t < sh.tiles; t += sh.step) {
       for (int s = s0; s < s1; ++s) {
-        uint32_t w[4], x[kXCols];
-        w[0] = w[1] = w[2] = w[3] = scale_word(nw, &bad);
-#pragma unroll
-        for (int c = 0; c < kMine; ++c) x[c] = scale_word(nx[c], &bad);
-        if (s + 1 < s1) load(t, s + 1);
-        else if (t + sh.step < sh.tiles) load(t + sh.step, s0);
-        if (kMeet) {
-#pragma unroll
-          for (int c = 0; c < kMine; ++c) mi->cells[sb][32 * (q * kMine + c) + lane] = x[c];
+        if (s == s0 || s % kRun == 0) {
+          cp_async_wait<kFetches - 2>();
           asm volatile("bar.sync 1, %0;" ::"n"(kScaleWarps * 32) : "memory");
-#pragma unroll
-          for (int c = 0; c < kXCols; ++c) x[c] = mi->cells[sb][32 * c + lane];
+          fetch();   // into the place that every warp had read before the barrier
+          if (++slot == kFetches) slot = 0;
         }
+        const uint4* in = reinterpret_cast<const uint4*>(ring + slot * kFetch);
+        auto piece = [&](int r) { return in[r * kRun + ((s % kRun) ^ (r & (kRun - 1)))]; };
+        uint32_t w[8], x[kTokCols];
+        w[0] = w[1] = w[2] = w[3] = scale_word(piece(kTok), &bad);
+        if (PAIR) w[4] = w[5] = w[6] = w[7] = scale_word(piece(kTok + kBlocks - 1), &bad);
+#pragma unroll
+        for (int c = 0; c < kTokCols; ++c)
+          x[c] = scale_word(piece(kTok < 32 ? lane % kTok : 32 * c + lane), &bad);
         if (sturn > 0) prod_wait(&mi->sf_empty[sb], (sturn - 1) & 1, mi, a.status);
         tc_fence_after();
-        tmem_put<4>(ts + sb * kSfBuf, w);
-        tmem_put<kXCols>(ts + sb * kSfBuf + 4, x);
+        if (PAIR) {
+          tmem_put<kTokCols>(ts + sb * kSfBuf, x);
+          tmem_put<8>(ts + sb * kSfBuf + 4, w);
+        } else {
+          tmem_put<4>(ts + sb * kSfBuf, w);
+          tmem_put<kTokCols>(ts + sb * kSfBuf + 4, x);
+        }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
@@ -551,9 +589,10 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
       const int last = i < sb ? sturn : sturn - 1;
       if (last >= 0) prod_wait(&mi->sf_empty[i], last & 1, mi, a.status);
     }
+    cp_async_wait<0>();
     if (q == 0 && bad) set_status(a.status, ESS_ERR_DEVICE_CHECK);
   } else {
-    // epilogue: lane l of warp q holds output column 32 q + l
+    // epilogue: lane l of warp q holds output column 32 q + l (a pair's: token 32 q + l)
     constexpr int kBlocks = kAcc / 32, kLive = BN < 32 ? BN : 32;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     auto store = [&](int t, int b, const float* v) {
@@ -602,7 +641,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
         else store(sh.first, b, sum + 32 * b);
       }
     } else {
-      int i = 0, turn = 0;
+      int i = 0;
       for (int t = sh.first; t < sh.tiles; t += sh.step, ++i) {
         prod_wait(&mi->acc_full[i & 1], (i >> 1) & 1, mi, a.status);
         tc_fence_after();
@@ -620,29 +659,31 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
           }
           if (!PAIR && parts > 1) {
             send(b, v);
-          } else if (PAIR && a.blocks) {
-            // Through shared memory, so that a token's 128 columns leave together:
-            // stored from here, in runs of 64 bytes, a tile took 19500 cycles.
-            uint16_t* o = blocks + (turn & 1) * kOutBlk;
-            if (tid == 0) bulk_wait_read<1>();   // the block before the last one has left
-            asm volatile("bar.sync 2, %0;" ::"n"(kEpiWarps * 32) : "memory");
+          } else if (PAIR) {
+            // lane l of warp q holds a token, the columns are neighbours: two sectors
+            const int tok = m_of(t) + warp * 32 + lane, f = n_of(t) + 32 * b;
+            if (tok < a.n) {
+              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + tok * a.stride + f;
+              if (a.runs && f + 32 <= a.outs) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              o[c * 128 + warp * 32 + lane] = static_cast<uint16_t>(bf16_bits(v[c]));
-            fence_proxy_async_smem();
-            asm volatile("bar.sync 2, %0;" ::"n"(kEpiWarps * 32) : "memory");
-            if (tid == 0) {
-              if (m_of(t) < a.outs && n_of(t) + 32 * b < a.n)
-                tma_store_2d(&omap, smem_u32(o), m_of(t), n_of(t) + 32 * b);
-              bulk_commit();
+                for (int h = 0; h < 2; ++h) {
+                  uint32_t p[8];
+#pragma unroll
+                  for (int c = 0; c < 8; ++c)
+                    p[c] = bf16x2_bits(v[16 * h + 2 * c], v[16 * h + 2 * c + 1]);
+                  st_global_32(o + 16 * h, p);
+                }
+              } else {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (f + c < a.outs) o[c] = __float2bfloat16_rn(v[c]);
+              }
             }
-            ++turn;
           } else {
             store(t, b, v);
           }
         }
       }
-      if (PAIR && a.blocks && tid == 0) bulk_wait_all();
     }
   }
 
@@ -673,8 +714,8 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
 }
 
 template <int BN, bool PAIR, typename Out>
-cudaError_t launch_product(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& o,
-                           const ProdArgs& a, int parts, int ctas, int dev, cudaStream_t st) {
+cudaError_t launch_product(const CUtensorMap& am, const CUtensorMap& bm, const ProdArgs& a,
+                           int parts, int ctas, int dev, cudaStream_t st) {
   auto kernel = product_kernel<BN, PAIR, Out>;
   constexpr uint32_t kSmem = prod_smem(BN, PAIR, sizeof(Out) == 4);
   static std::atomic<unsigned long long> done{0};   // allowed once per device
@@ -700,14 +741,14 @@ cudaError_t launch_product(const CUtensorMap& w, const CUtensorMap& x, const CUt
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 3;
-  return cudaLaunchKernelEx(&cfg, kernel, w, x, o, a);
+  return cudaLaunchKernelEx(&cfg, kernel, am, bm, a);
 }
 
 template <int BN>
 cudaError_t launch_single(bool fp32, const CUtensorMap& w, const CUtensorMap& x, const ProdArgs& a,
                           int parts, int ctas, int dev, cudaStream_t st) {
-  return fp32 ? launch_product<BN, false, float>(w, x, w, a, parts, ctas, dev, st)
-              : launch_product<BN, false, __nv_bfloat16>(w, x, w, a, parts, ctas, dev, st);
+  return fp32 ? launch_product<BN, false, float>(w, x, a, parts, ctas, dev, st)
+              : launch_product<BN, false, __nv_bfloat16>(w, x, a, parts, ctas, dev, st);
 }
 
 int sms_of(int dev) {
@@ -812,8 +853,8 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   const long long pair_tiles = static_cast<long long>(cover(outs, 256)) * cover(n, 256);
   const bool pair = !fp32 && n > 128 && pair_tiles >= sms / 2;
   const int bn = pair ? 256 : n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : 128;
-  a.m_tiles = cover(outs, pair ? 256 : 128);
-  a.n_tiles = cover(n, bn);
+  a.m_tiles = pair ? cover(n, 256) : cover(outs, 128);
+  a.n_tiles = pair ? cover(outs, 256) : cover(n, bn);
   const long long tiles = static_cast<long long>(a.m_tiles) * a.n_tiles;
   if (tiles > 0x3fffffffLL) return ESS_ERR_UNSUPPORTED;
   int parts = 1, ctas;
@@ -824,20 +865,16 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
     while (parts < 8 && tiles * parts * 2 <= slots && a.groups >= 4 * parts) parts *= 2;
     ctas = static_cast<int>(tiles) * parts;
   }
-  CUtensorMap wm, xm, om;
+  CUtensorMap wm, xm;
   if (!encode_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, ins, outs, ins, 128, 128) ||
       !encode_map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, ins, n, ins, 128, pair ? 128 : bn))
     return ESS_ERR_CUDA;
-  a.blocks = pair && aligned16(out) && out_stride % 8 == 0;
-  if (a.blocks &&
-      !encode_map_2d(&om, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, outs, n,
-                     static_cast<uint64_t>(out_stride) * 2, 128, 32, false))
-    return ESS_ERR_CUDA;
+  a.runs = aligned_to(out, 32) && out_stride % 16 == 0;
   if (!fp32 && outs <= 64) ++key_norms();   // rows of 64 bf16 values may be indexer keys too
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   const bool f = fp32 != 0;
-  if (pair) e = launch_product<256, true, __nv_bfloat16>(wm, xm, a.blocks ? om : wm, a, parts, ctas, dev, st);
+  if (pair) e = launch_product<256, true, __nv_bfloat16>(xm, wm, a, parts, ctas, dev, st);
   else if (bn == 16) e = launch_single<16>(f, wm, xm, a, parts, ctas, dev, st);
   else if (bn == 32) e = launch_single<32>(f, wm, xm, a, parts, ctas, dev, st);
   else if (bn == 64) e = launch_single<64>(f, wm, xm, a, parts, ctas, dev, st);
