@@ -130,6 +130,7 @@ constexpr int kTmaWarp = kEpiWarps + kScaleWarps, kProdMmaWarp = kTmaWarp + 1;
 constexpr int kProdThreads = (kProdMmaWarp + 1) * 32;
 constexpr uint32_t kATile = 128 * 128;   // bytes of the first operand's part of a stage
 constexpr int kMaxStages = 6;
+constexpr uint32_t kOutBlock = 32 * 128;  // results on their way out: 32 tokens, 64 columns
 constexpr int kOverlap = 32;             // columns that the two accumulators of a pair share
 
 // Groups of K that one accumulator adds up when results are fp32.  The tensor core
@@ -158,7 +159,7 @@ struct ProdMisc {
 // fetch brings prod_run neighbouring pieces of each of the CTA's tokens and of its one
 // or two blocks of the weight, as L2 serves a whole line for the price of a piece (with
 // single pieces 8192 x 4096 x 8192 took 212 us).
-constexpr int prod_run(bool pair) { return pair ? 8 : 2; }
+constexpr int prod_run(bool pair) { return pair ? 4 : 2; }
 constexpr int prod_fetches(bool pair) { return pair ? 2 : 3; }   // in flight or in use
 constexpr int prod_tokens(int bn, bool pair) { return pair ? 128 : bn; }   // of one CTA
 constexpr uint32_t prod_fetch_bytes(int bn, bool pair) {
@@ -166,7 +167,8 @@ constexpr uint32_t prod_fetch_bytes(int bn, bool pair) {
 }
 constexpr uint32_t prod_smem(int bn, bool pair, bool sums) {
   return prod_stages(bn, pair, sums) * prod_stage_bytes(bn, pair) +
-         prod_fetches(pair) * prod_fetch_bytes(bn, pair) + sizeof(ProdMisc);
+         prod_fetches(pair) * prod_fetch_bytes(bn, pair) + (pair ? kEpiWarps * kOutBlock : 0) +
+         sizeof(ProdMisc);
 }
 
 struct ProdArgs {
@@ -176,7 +178,7 @@ struct ProdArgs {
   int m_tiles, n_tiles;
   void* out;
   long long stride;
-  bool runs;              // rows of out are multiples of 32 bytes, 32-byte aligned
+  bool blocks;            // a pair's results leave through omap
   bool wide;              // rows of scales are multiples of 16 bytes, 16-byte aligned
   int* status;
 };
@@ -206,6 +208,14 @@ __device__ __forceinline__ bool prod_elect() {
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(p));
   return p != 0;
+}
+// a block of shared memory to global memory; what lies outside the tensor is left out
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(m)),
+      "r"(src), "r"(x), "r"(y)
+      : "memory");
 }
 // arrive on a barrier of either CTA of a pair, behind everything before it
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
@@ -311,12 +321,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t t, float* v) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-// 32 bytes, 32-byte aligned, in one store
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
 __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
@@ -360,7 +364,7 @@ struct ProdShare {
 template <int BN, bool PAIR, typename Out>
 __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out) == 4) ? 1 : 2)
     product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
-                   const ProdArgs a) {
+                   const __grid_constant__ CUtensorMap omap, const ProdArgs a) {
   constexpr bool kSums = sizeof(Out) == 4;   // short sums, added up in registers
   static_assert(!(PAIR && kSums), "pairs have no registers for sums");
   constexpr int kStages = prod_stages(BN, PAIR, kSums);
@@ -376,7 +380,13 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + kStages * kStage;
   constexpr uint32_t kFetch = prod_fetch_bytes(BN, PAIR);
-  ProdMisc* mi = reinterpret_cast<ProdMisc*>(ring + prod_fetches(PAIR) * kFetch);
+  uint8_t* blocks = smem;   // of a pair: behind the stages, at multiples of 1024
+  ProdMisc* mi;
+  if (PAIR) {
+    blocks = smem + kStages * kStage;
+    ring = blocks + kEpiWarps * kOutBlock;
+  }
+  mi = reinterpret_cast<ProdMisc*>(ring + prod_fetches(PAIR) * kFetch);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t rank = cluster_ctarank();
@@ -397,6 +407,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
     fence_mbar_init();
     tma_prefetch_desc(&amap);
     tma_prefetch_desc(&bmap);
+    if (PAIR && a.blocks) tma_prefetch_desc(&omap);
   }
   if (warp == kProdMmaWarp) prod_alloc<PAIR>(smem_u32(&mi->tmem), kCols);
   __syncwarp();
@@ -416,7 +427,8 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
   sh.g1 = PAIR ? a.groups : static_cast<int>(static_cast<long long>(a.groups) * (rank + 1) / parts);
   // tile -> first row of this CTA's A, first row of B
   auto m_of = [&](int t) {
-    return PAIR ? (t / a.n_tiles) * 256 + static_cast<int>(rank) * 128 : (t % a.m_tiles) * 128;
+    return PAIR ? (t / a.n_tiles) * 256 + static_cast<int>(rank) * 128
+                : (t % a.m_tiles) * 128;
   };
   auto n_of = [&](int t) { return (PAIR ? t % a.n_tiles : t / a.m_tiles) * BN; };
 
@@ -660,30 +672,41 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
           if (!PAIR && parts > 1) {
             send(b, v);
           } else if (PAIR) {
-            // lane l of warp q holds a token, the columns are neighbours: two sectors
+            // Lane l of warp q holds a token.  Its columns go through shared memory, 64 at
+            // a time, so that they leave in whole lines: L2 serves a line for the price of
+            // a sector, and stored from here they cost 173 us instead of 150.
             const int tok = m_of(t) + warp * 32 + lane, f = n_of(t) + 32 * b;
-            if (tok < a.n) {
-              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + tok * a.stride + f;
-              if (a.runs && f + 32 <= a.outs) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  uint32_t p[8];
-#pragma unroll
-                  for (int c = 0; c < 8; ++c)
-                    p[c] = bf16x2_bits(v[16 * h + 2 * c], v[16 * h + 2 * c + 1]);
-                  st_global_32(o + 16 * h, p);
-                }
-              } else {
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  if (f + c < a.outs) o[c] = __float2bfloat16_rn(v[c]);
+            if (a.blocks) {
+              uint8_t* o = blocks + warp * kOutBlock;
+              if ((j & 1) == 0) {   // the block before has left
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
               }
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<uint4*>(o + sw128_off(lane, 4 * (b & 1) + c)) =
+                    pack8_bf16(v + 8 * c);
+              if ((j & 1) == 1) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                const int f0 = n_of(t) + 32 * (b & ~1), t0 = m_of(t) + warp * 32;
+                if (lane == 0) {
+                  if (f0 < a.outs && t0 < a.n) tma_store_2d(&omap, smem_u32(o), f0, t0);
+                  bulk_commit();
+                }
+              }
+            } else if (tok < a.n) {
+              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + tok * a.stride + f;
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (f + c < a.outs) o[c] = __float2bfloat16_rn(v[c]);
             }
           } else {
             store(t, b, v);
           }
         }
       }
+      if (PAIR && a.blocks && lane == 0) bulk_wait_all();
     }
   }
 
@@ -714,8 +737,8 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
 }
 
 template <int BN, bool PAIR, typename Out>
-cudaError_t launch_product(const CUtensorMap& am, const CUtensorMap& bm, const ProdArgs& a,
-                           int parts, int ctas, int dev, cudaStream_t st) {
+cudaError_t launch_product(const CUtensorMap& am, const CUtensorMap& bm, const CUtensorMap& om,
+                           const ProdArgs& a, int parts, int ctas, int dev, cudaStream_t st) {
   auto kernel = product_kernel<BN, PAIR, Out>;
   constexpr uint32_t kSmem = prod_smem(BN, PAIR, sizeof(Out) == 4);
   static std::atomic<unsigned long long> done{0};   // allowed once per device
@@ -741,14 +764,14 @@ cudaError_t launch_product(const CUtensorMap& am, const CUtensorMap& bm, const P
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 3;
-  return cudaLaunchKernelEx(&cfg, kernel, am, bm, a);
+  return cudaLaunchKernelEx(&cfg, kernel, am, bm, om, a);
 }
 
 template <int BN>
 cudaError_t launch_single(bool fp32, const CUtensorMap& w, const CUtensorMap& x, const ProdArgs& a,
                           int parts, int ctas, int dev, cudaStream_t st) {
-  return fp32 ? launch_product<BN, false, float>(w, x, a, parts, ctas, dev, st)
-              : launch_product<BN, false, __nv_bfloat16>(w, x, a, parts, ctas, dev, st);
+  return fp32 ? launch_product<BN, false, float>(w, x, w, a, parts, ctas, dev, st)
+              : launch_product<BN, false, __nv_bfloat16>(w, x, w, a, parts, ctas, dev, st);
 }
 
 int sms_of(int dev) {
@@ -865,16 +888,20 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
     while (parts < 8 && tiles * parts * 2 <= slots && a.groups >= 4 * parts) parts *= 2;
     ctas = static_cast<int>(tiles) * parts;
   }
-  CUtensorMap wm, xm;
+  CUtensorMap wm, xm, om;
   if (!encode_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, ins, outs, ins, 128, 128) ||
       !encode_map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, ins, n, ins, 128, pair ? 128 : bn))
     return ESS_ERR_CUDA;
-  a.runs = aligned_to(out, 32) && out_stride % 16 == 0;
+  a.blocks = pair && aligned16(out) && out_stride % 8 == 0;
+  if (!a.blocks) om = wm;   // not used
+  else if (!encode_map_2d(&om, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, outs, n,
+                          static_cast<uint64_t>(out_stride) * 2, 64, 32))
+    return ESS_ERR_CUDA;
   if (!fp32 && outs <= 64) ++key_norms();   // rows of 64 bf16 values may be indexer keys too
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   const bool f = fp32 != 0;
-  if (pair) e = launch_product<256, true, __nv_bfloat16>(xm, wm, a, parts, ctas, dev, st);
+  if (pair) e = launch_product<256, true, __nv_bfloat16>(xm, wm, om, a, parts, ctas, dev, st);
   else if (bn == 16) e = launch_single<16>(f, wm, xm, a, parts, ctas, dev, st);
   else if (bn == 32) e = launch_single<32>(f, wm, xm, a, parts, ctas, dev, st);
   else if (bn == 64) e = launch_single<64>(f, wm, xm, a, parts, ctas, dev, st);
