@@ -140,8 +140,8 @@ constexpr int kOverlap = 32;             // columns that the two accumulators of
 // results (2^-9) the whole of K is one sum.
 constexpr int kSumGroups = 8;
 
-constexpr int prod_stages(int bn, bool pair, bool sums) {
-  return pair ? 6 : bn <= 16 ? 6 : bn <= 32 ? 5 : bn <= 64 ? 4 : sums ? 6 : 3;
+constexpr int prod_stages(int bn, bool pair) {
+  return pair ? 6 : bn <= 16 ? 5 : bn <= 32 ? 4 : bn <= 64 ? 3 : 4;
 }
 constexpr int prod_b_rows(int bn, bool pair) { return pair ? bn / 2 : bn; }   // a CTA's part of B
 constexpr uint32_t prod_stage_bytes(int bn, bool pair) {
@@ -152,6 +152,7 @@ struct ProdMisc {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t sf_full[2], sf_empty[2];
   uint64_t acc_full[2], acc_free[2];
+  uint64_t sums_here;
   uint32_t tmem;
   int abort;
 };
@@ -165,9 +166,9 @@ constexpr int prod_tokens(int bn, bool pair) { return pair ? 128 : bn; }   // of
 constexpr uint32_t prod_fetch_bytes(int bn, bool pair) {
   return (prod_tokens(bn, pair) + (pair ? 2 : 1)) * prod_run(pair) * 16;
 }
-constexpr uint32_t prod_smem(int bn, bool pair, bool sums) {
-  return prod_stages(bn, pair, sums) * prod_stage_bytes(bn, pair) +
-         prod_fetches(pair) * prod_fetch_bytes(bn, pair) + (pair ? kEpiWarps * kOutBlock : 0) +
+constexpr uint32_t prod_smem(int bn, bool pair) {
+  return prod_stages(bn, pair) * prod_stage_bytes(bn, pair) +
+         prod_fetches(pair) * prod_fetch_bytes(bn, pair) + (pair ? kEpiWarps * kOutBlock : bn * 512) +
          sizeof(ProdMisc);
 }
 
@@ -321,8 +322,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t t, float* v) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+// shared memory of this CTA -> of another one of the cluster, counted on its barrier
+__device__ __forceinline__ void bulk_to_cta(uint32_t cluster_dst, uint32_t src, uint32_t bytes,
+                                            uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+      "[%3];" ::"r"(cluster_dst),
+      "r"(src), "r"(bytes), "r"(cluster_bar)
+      : "memory");
 }
 
 // Four scales from global to shared memory; groups past the last count as 1.  wide:
@@ -367,7 +374,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
                    const __grid_constant__ CUtensorMap omap, const ProdArgs a) {
   constexpr bool kSums = sizeof(Out) == 4;   // short sums, added up in registers
   static_assert(!(PAIR && kSums), "pairs have no registers for sums");
-  constexpr int kStages = prod_stages(BN, PAIR, kSums);
+  constexpr int kStages = prod_stages(BN, PAIR);
   constexpr uint32_t kStage = prod_stage_bytes(BN, PAIR);
   constexpr int kBRows = prod_b_rows(BN, PAIR);
   constexpr int kAcc = BN < 32 ? 32 : BN;                   // columns of an accumulator
@@ -378,15 +385,13 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
   constexpr uint32_t kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
   static_assert(kNeed <= kCols, "TMEM columns");
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* ring = smem + kStages * kStage;
+  uint8_t* ring;            // of scales
   constexpr uint32_t kFetch = prod_fetch_bytes(BN, PAIR);
-  uint8_t* blocks = smem;   // of a pair: behind the stages, at multiples of 1024
-  ProdMisc* mi;
-  if (PAIR) {
-    blocks = smem + kStages * kStage;
-    ring = blocks + kEpiWarps * kOutBlock;
-  }
-  mi = reinterpret_cast<ProdMisc*>(ring + prod_fetches(PAIR) * kFetch);
+  // a pair's results on their way out (at multiples of 1024), or the sums of a tile's
+  // tokens [part][token of this CTA's share][128] from the cluster's CTAs
+  uint8_t* blocks = smem + kStages * kStage;
+  ring = blocks + (PAIR ? kEpiWarps * kOutBlock : BN * 512);
+  ProdMisc* mi = reinterpret_cast<ProdMisc*>(ring + prod_fetches(PAIR) * kFetch);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t rank = cluster_ctarank();
@@ -403,8 +408,10 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
       mbar_init(smem_u32(&mi->acc_full[i]), 1);
       mbar_init(smem_u32(&mi->acc_free[i]), kEpiWarps * (PAIR ? 2 : 1));
     }
+    mbar_init(smem_u32(&mi->sums_here), 1);
     mi->abort = 0;
     fence_mbar_init();
+    if (!PAIR && parts > 1) mbar_arrive_expect_tx(smem_u32(&mi->sums_here), BN * 512);
     tma_prefetch_desc(&amap);
     tma_prefetch_desc(&bmap);
     if (PAIR && a.blocks) tma_prefetch_desc(&omap);
@@ -616,16 +623,20 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
       for (int c = 0; c < kLive; ++c)
         if (c < left) o[c * a.stride] = static_cast<Out>(v[c]);
     };
-    // this part's sums of a block of tokens, to the CTAs that add them up
-    auto send = [&](int b, const float* v) {
-      constexpr int kLogBn = BN == 16 ? 4 : BN == 32 ? 5 : BN == 64 ? 6 : BN == 128 ? 7 : 8;
-      const int lg = 31 - __clz(static_cast<int>(parts)), share = BN >> lg;
-      const uint32_t to = smem_u32(smem) + (rank * share * 128 + warp * 32 + lane) * 4;
+    // This part's sums of a block of tokens, into the stages, which nothing uses any
+    // more, and from there to the CTAs that add them up, [token][128] floats.
+    auto keep = [&](int b, const float* v) {
+      float* o = reinterpret_cast<float*>(smem) + 32 * b * 128 + warp * 32 + lane;
 #pragma unroll
-      for (int c = 0; c < kLive; ++c) {
-        const int tok = 32 * b + c;
-        st_cluster_f32(dsmem_addr(to + (tok & (share - 1)) * 512, tok >> (kLogBn - lg)), v[c]);
-      }
+      for (int c = 0; c < kLive; ++c) o[c * 128] = v[c];
+    };
+    auto send = [&] {
+      fence_proxy_async_smem();
+      asm volatile("bar.sync 2, %0;" ::"n"(kEpiWarps * 32) : "memory");
+      const uint32_t bytes = BN * 512 / parts;
+      if (tid < static_cast<int>(parts))
+        bulk_to_cta(dsmem_addr(smem_u32(blocks) + rank * bytes, tid), smem_u32(smem) + tid * bytes,
+                    bytes, dsmem_addr(smem_u32(&mi->sums_here), tid));
     };
     if (kSums) {
       float sum[kAcc];
@@ -646,18 +657,17 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&mi->acc_free[i & 1]));
       }
-      if (parts > 1) cluster_sync();
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
-        if (parts > 1) send(b, sum + 32 * b);
+        if (parts > 1) keep(b, sum + 32 * b);
         else store(sh.first, b, sum + 32 * b);
       }
+      if (parts > 1) send();
     } else {
       int i = 0;
       for (int t = sh.first; t < sh.tiles; t += sh.step, ++i) {
         prod_wait(&mi->acc_full[i & 1], (i >> 1) & 1, mi, a.status);
         tc_fence_after();
-        if (!PAIR && parts > 1) cluster_sync();   // one tile a CTA
 #pragma unroll 1
         for (int j = 0; j < kBlocks; ++j) {
           // the columns that the next tile's accumulator shares come first
@@ -670,58 +680,58 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
             if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&mi->acc_free[0]), 0));
           }
           if (!PAIR && parts > 1) {
-            send(b, v);
+            keep(b, v);
           } else if (PAIR) {
             // Lane l of warp q holds a token.  Its columns go through shared memory, 64 at
             // a time, so that they leave in whole lines: L2 serves a line for the price of
-            // a sector, and stored from here they cost 173 us instead of 150.
-            const int tok = m_of(t) + warp * 32 + lane, f = n_of(t) + 32 * b;
-            if (a.blocks) {
-              uint8_t* o = blocks + warp * kOutBlock;
-              if ((j & 1) == 0) {   // the block before has left
-                if (lane == 0) bulk_wait_read<0>();
-                __syncwarp();
-              }
+            // a sector, and 64 bytes a token at a time took 190 us instead of 183.
+            uint8_t* o = blocks + warp * kOutBlock;
+            if ((j & 1) == 0) {   // the block before has left
+              if (a.blocks && lane == 0) bulk_wait_read<0>();
+              __syncwarp();
+            }
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                *reinterpret_cast<uint4*>(o + sw128_off(lane, 4 * (b & 1) + c)) =
-                    pack8_bf16(v + 8 * c);
-              if ((j & 1) == 1) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                const int f0 = n_of(t) + 32 * (b & ~1), t0 = m_of(t) + warp * 32;
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4*>(o + sw128_off(lane, 4 * (b & 1) + c)) = pack8_bf16(v + 8 * c);
+            if ((j & 1) == 1) {
+              const int f0 = n_of(t) + 32 * (b & ~1), t0 = m_of(t) + warp * 32;
+              if (a.blocks) fence_proxy_async_smem();
+              __syncwarp();
+              if (a.blocks) {
                 if (lane == 0) {
                   if (f0 < a.outs && t0 < a.n) tma_store_2d(&omap, smem_u32(o), f0, t0);
                   bulk_commit();
                 }
-              }
-            } else if (tok < a.n) {
-              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + tok * a.stride + f;
+              } else {
+                // rows that TMA does not take (not multiples of 16 bytes)
+                for (int r = 0; r < min(32, a.n - t0); ++r) {
+                  uint16_t* row = static_cast<uint16_t*>(a.out) + (t0 + r) * a.stride + f0;
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (f + c < a.outs) o[c] = __float2bfloat16_rn(v[c]);
+                  for (int c = lane; c < 64; c += 32)
+                    if (f0 + c < a.outs)
+                      row[c] = *reinterpret_cast<uint16_t*>(o + sw128_off(r, c >> 3) + (c & 7) * 2);
+                }
+              }
             }
           } else {
             store(t, b, v);
           }
         }
+        if (!PAIR && parts > 1) send();
       }
       if (PAIR && a.blocks && lane == 0) bulk_wait_all();
     }
   }
 
   if (!PAIR && parts > 1) {
-    // The cluster's CTAs hold the same tile's sums over their parts of K: each adds
-    // up the tokens [BN rank / parts, BN (rank + 1) / parts), in the order of the
-    // parts, in the ring, which nothing uses any more once all have their sums.
-    __syncwarp();
-    if (warp >= kEpiWarps) cluster_sync();   // all have their sums (see the epilogue)
-    cluster_sync();                          // all have sent them
+    // The cluster's CTAs held the same tile's sums over their parts of K: each adds up
+    // the tokens [BN rank / parts, BN (rank + 1) / parts), in the order of the parts.
+    prod_wait(&mi->sums_here, 0, mi, a.status);
     const int share = BN / static_cast<int>(parts);
     const int f = m_of(sh.first) + (tid & 127);
     const int x0 = n_of(sh.first) + static_cast<int>(rank) * share;
     if (tid < 256 && f < a.outs) {
-      const float* in = reinterpret_cast<const float*>(smem) + (tid & 127);
+      const float* in = reinterpret_cast<const float*>(blocks) + (tid & 127);
       for (int c = tid >> 7; c < share && x0 + c < a.n; c += 2) {
         float s = in[c * 128];
         for (uint32_t p = 1; p < parts; ++p) s += in[(p * share + c) * 128];
@@ -740,7 +750,7 @@ template <int BN, bool PAIR, typename Out>
 cudaError_t launch_product(const CUtensorMap& am, const CUtensorMap& bm, const CUtensorMap& om,
                            const ProdArgs& a, int parts, int ctas, int dev, cudaStream_t st) {
   auto kernel = product_kernel<BN, PAIR, Out>;
-  constexpr uint32_t kSmem = prod_smem(BN, PAIR, sizeof(Out) == 4);
+  constexpr uint32_t kSmem = prod_smem(BN, PAIR);
   static std::atomic<unsigned long long> done{0};   // allowed once per device
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
   if (!(done.load(std::memory_order_relaxed) & bit)) {
@@ -873,9 +883,12 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   a.wide = a.groups % 4 == 0 && aligned16(x_scales) && aligned16(w_scales);
   a.status = status;
   auto cover = [](long long v, int by) { return static_cast<int>((v + by - 1) / by); };
+  // Pairs from a quarter of the SMs on (us): 512 x 4096 x 8192, 64 tiles, 18.3, in tiles
+  // of 128 x 64 31.2; 256 x 4096 x 8192, 32 tiles, 17.0 against 16.4; 1024 x 4096 x 1600,
+  // 28 tiles, 17.2 against 16.2.
   const long long pair_tiles = static_cast<long long>(cover(outs, 256)) * cover(n, 256);
-  const bool pair = !fp32 && n > 128 && pair_tiles >= sms / 2;
-  const int bn = pair ? 256 : n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : 128;
+  const bool pair = !fp32 && n > 128 && pair_tiles >= sms / 4;
+  const int bn = pair ? 256 : n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 || !fp32 ? 64 : 128;
   a.m_tiles = pair ? cover(n, 256) : cover(outs, 128);
   a.n_tiles = pair ? cover(outs, 256) : cover(n, bn);
   const long long tiles = static_cast<long long>(a.m_tiles) * a.n_tiles;
@@ -884,6 +897,9 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   if (pair) {
     ctas = 2 * static_cast<int>(std::min<long long>(tiles, sms / 2));
   } else {
+    // K is cut until every CTA slot is taken or a CTA has two to three stages: 4 x 4096 x
+    // 1600 takes 10.5 us uncut, 7.2 in two parts, 5.1 in four, 4.1 in eight; 128 x 4096 x
+    // 8192 12.8, 13.2, 13.1.
     const int slots = (bn == 128 && fp32 ? 1 : 2) * sms;   // CTAs that run at once
     while (parts < 8 && tiles * parts * 2 <= slots && a.groups >= 4 * parts) parts *= 2;
     ctas = static_cast<int>(tiles) * parts;
@@ -905,7 +921,7 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   else if (bn == 16) e = launch_single<16>(f, wm, xm, a, parts, ctas, dev, st);
   else if (bn == 32) e = launch_single<32>(f, wm, xm, a, parts, ctas, dev, st);
   else if (bn == 64) e = launch_single<64>(f, wm, xm, a, parts, ctas, dev, st);
-  else e = launch_single<128>(f, wm, xm, a, parts, ctas, dev, st);
+  else e = launch_product<128, false, float>(wm, xm, wm, a, parts, ctas, dev, st);
   return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
 }
 
