@@ -180,6 +180,7 @@ struct ProdArgs {
   void* out;
   long long stride;
   bool blocks;            // a pair's results leave through omap
+  bool keys;              // the results may be indexer keys: nothing starts early
   bool wide;              // rows of scales are multiples of 16 bytes, 16-byte aligned
   int* status;
 };
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
   tc_fence_after();
   const uint32_t tmem = mi->tmem;
   pdl_wait_previous();
-  pdl_launch_dependents();
+  if (!a.keys) pdl_launch_dependents();
 
   ProdShare sh;
   sh.tiles = a.m_tiles * a.n_tiles;
@@ -820,8 +821,7 @@ ess_status ess_quant(const void* x, int64_t x_stride, int64_t n, int32_t dim, in
   a.groups = (dim - 1) / 128 + 1;
   a.codes = static_cast<uint8_t*>(codes);
   a.scales = scales;
-  a.mul = 0;
-  a.shift = -1;
+  fast_divisor(a.groups, &a.mul, &a.shift);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (square) {
     const long long high = (n + 127) / 128;
@@ -832,13 +832,6 @@ ess_status ess_quant(const void* x, int64_t x_stride, int64_t n, int32_t dim, in
                : ESS_ERR_CUDA;
   }
   if (dim <= 128) ++key_norms();   // the next indexer of each layer waits
-  if (a.groups > 1) {
-    // i / groups for i < 2^31: ceil(2^(32 + shift) / groups) with 2^shift < groups <= 2^(shift + 1)
-    int s = 0;
-    while ((2 << s) < a.groups) ++s;
-    a.shift = s;
-    a.mul = static_cast<uint32_t>(((1ull << (32 + s)) + a.groups - 1) / a.groups);
-  }
   // rows of one launch: below 2^30 groups
   const int most = static_cast<int>(std::max(1LL, (1LL << 30) / a.groups));
   for (long long r = 0; r < n; r += most) {
@@ -908,12 +901,15 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   if (!encode_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, ins, outs, ins, 128, 128) ||
       !encode_map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, ins, n, ins, 128, pair ? 128 : bn))
     return ESS_ERR_CUDA;
-  a.blocks = pair && aligned16(out) && out_stride % 8 == 0;
+  // (a row's end has to be one of 16 bytes too: TMA cuts a block off there, not within)
+  a.blocks = pair && aligned16(out) && out_stride % 8 == 0 && outs % 8 == 0;
   if (!a.blocks) om = wm;   // not used
   else if (!encode_map_2d(&om, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, outs, n,
                           static_cast<uint64_t>(out_stride) * 2, 64, 32))
     return ESS_ERR_CUDA;
-  if (!fp32 && outs <= 64) ++key_norms();   // rows of 64 bf16 values may be indexer keys too
+  // rows of 64 bf16 values may be indexer keys, which an indexer loads ahead of its wait
+  a.keys = !fp32 && outs <= 64;
+  if (a.keys) ++key_norms();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   const bool f = fp32 != 0;

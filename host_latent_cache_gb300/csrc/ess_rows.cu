@@ -30,7 +30,17 @@ struct RopeFreq {
   // modulo 2^64 is the angle, off by the fraction's own error times the
   // position (2^-33 of a turn at 2^31), with no range reduction
   unsigned long long f[32];
+  int axis[32];            // whose position turns a pair
 };
+
+// The sine and cosine of a position's turns: the top 32 bits as a signed fraction of a turn,
+// in radians within +-pi, where the hardware's are off by at most 2^-21: far below half
+// a bf16 step of the pair's larger value (and of the result, unless the two products cancel).
+__device__ __forceinline__ float2 turn(int32_t pos, unsigned long long freq) {
+  const unsigned long long t = static_cast<unsigned long long>(static_cast<long long>(pos)) * freq;
+  const float h = static_cast<float>(static_cast<int32_t>(t >> 32)) * (3.14159265358979f * 0x1p-31f);
+  return make_float2(__cosf(h), __sinf(h));
+}
 
 // x modulo 1 as a binary fraction of 2^64
 unsigned long long binary_fraction(double x) {
@@ -53,7 +63,7 @@ struct WriteArgs {
   long long n;
   const uint16_t* gamma;
   float eps;
-  const int32_t* pos;      // null: no rotation
+  const int32_t* pos;      // [axes][n]; null: no rotation
   int halves;
   const int64_t* slots;
   uint8_t* rows;
@@ -68,7 +78,9 @@ struct RawRow {
   int32_t pos;
   long long slot;
 
-  __device__ __forceinline__ void load(const WriteArgs& a, long long i, int lane) {
+  // pos_at: the positions that turn this lane's pair
+  __device__ __forceinline__ void load(const WriteArgs& a, const int32_t* pos_at, long long i,
+                                       int lane) {
     const uint16_t* x = a.kv + i * a.stride;
     slot = a.slots[i];
     u0 = reinterpret_cast<const uint4*>(x)[lane];
@@ -80,7 +92,7 @@ struct RawRow {
       ra = *reinterpret_cast<const uint32_t*>(x + kLatent + 2 * lane);
       rb = 0u;
     }
-    pos = a.pos ? a.pos[i] : 0;
+    pos = a.pos ? pos_at[i] : 0;
   }
 };
 
@@ -99,8 +111,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
   const long long step = static_cast<long long>(gridDim.x) * kRowWarps;
   long long i = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
   if (i >= a.n) return;
+  const int32_t* pos_at = a.pos ? a.pos + fr.axis[lane] * a.n : nullptr;
   RawRow next;
-  next.load(a, i, lane);
+  next.load(a, pos_at, i, lane);
   float gm[16];
   if (a.gamma) {
     const uint4* gv = reinterpret_cast<const uint4*>(a.gamma);
@@ -112,7 +125,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
   asm volatile("" : "+l"(freq));
   for (; i < a.n; i += step) {
     const RawRow row = next;
-    if (i + step < a.n) next.load(a, i + step, lane);
+    if (i + step < a.n) next.load(a, pos_at, i + step, lane);
     if (row.slot < 0) continue;
     if (row.slot >= a.n_rows) {
       if (lane == 0) set_status(a.status, ESS_ERR_DEVICE_CHECK);
@@ -143,14 +156,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
       ra &= 0xffffu;
     }
     if (a.pos) {
-      const unsigned long long turn =
-          static_cast<unsigned long long>(static_cast<long long>(row.pos)) * freq;
-      // the top 32 bits as a signed fraction of a turn, in radians within
-      // +-pi, where the hardware's sine and cosine are off by at most 2^-21: far
-      // below half a bf16 step of the pair's larger value (and of the result,
-      // unless the two products cancel)
-      const float h = static_cast<float>(static_cast<int32_t>(turn >> 32)) * (3.14159265358979f * 0x1p-31f);
-      const float sn = __sinf(h), cs = __cosf(h);
+      const float2 cs_sn = turn(row.pos, freq);
+      const float cs = cs_sn.x, sn = cs_sn.y;
       const float xa = bf16_lo(ra), xb = bf16_lo(rb);
       ra = bf16_bits(xa * cs - xb * sn);
       rb = bf16_bits(xa * sn + xb * cs);
@@ -241,6 +248,100 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_read_kernel(
     o[32 + lane] = widen8_e2m1(c1, b1);
   }
   if (lane < 8) o[64 + lane] = rope;
+}
+
+struct RotateArgs {
+  const uint16_t* x;
+  long long row, head;         // elements from token to token and from head to head
+  uint16_t* out;
+  long long out_row, out_head;
+  long long n;
+  int heads;
+  int chunks;                  // ceil(heads / kTurnHeads)
+  uint32_t items;              // n * chunks, below 2^31
+  uint32_t mul;                // i / chunks = umulhi(i, mul) >> shift
+  int shift;                   // -1: one chunk
+  const int32_t* pos;          // [axes][n]
+  int halves;
+  int early;                   // what follows may start beside this kernel
+};
+
+constexpr int kTurnHeads = 4;
+constexpr int kTurnThreads = 256;
+constexpr int kTurnCtas = 152 * 6;   // one wave
+
+// Rotates rows of 64 values.  Eight lanes take kTurnHeads heads of one token, all in
+// flight, a lane the pairs 4 l .. 4 l + 3, whose sines and cosines it computes once for
+// them.  Bound by memory: 8191 tokens x 128 heads TURN us.
+__global__ void __launch_bounds__(kTurnThreads) rotate_kernel(const RotateArgs a,
+                                                              const __grid_constant__ RopeFreq fr) {
+  pdl_wait_previous();
+  if (a.early) pdl_launch_dependents();
+  const int l = threadIdx.x & 7;
+  unsigned long long f[4];
+  const int32_t* pos[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = fr.f[4 * l + i];
+    pos[i] = a.pos + fr.axis[4 * l + i] * a.n;
+  }
+  const uint32_t step = gridDim.x * (kTurnThreads / 8);
+  for (uint32_t it = blockIdx.x * (kTurnThreads / 8) + (threadIdx.x >> 3); it < a.items; it += step) {
+    const uint32_t t = a.shift < 0 ? it : __umulhi(it, a.mul) >> a.shift;
+    const int h0 = static_cast<int>(it - t * static_cast<uint32_t>(a.chunks)) * kTurnHeads;
+    const int some = min(kTurnHeads, a.heads - h0);
+    const uint16_t* x = a.x + t * a.row + h0 * a.head;
+    uint16_t* o = a.out + t * a.out_row + h0 * a.out_head;
+    uint4 v[kTurnHeads];
+#pragma unroll
+    for (int h = 0; h < kTurnHeads; ++h) {
+      v[h] = make_uint4(0u, 0u, 0u, 0u);
+      if (h >= some) continue;
+      if (a.halves) {
+        const uint2 p = reinterpret_cast<const uint2*>(x + h * a.head)[l];
+        const uint2 r = reinterpret_cast<const uint2*>(x + h * a.head + 32)[l];
+        v[h] = make_uint4(p.x, p.y, r.x, r.y);
+      } else {
+        v[h] = reinterpret_cast<const uint4*>(x + h * a.head)[l];
+      }
+    }
+    float2 cs[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cs[i] = turn(pos[i][t], f[i]);
+#pragma unroll
+    for (int h = 0; h < kTurnHeads; ++h) {
+      if (h >= some) continue;
+      float y[8];
+      unpack8(v[h], y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // the first and second value of pair i; halves: 0..3 and 4..7
+        float& p = a.halves ? y[i] : y[2 * i];
+        float& r = a.halves ? y[4 + i] : y[2 * i + 1];
+        const float u = p * cs[i].x - r * cs[i].y, w = p * cs[i].y + r * cs[i].x;
+        p = u;
+        r = w;
+      }
+      const uint4 w = pack8_bf16(y);
+      if (a.halves) {
+        reinterpret_cast<uint2*>(o + h * a.out_head)[l] = make_uint2(w.x, w.y);
+        reinterpret_cast<uint2*>(o + h * a.out_head + 32)[l] = make_uint2(w.z, w.w);
+      } else {
+        reinterpret_cast<uint4*>(o + h * a.out_head)[l] = w;
+      }
+    }
+  }
+}
+
+// Frequencies and axes (axis null: all pairs turn by the first); false for a bad one.
+bool rope_freq(const double* inv_freq, int axes, const int32_t* axis, RopeFreq* fr) {
+  for (int i = 0; i < 32; ++i) {
+    if (!std::isfinite(inv_freq[i])) return false;
+    if (axis && (axis[i] < 0 || axis[i] >= axes)) return false;
+    fr->f[i] = turns_of(inv_freq[i]);
+    fr->axis[i] = axis ? axis[i] : 0;
+  }
+  return true;
 }
 
 __global__ void status_take_kernel(int* status, int* taken) {
@@ -398,17 +499,21 @@ ess_status ess_cache_write(const void* kv, int64_t kv_stride, int64_t n, const v
                            float eps, const double* inv_freq, const int32_t* pos, int32_t pairs,
                            const int64_t* slots, void* rows, int64_t n_rows, int32_t format,
                            int32_t* status, ess_stream_t stream) {
+  return ess_cache_write_axes(kv, kv_stride, n, gamma, eps, inv_freq, pos, 1, nullptr, pairs, slots,
+                              rows, n_rows, format, status, stream);
+}
+
+ess_status ess_cache_write_axes(const void* kv, int64_t kv_stride, int64_t n, const void* gamma,
+                                float eps, const double* inv_freq, const int32_t* pos,
+                                int32_t axes, const int32_t* axis, int32_t pairs,
+                                const int64_t* slots, void* rows, int64_t n_rows, int32_t format,
+                                int32_t* status, ess_stream_t stream) {
   if (format < ESS_ROW_BF16 || format > ESS_ROW_Q4 || n < 0 || n > kMaxRows || n_rows < 0)
     return ESS_ERR_INVALID_ARG;
   if (kv_stride < kRowDim || kv_stride % 8 != 0 || !(eps >= 0.0f)) return ESS_ERR_INVALID_ARG;
   if (pairs != ESS_ROPE_ADJACENT && pairs != ESS_ROPE_HALVES) return ESS_ERR_INVALID_ARG;
   RopeFreq fr = {};
-  if (inv_freq) {
-    for (int i = 0; i < 32; ++i) {
-      if (!std::isfinite(inv_freq[i])) return ESS_ERR_INVALID_ARG;
-      fr.f[i] = turns_of(inv_freq[i]);
-    }
-  }
+  if (inv_freq && (axes < 1 || !rope_freq(inv_freq, axes, axis, &fr))) return ESS_ERR_INVALID_ARG;
   if (n == 0) return ESS_OK;
   if (!kv || !slots || !rows || (inv_freq && !pos) || !aligned16(kv) || !aligned16(rows) ||
       (gamma && !aligned16(gamma)) || !aligned_to(slots, 8) || !aligned_to(status, 4) ||
@@ -438,6 +543,49 @@ ess_status ess_cache_write(const void* kv, int64_t kv_stride, int64_t n, const v
   else
     e = launch_pdl_once(cache_write_kernel<ESS_ROW_Q4>, grid, block, 0, st, a, fr);
   return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
+}
+
+ess_status ess_rotate(const void* x, int64_t x_row, int64_t x_head, int64_t n, int32_t heads,
+                      const double* inv_freq, const int32_t* pos, int32_t axes,
+                      const int32_t* axis, int32_t pairs, void* out, int64_t out_row,
+                      int64_t out_head, ess_stream_t stream) {
+  if (n < 0 || heads < 1 || !inv_freq || axes < 1 ||
+      (pairs != ESS_ROPE_ADJACENT && pairs != ESS_ROPE_HALVES))
+    return ESS_ERR_INVALID_ARG;
+  RopeFreq fr = {};
+  if (!rope_freq(inv_freq, axes, axis, &fr)) return ESS_ERR_INVALID_ARG;
+  if (x_row % 8 != 0 || x_head % 8 != 0 || out_row % 8 != 0 || out_head % 8 != 0 || x_row < 0 ||
+      x_head < 0 || (n > 1 && out_row < 64) || (heads > 1 && out_head < 64))
+    return ESS_ERR_INVALID_ARG;
+  RotateArgs a;
+  a.chunks = (heads - 1) / kTurnHeads + 1;
+  if (n > 0x7fffffffLL / a.chunks) return ESS_ERR_UNSUPPORTED;
+  if (n == 0) return ESS_OK;
+  if (!x || !pos || !out || !aligned16(x) || !aligned16(out) || !aligned_to(pos, 4) ||
+      (x == out && ((n > 1 && x_row != out_row) || (heads > 1 && x_head != out_head))))
+    return ESS_ERR_INVALID_ARG;
+  a.x = static_cast<const uint16_t*>(x);
+  a.row = x_row;
+  a.head = x_head;
+  a.out = static_cast<uint16_t*>(out);
+  a.out_row = out_row;
+  a.out_head = out_head;
+  a.n = n;
+  a.heads = heads;
+  a.items = static_cast<uint32_t>(n * a.chunks);
+  fast_divisor(a.chunks, &a.mul, &a.shift);
+  a.pos = pos;
+  a.halves = pairs == ESS_ROPE_HALVES;
+  // Rows of 64 bf16 values side by side may be indexer keys, which an indexer loads
+  // ahead of its own wait: the next one of each layer waits, and nothing starts early.
+  a.early = heads > 1 && out_head != 64 && out_row != 64;
+  if (!a.early) ++key_norms();
+  constexpr int kPer = kTurnThreads / 8;
+  const dim3 grid(std::min<uint32_t>((a.items + kPer - 1) / kPer, kTurnCtas));
+  return launch_pdl_once(rotate_kernel, grid, dim3(kTurnThreads), 0,
+                         static_cast<cudaStream_t>(stream), a, fr) == cudaSuccess
+             ? ESS_OK
+             : ESS_ERR_CUDA;
 }
 
 ess_status ess_cache_read(const void* rows, int64_t n_rows, int32_t format, const int64_t* slots,

@@ -17,6 +17,18 @@ inline bool aligned_to(const void* p, uintptr_t n) {
 }
 inline bool aligned16(const void* p) { return aligned_to(p, 16); }
 
+// i / d = umulhi(i, mul) >> shift for i < 2^31: mul = ceil(2^(32 + shift) / d) with
+// 2^shift < d <= 2^(shift + 1); d = 1 gives shift -1, and i itself.
+inline void fast_divisor(int d, uint32_t* mul, int* shift) {
+  *mul = 0;
+  *shift = -1;
+  if (d == 1) return;
+  int s = 0;
+  while ((2LL << s) < d) ++s;
+  *shift = s;
+  *mul = static_cast<uint32_t>(((1ull << (32 + s)) + d - 1) / d);
+}
+
 __host__ __device__ constexpr int row_bytes_of(int format) {
   return format == ESS_ROW_BF16 ? kRowBytes : format == ESS_ROW_COMPACT ? 656 : kQ4RowBytes;
 }

@@ -47,7 +47,7 @@ EXPORTS = (
     "ess_pool_bind_layer_compact", "ess_prefill_run", "ess_row_bytes", "ess_status_take",
     "ess_cache_write",
     "ess_cache_read", "ess_cache_mla_bytes", "ess_cache_mla", "ess_norm_quant",
-    "ess_quant", "ess_product",
+    "ess_quant", "ess_product", "ess_cache_write_axes", "ess_rotate",
 )
 
 # void (*)(void* user, int32_t layer, void* buffer, void* stream)
@@ -137,6 +137,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "ess_cache_mla": [P, P, L, I, P, I, I, P, I, I, I, P, I, F, P, P, P, ctypes.c_size_t, P,
                           P],
         "ess_norm_quant": [P, L, P, L, P, F, L, I, P, P, P, P],
+        "ess_cache_write_axes": [P, L, L, P, F, P, P, I, P, I, P, P, L, I, P, P],
+        "ess_rotate": [P, L, L, L, I, P, P, I, P, I, P, L, L, P],
         "ess_quant": [P, L, L, I, I, P, P, P],
         "ess_product": [P, P, L, P, P, I, I, P, L, I, P, P],
     }
@@ -437,6 +439,22 @@ def ess_row_bytes(fmt: int) -> int:
 
 def ess_status_take(status, taken, stream=None) -> None:
     check(load().ess_status_take(_p(status), _p(taken), _stream(stream)), "ess_status_take")
+
+
+def ess_cache_write_axes(kv, kv_stride: int, n: int, gamma, eps: float, inv_freq, pos, axes: int,
+                         axis, pairs: int, slots, rows, n_rows: int, fmt: int, status=None,
+                         stream=None) -> None:
+    """inv_freq: a (ctypes.c_double * 32) array of radians per position, or None; axis: a
+    (ctypes.c_int32 * 32) array, or None."""
+    check(load().ess_cache_write_axes(_p(kv), kv_stride, n, _p(gamma), eps, inv_freq, _p(pos), axes,
+                                      axis, pairs, _p(slots), _p(rows), n_rows, fmt, _p(status),
+                                      _stream(stream)), "ess_cache_write_axes")
+
+
+def ess_rotate(x, x_row: int, x_head: int, n: int, heads: int, inv_freq, pos, axes: int, axis,
+               pairs: int, out, out_row: int, out_head: int, stream=None) -> None:
+    check(load().ess_rotate(_p(x), x_row, x_head, n, heads, inv_freq, _p(pos), axes, axis, pairs,
+                            _p(out), out_row, out_head, _stream(stream)), "ess_rotate")
 
 
 def ess_cache_write(kv, kv_stride: int, n: int, gamma, eps: float, inv_freq, pos, pairs: int,

@@ -13,6 +13,7 @@ ValueError; nothing is copied or converted on the way.
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 import weakref
 from typing import Optional, Sequence
@@ -135,6 +136,32 @@ def release_workspaces() -> None:
             ws.buf = None
 
 
+@functools.lru_cache(maxsize=64)
+def _doubles(values):
+    _need(len(values) == ROPE // 2, f"inv_freq has {len(values)} entries, not {ROPE // 2}")
+    return (ctypes.c_double * len(values))(*values)
+
+
+@functools.lru_cache(maxsize=64)
+def _axis_of(axes, count: int):
+    _need(len(axes) == ROPE // 2, f"axes has {len(axes)} entries, not {ROPE // 2}")
+    _need(all(0 <= a < count for a in axes), f"axes: numbers from 0 to {count - 1} are needed")
+    return (ctypes.c_int32 * len(axes))(*axes)
+
+
+def _turns(inv_freq: Sequence[float], pos, axes, n: int, index: int):
+    """(frequencies, number of axes, axis of each pair or None) of a rotation of n rows."""
+    # by their numbers: a tensor's entries may change later
+    freq = _doubles(tuple(map(float, inv_freq)))
+    if axes is None:
+        _check(pos, "pos", _I32, (n,), index)
+        return freq, 1, None
+    _need(isinstance(pos, torch.Tensor) and pos.dim() == 2 and 1 <= pos.shape[0] <= MOST,
+          "pos: [axes][n] is needed where axes are given")
+    _check(pos, "pos", _I32, (pos.shape[0], n), index)
+    return freq, pos.shape[0], _axis_of(tuple(map(int, axes)), pos.shape[0])
+
+
 class RowCache:
     """A caller's tensor of cache rows, uint8 [n_rows][row bytes], with the
     calls on it.  `status` is a device int32 that keeps the first device-side
@@ -153,7 +180,6 @@ class RowCache:
         self._index = rows.get_device()
         _check(rows, "rows", torch.uint8, (self.n_rows, ess.ess_row_bytes(self._f)), self._index)
         self.status = _new_status(self._index)
-        self._freq = (None, None)
         self._ws = {}       # by stream, shared with the other caches that run on it
         self._bytes = {}    # by shape
 
@@ -163,21 +189,14 @@ class RowCache:
         is kept for a later poll."""
         return _take_status(self.status, self._index)
 
-    def _freqs(self, inv_freq: Sequence[float]):
-        key = tuple(map(float, inv_freq))   # numbers: a tensor's entries may change later
-        old, freq = self._freq
-        if old != key:
-            _need(len(key) == ROPE // 2, f"inv_freq has {len(key)} entries, not {ROPE // 2}")
-            freq = (ctypes.c_double * len(key))(*key)
-            self._freq = (key, freq)
-        return freq
-
     def write(self, kv, slots, gamma=None, eps: float = 1e-6, pos=None, inv_freq=None,
-              pairs: str = "adjacent") -> None:
+              pairs: str = "adjacent", axes=None) -> None:
         """Rows kv bf16 [n][576] (any row stride that is a multiple of 8) into
         the rows `slots` int64 [n] (negative: not written): the first 512
         values normed when gamma bf16 [512] is given, the last 64 rotated by
-        pos int32 [n] when inv_freq (32 radians per position) is given."""
+        pos int32 [n] when inv_freq (32 radians per position) is given.  With
+        `axes` (32 axis numbers) pair i turns by the position on axis axes[i]
+        of pos int32 [axes][n] (time, height, width)."""
         at = self._index
         _need(isinstance(slots, torch.Tensor) and slots.dim() == 1, "slots: [n] is needed")
         n = slots.shape[0]
@@ -186,15 +205,16 @@ class RowCache:
         _need(pairs in PAIRS, f"pairs {pairs!r} is none of {', '.join(PAIRS)}")
         if gamma is not None:
             _check(gamma, "gamma", _BF16, (LATENT,), at)
-        freq = None
+        freq, count, axis = None, 1, None
         if inv_freq is None:
+            _need(axes is None, "axes without inv_freq")
             pos = None
         else:
-            freq = self._freqs(inv_freq)
-            _check(pos, "pos", _I32, (n,), at)
+            freq, count, axis = _turns(inv_freq, pos, axes, n, at)
         with _OnDevice(self._index) as stream:
-            ess.ess_cache_write(kv, _row_stride(kv), n, gamma, eps, freq, pos, PAIRS[pairs], slots,
-                                self.rows, self.n_rows, self._f, self.status, stream)
+            ess.ess_cache_write_axes(kv, _row_stride(kv), n, gamma, eps, freq, pos, count, axis,
+                                     PAIRS[pairs], slots, self.rows, self.n_rows, self._f,
+                                     self.status, stream)
 
     def read(self, slots, out=None):
         """The rows `slots` int64 [n] as bf16 [n][576]; zeros for a negative slot."""
@@ -344,3 +364,32 @@ def norm_q8(x, gamma, eps: float = 1e-6, residual=None, residual_out=None, codes
         ess.ess_norm_quant(x, _row_stride(x), residual, r_stride, gamma, eps, n, dim, residual_out,
                            codes, scales, stream)
     return codes, scales, residual_out
+
+
+def rotate(x, pos, inv_freq, pairs: str = "adjacent", axes=None, out=None):
+    """Rows x bf16 [n][heads][64] (any strides from token to token and head to head that are
+    multiples of 8) rotated by position, as `RowCache.write` rotates the cache's: queries.
+    pos int32 [n], or with `axes` [axes][n].  Into `out`, of any such strides, which may be
+    x itself; a new tensor without it.  The inverse is the rotation by -inv_freq."""
+    _need(isinstance(x, torch.Tensor) and x.dim() == 3 and x.is_cuda,
+          f"x: a CUDA tensor [n][heads][{ROPE}] is needed")
+    n, heads, dim = x.shape
+    at = x.get_device()
+    _need(dim == ROPE and heads >= 1, f"x: [n][heads][{ROPE}] with at least one head is needed")
+    _need(heads <= MOST, "more than 2^31 - 1 heads")
+    _need(pairs in PAIRS, f"pairs {pairs!r} is none of {', '.join(PAIRS)}")
+    freq, count, axis = _turns(inv_freq, pos, axes, n, at)
+    if out is None:
+        out = torch.empty((n, heads, ROPE), dtype=_BF16, device=x.device)
+    strides = []
+    for t, name in ((x, "x"), (out, "out")):
+        if not (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.shape == x.shape
+                and t.is_cuda and t.get_device() == at and t.stride(2) == 1):
+            _refuse(t, name, _BF16, x.shape, at)
+        # of a single token or head, any that the kernel takes
+        head = t.stride(1) if heads > 1 else ROPE
+        strides += [t.stride(0) if n > 1 else heads * max(head, ROPE), head]
+    with _OnDevice(at) as stream:
+        ess.ess_rotate(x, strides[0], strides[1], n, heads, freq, pos, count, axis, PAIRS[pairs],
+                       out, strides[2], strides[3], stream)
+    return out

@@ -579,6 +579,37 @@ ess_status ess_cache_write(const void* kv, int64_t kv_stride, int64_t n, const v
                            const int64_t* slots, void* rows, int64_t n_rows, int32_t format,
                            int32_t* status, ess_stream_t stream);
 
+/* The same with positions on several axes (time, height and width of images and video):
+ *   axes  number of axes, at least 1
+ *   axis  host int32 [32], read before the call returns: pair i turns by the position
+ *         on axis axis[i], 0 <= axis[i] < axes; NULL: all by the first
+ *   pos   device int32 [axes][n]
+ * Errors: as ess_cache_write, and ESS_ERR_INVALID_ARG for axes or an axis out of range
+ * where inv_freq is given. */
+ess_status ess_cache_write_axes(const void* kv, int64_t kv_stride, int64_t n, const void* gamma,
+                                float eps, const double* inv_freq, const int32_t* pos,
+                                int32_t axes, const int32_t* axis, int32_t pairs,
+                                const int64_t* slots, void* rows, int64_t n_rows, int32_t format,
+                                int32_t* status, ess_stream_t stream);
+
+/* Rotate rows of 64 values by position: queries, as ess_cache_write rotates k^R.
+ *   x         device bf16 [n][heads][64]: element strides x_row from token to token and
+ *             x_head from head to head, multiples of 8 (0 repeats), 16-byte aligned
+ *   inv_freq, pairs         as in ess_cache_write; the inverse rotation (its gradient)
+ *                           is that of the negative frequencies
+ *   pos, axes, axis         as in ess_cache_write_axes
+ *   out       device bf16 [n][heads][64] with strides of its own, at least 64; it may be x
+ *             with x's strides, and shares no memory with x otherwise
+ * Each value is formed in fp32, with the sine's and cosine's bound of ess_cache_write,
+ * and rounded once.  What lies between the rows is left as it was.  n = 0 launches nothing.
+ * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or negative argument, a stride, axis,
+ * pairs or frequency out of range; ESS_ERR_UNSUPPORTED when n * ceil(heads / 4) is 2^31 or
+ * more. */
+ess_status ess_rotate(const void* x, int64_t x_row, int64_t x_head, int64_t n, int32_t heads,
+                      const double* inv_freq, const int32_t* pos, int32_t axes,
+                      const int32_t* axis, int32_t pairs, void* out, int64_t out_row,
+                      int64_t out_head, ess_stream_t stream);
+
 /* Rows of a device row cache as bf16 rows, exactly (the prefix of a chunked
  * prompt, or a check of what the cache holds).
  *   slots  device int64 [n]: the cache row of each output row; a negative one
