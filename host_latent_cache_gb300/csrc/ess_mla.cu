@@ -136,6 +136,11 @@ struct MlaArgs {
   float c2;                // sm_scale * log2(e)
   uint16_t* out;
   float* lse;
+  const int32_t* cu;       // chunks: [batch + 1] first query token of each request
+  int total;               // chunks: query tokens
+  int unit_rows;           // chunks: query rows that share tiles: 128, or a token's heads
+  int pairs;               // chunks: pairs of the launch
+  int4* rec;               // chunks: [pairs] which units the pairs cut
   int2* span;              // [entries][row_tiles]: first pair * 2 + slot, last pair
   float* part_o;           // [pairs][2][512 / 8][128][8]: a lane's 32 bytes beside its neighbours'
   float4* part_ml;         // [pairs][2][128]: reference, sum, c2 of the row
@@ -149,6 +154,110 @@ __device__ __forceinline__ int request_len(const MlaArgs& a, int b) {
 }
 __device__ __forceinline__ int entry_len(const MlaArgs& a, int v) {
   return a.tokens ? min(a.k, request_len(a, v / a.ways)) : request_len(a, v);
+}
+
+// ---------------------------------------------------------------- chunks
+// Requests with any number of new tokens each (CHUNK).  Request b's queries are the rows
+// [start, start + n) x heads of q, its newest tokens.  What a segment belongs to is a
+// unit: unit_rows neighbouring query rows of a request, dense 128 of them, listed one
+// token's heads.  A unit's tokens end with those that its last row sees; rows that see
+// fewer are masked.  Every unit has a tile, though none of its tokens may exist, so that
+// every row is written.  The join finds the units that were cut from what each pair
+// leaves in rec: x the first query row of the unit that the pair starts inside of (-1:
+// none), y that unit's rows, w the slot of the partial that the pair ends with.
+struct Chunk {
+  int start, n;   // n = 0 for offsets that are out of order or range
+  bool ok;
+};
+__device__ __forceinline__ Chunk chunk_of(const MlaArgs& a, int b) {
+  const int lo = a.cu[b], hi = a.cu[b + 1];
+  const bool ok = lo >= 0 && lo <= hi && hi <= a.total;
+  return Chunk{ok ? lo : 0, ok ? hi - lo : 0, ok};
+}
+__device__ __forceinline__ int units_of(const MlaArgs& a, int n) {
+  return (n * a.heads + a.unit_rows - 1) / a.unit_rows;
+}
+// Tokens that the last row of unit u of a request sees.
+__device__ __forceinline__ int unit_sees(const MlaArgs& a, int T, int n, int u) {
+  const int last = min(n * a.heads, (u + 1) * a.unit_rows) - 1;
+  return max(T - n + last / a.heads + 1, 0);
+}
+// Listed: entries of a unit's list; dense: its tokens.
+__device__ __forceinline__ int unit_len(const MlaArgs& a, int T, int n, int u) {
+  const int sees = unit_sees(a, T, n, u);
+  return a.tokens ? min(a.k, sees) : sees;
+}
+__device__ __forceinline__ int unit_tiles(int len) { return max((len + kMt - 1) / kMt, 1); }
+
+// A walk over the units of all requests.
+struct UnitWalk {
+  int b, u, units, n, T;
+  __device__ __forceinline__ void load(const MlaArgs& a) {
+    n = chunk_of(a, b).n;
+    T = request_len(a, b);
+    units = units_of(a, n);
+  }
+  // unit0[b]: units of the requests before b
+  __device__ __forceinline__ void start(const MlaArgs& a, const int* unit0, int v, bool live) {
+    int lo = 0, hi = live ? a.batch - 1 : 0;   // the last request that starts at v or before
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (unit0[mid] <= v) lo = mid;
+      else hi = mid - 1;
+    }
+    b = lo;
+    load(a);
+    u = live ? v - unit0[b] : 0;
+  }
+  __device__ __forceinline__ int tiles(const MlaArgs& a) const {
+    return unit_tiles(unit_len(a, T, n, u));
+  }
+  __device__ __forceinline__ void next(const MlaArgs& a) {
+    for (++u; u >= units && b + 1 < a.batch; u = 0) {
+      ++b;
+      load(a);
+    }
+  }
+};
+constexpr int kMaxChunkBatch = 32768;   // their first units fit the operands' place
+
+// Units of all requests; unit0[b], those before request b.  All threads call it.
+__device__ __forceinline__ int chunk_units(const MlaArgs& a, int* unit0, int* sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.batch + kMlaThreads - 1) / kMlaThreads;
+  const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
+  int mine = 0;
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    const Chunk c = chunk_of(a, b);
+    const int T = a.T[b];
+    bad |= !c.ok || T < 0 || T > static_cast<long long>(a.max_pages) * a.page;
+    mine += units_of(a, c.n);
+  }
+  if (bad && blockIdx.x == 0) set_status(a.status, ESS_ERR_DEVICE_CHECK);
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
+  if (lane == 31) sums[warp] = before;
+  __syncthreads();
+  int all = lane < kMlaThreads / 32 ? sums[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, all, o);
+    if (lane >= o) all += x;
+  }
+  const int total = __shfl_sync(0xffffffffu, all, 31);
+  const int earlier = __shfl_sync(0xffffffffu, all, max(warp - 1, 0));
+  before += (warp > 0 ? earlier : 0) - mine;
+  for (int b = b0; b < b1; ++b) {
+    unit0[b] = before;
+    before += units_of(a, chunk_of(a, b).n);
+  }
+  __syncthreads();
+  return total;
 }
 
 // ---------------------------------------------------------------- pair PTX
@@ -290,7 +399,9 @@ __device__ __forceinline__ float row_lse(float m, float c2, float l) {
   return l > 0.0f || l != l ? (fmaf(m, c2, -kLift) + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// The tiles of one pair, in order: entry v, row tile rt, token tile.
+// The tiles of one pair, in order: entry v, row tile rt, token tile (chunks: request v,
+// unit rt of it).
+template <bool CHUNK>
 struct Tiles {
   int left;   // tiles from this one on
   int v, rt, tile, nt, len;
@@ -299,14 +410,19 @@ struct Tiles {
   __device__ __forceinline__ Tiles(const MlaArgs& a, const Misc* mi) {
     left = static_cast<int>(mi->end_tile - mi->first_tile);
     v = mi->start_v;
-    load(a);
     rt = mi->start_rt;
+    load(a);
     tile = mi->start_tile;
     begins = true;
   }
   __device__ __forceinline__ void load(const MlaArgs& a) {
-    len = entry_len(a, v);
-    nt = (len + kMt - 1) / kMt;
+    if (CHUNK) {
+      len = unit_len(a, request_len(a, v), chunk_of(a, v).n, rt);
+      nt = unit_tiles(len);
+    } else {
+      len = entry_len(a, v);
+      nt = (len + kMt - 1) / kMt;
+    }
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
   // of a segment: a run of tiles of one entry and row tile
@@ -317,7 +433,14 @@ struct Tiles {
     --left;
     if (++tile == nt && left > 0) {
       tile = 0;
-      if (++rt == a.row_tiles) {
+      ++rt;
+      if (CHUNK) {
+        while (v + 1 < a.batch && rt >= units_of(a, chunk_of(a, v).n)) {
+          rt = 0;
+          ++v;
+        }
+        load(a);
+      } else if (rt == a.row_tiles) {
         rt = 0;
         do {   // a tile is left, so an entry that has one follows
           ++v;
@@ -328,18 +451,45 @@ struct Tiles {
   }
 };
 
+// Where a segment's query rows lie: row r of the pair is row first + r of q and out, for
+// r < rows.
+struct QueryRows {
+  size_t first;
+  int rows;
+};
+template <bool CHUNK>
+__device__ __forceinline__ QueryRows query_rows(const MlaArgs& a, int v, int rt) {
+  if (CHUNK) {
+    const Chunk c = chunk_of(a, v);
+    return QueryRows{static_cast<size_t>(c.start) * a.heads + static_cast<size_t>(rt) * a.unit_rows,
+                     min(c.n * a.heads - rt * a.unit_rows, a.unit_rows)};
+  }
+  return QueryRows{static_cast<size_t>(v) * a.entry_rows + rt * kPairRows,
+                   a.entry_rows - rt * kPairRows};
+}
+
 // The cache rows of a lane's four tokens e, e + 32, .. of an entry, -1 for one
 // that is not.  The four list entries are loaded together, then the four page
 // table entries, so that a tile costs one latency of each.
-__device__ __forceinline__ void token_rows(const MlaArgs& a, int v, int len, int e, int* row) {
+template <bool CHUNK>
+__device__ __forceinline__ void token_rows(const MlaArgs& a, int v, int rt, int len, int e,
+                                           int* row) {
   int t[4], pg[4];
-  const int b = a.tokens ? v / a.ways : v;
-  const int T = a.tokens ? request_len(a, b) : len;
+  const int b = a.tokens && !CHUNK ? v / a.ways : v;
+  int T = len, list = v;   // tokens that may be named, and by which list
+  if (a.tokens) {
+    T = request_len(a, b);
+    if (CHUNK) {
+      const Chunk c = chunk_of(a, b);
+      T = unit_sees(a, T, c.n, rt);
+      list = c.start + rt;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int x = e + 32 * j;
     t[j] = x;
-    if (a.tokens) t[j] = x < len ? a.tokens[static_cast<size_t>(v) * a.k + x] : -1;
+    if (a.tokens) t[j] = x < len ? a.tokens[static_cast<size_t>(list) * a.k + x] : -1;
     else if (x >= len) t[j] = -1;
   }
   const int32_t* table = a.page_table + static_cast<size_t>(b) * a.max_pages;
@@ -386,13 +536,14 @@ __device__ __forceinline__ uint4 pick4(bool p, const uint4& a, const uint4& b) {
 // ---------------------------------------------------------------- roles
 // One warp resolves the cache rows of the tiles to come, four tokens a lane,
 // up to kRing tiles ahead, so that the page table's latency meets nobody.
+template <bool CHUNK>
 __device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
   const int lane = threadIdx.x & 31;
-  Tiles it(a, mi);
+  Tiles<CHUNK> it(a, mi);
   int slot = 0, turn = 0;
   for (int g = 0; it.more(); ++g) {
     int row[4];
-    token_rows(a, it.v, it.len, it.tile * kMt + lane, row);
+    token_rows<CHUNK>(a, it.v, it.rt, it.len, it.tile * kMt + lane, row);
     if (turn > 0) wait_or_abort(&mi->row_free[slot], (turn - 1) & 1, mi, a.status);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -401,10 +552,10 @@ __device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
       if (lane == 0) mi->mask[slot][j] = m;
     }
     if (it.first() && g > 0) {   // the segment's queries into L2
-      const int row0 = it.rt * kPairRows + static_cast<int>(cluster_ctarank()) * kCtaRows;
-      const char* q = reinterpret_cast<const char*>(
-          a.q + (static_cast<size_t>(it.v) * a.entry_rows + row0) * kRowDim);
-      const int bytes = min(kCtaRows, a.entry_rows - row0) * kRowDim * 2;
+      const QueryRows r = query_rows<CHUNK>(a, it.v, it.rt);
+      const int row0 = static_cast<int>(cluster_ctarank()) * kCtaRows;
+      const char* q = reinterpret_cast<const char*>(a.q + (r.first + row0) * kRowDim);
+      const int bytes = min(kCtaRows, r.rows - row0) * kRowDim * 2;
       for (int x = lane * 128; x < bytes; x += 32 * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(q + x));
     }
@@ -426,11 +577,19 @@ __device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
 // part, divided alike, as bf16.  A lane takes unit 32 h + 4 (lane % 8) + lane / 8:
 // chunk 8 h + lane % 8, its unit lane / 8; eight lanes then fill the places of one
 // swizzled row.
-template <int kFly>
+template <bool CHUNK, int kFly>
 __device__ __forceinline__ void load_queries(const MlaArgs& a, uint8_t* smem, Misc* mi, int v,
-                                             int row0, int warp, int lane, int seg) {
+                                             int rt, int q0, int warp, int lane, int seg) {
   constexpr int kRows = kCtaRows / kWidenWarps;
   uint8_t* sq = smem + kOffQ;
+  int row0 = rt * kPairRows + q0, rows = a.entry_rows;
+  size_t first = static_cast<size_t>(v) * a.entry_rows;
+  if (CHUNK) {
+    const Chunk c = chunk_of(a, v);
+    row0 = rt * a.unit_rows + q0;
+    rows = min(c.n * a.heads, (rt + 1) * a.unit_rows);
+    first = static_cast<size_t>(c.start) * a.heads;
+  }
   const int un = 4 * (lane & 7) + (lane >> 3);
 #pragma unroll 1
   for (int i0 = 0; i0 < kRows; i0 += kFly) {
@@ -441,8 +600,8 @@ __device__ __forceinline__ void load_queries(const MlaArgs& a, uint8_t* smem, Mi
       const int row = row0 + warp * kRows + i0 + i;
       u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
       rope[i] = 0u;
-      if (row < a.entry_rows) {
-        const uint16_t* q = a.q + (static_cast<size_t>(v) * a.entry_rows + row) * kRowDim;
+      if (row < rows) {
+        const uint16_t* q = a.q + (first + row) * kRowDim;
         u[i][0] = reinterpret_cast<const uint4*>(q)[un];
         u[i][1] = reinterpret_cast<const uint4*>(q)[32 + un];
         rope[i] = reinterpret_cast<const uint32_t*>(q + kLatent)[lane];
@@ -496,6 +655,7 @@ __device__ __forceinline__ void load_queries(const MlaArgs& a, uint8_t* smem, Mi
 //
 // K is written in two halves of its dims and V in two halves of the tokens,
 // each as soon as the MMAs that read the half before it are done.
+template <bool CHUNK>
 __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc* mi,
                                            uint32_t rank) {
   const int wt = threadIdx.x - kWidenWarp0 * 32;
@@ -551,7 +711,7 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
   // g - 1, V of tile g beside QK of tile g + 1.  Slot s of the rows holds tile
   // g for the (g / kRing)th time.
   const int q0 = static_cast<int>(rank) * kCtaRows;
-  load_queries<4>(a, smem, mi, mi->start_v, mi->start_rt * kPairRows + q0, w, lane, 0);
+  load_queries<CHUNK, 4>(a, smem, mi, mi->start_v, mi->start_rt, q0, w, lane, 0);
   int seg = 0;
   wait_or_abort(&mi->row_full[0], 0, mi, a.status);
   load_k(0);
@@ -592,7 +752,7 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
       // registers too the tile loop spills, or with two rows in flight costs 2 %.)
       if (next.x >= 0) {
         wait_or_abort(&mi->q_free, seg & 1, mi, a.status);
-        load_queries<2>(a, smem, mi, next.x, next.y * kPairRows + q0, w, lane, ++seg);
+        load_queries<CHUNK, 2>(a, smem, mi, next.x, next.y, q0, w, lane, ++seg);
       }
       load_v(slot1);
       __syncwarp();
@@ -613,6 +773,7 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
 // one elected lane issues: with uniform control flow the descriptors stay in
 // uniform registers, and an MMA is issued every 32 cycles (N = 128).  The two
 // MMAs of PV that share a slice of P read it from shared memory once.
+template <bool CHUNK>
 __device__ __forceinline__ void mma_role(const MlaArgs& a, uint8_t* smem, Misc* mi,
                                          uint32_t tmem) {
   const uint64_t dq = make_sdesc_sw128(smem_u32(smem + kOffQ), 16, 1024);
@@ -644,7 +805,7 @@ __device__ __forceinline__ void mma_role(const MlaArgs& a, uint8_t* smem, Misc* 
   };
   int seg = 0;
   bool acc = false;   // the tile before was not the first of its segment
-  Tiles it(a, mi);
+  Tiles<CHUNK> it(a, mi);
   for (int g = 0; it.more(); ++g) {
     const bool first = it.first(), last = it.last();
     if (first) {
@@ -676,6 +837,7 @@ __device__ __forceinline__ void mma_role(const MlaArgs& a, uint8_t* smem, Misc* 
 
 // Eight warps.  Four threads share a query row: (half, sub) names 32 of a
 // tile's tokens, and 128 of the row's output dims.
+template <bool CHUNK>
 __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Misc* mi,
                                              uint32_t rank, uint32_t tmem, int pair) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -687,13 +849,20 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
   const int bar_id = 1 + (warp & 1);   // the four warps that hold the same rows
   float m = -INFINITY, l = 0.0f, c2 = 0.0f;
   int limit = 0, seg_first_tile = 0, seg = 0;
-  Tiles it(a, mi);
+  Tiles<CHUNK> it(a, mi);
   for (int g = 0; it.more(); ++g) {
     const bool first = it.first(), last = it.last();
     if (first) {
-      const int row = it.rt * kPairRows + static_cast<int>(rank) * kCtaRows + r;
-      limit = row >= a.entry_rows ? 0 : it.len;
-      if (!a.tokens && limit) limit = it.len - (a.ways - 1) + row / a.heads;
+      if (CHUNK) {
+        const int row = it.rt * a.unit_rows + static_cast<int>(rank) * kCtaRows + r;
+        const int n = chunk_of(a, it.v).n;
+        limit = row - it.rt * a.unit_rows >= a.unit_rows || row >= n * a.heads ? 0 : it.len;
+        if (!a.tokens && limit) limit = request_len(a, it.v) - n + row / a.heads + 1;
+      } else {
+        const int row = it.rt * kPairRows + static_cast<int>(rank) * kCtaRows + r;
+        limit = row >= a.entry_rows ? 0 : it.len;
+        if (!a.tokens && limit) limit = it.len - (a.ways - 1) + row / a.heads;
+      }
       // The rows' powers of two.  Those of the segment after the next wait for
       // this one's P, so two places and two barriers are enough.
       wait_or_abort(&mi->q_here[seg & 1], (seg >> 1) & 1, mi, a.status);
@@ -782,8 +951,9 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
     if (!last) {
       it.next(a);
     } else {
-      const int v = it.v, row0 = it.rt * kPairRows + static_cast<int>(rank) * kCtaRows;
-      const int span = it.v * a.row_tiles + it.rt;
+      const QueryRows qr = query_rows<CHUNK>(a, it.v, it.rt);
+      const int row0 = static_cast<int>(rank) * kCtaRows;
+      const int span = CHUNK ? 0 : it.v * a.row_tiles + it.rt;
       const bool ends = it.tile + 1 == it.nt;
       const bool whole = seg_first_tile == 0 && ends;
       const int slot = pair * 2 + (seg == 0 ? 0 : 1);
@@ -796,8 +966,8 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       named_sync(bar_id, kSoftWarps * 16);
       ok = wait_or_abort(&mi->pv_done, g & 1, mi, a.status) && ok;
       tc_fence_after();
-      const bool mine = row0 + r < a.entry_rows;
-      const size_t orow = static_cast<size_t>(v) * a.entry_rows + row0 + r;
+      const bool mine = row0 + r < qr.rows;
+      const size_t orow = qr.first + row0 + r;
       const float inv = !whole ? 1.0f : (lt > 0.0f || lt != lt ? 1.0f / lt : 0.0f);
       const int prow = static_cast<int>(rank) * kCtaRows + r;
       // column 64 q + 8 c + e holds dim 256 half + 32 c + 8 q + e: a thread
@@ -832,8 +1002,12 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
         }
       }
       if (tid == 0 && rank == 0) {
-        if (seg_first_tile == 0) a.span[span].x = slot;
-        if (ends) a.span[span].y = pair;
+        if (CHUNK) {
+          if (!ends) a.rec[pair].w = slot;   // of the pair's last partial
+        } else {
+          if (seg_first_tile == 0) a.span[span].x = slot;
+          if (ends) a.span[span].y = pair;
+        }
       }
       tc_fence_before();
     }
@@ -842,6 +1016,7 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
   wait_or_abort(&mi->q_free, (seg - 1) & 1, mi, a.status);
 }
 
+template <bool CHUNK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     cache_mla_kernel(const MlaArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -890,15 +1065,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   // between two that share a request.  (Few entries are scanned by every warp,
   // without the block: 0.3 us of a small call.)
   constexpr int kSegShift = 43;   // tiles below, segments above
-  const int per = (a.entries + kMlaThreads - 1) / kMlaThreads;
-  const bool few = a.entries <= 32;   // then each warp scans them
-  const int v0 = min(a.entries, few ? lane : tid * per), v1 = min(a.entries, v0 + per);
+  // Chunks scan units, whose requests are found among the requests' first units, kept
+  // where the operands will be.
+  int* unit0 = reinterpret_cast<int*>(smem);
+  const int entries = CHUNK ? chunk_units(a, unit0, reinterpret_cast<int*>(mi->xch)) : a.entries;
+  const int per = (entries + kMlaThreads - 1) / kMlaThreads;
+  const bool few = !CHUNK && entries <= 32;   // then each warp scans them
+  const int v0 = min(entries, few ? lane : tid * per), v1 = min(entries, v0 + per);
   long long mine = 0;
   int nt0 = 0;
-  for (int v = v0; v < v1; ++v) {
-    const int nt = (entry_len(a, v) + kMt - 1) / kMt;
-    if (v == v0) nt0 = nt;
-    if (nt > 0) mine += (static_cast<long long>(nt) + (1LL << kSegShift)) * a.row_tiles;
+  UnitWalk walk0;   // at unit v0
+  if (CHUNK) {
+    walk0.start(a, unit0, v0, v0 < v1);
+    UnitWalk w = walk0;
+    for (int v = v0; v < v1; ++v, w.next(a)) mine += w.tiles(a) + (1LL << kSegShift);
+  } else {
+    for (int v = v0; v < v1; ++v) {
+      const int nt = (entry_len(a, v) + kMt - 1) / kMt;
+      if (v == v0) nt0 = nt;
+      if (nt > 0) mine += (static_cast<long long>(nt) + (1LL << kSegShift)) * a.row_tiles;
+    }
   }
   long long before = mine;
 #pragma unroll
@@ -941,6 +1127,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     if (at == all && tid == 0) mi->end_tile = tiles;   // of the last pair (and idle ones)
     if (at < pos0 || at >= pos1) continue;
     long long off = at - pos0, t = tiles_before;
+    if (CHUNK) {
+      UnitWalk w = walk0;
+      int nt = w.tiles(a);
+      for (; off >= nt + cost; w.next(a), nt = w.tiles(a)) {
+        off -= nt + cost;
+        t += nt;
+      }
+      const int tile = max(static_cast<int>(off) - cost, 0);
+      if (end) {
+        mi->end_tile = t + tile;
+      } else {
+        mi->start_v = w.b;
+        mi->start_rt = w.u;
+        mi->start_tile = tile;
+        mi->first_tile = t + tile;
+      }
+      continue;
+    }
     int v = v0, nt, rt = 0;
     for (;; ++v) {
       nt = v == v0 ? nt0 : (entry_len(a, v) + kMt - 1) / kMt;
@@ -967,16 +1171,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   tc_fence_after();
   const uint32_t tmem = mi->tmem;
 
+  if (CHUNK && rank == 0 && tid == kMmaWarp * 32) {   // see the join
+    const bool inside = pair < tiles && mi->start_tile > 0;
+    QueryRows q{0, 0};
+    if (inside) q = query_rows<CHUNK>(a, mi->start_v, mi->start_rt);
+    a.rec[pair].x = inside ? static_cast<int>(q.first) : -1;
+    a.rec[pair].y = q.rows;
+  }
+  __syncwarp();
   if (pair >= tiles) {
     // nothing to do: both CTAs of the pair
   } else if (warp < kSoftWarps) {
-    softmax_role(a, smem, mi, rank, tmem, pair);
+    softmax_role<CHUNK>(a, smem, mi, rank, tmem, pair);
   } else if (warp == kMmaWarp) {
-    if (rank == 0) mma_role(a, smem, mi, tmem);
+    if (rank == 0) mma_role<CHUNK>(a, smem, mi, tmem);
   } else if (warp == kRowWarp) {
-    row_role(a, mi);
+    row_role<CHUNK>(a, mi);
   } else {
-    widen_role(a, smem, mi, rank);
+    widen_role<CHUNK>(a, smem, mi, rank);
   }
   tc_fence_before();
   __syncthreads();
@@ -994,7 +1206,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
 // and O took 4.0 us to leave a CTA; 2.2 now), and four rows here fill a line.
 constexpr int kJoinThreads = 64;
 
-template <int ROWS, int SLICE, int GROUPS, int FLY>
+// CHUNK: of the rows of the units that pairs cut, 128 a unit.
+template <bool CHUNK, int ROWS, int SLICE, int GROUPS, int FLY>
 __global__ void __launch_bounds__(SLICE* ROWS* GROUPS) cache_mla_join_kernel(
     const MlaArgs a, int all_rows) {
   constexpr int kSlices = kJoinThreads / SLICE;
@@ -1007,28 +1220,56 @@ __global__ void __launch_bounds__(SLICE* ROWS* GROUPS) cache_mla_join_kernel(
                 (at & 1);                               // dims 4t .. and 256 + 4t ..
   const int x = static_cast<int>(blockIdx.x / kSlices) * ROWS + (at >> 1) % ROWS;   // (b, m, h)
   const bool real = x < all_rows;
-  const int xr = real ? x : 0;
-  const int h = xr % a.heads, bm = xr / a.heads, b = bm / a.ways, m = bm % a.ways;
-  const int v = a.tokens ? bm : b;
-  const int row = a.tokens ? h : m * a.heads + h;
-  const int T = a.T[b];
-  const int2 sp = a.span[static_cast<size_t>(v) * a.row_tiles + row / kPairRows];
-  if (real && h == 0 && m == 0 && t == 0 &&
-      (T < 0 || T > static_cast<long long>(a.max_pages) * a.page))
-    set_status(a.status, ESS_ERR_DEVICE_CHECK);
-  const bool empty = entry_len(a, v) == 0;   // then nothing wrote its span
-  const bool join = real && !empty && sp.x >> 1 != sp.y;   // else one pair wrote the row
-  const int p0 = join ? sp.x >> 1 : 0;
-  uint2* out = reinterpret_cast<uint2*>(a.out + static_cast<size_t>(x) * kLatent) + t;
-  if (real && empty && g == 0) {
-    out[0] = out[kJoinThreads] = make_uint2(0u, 0u);
-    if (t == 0 && a.lse) a.lse[x] = -INFINITY;
+  bool join;                 // else one pair wrote the row
+  int p0 = 0, first = 0, last = -1, pr;   // its first pair, that one's slot, its last pair
+  size_t orow = x;
+  if (CHUNK) {
+    // the x / 128th unit that is cut: the pair that is the first to start inside of it
+    const int lane = threadIdx.x & 31;
+    int left = x / kPairRows, p = 0;
+    for (int i0 = 0; i0 < a.pairs && p == 0; i0 += 32) {
+      const int i = i0 + lane;
+      const int at = i < a.pairs ? a.rec[i].x : -1, before = i > 0 && i < a.pairs ? a.rec[i - 1].x : -1;
+      const uint32_t cut = __ballot_sync(0xffffffffu, i > 0 && at >= 0 && at != before);
+      if (left >= __popc(cut)) left -= __popc(cut);
+      else p = i0 + static_cast<int>(__fns(cut, 0, left + 1));
+    }
+    pr = x % kPairRows;
+    const int4 rec = a.rec[p];
+    join = real && p > 0 && pr < rec.y;
+    if (join) {
+      p0 = p - 1;
+      first = a.rec[p0].w;
+      for (last = p; last + 1 < a.pairs && a.rec[last + 1].x == rec.x;) ++last;
+      orow = static_cast<size_t>(rec.x) + pr;
+    }
+  } else {
+    const int xr = real ? x : 0;
+    const int h = xr % a.heads, bm = xr / a.heads, b = bm / a.ways, m = bm % a.ways;
+    const int v = a.tokens ? bm : b;
+    const int row = a.tokens ? h : m * a.heads + h;
+    const int T = a.T[b];
+    const int2 sp = a.span[static_cast<size_t>(v) * a.row_tiles + row / kPairRows];
+    if (real && h == 0 && m == 0 && t == 0 &&
+        (T < 0 || T > static_cast<long long>(a.max_pages) * a.page))
+      set_status(a.status, ESS_ERR_DEVICE_CHECK);
+    const bool empty = entry_len(a, v) == 0;   // then nothing wrote its span
+    join = real && !empty && sp.x >> 1 != sp.y;
+    p0 = join ? sp.x >> 1 : 0;
+    first = sp.x;
+    last = join ? sp.y : -1;
+    pr = row % kPairRows;
+    if (real && empty && g == 0) {
+      uint2* out = reinterpret_cast<uint2*>(a.out + static_cast<size_t>(x) * kLatent) + t;
+      out[0] = out[kJoinThreads] = make_uint2(0u, 0u);
+      if (t == 0 && a.lse) a.lse[x] = -INFINITY;
+    }
   }
+  uint2* out = reinterpret_cast<uint2*>(a.out + orow * kLatent) + t;
   if (GROUPS == 1 && !join) return;
-  const int pr = row % kPairRows, last = join ? sp.y : -1;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   // of every part
-  const float c2 = join ? a.part_ml[static_cast<size_t>(sp.x) * kPairRows + pr].z : 0.0f;
+  const float c2 = join ? a.part_ml[static_cast<size_t>(first) * kPairRows + pr].z : 0.0f;
   float mx = -INFINITY, l = 0.0f;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int pb = p0 + g; pb <= last; pb += FLY * GROUPS) {
@@ -1037,7 +1278,7 @@ __global__ void __launch_bounds__(SLICE* ROWS* GROUPS) cache_mla_join_kernel(
 #pragma unroll
     for (int q = 0; q < FLY; ++q) {
       const int p = pb + q * GROUPS;
-      const size_t i = p == p0 ? sp.x : 2 * p;
+      const size_t i = p == p0 ? first : 2 * p;
       const float4* po = reinterpret_cast<const float4*>(a.part_o + i * kPairRows * kLatent) +
                          ((t >> 1) * kPairRows + pr) * 2 + (t & 1);
       const bool in = p <= last;
@@ -1105,13 +1346,13 @@ __global__ void __launch_bounds__(SLICE* ROWS* GROUPS) cache_mla_join_kernel(
         make_uint2(bf16x2_bits(acc[4 * e] * inv, acc[4 * e + 1] * inv),
                    bf16x2_bits(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
   if (t == 0 && a.lse)
-    a.lse[x] = row_lse(mx, c2, l);
+    a.lse[orow] = row_lse(mx, c2, l);
 }
 
-template <int ROWS, int SLICE, int GROUPS, int FLY>
+template <bool CHUNK, int ROWS, int SLICE, int GROUPS, int FLY>
 cudaError_t launch_join(const MlaArgs& a, long long all_rows, cudaStream_t st) {
   const long long ctas = (all_rows + ROWS - 1) / ROWS * (kJoinThreads / SLICE);
-  return launch_pdl_once(cache_mla_join_kernel<ROWS, SLICE, GROUPS, FLY>,
+  return launch_pdl_once(cache_mla_join_kernel<CHUNK, ROWS, SLICE, GROUPS, FLY>,
                          dim3(static_cast<unsigned>(ctas)), dim3(SLICE * ROWS * GROUPS), 0, st, a,
                          static_cast<int>(all_rows));
 }
@@ -1123,12 +1364,13 @@ ess_status check_shape(int batch, int ways, int heads) {
 }
 
 // The kernel's shared memory, allowed once per device.
+template <bool CHUNK>
 cudaError_t allow_smem(int dev) {
   static std::atomic<unsigned long long> done{0};
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
   if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(
-      cache_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMlaSmem));
+      cache_mla_kernel<CHUNK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMlaSmem));
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
@@ -1148,6 +1390,24 @@ MlaLayout mla_layout(int batch, int ways) {
   o += static_cast<size_t>(kMaxPairs) * 2 * kPairRows * kLatent * sizeof(float);
   L.total = o;
   return L;
+}
+
+struct ChunkLayout {
+  size_t rec, part_o, part_ml, total;
+};
+ChunkLayout chunk_layout() {
+  ChunkLayout L;
+  L.rec = 0;
+  L.part_ml = (kMaxPairs * sizeof(int4) + 255) & ~static_cast<size_t>(255);
+  L.part_o = L.part_ml + static_cast<size_t>(kMaxPairs) * 2 * kPairRows * sizeof(float4);
+  L.total = L.part_o + static_cast<size_t>(kMaxPairs) * 2 * kPairRows * kLatent * sizeof(float);
+  return L;
+}
+
+int page_shift(int page) {   // log2, or -1
+  for (int i = 0; i < 31; ++i)
+    if (page == 1 << i) return i;
+  return -1;
 }
 
 }  // namespace
@@ -1188,16 +1448,14 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ESS_ERR_CUDA;
   const long long all_rows = static_cast<long long>(batch) * ways * heads;
-  MlaArgs a;
+  MlaArgs a = {};
   a.q = static_cast<const uint16_t*>(q);
   a.rows = static_cast<const uint8_t*>(rows);
   a.n_rows = static_cast<int>(n_rows);
   a.page_table = page_table;
   a.max_pages = max_pages;
   a.page = page;
-  a.page_shift = -1;
-  for (int i = 0; i < 31; ++i)
-    if (page == 1 << i) a.page_shift = i;
+  a.page_shift = page_shift(page);
   a.T = T;
   a.batch = batch;
   a.ways = ways;
@@ -1223,9 +1481,9 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
                            kMt - 1) /
                           kMt);
   const int pairs = static_cast<int>(std::min<long long>(most, kMaxPairs));
-  cudaError_t e = allow_smem(dev);
+  cudaError_t e = allow_smem<false>(dev);
   if (e != cudaSuccess) return ESS_ERR_CUDA;
-  e = launch_pdl_once(cache_mla_kernel, dim3(2 * pairs), dim3(kMlaThreads), kMlaSmem, st, a);
+  e = launch_pdl_once(cache_mla_kernel<false>, dim3(2 * pairs), dim3(kMlaThreads), kMlaSmem, st, a);
   if (e != cudaSuccess) return ESS_ERR_CUDA;
   // Few rows with many parts (a 4096-token request: 32) are cut into many small
   // slices: 12.1 us a call, where whole rows took 14.4.  Many rows (2048 and more
@@ -1235,9 +1493,82 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
   // 19.7.  Only rows are counted, as the parts of a row are known on the device: one
   // 128K request among 31 of 512 tokens, with some 70 parts a row in one group, takes
   // 69 us where it takes 42 alone.
-  if (all_rows <= 608) e = launch_join<4, 8, 16, 2>(a, all_rows, st);
-  else if (all_rows < 2048) e = launch_join<4, 64, 2, 4>(a, all_rows, st);
-  else e = launch_join<4, 64, 1, 2>(a, all_rows, st);
+  if (all_rows <= 608) e = launch_join<false, 4, 8, 16, 2>(a, all_rows, st);
+  else if (all_rows < 2048) e = launch_join<false, 4, 64, 2, 4>(a, all_rows, st);
+  else e = launch_join<false, 4, 64, 1, 2>(a, all_rows, st);
+  return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
+}
+
+ess_status ess_cache_chunk_bytes(size_t* bytes) {
+  if (!bytes) return ESS_ERR_INVALID_ARG;
+  *bytes = chunk_layout().total;
+  return ESS_OK;
+}
+
+ess_status ess_cache_chunk(const void* q, int64_t total, const int32_t* cu, const void* rows,
+                           int64_t n_rows, int32_t format, const int32_t* page_table,
+                           int32_t max_pages, int32_t page, const int32_t* T, int32_t batch,
+                           int32_t heads, const int32_t* tokens, int32_t k, float sm_scale,
+                           void* out, float* lse, void* workspace, size_t ws_bytes,
+                           int32_t* status, ess_stream_t stream) {
+  if (batch < 1 || heads < 1 || total < 0) return ESS_ERR_INVALID_ARG;
+  if (heads > kMaxCacheHeads || batch > kMaxChunkBatch || total > (0x7fffff00LL - 128) / heads)
+    return ESS_ERR_UNSUPPORTED;
+  if (format < ESS_ROW_BF16 || format > ESS_ROW_Q4 || n_rows < 1 || max_pages < 1 || page < 1 ||
+      (tokens && k < 1) || !(sm_scale > 0.0f) || !std::isfinite(sm_scale))
+    return ESS_ERR_INVALID_ARG;
+  if (format != ESS_ROW_Q4 || n_rows > 0x7fffffffLL ||
+      static_cast<long long>(max_pages) * page > 0x7fffff00LL || k > 0x7fffff00)
+    return ESS_ERR_UNSUPPORTED;
+  if (total == 0) return ESS_OK;
+  if (!q || !cu || !rows || !page_table || !T || !out || !workspace || !aligned16(q) ||
+      !aligned16(rows) || !aligned16(out) || !aligned_to(workspace, 256) || !aligned_to(cu, 4) ||
+      !aligned_to(page_table, 4) || !aligned_to(T, 4) || !aligned_to(tokens, 4) ||
+      !aligned_to(lse, 4) || !aligned_to(status, 4))
+    return ESS_ERR_INVALID_ARG;
+  const ChunkLayout L = chunk_layout();
+  if (ws_bytes < L.total) return ESS_ERR_OOM;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ESS_ERR_CUDA;
+  MlaArgs a = {};
+  a.q = static_cast<const uint16_t*>(q);
+  a.rows = static_cast<const uint8_t*>(rows);
+  a.n_rows = static_cast<int>(n_rows);
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.page = page;
+  a.page_shift = page_shift(page);
+  a.T = T;
+  a.batch = batch;
+  a.heads = heads;
+  a.tokens = tokens;
+  a.k = k;
+  a.cu = cu;
+  a.total = static_cast<int>(total);
+  a.unit_rows = tokens ? heads : kPairRows;
+  a.c2 = std::min(sm_scale * 1.4426950408889634f, FLT_MAX);
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  char* ws = static_cast<char*>(workspace);
+  a.rec = reinterpret_cast<int4*>(ws + L.rec);
+  a.part_o = reinterpret_cast<float*>(ws + L.part_o);
+  a.part_ml = reinterpret_cast<float4*>(ws + L.part_ml);
+  a.status = status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // no more pairs than tiles there can be
+  const long long context = static_cast<long long>(max_pages) * page;
+  const long long units = tokens ? total : total * heads / kPairRows + std::min<long long>(total, batch);
+  const long long most = units * (((tokens ? std::min<long long>(k, context) : context) + kMt - 1) / kMt);
+  a.pairs = static_cast<int>(std::max(1LL, std::min<long long>(most, kMaxPairs)));
+  cudaError_t e = allow_smem<true>(dev);
+  if (e != cudaSuccess) return ESS_ERR_CUDA;
+  e = launch_pdl_once(cache_mla_kernel<true>, dim3(2 * a.pairs), dim3(kMlaThreads), kMlaSmem, st, a);
+  if (e == cudaSuccess && a.pairs > 1) {
+    const long long cut = std::min<long long>(units, a.pairs - 1) * kPairRows;
+    // few units have many parts each
+    if (units <= 8) e = launch_join<true, 4, 8, 16, 2>(a, cut, st);
+    else e = launch_join<true, 4, 64, 2, 4>(a, cut, st);
+  }
   return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
 }
 

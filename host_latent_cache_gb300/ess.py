@@ -47,7 +47,7 @@ EXPORTS = (
     "ess_pool_bind_layer_compact", "ess_prefill_run", "ess_row_bytes", "ess_status_take",
     "ess_cache_write",
     "ess_cache_read", "ess_cache_mla_bytes", "ess_cache_mla", "ess_norm_quant",
-    "ess_quant", "ess_product", "ess_cache_write_axes", "ess_rotate",
+    "ess_cache_chunk_bytes", "ess_cache_chunk", "ess_quant", "ess_product", "ess_cache_write_axes", "ess_rotate",
 )
 
 # void (*)(void* user, int32_t layer, void* buffer, void* stream)
@@ -139,6 +139,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "ess_norm_quant": [P, L, P, L, P, F, L, I, P, P, P, P],
         "ess_cache_write_axes": [P, L, L, P, F, P, P, I, P, I, P, P, L, I, P, P],
         "ess_rotate": [P, L, L, L, I, P, P, I, P, I, P, L, L, P],
+        "ess_cache_chunk_bytes": [ctypes.POINTER(ctypes.c_size_t)],
+        "ess_cache_chunk": [P, L, P, P, L, I, P, I, I, P, I, I, P, I, F, P, P, P, ctypes.c_size_t, P,
+                            P],
         "ess_quant": [P, L, L, I, I, P, P, P],
         "ess_product": [P, P, L, P, P, I, I, P, L, I, P, P],
     }
@@ -484,6 +487,21 @@ def ess_cache_mla(q, rows, n_rows: int, fmt: int, page_table, max_pages: int, pa
                                _p(T), batch, ways, heads, _p(tokens), k, sm_scale, _p(out),
                                _p(lse), _p(workspace), ws_bytes, _p(status), _stream(stream)),
           "ess_cache_mla")
+
+
+def ess_cache_chunk_bytes() -> int:
+    n = ctypes.c_size_t(0)
+    check(load().ess_cache_chunk_bytes(ctypes.byref(n)), "ess_cache_chunk_bytes")
+    return n.value
+
+
+def ess_cache_chunk(q, total: int, cu, rows, n_rows: int, fmt: int, page_table, max_pages: int,
+                    page: int, T, batch: int, heads: int, tokens, k: int, sm_scale: float, out, lse,
+                    workspace, ws_bytes: int, status=None, stream=None) -> None:
+    check(load().ess_cache_chunk(_p(q), total, _p(cu), _p(rows), n_rows, fmt, _p(page_table),
+                                 max_pages, page, _p(T), batch, heads, _p(tokens), k, sm_scale,
+                                 _p(out), _p(lse), _p(workspace), ws_bytes, _p(status),
+                                 _stream(stream)), "ess_cache_chunk")
 
 
 def ess_norm_quant(x, x_stride: int, residual, residual_stride: int, gamma, eps: float, n: int,

@@ -136,6 +136,11 @@ def release_workspaces() -> None:
             ws.buf = None
 
 
+@functools.lru_cache(maxsize=None)
+def _chunk_bytes() -> int:
+    return ess.ess_cache_chunk_bytes()
+
+
 @functools.lru_cache(maxsize=64)
 def _doubles(values):
     _need(len(values) == ROPE // 2, f"inv_freq has {len(values)} entries, not {ROPE // 2}")
@@ -233,7 +238,13 @@ class RowCache:
     def workspace(self, batch: int, ways: int, heads: int) -> torch.Tensor:
         """A workspace for `attend`; one for each stream, or captured graph,
         that may run beside another."""
-        n = ess.ess_cache_mla_bytes(batch, ways, heads)
+        return self._new_workspace(ess.ess_cache_mla_bytes(batch, ways, heads))
+
+    def chunk_workspace(self) -> torch.Tensor:
+        """A workspace for `attend_chunk`, of any shape; as `workspace`."""
+        return self._new_workspace(ess.ess_cache_chunk_bytes())
+
+    def _new_workspace(self, n: int) -> torch.Tensor:
         buf = torch.empty(n + 256, dtype=torch.uint8, device=self.device)
         off = (-buf.data_ptr()) % 256
         return buf[off:off + n]
@@ -292,10 +303,14 @@ class RowCache:
                     workspace = self.workspace(batch, ways, heads)
                 else:
                     kept = self._ws.get(stream) or self._share(stream)
+                    need = self._bytes.get((batch, ways, heads))
+                    if need is None:
+                        need = ess.ess_cache_mla_bytes(batch, ways, heads)
+                        self._bytes[batch, ways, heads] = need
                     with kept.lock:
                         self._attend(q, page_table, max_pages, page, T, batch, ways, heads,
-                                     tokens, k, sm_scale, out, lse,
-                                     self._enough(kept, batch, ways, heads), stream)
+                                     tokens, k, sm_scale, out, lse, self._enough(kept, need),
+                                     stream)
                     return out, lse
             self._attend(q, page_table, max_pages, page, T, batch, ways, heads, tokens, k, sm_scale,
                          out, lse, workspace, stream)
@@ -309,13 +324,72 @@ class RowCache:
             self._ws[stream] = kept
         return kept
 
-    def _enough(self, kept: _Workspace, batch: int, ways: int, heads: int) -> torch.Tensor:
-        need = self._bytes.get((batch, ways, heads))
-        if need is None:
-            need = self._bytes[batch, ways, heads] = ess.ess_cache_mla_bytes(batch, ways, heads)
+    def _enough(self, kept: _Workspace, need: int) -> torch.Tensor:
         if kept.buf is None or kept.buf.numel() < need:
-            kept.buf = self.workspace(batch, ways, heads)
+            kept.buf = self._new_workspace(need)
         return kept.buf
+
+    def attend_chunk(self, q, cu, page_table, T, sm_scale: float, tokens=None, out=None, lse=None,
+                     workspace=None):
+        """Attention of chunks of new tokens: q bf16 [total][heads][576], of which
+        request b has the tokens cu[b] to cu[b + 1] - 1 (cu int32 [batch + 1]), its
+        newest of T[b] (int32 [batch]), each attending to itself and all before it
+        (page_table int32 [batch][max_pages]), or to tokens int32 [total][k].
+        Returns (out bf16 [total][heads][512], lse float32 [total][heads]); tokens of q
+        outside all requests leave their places in both as they were.  Workspaces,
+        threads and empty arguments as in `attend`."""
+        at = self._index
+        _need(isinstance(q, torch.Tensor) and q.dim() == 3 and q.shape[1] >= 1,
+              "q: [total][heads][576] is needed")
+        total, heads, _ = q.shape
+        _check(q, "q", _BF16, (total, heads, ROW), at)
+        _need(isinstance(page_table, torch.Tensor) and page_table.dim() == 2,
+              "page_table: [batch][max_pages] is needed")
+        batch, max_pages = page_table.shape
+        _check(page_table, "page_table", _I32, (batch, max_pages), at)
+        _check(T, "T", _I32, (batch,), at)
+        _check(cu, "cu", _I32, (batch + 1,), at)
+        k = 0
+        if tokens is not None:
+            _need(isinstance(tokens, torch.Tensor) and tokens.dim() == 2,
+                  "tokens: [total][k] is needed")
+            k = tokens.shape[1]
+            _check(tokens, "tokens", _I32, (total, k), at)
+        _need(max(max_pages, k, batch, heads) <= MOST,
+              "more than 2^31 - 1 pages, listed tokens, requests or heads")
+        if out is None:
+            out = torch.empty((total, heads, LATENT), dtype=_BF16, device=self.device)
+        else:
+            _check(out, "out", _BF16, (total, heads, LATENT), at)
+        if lse is None:
+            lse = torch.empty((total, heads), dtype=torch.float32, device=self.device)
+        else:
+            _check(lse, "lse", torch.float32, (total, heads), at)
+        if workspace is not None:
+            _need(_is(workspace, torch.uint8, (workspace.numel(),), at)
+                  if isinstance(workspace, torch.Tensor) else False,
+                  f"workspace: contiguous uint8 [bytes] on cuda:{at} is needed")
+        if batch == 0 or total == 0:
+            return out, lse
+        page = self.page
+        if k == 0 and tokens is not None:      # as lists that hold nothing
+            k = 1
+            tokens = torch.full((total, 1), -1, dtype=_I32, device=self.device)
+        if max_pages == 0:                     # as one page that is not there
+            max_pages = page = 1
+            page_table = torch.full((batch, 1), -1, dtype=_I32, device=self.device)
+        args = (q, total, cu, self.rows, self.n_rows, self._f, page_table, max_pages, page, T, batch,
+                heads, tokens, k, sm_scale, out, lse)
+        with _OnDevice(at) as stream:
+            if workspace is None and not torch._C._cuda_isCurrentStreamCapturing():
+                kept = self._ws.get(stream) or self._share(stream)
+                with kept.lock:
+                    buf = self._enough(kept, _chunk_bytes())
+                    ess.ess_cache_chunk(*args, buf, buf.numel(), self.status, stream)
+            else:
+                buf = self.chunk_workspace() if workspace is None else workspace
+                ess.ess_cache_chunk(*args, buf, buf.numel(), self.status, stream)
+        return out, lse
 
     def _attend(self, q, page_table, max_pages, page, T, batch, ways, heads, tokens, k, sm_scale,
                 out, lse, workspace, stream) -> None:

@@ -665,6 +665,43 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
                          const int32_t* tokens, int32_t k, float sm_scale, void* out, float* lse,
                          void* workspace, size_t ws_bytes, int32_t* status, ess_stream_t stream);
 
+/* Bytes of device workspace that ess_cache_chunk needs, whatever its shape.
+ * Errors: ESS_ERR_INVALID_ARG for a null argument. */
+ess_status ess_cache_chunk_bytes(size_t* bytes);
+
+/* Absorbed-MLA attention of chunks of new tokens (prompts, or parts of them) over a
+ * device row cache: requests with any number of query tokens each, side by side.
+ *   q          device bf16 [total][heads][576], 16-byte aligned
+ *   cu         device int32 [batch + 1]: request b's queries are the tokens cu[b] to
+ *              cu[b + 1] - 1 of q, its newest ones: token i of its n is token T_b - n + i,
+ *              whose row (like those before it) is in the cache.  Tokens of q outside
+ *              all requests are not read, and their places in out and lse are left as
+ *              they were.
+ *   T          device int32 [batch]: tokens of each request, the new ones included
+ *   tokens     NULL: token i attends to the tokens t <= T_b - n + i.  Otherwise device
+ *              int32 [total][k]: a query token attends to those of its first
+ *              min(k, T_b - n + i + 1) entries that are tokens, whatever their order; a
+ *              negative entry is no token.
+ *   out        device bf16 [total][heads][512], 16-byte aligned
+ *   lse        device float [total][heads], or NULL
+ *   workspace  device, 256-byte aligned, at least ess_cache_chunk_bytes; calls that
+ *              share one are ordered by the caller
+ * rows, page_table, the results and the roundings are as in ess_cache_mla.  A query that
+ * attends to nothing (n above T_b) gets zeros and lse = -infinity.  A length outside its
+ * range, offsets that are negative, fall or pass total (the request then has no queries),
+ * a token past its query's and a page outside the cache report ESS_ERR_DEVICE_CHECK in
+ * status; such a token is left out.  total = 0 launches nothing.
+ * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or non-positive argument or a scale
+ * that is not finite; ESS_ERR_UNSUPPORTED for more than 128 heads or 32768 requests,
+ * another format, more than 2^31 - 1 rows, max_pages * page or k above 2^31 - 256, or
+ * total * heads of 2^31 - 384 or more; ESS_ERR_OOM for a workspace that is too small. */
+ess_status ess_cache_chunk(const void* q, int64_t total, const int32_t* cu, const void* rows,
+                           int64_t n_rows, int32_t format, const int32_t* page_table,
+                           int32_t max_pages, int32_t page, const int32_t* T, int32_t batch,
+                           int32_t heads, const int32_t* tokens, int32_t k, float sm_scale,
+                           void* out, float* lse, void* workspace, size_t ws_bytes,
+                           int32_t* status, ess_stream_t stream);
+
 /* Root-mean-square norm with the residual's addition and e4m3 output.
  *   x             device bf16, n rows of dim values, x_stride elements apart
  *   residual      device bf16, n rows, residual_stride apart, or NULL
