@@ -78,8 +78,11 @@ constexpr int kWidenWarps = 16;
 constexpr int kRowWarp = kWidenWarp0 + kWidenWarps;
 constexpr int kMlaThreads = (kRowWarp + 1) * 32;
 // What a segment costs beside its tiles, in tiles, when they are dealt: ragged
-// requests to 8192 took 97.3 us with 0, 94.1 with 1, 91.9 with 2, 92.3 with 3.
+// requests to 8192 took 97.3 us with 0, 94.1 with 1, 91.9 with 2, 92.3 with 3.  A chunk's
+// segments cost more, about 6 us, and may be short: ragged chunks to 8192 tokens, one
+// of them a prompt of 200 without a prefix, took 647 us with 2, 552 with 3 or 4.
 constexpr int kSegmentCost = 2;
+constexpr int kChunkSegmentCost = 3;
 constexpr int kRing = 3;              // tiles whose rows are known ahead of their use
 
 constexpr uint32_t kKBlk = 8192;      // [64 rows][64 dims], 128-byte swizzled
@@ -1109,7 +1112,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   }
   constexpr long long kTileMask = (1LL << kSegShift) - 1;
   const long long tiles = total & kTileMask;
-  const int cost = tiles >= static_cast<long long>(kSegmentCost + 1) * pairs ? kSegmentCost : 0;
+  constexpr int kCost = CHUNK ? kChunkSegmentCost : kSegmentCost;
+  const int cost = tiles >= static_cast<long long>(kCost + 1) * pairs ? kCost : 0;
   const long long tiles_before = before & kTileMask;
   const long long pos0 = tiles_before + cost * (before >> kSegShift);
   const long long pos1 = pos0 + (mine & kTileMask) + cost * (mine >> kSegShift);
@@ -1225,23 +1229,39 @@ __global__ void __launch_bounds__(SLICE* ROWS* GROUPS) cache_mla_join_kernel(
   size_t orow = x;
   if (CHUNK) {
     // the x / 128th unit that is cut: the pair that is the first to start inside of it
+    // (all records at once, as one after another takes a latency each)
+    constexpr int kPer = (kMaxPairs + 31) / 32;
     const int lane = threadIdx.x & 31;
-    int left = x / kPairRows, p = 0;
-    for (int i0 = 0; i0 < a.pairs && p == 0; i0 += 32) {
-      const int i = i0 + lane;
-      const int at = i < a.pairs ? a.rec[i].x : -1, before = i > 0 && i < a.pairs ? a.rec[i - 1].x : -1;
-      const uint32_t cut = __ballot_sync(0xffffffffu, i > 0 && at >= 0 && at != before);
-      if (left >= __popc(cut)) left -= __popc(cut);
-      else p = i0 + static_cast<int>(__fns(cut, 0, left + 1));
+    int at[kPer], before[kPer];
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) {
+      const int i = 32 * c + lane;
+      at[c] = i < a.pairs ? a.rec[i].x : -1;
+      before[c] = i > 0 && i < a.pairs ? a.rec[i - 1].x : -1;
     }
+    int left = x / kPairRows, p = 0, unit = -1, inside = 0;
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) {
+      const uint32_t cut = __ballot_sync(0xffffffffu, at[c] >= 0 && at[c] != before[c] &&
+                                                          32 * c + lane > 0);
+      const int here = left < __popc(cut) && p == 0 ? static_cast<int>(__fns(cut, 0, left + 1)) : -1;
+      left -= __popc(cut);
+      const int u = __shfl_sync(0xffffffffu, at[c], max(here, 0));
+      if (here >= 0) {
+        p = 32 * c + here;
+        unit = u;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kPer; ++c)   // pairs that start inside of it, side by side
+      inside += __popc(__ballot_sync(0xffffffffu, at[c] >= 0 && at[c] == unit));
     pr = x % kPairRows;
-    const int4 rec = a.rec[p];
-    join = real && p > 0 && pr < rec.y;
+    join = real && p > 0 && pr < a.rec[p].y;
     if (join) {
       p0 = p - 1;
       first = a.rec[p0].w;
-      for (last = p; last + 1 < a.pairs && a.rec[last + 1].x == rec.x;) ++last;
-      orow = static_cast<size_t>(rec.x) + pr;
+      last = p0 + inside;
+      orow = static_cast<size_t>(unit) + pr;
     }
   } else {
     const int xr = real ? x : 0;
