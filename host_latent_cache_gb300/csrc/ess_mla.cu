@@ -142,6 +142,7 @@ struct MlaArgs {
   const int32_t* cu;       // chunks: [batch + 1] first query token of each request
   int total;               // chunks: query tokens
   int unit_rows;           // chunks: query rows that share tiles: 128, or a token's heads
+  bool wide_out;           // chunks: out is 32-byte aligned
   int pairs;               // chunks: pairs of the launch
   int4* rec;               // chunks: [pairs] which units the pairs cut
   int2* span;              // [entries][row_tiles]: first pair * 2 + slot, last pair
@@ -986,9 +987,19 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
           uint16_t* dst = a.out + orow * kLatent + d0 + 32 * c;
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] *= inv;
+          if (CHUNK && a.wide_out) {
+            // 32 bytes a store: half as many requests (a row a lane, each has its own line)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            reinterpret_cast<uint4*>(dst)[x] = pack8_bf16(o + 8 * x);
+            for (int x = 0; x < 2; ++x) {
+              const uint4 lo = pack8_bf16(o + 16 * x), hi = pack8_bf16(o + 16 * x + 8);
+              const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+              st_global_32(reinterpret_cast<float*>(dst) + 8 * x, reinterpret_cast<const float*>(w));
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              reinterpret_cast<uint4*>(dst)[x] = pack8_bf16(o + 8 * x);
+          }
         } else {
           float* dst = a.part_o + static_cast<size_t>(slot) * kPairRows * kLatent +
                        ((d0 + 32 * c) / 8 * kPairRows + prow) * 8;
@@ -1565,6 +1576,7 @@ ess_status ess_cache_chunk(const void* q, int64_t total, const int32_t* cu, cons
   a.k = k;
   a.cu = cu;
   a.total = static_cast<int>(total);
+  a.wide_out = aligned_to(out, 32);
   a.unit_rows = tokens ? heads : kPairRows;
   a.c2 = std::min(sm_scale * 1.4426950408889634f, FLT_MAX);
   a.out = static_cast<uint16_t*>(out);
