@@ -47,7 +47,7 @@ struct QuantArgs {
 };
 
 constexpr int kQuantThreads = 256;
-constexpr int kQuantItems = 4;     // groups in flight per 16 lanes
+constexpr int kQuantItems = 2;     // groups in flight per 16 lanes
 
 // Sixteen lanes a group of 128 values, 16 bytes a lane.
 __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const QuantArgs a) {
