@@ -1255,7 +1255,12 @@ __global__ void __launch_bounds__(SLICE* ROWS* GROUPS) cache_mla_join_kernel(
     for (int c = 0; c < kPer; ++c) {
       const uint32_t cut = __ballot_sync(0xffffffffu, at[c] >= 0 && at[c] != before[c] &&
                                                           32 * c + lane > 0);
-      const int here = left < __popc(cut) && p == 0 ? static_cast<int>(__fns(cut, 0, left + 1)) : -1;
+      int here = -1;
+      if (left < __popc(cut) && p == 0) {
+        uint32_t bits = cut;
+        for (int i = 0; i < left; ++i) bits &= bits - 1;
+        here = __ffs(bits) - 1;
+      }
       left -= __popc(cut);
       const int u = __shfl_sync(0xffffffffu, at[c], max(here, 0));
       if (here >= 0) {
