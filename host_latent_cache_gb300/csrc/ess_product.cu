@@ -8,11 +8,6 @@
 // row and 32 values of K, from TMEM, at the full 8-bit rate, and no accumulator
 // is read before its sum is complete.
 //
-// The weight's rows are the MMA's M (128 a CTA), the tokens its N: a product with
-// few tokens, which is bound by reading the weight, then wastes no tensor width,
-// and a thread of the epilogue holds one output column, so a warp writes runs of
-// neighbouring columns.
-//
 //   warps 0-3  epilogue: accumulators out of TMEM, converted and stored
 //   warps 4-7  scales: fp32 scales -> exponent bytes -> TMEM.  The four bytes of a
 //              32-bit cell are four groups of K; row 32 c + l sits in column c of
@@ -20,10 +15,29 @@
 //   warp 8     TMA: 128 bytes of K of both operands a stage, 128B swizzle
 //   warp 9     MMA
 //
-// Few tokens: one tile a CTA, two CTAs an SM; the CTAs of a cluster share a tile,
-// each with a part of K, and add their fp32 accumulators up through distributed
-// shared memory, in order.  Many tokens: pairs of CTAs (cta_group::2) compute 256 x
-// 256 tiles, walking over tiles, the epilogue of one beside the MMAs of the next.
+// Few tokens: tiles of 128 weight rows (the MMA's M) x 16 to 64 tokens, one a CTA and
+// two CTAs an SM, so that reading the weight, which bounds them, wastes no tensor width
+// and a warp of the epilogue writes runs of neighbouring columns.  The CTAs of a cluster
+// share a tile, each with a part of K; each adds up the sums of its part of the tokens,
+// which come to it by bulk copies between the CTAs' shared memories, in the order of the
+// parts.  Many tokens: pairs of CTAs (cta_group::2) compute 256 tokens x 256 columns,
+// walking over tiles, the epilogue of one beside the MMAs of the next: two accumulators
+// of 256 columns and the scales need 536 of 512, so they share 32, which are read first.
+//
+// Measured (bytes that the call cannot do without, or flops, / time): 8192 x 4096 x 8192
+// 183 us (3.0 PFLOP/s, 78 % of twice the measured bf16 rate; a library's product with the
+// same scale form takes 150 to 179, by the codes), 8192 x 1024 x 24576 169 us, 2048 x 4096
+// x 8192 55, 512 x 4096 x 8192 18.3, 333 x 4112 x 1601 12.8, 64 x 4096 x 8192 9.5, 32 x
+// 1024 x 24576 6.7 (4.0 TB/s), 4 x 4096 x 1600 4.1; a launch that does nothing else 2.9.
+// fp32 results: 2048 x 4096 x 8192 115 us, in tiles for few tokens (pairs have no
+// registers for their sums).
+// What bounds a large one: the tensor pipe is busy for 61 % of an SM's active cycles, 1100
+// to 2000 cycles between two tiles and some 190 to 250 a stage of 512 are lost, and no
+// other unit is above 40 %: L2 30 %, its crossbar 37 %, shared memory's banks 14 %, DRAM
+// 10 %.  Without the operands' loads a stage takes 600 cycles, with them 800, whatever
+// their depth (four, five or six stages), the order of tiles, multicast to a second pair
+// (clusters of four, of which 36 fit, 194 us) or where they come from.  Seconds on end it
+// is held at 1.8 GHz by the power limit, 202 us.
 #include <algorithm>
 #include <atomic>
 #include <cstddef>
@@ -49,7 +63,9 @@ struct QuantArgs {
 constexpr int kQuantThreads = 256;
 constexpr int kQuantItems = 2;     // groups in flight per 16 lanes
 
-// Sixteen lanes a group of 128 values, 16 bytes a lane.
+// Sixteen lanes a group of 128 values, 16 bytes a lane.  16384 x 4096 take 38.5 us (5.3
+// TB/s; two streams one of which is half as wide: a copy reaches 6.8), with one, two or
+// four groups in flight alike, with eight 43.5; 16 rows 1.6 us.
 __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const QuantArgs a) {
   pdl_wait_previous();
   // rows of 128 values may be bound indexer keys: nothing starts before they are written
@@ -84,7 +100,8 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const QuantAr
   }
 }
 
-// One CTA a block of 128 x 128: 16 lanes a row, 16 rows at a time.
+// One CTA a block of 128 x 128: 16 lanes a row, 16 rows at a time.  16384 x 4096 take
+// 37.6 us, 1600 x 4096 3.1.
 __global__ void __launch_bounds__(kQuantThreads) quant_square_kernel(const QuantArgs a) {
   __shared__ float part[kQuantThreads / 32];
   pdl_wait_previous();
@@ -141,7 +158,7 @@ constexpr int kOverlap = 32;             // columns that the two accumulators of
 constexpr int kSumGroups = 8;
 
 constexpr int prod_stages(int bn, bool pair) {
-  return pair ? 6 : bn <= 16 ? 5 : bn <= 32 ? 4 : bn <= 64 ? 3 : 4;
+  return pair ? 6 : bn <= 16 ? 5 : bn <= 32 ? 4 : 3;
 }
 constexpr int prod_b_rows(int bn, bool pair) { return pair ? bn / 2 : bn; }   // a CTA's part of B
 constexpr uint32_t prod_stage_bytes(int bn, bool pair) {
@@ -370,7 +387,7 @@ struct ProdShare {
 };
 
 template <int BN, bool PAIR, typename Out>
-__global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out) == 4) ? 1 : 2)
+__global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
     product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                    const __grid_constant__ CUtensorMap omap, const ProdArgs a) {
   constexpr bool kSums = sizeof(Out) == 4;   // short sums, added up in registers
@@ -412,7 +429,9 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
     mbar_init(smem_u32(&mi->sums_here), 1);
     mi->abort = 0;
     fence_mbar_init();
-    if (!PAIR && parts > 1) mbar_arrive_expect_tx(smem_u32(&mi->sums_here), BN * 512);
+    if (!PAIR && parts > 1)
+      mbar_arrive_expect_tx(smem_u32(&mi->sums_here),
+                            parts * 512 * (BN * (rank + 1) / parts - BN * rank / parts));
     tma_prefetch_desc(&amap);
     tma_prefetch_desc(&bmap);
     if (PAIR && a.blocks) tma_prefetch_desc(&omap);
@@ -443,10 +462,12 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
   if (warp == kTmaWarp) {
     if (prod_elect()) {
       int stage = 0, turn = 0;
-      for (int t = sh.first; t < sh.tiles; t += sh.step) {
+      bool ok = true;   // after a wait that gave up nothing more is loaded
+      for (int t = sh.first; ok && t < sh.tiles; t += sh.step) {
         const int m0 = m_of(t), n0 = n_of(t) + (PAIR ? static_cast<int>(rank) * kBRows : 0);
         for (int g = sh.g0; g < sh.g1; ++g) {
-          if (turn > 0) prod_wait(&mi->empty[stage], (turn - 1) & 1, mi, a.status);
+          if (turn > 0) ok = prod_wait(&mi->empty[stage], (turn - 1) & 1, mi, a.status);
+          if (!ok) break;
           const uint32_t dst = smem_u32(smem + stage * kStage), bar = smem_u32(&mi->full[stage]);
           if (PAIR) {
             if (rank == 0) mbar_arrive_expect_tx(bar, 2 * kStage);
@@ -634,10 +655,11 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
     auto send = [&] {
       fence_proxy_async_smem();
       asm volatile("bar.sync 2, %0;" ::"n"(kEpiWarps * 32) : "memory");
-      const uint32_t bytes = BN * 512 / parts;
-      if (tid < static_cast<int>(parts))
-        bulk_to_cta(dsmem_addr(smem_u32(blocks) + rank * bytes, tid), smem_u32(smem) + tid * bytes,
-                    bytes, dsmem_addr(smem_u32(&mi->sums_here), tid));
+      if (tid < static_cast<int>(parts)) {
+        const uint32_t t0 = BN * tid / parts, some = BN * (tid + 1) / parts - t0;
+        bulk_to_cta(dsmem_addr(smem_u32(blocks) + rank * some * 512, tid), smem_u32(smem) + t0 * 512,
+                    some * 512, dsmem_addr(smem_u32(&mi->sums_here), tid));
+      }
     };
     if (kSums) {
       float sum[kAcc];
@@ -728,9 +750,10 @@ __global__ void __launch_bounds__(kProdThreads, PAIR || (BN == 128 && sizeof(Out
     // The cluster's CTAs held the same tile's sums over their parts of K: each adds up
     // the tokens [BN rank / parts, BN (rank + 1) / parts), in the order of the parts.
     prod_wait(&mi->sums_here, 0, mi, a.status);
-    const int share = BN / static_cast<int>(parts);
+    const int t0 = static_cast<int>(BN * rank / parts);
+    const int share = static_cast<int>(BN * (rank + 1) / parts) - t0;
     const int f = m_of(sh.first) + (tid & 127);
-    const int x0 = n_of(sh.first) + static_cast<int>(rank) * share;
+    const int x0 = n_of(sh.first) + t0;
     if (tid < 256 && f < a.outs) {
       const float* in = reinterpret_cast<const float*>(blocks) + (tid & 127);
       for (int c = tid >> 7; c < share && x0 + c < a.n; c += 2) {
@@ -881,7 +904,7 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   // 28 tiles, 17.2 against 16.2.
   const long long pair_tiles = static_cast<long long>(cover(outs, 256)) * cover(n, 256);
   const bool pair = !fp32 && n > 128 && pair_tiles >= sms / 4;
-  const int bn = pair ? 256 : n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 || !fp32 ? 64 : 128;
+  const int bn = pair ? 256 : n <= 16 ? 16 : n <= 32 ? 32 : 64;
   a.m_tiles = pair ? cover(n, 256) : cover(outs, 128);
   a.n_tiles = pair ? cover(outs, 256) : cover(n, bn);
   const long long tiles = static_cast<long long>(a.m_tiles) * a.n_tiles;
@@ -890,11 +913,10 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   if (pair) {
     ctas = 2 * static_cast<int>(std::min<long long>(tiles, sms / 2));
   } else {
-    // K is cut until every CTA slot is taken or a CTA has two to three stages: 4 x 4096 x
+    // K is cut as long as two CTAs an SM run at once and each has two stages: 4 x 4096 x
     // 1600 takes 10.5 us uncut, 7.2 in two parts, 5.1 in four, 4.1 in eight; 128 x 4096 x
     // 8192 12.8, 13.2, 13.1.
-    const int slots = (bn == 128 && fp32 ? 1 : 2) * sms;   // CTAs that run at once
-    while (parts < 8 && tiles * parts * 2 <= slots && a.groups >= 4 * parts) parts *= 2;
+    while (parts < 8 && tiles * (parts + 1) <= 2 * sms && a.groups >= 2 * (parts + 1)) ++parts;
     ctas = static_cast<int>(tiles) * parts;
   }
   CUtensorMap wm, xm, om;
@@ -916,8 +938,7 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   if (pair) e = launch_product<256, true, __nv_bfloat16>(xm, wm, om, a, parts, ctas, dev, st);
   else if (bn == 16) e = launch_single<16>(f, wm, xm, a, parts, ctas, dev, st);
   else if (bn == 32) e = launch_single<32>(f, wm, xm, a, parts, ctas, dev, st);
-  else if (bn == 64) e = launch_single<64>(f, wm, xm, a, parts, ctas, dev, st);
-  else e = launch_product<128, false, float>(wm, xm, wm, a, parts, ctas, dev, st);
+  else e = launch_single<64>(f, wm, xm, a, parts, ctas, dev, st);
   return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
 }
 
