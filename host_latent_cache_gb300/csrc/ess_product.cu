@@ -236,10 +236,13 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src,
       "r"(src), "r"(x), "r"(y)
       : "memory");
 }
-// arrive on a barrier of either CTA of a pair, behind everything before it
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
+// Arrive on a barrier of either CTA of a pair.  The default (CTA-scope) release is enough:
+// what it orders are this CTA's reads and writes of TMEM, which tcgen05.wait and
+// tcgen05.fence have put before it.  A cluster-scope release waits for the warp's loads in
+// flight: the scales' fetches then held up every round of four groups (8192 x 4096 x 8192
+// 183 us instead of REL).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // a load into this CTA that counts its bytes on the even CTA's barrier
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m,
@@ -617,7 +620,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (PAIR) mbar_arrive_cluster(dsmem_addr(smem_u32(&mi->sf_full[sb]), 0));
+          if (PAIR) mbar_arrive_pair(dsmem_addr(smem_u32(&mi->sf_full[sb]), 0));
           else mbar_arrive(smem_u32(&mi->sf_full[sb]));
         }
         if (++sb == 2) {
@@ -700,7 +703,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
           if (PAIR && j == 0) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&mi->acc_free[0]), 0));
+            if (lane == 0) mbar_arrive_pair(dsmem_addr(smem_u32(&mi->acc_free[0]), 0));
           }
           if (!PAIR && parts > 1) {
             keep(b, v);
