@@ -146,9 +146,9 @@ constexpr int kEpiWarps = 4, kScaleWarps = 4;
 constexpr int kTmaWarp = kEpiWarps + kScaleWarps, kProdMmaWarp = kTmaWarp + 1;
 constexpr int kProdThreads = (kProdMmaWarp + 1) * 32;
 constexpr uint32_t kATile = 128 * 128;   // bytes of the first operand's part of a stage
-constexpr int kMaxStages = 6;
-constexpr uint32_t kOutBlock = 32 * 128;  // results on their way out: 32 tokens, 64 columns
-constexpr int kOverlap = 32;             // columns that the two accumulators of a pair share
+constexpr int kMaxStages = 8;
+constexpr uint32_t kOutBlock = 32 * 128;  // results on their way out: 32 tokens, 128 bytes each
+constexpr int kOverlap = 32;             // columns that two accumulators of 256 share
 
 // Groups of K that one accumulator adds up when results are fp32.  The tensor core
 // cuts off what an addition shifts out, so a sum drifts towards zero with each of
@@ -158,7 +158,7 @@ constexpr int kOverlap = 32;             // columns that the two accumulators of
 constexpr int kSumGroups = 8;
 
 constexpr int prod_stages(int bn, bool pair) {
-  return pair ? 6 : bn <= 16 ? 5 : bn <= 32 ? 4 : 3;
+  return pair ? (bn == 256 ? 6 : 8) : bn <= 16 ? 5 : bn <= 32 ? 4 : 3;
 }
 constexpr int prod_b_rows(int bn, bool pair) { return pair ? bn / 2 : bn; }   // a CTA's part of B
 constexpr uint32_t prod_stage_bytes(int bn, bool pair) {
@@ -179,9 +179,10 @@ struct ProdMisc {
 // single pieces 8192 x 4096 x 8192 took 212 us).
 constexpr int prod_run(bool pair) { return pair ? 4 : 2; }
 constexpr int prod_fetches(bool pair) { return pair ? 2 : 3; }   // in flight or in use
+constexpr int prod_blocks(int bn, bool pair) { return pair ? bn / 128 : 1; }   // of the weight
 constexpr int prod_tokens(int bn, bool pair) { return pair ? 128 : bn; }   // of one CTA
 constexpr uint32_t prod_fetch_bytes(int bn, bool pair) {
-  return (prod_tokens(bn, pair) + (pair ? 2 : 1)) * prod_run(pair) * 16;
+  return (prod_tokens(bn, pair) + prod_blocks(bn, pair)) * prod_run(pair) * 16;
 }
 constexpr uint32_t prod_smem(int bn, bool pair) {
   return prod_stages(bn, pair) * prod_stage_bytes(bn, pair) +
@@ -394,12 +395,14 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
     product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                    const __grid_constant__ CUtensorMap omap, const ProdArgs a) {
   constexpr bool kSums = sizeof(Out) == 4;   // short sums, added up in registers
-  static_assert(!(PAIR && kSums), "pairs have no registers for sums");
+  static_assert(!kSums || BN <= 128, "sums in registers");
   constexpr int kStages = prod_stages(BN, PAIR);
   constexpr uint32_t kStage = prod_stage_bytes(BN, PAIR);
   constexpr int kBRows = prod_b_rows(BN, PAIR);
   constexpr int kAcc = BN < 32 ? 32 : BN;                   // columns of an accumulator
-  constexpr uint32_t kAcc2 = PAIR ? kAcc - kOverlap : kSums ? kAcc : 0;   // the second one
+  constexpr bool kShared = BN == 256;        // two that share columns
+  constexpr bool kTwo = !kShared && (PAIR || kSums);   // two of their own
+  constexpr uint32_t kAcc2 = kShared ? kAcc - kOverlap : kTwo ? kAcc : 0;   // the second one
   constexpr uint32_t kColSf = kAcc2 + kAcc;
   constexpr uint32_t kSfBuf = 4 + (BN <= 128 ? 4 : 8);      // columns of scales: A's, B's
   constexpr uint32_t kNeed = kColSf + 2 * kSfBuf;
@@ -512,10 +515,10 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
           const bool first = g == sh.g0 || (kSums && (g - sh.g0) % kSumGroups == 0);
           const bool last = g + 1 == sh.g1 || (kSums && (g + 1 - sh.g0) % kSumGroups == 0);
           if (first) {
-            // the accumulator is read out: of a pair's, the part that the sum before
-            // shares with it, and so all of the one before that
-            if (PAIR && i > 0) ok = prod_wait(&mi->acc_free[0], (i - 1) & 1, mi, a.status) && ok;
-            if (kSums && i > 1)
+            // the accumulator is read out: where two share columns, the part that the sum
+            // before shares with it, and so all of the one before that
+            if (kShared && i > 0) ok = prod_wait(&mi->acc_free[0], (i - 1) & 1, mi, a.status) && ok;
+            if (kTwo && i > 1)
               ok = prod_wait(&mi->acc_free[i & 1], ((i >> 1) - 1) & 1, mi, a.status) && ok;
           }
           if (g == sh.g0 || (g & 3) == 0)
@@ -556,7 +559,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
     int sb = 0, sturn = 0;
     bool bad = false;
     constexpr int kTok = prod_tokens(BN, PAIR), kRun = prod_run(PAIR), kFetches = prod_fetches(PAIR);
-    constexpr int kBlocks = PAIR ? 2 : 1, kTokCols = kTok < 32 ? 1 : kTok / 32;
+    constexpr int kBlocks = prod_blocks(BN, PAIR), kTokCols = kTok < 32 ? 1 : kTok / 32;
     const int s0 = sh.g0 >> 2, s1 = ((sh.g1 - 1) >> 2) + 1;   // rounds
     const int me = q * 32 + lane;
     int lt = sh.first, ls = s0, lslot = 0;   // what is fetched next
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
         auto piece = [&](int r) { return in[r * kRun + ((s % kRun) ^ (r & (kRun - 1)))]; };
         uint32_t w[8], x[kTokCols];
         w[0] = w[1] = w[2] = w[3] = scale_word(piece(kTok), &bad);
-        if (PAIR) w[4] = w[5] = w[6] = w[7] = scale_word(piece(kTok + kBlocks - 1), &bad);
+        if (kBlocks == 2) w[4] = w[5] = w[6] = w[7] = scale_word(piece(kTok + kBlocks - 1), &bad);
 #pragma unroll
         for (int c = 0; c < kTokCols; ++c)
           x[c] = scale_word(piece(kTok < 32 ? lane % kTok : 32 * c + lane), &bad);
@@ -611,7 +614,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
         tc_fence_after();
         if (PAIR) {
           tmem_put<kTokCols>(ts + sb * kSfBuf, x);
-          tmem_put<8>(ts + sb * kSfBuf + 4, w);
+          tmem_put<4 * kBlocks>(ts + sb * kSfBuf + 4, w);
         } else {
           tmem_put<4>(ts + sb * kSfBuf, w);
           tmem_put<kTokCols>(ts + sb * kSfBuf + 4, x);
@@ -664,89 +667,97 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
                     some * 512, dsmem_addr(smem_u32(&mi->sums_here), tid));
       }
     };
-    if (kSums) {
-      float sum[kAcc];
-      const int n = (sh.g1 - sh.g0 + kSumGroups - 1) / kSumGroups;
-#pragma unroll
-      for (int c = 0; c < kAcc; ++c) sum[c] = 0.0f;
-      for (int i = 0; i < n; ++i) {
-        prod_wait(&mi->acc_full[i & 1], (i >> 1) & 1, mi, a.status);
-        tc_fence_after();
-#pragma unroll
-        for (int b = 0; b < kAcc; b += 16) {
-          float v[16];
-          tmem_ld16(tmem + lanes + (i & 1) * kAcc2 + b, v);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) sum[b + c] += v[c];
-        }
-        tc_fence_before();
+    // A pair's results: lane l of warp q holds a token.  Its columns go through shared
+    // memory, 128 bytes at a time, so that they leave in whole lines: L2 serves a line for
+    // the price of a sector.  j: the j-th block of 32 columns that is written of a tile.
+    auto leave = [&](int t, int j, int b, const float* v) {
+      constexpr int kPer = 4 / sizeof(Out);   // blocks of 32 columns in 128 bytes
+      uint8_t* o = blocks + warp * kOutBlock;
+      if (j % kPer == 0) {   // the ones before have left
+        if (a.blocks && lane == 0) bulk_wait_read<0>();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&mi->acc_free[i & 1]));
       }
+      if (sizeof(Out) == 2) {
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        if (parts > 1) keep(b, sum + 32 * b);
-        else store(sh.first, b, sum + 32 * b);
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(o + sw128_off(lane, 4 * (b & 1) + c)) = pack8_bf16(v + 8 * c);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<float4*>(o + sw128_off(lane, c)) =
+              make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
       }
-      if (parts > 1) send();
-    } else {
-      int i = 0;
-      for (int t = sh.first; t < sh.tiles; t += sh.step, ++i) {
+      if (j % kPer != kPer - 1) return;
+      const int f0 = n_of(t) + 32 * (b - b % kPer), t0 = m_of(t) + warp * 32;
+      if (a.blocks) fence_proxy_async_smem();
+      __syncwarp();
+      if (a.blocks) {
+        if (lane == 0) {
+          if (f0 < a.outs && t0 < a.n) tma_store_2d(&omap, smem_u32(o), f0, t0);
+          bulk_commit();
+        }
+        return;
+      }
+      // rows that TMA does not take (not multiples of 16 bytes)
+      constexpr int kUnit = 16 / sizeof(Out);
+      for (int r = 0; r < min(32, a.n - t0); ++r) {
+        Out* row = static_cast<Out*>(a.out) + (t0 + r) * a.stride + f0;
+#pragma unroll
+        for (int c = lane; c < 32 * kPer; c += 32)
+          if (f0 + c < a.outs)
+            row[c] = *reinterpret_cast<Out*>(o + sw128_off(r, c / kUnit) + c % kUnit * sizeof(Out));
+      }
+    };
+    auto read_out = [&](int i) {   // the i-th sum's accumulator may be used again
+      tc_fence_before();
+      __syncwarp();
+      if (lane != 0) return;
+      if (PAIR) mbar_arrive_pair(dsmem_addr(smem_u32(&mi->acc_free[kShared ? 0 : i & 1]), 0));
+      else mbar_arrive(smem_u32(&mi->acc_free[i & 1]));
+    };
+    int i = 0;   // counts sums
+    for (int t = sh.first; t < sh.tiles; t += sh.step) {
+      if (kSums) {
+        float sum[kAcc];
+#pragma unroll
+        for (int c = 0; c < kAcc; ++c) sum[c] = 0.0f;
+        for (int g = sh.g0; g < sh.g1; g += kSumGroups, ++i) {
+          prod_wait(&mi->acc_full[i & 1], (i >> 1) & 1, mi, a.status);
+          tc_fence_after();
+#pragma unroll
+          for (int b = 0; b < kAcc; b += 16) {
+            float v[16];
+            tmem_ld16(tmem + lanes + (i & 1) * kAcc2 + b, v);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) sum[b + c] += v[c];
+          }
+          read_out(i);
+        }
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+          if (PAIR) leave(t, b, b, sum + 32 * b);
+          else if (parts > 1) keep(b, sum + 32 * b);
+          else store(t, b, sum + 32 * b);
+        }
+      } else {
         prod_wait(&mi->acc_full[i & 1], (i >> 1) & 1, mi, a.status);
         tc_fence_after();
 #pragma unroll 1
         for (int j = 0; j < kBlocks; ++j) {
           // the columns that the next tile's accumulator shares come first
-          const int b = PAIR && (i & 1) == 0 ? kBlocks - 1 - j : j;
+          const int b = kShared && (i & 1) == 0 ? kBlocks - 1 - j : j;
           float v[32];
           tmem_ld32(tmem + lanes + (i & 1) * kAcc2 + 32 * b, v);
-          if (PAIR && j == 0) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_pair(dsmem_addr(smem_u32(&mi->acc_free[0]), 0));
-          }
-          if (!PAIR && parts > 1) {
-            keep(b, v);
-          } else if (PAIR) {
-            // Lane l of warp q holds a token.  Its columns go through shared memory, 64 at
-            // a time, so that they leave in whole lines: L2 serves a line for the price of
-            // a sector, and 64 bytes a token at a time took 190 us instead of 183.
-            uint8_t* o = blocks + warp * kOutBlock;
-            if ((j & 1) == 0) {   // the block before has left
-              if (a.blocks && lane == 0) bulk_wait_read<0>();
-              __syncwarp();
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              *reinterpret_cast<uint4*>(o + sw128_off(lane, 4 * (b & 1) + c)) = pack8_bf16(v + 8 * c);
-            if ((j & 1) == 1) {
-              const int f0 = n_of(t) + 32 * (b & ~1), t0 = m_of(t) + warp * 32;
-              if (a.blocks) fence_proxy_async_smem();
-              __syncwarp();
-              if (a.blocks) {
-                if (lane == 0) {
-                  if (f0 < a.outs && t0 < a.n) tma_store_2d(&omap, smem_u32(o), f0, t0);
-                  bulk_commit();
-                }
-              } else {
-                // rows that TMA does not take (not multiples of 16 bytes)
-                for (int r = 0; r < min(32, a.n - t0); ++r) {
-                  uint16_t* row = static_cast<uint16_t*>(a.out) + (t0 + r) * a.stride + f0;
-#pragma unroll
-                  for (int c = lane; c < 64; c += 32)
-                    if (f0 + c < a.outs)
-                      row[c] = *reinterpret_cast<uint16_t*>(o + sw128_off(r, c >> 3) + (c & 7) * 2);
-                }
-              }
-            }
-          } else {
-            store(t, b, v);
-          }
+          if (PAIR && j == (kShared ? 0 : kBlocks - 1)) read_out(i);
+          if (PAIR) leave(t, j, b, v);
+          else if (parts > 1) keep(b, v);
+          else store(t, b, v);
         }
-        if (!PAIR && parts > 1) send();
+        ++i;
       }
-      if (PAIR && a.blocks && lane == 0) bulk_wait_all();
+      if (!PAIR && parts > 1) send();
     }
+    if (PAIR && a.blocks && lane == 0) bulk_wait_all();
   }
 
   if (!PAIR && parts > 1) {
@@ -902,14 +913,18 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   a.wide = a.groups % 4 == 0 && aligned16(x_scales) && aligned16(w_scales);
   a.status = status;
   auto cover = [](long long v, int by) { return static_cast<int>((v + by - 1) / by); };
-  // Pairs from a quarter of the SMs on (us): 512 x 4096 x 8192, 64 tiles, 18.3, in tiles
-  // of 128 x 64 31.2; 256 x 4096 x 8192, 32 tiles, 17.0 against 16.4; 1024 x 4096 x 1600,
-  // 28 tiles, 17.2 against 16.2.
-  const long long pair_tiles = static_cast<long long>(cover(outs, 256)) * cover(n, 256);
-  const bool pair = !fp32 && n > 128 && pair_tiles >= sms / 4;
-  const int bn = pair ? 256 : n <= 16 ? 16 : n <= 32 ? 32 : 64;
+  // Pairs (256 tokens x 128 columns) where a fifth of the SMs gets a tile (us): 200 x 4096
+  // x 4096, 32 tiles, 11.2 against 12.6 in tiles of 128 x 64, 128 x 4096 x 8192, 64 tiles,
+  // 11.7 against 12.6, 333 x 4096 x 1600, 26 tiles, 11.1 against 10.7; up to 64 tokens the
+  // others: 64 x 4096 x 8192 9.6 against 11.5.  256 columns once tiles of 128 would take
+  // more than one wave: 1024 x 4096 x 1600, 52 of 128, 11.8 against 14.4; 512 x 4096 x
+  // 8192, 128 of 128, 18.8 against 15.8.  fp32 results' sums have registers for 128.
+  const long long pair_tiles = static_cast<long long>(cover(outs, 128)) * cover(n, 256);
+  const bool pair = n > 64 && pair_tiles >= sms / 5;
+  const bool wide = !fp32 && pair_tiles > sms / 2;
+  const int bn = pair ? (wide ? 256 : 128) : n <= 16 ? 16 : n <= 32 ? 32 : 64;
   a.m_tiles = pair ? cover(n, 256) : cover(outs, 128);
-  a.n_tiles = pair ? cover(outs, 256) : cover(n, bn);
+  a.n_tiles = pair ? cover(outs, bn) : cover(n, bn);
   const long long tiles = static_cast<long long>(a.m_tiles) * a.n_tiles;
   if (tiles > 0x3fffffffLL) return ESS_ERR_UNSUPPORTED;
   int parts = 1, ctas;
@@ -923,14 +938,17 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
     ctas = static_cast<int>(tiles) * parts;
   }
   CUtensorMap wm, xm, om;
-  if (!encode_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, ins, outs, ins, 128, 128) ||
+  if (!encode_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, ins, outs, ins, 128,
+                     pair ? bn / 2 : 128) ||
       !encode_map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, ins, n, ins, 128, pair ? 128 : bn))
     return ESS_ERR_CUDA;
   // (a row's end has to be one of 16 bytes too: TMA cuts a block off there, not within)
-  a.blocks = pair && aligned16(out) && out_stride % 8 == 0 && outs % 8 == 0;
+  const int size = fp32 ? 4 : 2;
+  a.blocks = pair && aligned16(out) && out_stride * size % 16 == 0 &&
+             static_cast<long long>(outs) * size % 16 == 0;
   if (!a.blocks) om = wm;   // not used
-  else if (!encode_map_2d(&om, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, outs, n,
-                          static_cast<uint64_t>(out_stride) * 2, 64, 32))
+  else if (!encode_map_2d(&om, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                          out, outs, n, static_cast<uint64_t>(out_stride) * size, 128 / size, 32))
     return ESS_ERR_CUDA;
   // rows of 64 bf16 values may be indexer keys, which an indexer loads ahead of its wait
   a.keys = !fp32 && outs <= 64;
@@ -938,7 +956,9 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   const bool f = fp32 != 0;
-  if (pair) e = launch_product<256, true, __nv_bfloat16>(xm, wm, om, a, parts, ctas, dev, st);
+  if (pair && f) e = launch_product<128, true, float>(xm, wm, om, a, parts, ctas, dev, st);
+  else if (pair && !wide) e = launch_product<128, true, __nv_bfloat16>(xm, wm, om, a, parts, ctas, dev, st);
+  else if (pair) e = launch_product<256, true, __nv_bfloat16>(xm, wm, om, a, parts, ctas, dev, st);
   else if (bn == 16) e = launch_single<16>(f, wm, xm, a, parts, ctas, dev, st);
   else if (bn == 32) e = launch_single<32>(f, wm, xm, a, parts, ctas, dev, st);
   else e = launch_single<64>(f, wm, xm, a, parts, ctas, dev, st);

@@ -143,7 +143,7 @@ def spread(s, high, n, dim):
 SHAPES = [(1, 16, 1), (2, 128, 128), (4, 4096, 1600), (16, 4096, 257), (17, 48, 129), (32, 1024, 2432),
           (33, 528, 640), (64, 640, 300), (65, 1040, 257), (128, 2048, 512), (129, 256, 300),
           (333, 4112, 1601), (300, 528, 9800), (257, 128, 9801), (600, 1040, 5000), (1000, 16, 2500),
-          (513, 4096, 4096)]
+          (513, 4096, 4096), (65, 528, 4000), (200, 1040, 4100), (1024, 272, 1601), (256, 4096, 9728)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
@@ -167,7 +167,7 @@ def test_products_of_whole_numbers_are_exact(P, n, ins, outs, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("n,ins,outs", [(3, 4096, 300), (40, 16384, 200), (200, 2064, 700), (400, 1024, 5000),
-                                        (9, 144, 70)])
+                                        (9, 144, 70), (70, 16384, 4100), (300, 4112, 9800)])
 def test_products_of_quantised_values(P, n, ins, outs, dtype):
     rng = np.random.default_rng(n)
     x = bf16(rng.normal(size=(n, ins)) * 2.0 ** rng.integers(-6, 6, size=(n, 1)))
@@ -188,7 +188,7 @@ def test_products_of_quantised_values(P, n, ins, outs, dtype):
         assert np.linalg.norm(err) <= 2e-6 * np.linalg.norm(want)
 
 
-@pytest.mark.parametrize("n,outs", [(5, 200), (200, 200), (300, 9800)])
+@pytest.mark.parametrize("n,outs", [(5, 200), (200, 200), (300, 9800), (100, 4200)])
 def test_a_nan_code_reaches_its_row_and_column_only(P, n, outs):
     rng = np.random.default_rng(n)
     _, xc = whole(rng, n, 256)
@@ -235,7 +235,8 @@ def test_other_scales_are_reported(P, n, where, scale):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("n,outs,stride,first", [(7, 130, 576, 3), (300, 200, 209, 1), (300, 9800, 9808, 8),
-                                                 (300, 9800, 9801, 1), (300, 9795, 10000, 16), (40, 64, 64, 0)])
+                                                 (300, 9800, 9801, 1), (300, 9795, 10000, 16), (40, 64, 64, 0),
+                                                 (100, 4200, 4208, 8), (100, 4196, 4200, 4), (100, 4198, 4201, 2)])
 def test_into_a_view(P, n, outs, stride, first, dtype):
     rng = np.random.default_rng(n + outs)
     x, xc = whole(rng, n, 272)
