@@ -161,6 +161,14 @@ __device__ __forceinline__ int entry_len(const MlaArgs& a, int v) {
 }
 
 // ---------------------------------------------------------------- chunks
+// (See the head of the file for the tiles.  Measured: 512 new tokens of 32768 x 128 heads
+// 3.35 ms, 1.38 PFLOP/s or 80 % of the measured sustained rate; seven ragged requests with
+// 563 new tokens to 8192 537 us, 1.21 PFLOP/s; lists of 2048 for 320 tokens 180 us; 16 new
+// tokens of 4096 x 16 heads 19.4 us.  A tile takes 1.95 us and a segment 5 beside its tiles:
+// the last softmax and P V, O's way out (2.0 of them, 2.8 in stores of 16 bytes), the next
+// queries, during which the tensor cores wait.  Under ncu, 128 new tokens of 8192: the data
+// path of shared memory and L1 72 %, the tensor pipe 53 %, DRAM 1 %.)
+//
 // Requests with any number of new tokens each (CHUNK).  Request b's queries are the rows
 // [start, start + n) x heads of q, its newest tokens.  What a segment belongs to is a
 // unit: unit_rows neighbouring query rows of a request, dense 128 of them, listed one
@@ -1239,45 +1247,61 @@ __global__ void __launch_bounds__(SLICE* ROWS* GROUPS) cache_mla_join_kernel(
   int p0 = 0, first = 0, last = -1, pr;   // its first pair, that one's slot, its last pair
   size_t orow = x;
   if (CHUNK) {
-    // the x / 128th unit that is cut: the pair that is the first to start inside of it
-    // (all records at once, as one after another takes a latency each)
-    constexpr int kPer = (kMaxPairs + 31) / 32;
-    const int lane = threadIdx.x & 31;
-    int at[kPer], before[kPer];
+    // The x / 128th unit that is cut: the pair that is the first to start inside of it,
+    // found by one warp from all records at once (one after another takes a latency each).
+    __shared__ int4 cut_unit;   // first pair, its slot, last pair, first row; and the rows
+    __shared__ int cut_rows;
+    if (threadIdx.x < 32) {
+      constexpr int kPer = (kMaxPairs + 31) / 32;
+      const int lane = threadIdx.x;
+      int4 rec[kPer];
+      int before[kPer];
 #pragma unroll
-    for (int c = 0; c < kPer; ++c) {
-      const int i = 32 * c + lane;
-      at[c] = i < a.pairs ? a.rec[i].x : -1;
-      before[c] = i > 0 && i < a.pairs ? a.rec[i - 1].x : -1;
-    }
-    int left = x / kPairRows, p = 0, unit = -1, inside = 0;
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) {
-      const uint32_t cut = __ballot_sync(0xffffffffu, at[c] >= 0 && at[c] != before[c] &&
-                                                          32 * c + lane > 0);
-      int here = -1;
-      if (left < __popc(cut) && p == 0) {
-        uint32_t bits = cut;
-        for (int i = 0; i < left; ++i) bits &= bits - 1;
-        here = __ffs(bits) - 1;
+      for (int c = 0; c < kPer; ++c) {
+        const int i = 32 * c + lane;
+        rec[c] = i < a.pairs ? a.rec[i] : make_int4(-1, 0, 0, 0);
+        before[c] = i > 0 && i < a.pairs ? a.rec[i - 1].x : -1;
       }
-      left -= __popc(cut);
-      const int u = __shfl_sync(0xffffffffu, at[c], max(here, 0));
-      if (here >= 0) {
-        p = 32 * c + here;
-        unit = u;
+      int left = x / kPairRows, p = 0, unit = -1, rows = 0, inside = 0, slot = 0;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) {
+        const uint32_t cut = __ballot_sync(0xffffffffu, rec[c].x >= 0 && rec[c].x != before[c] &&
+                                                            32 * c + lane > 0);
+        int here = -1;
+        if (left < __popc(cut) && p == 0) {
+          uint32_t bits = cut;
+          for (int i = 0; i < left; ++i) bits &= bits - 1;
+          here = __ffs(bits) - 1;
+        }
+        left -= __popc(cut);
+        const int u = __shfl_sync(0xffffffffu, rec[c].x, max(here, 0));
+        const int n = __shfl_sync(0xffffffffu, rec[c].y, max(here, 0));
+        if (here >= 0) {
+          p = 32 * c + here;
+          unit = u;
+          rows = n;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) {
+        // pairs that start inside of it, side by side, behind the one that begins it
+        inside += __popc(__ballot_sync(0xffffffffu, rec[c].x >= 0 && rec[c].x == unit));
+        const int w = __shfl_sync(0xffffffffu, rec[c].w, (p - 1) & 31);
+        if ((p - 1) >> 5 == c) slot = w;
+      }
+      if (lane == 0) {
+        cut_unit = make_int4(p - 1, slot, p - 1 + inside, unit);
+        cut_rows = p > 0 ? rows : 0;
       }
     }
-#pragma unroll
-    for (int c = 0; c < kPer; ++c)   // pairs that start inside of it, side by side
-      inside += __popc(__ballot_sync(0xffffffffu, at[c] >= 0 && at[c] == unit));
+    __syncthreads();
     pr = x % kPairRows;
-    join = real && p > 0 && pr < a.rec[p].y;
+    join = real && pr < cut_rows;
     if (join) {
-      p0 = p - 1;
-      first = a.rec[p0].w;
-      last = p0 + inside;
-      orow = static_cast<size_t>(unit) + pr;
+      p0 = cut_unit.x;
+      first = cut_unit.y;
+      last = cut_unit.z;
+      orow = static_cast<size_t>(cut_unit.w) + pr;
     }
   } else {
     const int xr = real ? x : 0;
@@ -1602,8 +1626,11 @@ ess_status ess_cache_chunk(const void* q, int64_t total, const int32_t* cu, cons
   e = launch_pdl_once(cache_mla_kernel<true>, dim3(2 * a.pairs), dim3(kMlaThreads), kMlaSmem, st, a);
   if (e == cudaSuccess && a.pairs > 1) {
     const long long cut = std::min<long long>(units, a.pairs - 1) * kPairRows;
-    // few units have many parts each
-    if (units <= 8) e = launch_join<true, 4, 8, 16, 2>(a, cut, st);
+    // Few units have many parts each; with more units than pairs a cut one has two or
+    // three: one group a row, two parts in flight (two chunks of 160 tokens with lists of
+    // 2048, 75 cut units: 189.8 us, with two groups and every warp reading the records 198.6).
+    if (units > a.pairs) e = launch_join<true, 4, 64, 1, 2>(a, cut, st);
+    else if (units <= 8) e = launch_join<true, 4, 8, 16, 2>(a, cut, st);
     else e = launch_join<true, 4, 64, 2, 4>(a, cut, st);
   }
   return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;

@@ -20,24 +20,23 @@
 // and a warp of the epilogue writes runs of neighbouring columns.  The CTAs of a cluster
 // share a tile, each with a part of K; each adds up the sums of its part of the tokens,
 // which come to it by bulk copies between the CTAs' shared memories, in the order of the
-// parts.  Many tokens: pairs of CTAs (cta_group::2) compute 256 tokens x 256 columns,
-// walking over tiles, the epilogue of one beside the MMAs of the next: two accumulators
-// of 256 columns and the scales need 536 of 512, so they share 32, which are read first.
+// parts.  Many tokens: pairs of CTAs (cta_group::2) compute tiles of 256 tokens x 256
+// columns, walking over them, the epilogue of one beside the MMAs of the next: two
+// accumulators of 256 columns and the scales need 536 of 512, so they share 32, which are
+// read first.  Few such tiles, and fp32 results, take 128 columns.
 //
-// Measured (bytes that the call cannot do without, or flops, / time): 8192 x 4096 x 8192
-// 183 us (3.0 PFLOP/s, 78 % of twice the measured bf16 rate; a library's product with the
-// same scale form takes 150 to 179, by the codes), 8192 x 1024 x 24576 169 us, 2048 x 4096
-// x 8192 55, 512 x 4096 x 8192 18.3, 333 x 4112 x 1601 12.8, 64 x 4096 x 8192 9.5, 32 x
-// 1024 x 24576 6.7 (4.0 TB/s), 4 x 4096 x 1600 4.1; a launch that does nothing else 2.9.
-// fp32 results: 2048 x 4096 x 8192 115 us, in tiles for few tokens (pairs have no
-// registers for their sums).
-// What bounds a large one: the tensor pipe is busy for 61 % of an SM's active cycles, 1100
-// to 2000 cycles between two tiles and some 190 to 250 a stage of 512 are lost, and no
-// other unit is above 40 %: L2 30 %, its crossbar 37 %, shared memory's banks 14 %, DRAM
-// 10 %.  Without the operands' loads a stage takes 600 cycles, with them 800, whatever
-// their depth (four, five or six stages), the order of tiles, multicast to a second pair
-// (clusters of four, of which 36 fit, 194 us) or where they come from.  Seconds on end it
-// is held at 1.8 GHz by the power limit, 202 us.
+// Measured (time; flops or the bytes that the call cannot do without / time): 8192 x 4096 x
+// 8192 (tokens x ins x outs) 153 us, 3.6 PFLOP/s or 93 % of twice the measured bf16 rate (a
+// library's product with the same form of scales takes 151); in fp32 209; 8192 x 1024 x
+// 24576 135, 2048 x 4096 x 8192 44, 512 x 4096 x 8192 15.8, 128 x 4096 x 8192 11.9, 333 x 4112
+// x 1601 13.0, 64 x 4096 x 8192 9.6, 32 x 1024 x 24576 6.8 (4.0 TB/s), 4 x 4096 x 1600 4.1; a
+// launch that multiplies 16 x 128 x 128 2.9.
+// What bounds them: a large product the tensor pipe, busy for 78 % of an SM's cycles under
+// ncu at 2048 tokens (L2 35 %, its crossbar 41 %, shared memory's banks 17 %), with some
+// 1000 cycles between two tiles; seconds on end the power limit.  Rows of K that are not
+// multiples of 128 bytes straddle L2's lines: 2048 x 4112 x 8192 57 us.  With one tile a
+// pair the chain of its stages, 0.2 us each, and with few tokens launch, first loads and
+// the exchange of sums beside the weight's stream.
 #include <algorithm>
 #include <atomic>
 #include <cstddef>
@@ -241,7 +240,7 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src,
 // what it orders are this CTA's reads and writes of TMEM, which tcgen05.wait and
 // tcgen05.fence have put before it.  A cluster-scope release waits for the warp's loads in
 // flight: the scales' fetches then held up every round of four groups (8192 x 4096 x 8192
-// 183 us instead of REL).
+// 183 us instead of 153).
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
