@@ -163,7 +163,7 @@ __device__ __forceinline__ int entry_len(const MlaArgs& a, int v) {
 // ---------------------------------------------------------------- chunks
 // (See the head of the file for the tiles.  Measured: 512 new tokens of 32768 x 128 heads
 // 3.35 ms, 1.38 PFLOP/s or 80 % of the measured sustained rate; seven ragged requests with
-// 563 new tokens to 8192 537 us, 1.21 PFLOP/s; lists of 2048 for 320 tokens 180 us; 16 new
+// 556 new tokens to 8192 537 us, 1.21 PFLOP/s; lists of 2048 for 320 tokens 190 us; 16 new
 // tokens of 4096 x 16 heads 19.4 us.  A tile takes 1.95 us and a segment 5 beside its tiles:
 // the last softmax and P V, O's way out (2.0 of them, 2.8 in stores of 16 bytes), the next
 // queries, during which the tensor cores wait.  Under ncu, 128 new tokens of 8192: the data
