@@ -60,66 +60,74 @@ struct QuantArgs {
 };
 
 constexpr int kQuantThreads = 256;
-constexpr int kQuantItems = 2;     // groups in flight per 16 lanes
 
-// Sixteen lanes a group of 128 values, 16 bytes a lane.  16384 x 4096 take 38.5 us (5.3
-// TB/s; two streams one of which is half as wide: a copy reaches 6.8), with one, two or
-// four groups in flight alike, with eight 43.5; 16 rows 1.6 us.
+// Sixteen neighbouring values (c and on) of a row, zeros behind its end.
+__device__ __forceinline__ void quant_load(const QuantArgs& a, bool live, int row, int c,
+                                           uint4* v) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    v[h] = make_uint4(0u, 0u, 0u, 0u);
+    if (live && c + 8 * h < a.dim)
+      v[h] = *reinterpret_cast<const uint4*>(a.x + row * a.stride + c + 8 * h);
+  }
+}
+// Their codes; wide: rows are multiples of 16 bytes.
+__device__ __forceinline__ void quant_store(const QuantArgs& a, int row, int c, const float* f,
+                                            int e, bool wide) {
+  uint8_t* o = a.codes + static_cast<size_t>(row) * a.dim + c;
+  const uint2 lo = pack8_e4m3(f, exp2i(-e)), hi = pack8_e4m3(f + 8, exp2i(-e));
+  if (wide) {
+    if (c < a.dim) *reinterpret_cast<uint4*>(o) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  } else {
+    if (c < a.dim) *reinterpret_cast<uint2*>(o) = lo;
+    if (c + 8 < a.dim) *reinterpret_cast<uint2*>(o + 8) = hi;
+  }
+}
+
+// Eight lanes a group of 128 values, sixteen values a lane, so that codes leave 16 bytes
+// a store: 16384 x 4096 take 32.6 us (6.2 TB/s, 92 % of the measured copy rate); sixteen
+// lanes, 8 bytes a store, 38.5 with one, two or four groups in flight.
 __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const QuantArgs a) {
   pdl_wait_previous();
   // rows of 128 values may be bound indexer keys: nothing starts before they are written
   if (a.dim > 128) pdl_launch_dependents();
-  const int lane = threadIdx.x & 15;
+  const int lane = threadIdx.x & 7;
   const uint32_t total = static_cast<uint32_t>(a.n) * static_cast<uint32_t>(a.groups);
-  const uint32_t first =
-      blockIdx.x * (kQuantThreads / 16 * kQuantItems) + (threadIdx.x >> 4);
-  uint4 v[kQuantItems];
-  int row[kQuantItems], g[kQuantItems];
-#pragma unroll
-  for (int q = 0; q < kQuantItems; ++q) {
-    const uint32_t i = first + q * (kQuantThreads / 16);
-    const uint32_t r = a.shift < 0 ? i : __umulhi(i, a.mul) >> a.shift;
-    row[q] = i < total ? static_cast<int>(r) : -1;
-    g[q] = static_cast<int>(i - r * static_cast<uint32_t>(a.groups));
-    v[q] = make_uint4(0u, 0u, 0u, 0u);
-    if (row[q] >= 0 && g[q] * 128 + lane * 8 < a.dim)
-      v[q] = reinterpret_cast<const uint4*>(a.x + row[q] * a.stride + g[q] * 128)[lane];
-  }
-#pragma unroll
-  for (int q = 0; q < kQuantItems; ++q) {
-    float f[8];
-    unpack8(v[q], f);
-    const int e = scale_exp<448>(group_max<16>(amax8(f)));
-    if (row[q] < 0) continue;
-    const int c = g[q] * 128 + lane * 8;
-    if (c < a.dim)
-      *reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(row[q]) * a.dim + c) =
-          pack8_e4m3(f, exp2i(-e));
-    if (lane == 0) a.scales[static_cast<size_t>(row[q]) * a.groups + g[q]] = exp2i(e);
-  }
+  const uint32_t i = blockIdx.x * (kQuantThreads / 8) + (threadIdx.x >> 3);
+  const uint32_t r = a.shift < 0 ? i : __umulhi(i, a.mul) >> a.shift;
+  const int row = static_cast<int>(r), g = static_cast<int>(i - r * static_cast<uint32_t>(a.groups));
+  const int c = g * 128 + lane * 16;
+  uint4 v[2];
+  quant_load(a, i < total, row, c, v);
+  float f[16];
+  unpack8(v[0], f);
+  unpack8(v[1], f + 8);
+  const int e = scale_exp<448>(group_max<8>(fmaxf(amax8(f), amax8(f + 8))));
+  if (i >= total) return;
+  quant_store(a, row, c, f, e, a.dim % 16 == 0);
+  if (lane == 0) a.scales[static_cast<size_t>(row) * a.groups + g] = exp2i(e);
 }
 
-// One CTA a block of 128 x 128: 16 lanes a row, 16 rows at a time.  16384 x 4096 take
-// 37.6 us, 1600 x 4096 3.1.
+// One CTA a block of 128 x 128: eight lanes a row, 32 rows at a time.  16384 x 4096 take
+// 37.2 us (5.4 TB/s), 1600 x 4096 3.0; with 512 threads 39.7, with 1024 45.9: all of a
+// block is loaded before any of it leaves, so several small CTAs an SM do better.
 __global__ void __launch_bounds__(kQuantThreads) quant_square_kernel(const QuantArgs a) {
   __shared__ float part[kQuantThreads / 32];
+  constexpr int kRows = kQuantThreads / 8, kTimes = 128 / kRows;
   pdl_wait_previous();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 15, r0 = blockIdx.y * 128 + (threadIdx.x >> 4);
-  const int c = blockIdx.x * 128 + lane * 8;
-  uint4 v[8];
+  const int r0 = blockIdx.y * 128 + (threadIdx.x >> 3);
+  const int c = blockIdx.x * 128 + (threadIdx.x & 7) * 16;
+  uint4 v[kTimes][2];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const int r = r0 + 16 * q;
-    v[q] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < a.n && c < a.dim) v[q] = *reinterpret_cast<const uint4*>(a.x + r * a.stride + c);
-  }
+  for (int q = 0; q < kTimes; ++q) quant_load(a, r0 + kRows * q < a.n, r0 + kRows * q, c, v[q]);
   float m = 0.0f;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    float f[8];
-    unpack8(v[q], f);
-    m = fmaxf(m, amax8(f));
+  for (int q = 0; q < kTimes; ++q) {
+    float f[16];
+    unpack8(v[q][0], f);
+    unpack8(v[q][1], f + 8);
+    m = fmaxf(m, fmaxf(amax8(f), amax8(f + 8)));
   }
   m = group_max<32>(m);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
@@ -127,14 +135,13 @@ __global__ void __launch_bounds__(kQuantThreads) quant_square_kernel(const Quant
 #pragma unroll
   for (int w = 0; w < kQuantThreads / 32; ++w) m = fmaxf(m, part[w]);
   const int e = scale_exp<448>(m);
+  const bool wide = a.dim % 16 == 0;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const int r = r0 + 16 * q;
-    float f[8];
-    unpack8(v[q], f);
-    if (r < a.n && c < a.dim)
-      *reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(r) * a.dim + c) =
-          pack8_e4m3(f, exp2i(-e));
+  for (int q = 0; q < kTimes; ++q) {
+    float f[16];
+    unpack8(v[q][0], f);
+    unpack8(v[q][1], f + 8);
+    if (r0 + kRows * q < a.n) quant_store(a, r0 + kRows * q, c, f, e, wide);
   }
   if (threadIdx.x == 0)
     a.scales[static_cast<size_t>(blockIdx.y) * a.groups + blockIdx.x] = exp2i(e);
@@ -877,7 +884,7 @@ ess_status ess_quant(const void* x, int64_t x_stride, int64_t n, int32_t dim, in
     b.codes += r * dim;
     b.scales += r * a.groups;
     const long long items = static_cast<long long>(b.n) * a.groups;
-    constexpr int kPer = kQuantThreads / 16 * kQuantItems;
+    constexpr int kPer = kQuantThreads / 8;
     if (launch_pdl_once(quant_rows_kernel, dim3(static_cast<unsigned>((items + kPer - 1) / kPer)),
                         dim3(kQuantThreads), 0, st, b) != cudaSuccess)
       return ESS_ERR_CUDA;
@@ -890,7 +897,8 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
                        int64_t out_stride, int32_t fp32, int32_t* status, ess_stream_t stream) {
   if (n < 0 || outs < 1 || ins < 1 || out_stride < outs || (fp32 != 0 && fp32 != 1))
     return ESS_ERR_INVALID_ARG;
-  if (ins % 16 != 0 || ins > 0x7fffff00 || outs > 0x7fffff00 || n > 0x7fffff00LL)
+  // (a tile's sums are waited for, for about a second: 2^26 values of K take a fifth)
+  if (ins % 16 != 0 || ins > 1 << 26 || outs > 0x7fffff00 || n > 0x7fffff00LL)
     return ESS_ERR_UNSUPPORTED;
   if (n == 0) return ESS_OK;
   if (!x || !x_scales || !w || !w_scales || !out || !aligned16(x) || !aligned16(w) ||

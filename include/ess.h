@@ -759,7 +759,8 @@ ess_status ess_quant(const void* x, int64_t x_stride, int64_t n, int32_t dim, in
  * sums are fp32 and rounded once.  A NaN code makes the outputs it enters NaN, and no
  * others.  One shape always adds in one order.  n = 0 launches nothing.
  * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or non-positive argument or
- * out_stride below outs; ESS_ERR_UNSUPPORTED when ins is not a multiple of 16. */
+ * out_stride below outs; ESS_ERR_UNSUPPORTED when ins is not a multiple of 16 or above
+ * 2^26, or n or outs above 2^31 - 256. */
 ess_status ess_product(const void* x, const float* x_scales, int64_t n, const void* w,
                        const float* w_scales, int32_t outs, int32_t ins, void* out,
                        int64_t out_stride, int32_t fp32, int32_t* status, ess_stream_t stream);

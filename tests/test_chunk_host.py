@@ -60,7 +60,7 @@ PRODUCT = dict(x=A16, xs=A16, n=4, w=A16, ws=A16, outs=128, ins=256, out=A16, st
     (dict(w=None), 1), (dict(w=BAD), 1), (dict(ws=None), 1), (dict(ws=ODD), 1), (dict(outs=0), 1),
     (dict(ins=0), 1), (dict(ins=24), 3), (dict(out=None), 1), (dict(out=P((1 << 20) + 1)), 1),
     (dict(out=ODD, fp32=1), 1), (dict(stride=127), 1), (dict(fp32=2), 1), (dict(status=ODD), 1),
-    (dict(n=1 << 31), 3),
+    (dict(n=1 << 31), 3), (dict(ins=(1 << 26) + 16), 3),
 ], ids=ids)
 def test_product_refusals(lib, change, code):
     a = {**PRODUCT, **change}

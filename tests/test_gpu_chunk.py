@@ -140,6 +140,53 @@ def test_rows_of_no_request_stay():
     assert (out[-9:] == 3.0).all() and (lse[-9:] == 3.0).all()
 
 
+def test_requests_may_start_behind_the_first_row():
+    c = Chunks(5, [(6, 90), (40, 400)], 33, gap=7)
+    c.cu = c.cu + 7
+    c.dev_cu = torch.from_numpy(c.cu).cuda()
+    out = torch.full((c.total, 33, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    out, lse = c.attend(out=out)
+    assert c.cache.poll() == ess.ESS_OK
+    c.check(out, lse)
+    assert (out[:7] == 3.0).all()
+
+
+@pytest.mark.parametrize("requests,heads,k", [
+    ([(1, 3)] * 2000, 1, 0), ([(2, 2), (0, 1), (1, 70)] * 900, 2, 0), ([(900, 1200), (1100, 1100)], 5, 8),
+    ([(2500, 2600)], 16, 0),
+], ids=["2000", "2700", "listed", "long"])
+def test_more_units_than_threads(requests, heads, k):
+    c = Chunks(len(requests) + k, requests, heads)
+    tokens = c.lists(k) if k else None
+    out, lse = c.attend(tokens)
+    assert c.cache.poll() == ess.ESS_OK
+    c.check(out, lse, tokens, some=0.02 if len(requests) < 9 else 0.3)
+
+
+def test_threads_on_one_stream():
+    """Calls of several threads, with the other attention among them, share a workspace."""
+    import threading
+    c, d = Chunks(17, [(60, 900), (20, 20)], 64), Chunks(18, [(4, 700), (4, 1500)], 64)
+    other = lambda: d.cache.attend(d.q.view(2, 4, 64, 576), d.dev_table, d.T, d.scale)
+    want, want_other = c.attend()[0], other()[0]
+    torch.cuda.synchronize()
+    got, bad = [], []
+
+    def work(f, w):
+        try:
+            for _ in range(20):
+                got.append((f()[0], w))
+        except Exception as e:   # noqa: BLE001
+            bad.append(e)
+    threads = [threading.Thread(target=work, args=a) for a in ((c.attend, want), (other, want_other)) * 2]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad and len(got) == 80 and all(torch.equal(o, w) for o, w in got)
+
+
 def test_more_queries_than_tokens():
     """The first queries then have no token at all."""
     c = Chunks(4, [(10, 4), (300, 150), (2, 0)], 128)
