@@ -422,8 +422,9 @@ struct Tiles {
   __device__ __forceinline__ Tiles(const MlaArgs& a, const Misc* mi) {
     left = static_cast<int>(mi->end_tile - mi->first_tile);
     v = mi->start_v;
-    rt = mi->start_rt;
+    if (CHUNK) rt = mi->start_rt;
     load(a);
+    rt = mi->start_rt;
     tile = mi->start_tile;
     begins = true;
   }
@@ -445,14 +446,14 @@ struct Tiles {
     --left;
     if (++tile == nt && left > 0) {
       tile = 0;
-      ++rt;
       if (CHUNK) {
+        ++rt;
         while (v + 1 < a.batch && rt >= units_of(a, chunk_of(a, v).n)) {
           rt = 0;
           ++v;
         }
         load(a);
-      } else if (rt == a.row_tiles) {
+      } else if (++rt == a.row_tiles) {
         rt = 0;
         do {   // a tile is left, so an entry that has one follows
           ++v;
@@ -463,21 +464,16 @@ struct Tiles {
   }
 };
 
-// Where a segment's query rows lie: row r of the pair is row first + r of q and out, for
+// Where a unit's query rows lie: row r of the pair is row first + r of q and out, for
 // r < rows.
 struct QueryRows {
   size_t first;
   int rows;
 };
-template <bool CHUNK>
 __device__ __forceinline__ QueryRows query_rows(const MlaArgs& a, int v, int rt) {
-  if (CHUNK) {
-    const Chunk c = chunk_of(a, v);
-    return QueryRows{static_cast<size_t>(c.start) * a.heads + static_cast<size_t>(rt) * a.unit_rows,
-                     min(c.n * a.heads - rt * a.unit_rows, a.unit_rows)};
-  }
-  return QueryRows{static_cast<size_t>(v) * a.entry_rows + rt * kPairRows,
-                   a.entry_rows - rt * kPairRows};
+  const Chunk c = chunk_of(a, v);
+  return QueryRows{static_cast<size_t>(c.start) * a.heads + static_cast<size_t>(rt) * a.unit_rows,
+                   min(c.n * a.heads - rt * a.unit_rows, a.unit_rows)};
 }
 
 // The cache rows of a lane's four tokens e, e + 32, .. of an entry, -1 for one
@@ -487,15 +483,17 @@ template <bool CHUNK>
 __device__ __forceinline__ void token_rows(const MlaArgs& a, int v, int rt, int len, int e,
                                            int* row) {
   int t[4], pg[4];
-  const int b = a.tokens && !CHUNK ? v / a.ways : v;
-  int T = len, list = v;   // tokens that may be named, and by which list
-  if (a.tokens) {
-    T = request_len(a, b);
-    if (CHUNK) {
+  const int b = !CHUNK && a.tokens ? v / a.ways : v;
+  int T, list = v;   // tokens that may be named, and by which list
+  if constexpr (CHUNK) {
+    T = len;
+    if (a.tokens) {
       const Chunk c = chunk_of(a, b);
-      T = unit_sees(a, T, c.n, rt);
+      T = unit_sees(a, request_len(a, b), c.n, rt);
       list = c.start + rt;
     }
+  } else {
+    T = a.tokens ? request_len(a, b) : len;
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -564,10 +562,12 @@ __device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
       if (lane == 0) mi->mask[slot][j] = m;
     }
     if (it.first() && g > 0) {   // the segment's queries into L2
-      const QueryRows r = query_rows<CHUNK>(a, it.v, it.rt);
-      const int row0 = static_cast<int>(cluster_ctarank()) * kCtaRows;
-      const char* q = reinterpret_cast<const char*>(a.q + (r.first + row0) * kRowDim);
-      const int bytes = min(kCtaRows, r.rows - row0) * kRowDim * 2;
+      const int row0 = (CHUNK ? 0 : it.rt * kPairRows) +
+                       static_cast<int>(cluster_ctarank()) * kCtaRows;
+      QueryRows unit{static_cast<size_t>(it.v) * a.entry_rows, a.entry_rows};
+      if constexpr (CHUNK) unit = query_rows(a, it.v, it.rt);
+      const char* q = reinterpret_cast<const char*>(a.q + (unit.first + row0) * kRowDim);
+      const int bytes = min(kCtaRows, unit.rows - row0) * kRowDim * 2;
       for (int x = lane * 128; x < bytes; x += 32 * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(q + x));
     }
@@ -594,9 +594,10 @@ __device__ __forceinline__ void load_queries(const MlaArgs& a, uint8_t* smem, Mi
                                              int rt, int q0, int warp, int lane, int seg) {
   constexpr int kRows = kCtaRows / kWidenWarps;
   uint8_t* sq = smem + kOffQ;
-  int row0 = rt * kPairRows + q0, rows = a.entry_rows;
-  size_t first = static_cast<size_t>(v) * a.entry_rows;
-  if (CHUNK) {
+  int row0 = rt * kPairRows + q0;
+  int rows = 0;
+  size_t first = 0;
+  if constexpr (CHUNK) {
     const Chunk c = chunk_of(a, v);
     row0 = rt * a.unit_rows + q0;
     rows = min(c.n * a.heads, (rt + 1) * a.unit_rows);
@@ -612,8 +613,9 @@ __device__ __forceinline__ void load_queries(const MlaArgs& a, uint8_t* smem, Mi
       const int row = row0 + warp * kRows + i0 + i;
       u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
       rope[i] = 0u;
-      if (row < rows) {
-        const uint16_t* q = a.q + (first + row) * kRowDim;
+      if (row < (CHUNK ? rows : a.entry_rows)) {
+        const uint16_t* q =
+            a.q + ((CHUNK ? first : static_cast<size_t>(v) * a.entry_rows) + row) * kRowDim;
         u[i][0] = reinterpret_cast<const uint4*>(q)[un];
         u[i][1] = reinterpret_cast<const uint4*>(q)[32 + un];
         rope[i] = reinterpret_cast<const uint32_t*>(q + kLatent)[lane];
@@ -963,9 +965,11 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
     if (!last) {
       it.next(a);
     } else {
-      const QueryRows qr = query_rows<CHUNK>(a, it.v, it.rt);
-      const int row0 = static_cast<int>(rank) * kCtaRows;
-      const int span = CHUNK ? 0 : it.v * a.row_tiles + it.rt;
+      const int v = it.v;
+      const int row0 = (CHUNK ? 0 : it.rt * kPairRows) + static_cast<int>(rank) * kCtaRows;
+      const int span = it.v * a.row_tiles + it.rt;
+      QueryRows unit{0, 0};
+      if constexpr (CHUNK) unit = query_rows(a, it.v, it.rt);
       const bool ends = it.tile + 1 == it.nt;
       const bool whole = seg_first_tile == 0 && ends;
       const int slot = pair * 2 + (seg == 0 ? 0 : 1);
@@ -978,8 +982,9 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       named_sync(bar_id, kSoftWarps * 16);
       ok = wait_or_abort(&mi->pv_done, g & 1, mi, a.status) && ok;
       tc_fence_after();
-      const bool mine = row0 + r < qr.rows;
-      const size_t orow = qr.first + row0 + r;
+      const bool mine = row0 + r < (CHUNK ? unit.rows : a.entry_rows);
+      const size_t orow =
+          (CHUNK ? unit.first : static_cast<size_t>(v) * a.entry_rows) + row0 + r;
       const float inv = !whole ? 1.0f : (lt > 0.0f || lt != lt ? 1.0f / lt : 0.0f);
       const int prow = static_cast<int>(rank) * kCtaRows + r;
       // column 64 q + 8 c + e holds dim 256 half + 32 c + 8 q + e: a thread
@@ -1197,7 +1202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   if (CHUNK && rank == 0 && tid == kMmaWarp * 32) {   // see the join
     const bool inside = pair < tiles && mi->start_tile > 0;
     QueryRows q{0, 0};
-    if (inside) q = query_rows<CHUNK>(a, mi->start_v, mi->start_rt);
+    if (inside) q = query_rows(a, mi->start_v, mi->start_rt);
     a.rec[pair].x = inside ? static_cast<int>(q.first) : -1;
     a.rec[pair].y = q.rows;
   }
