@@ -79,8 +79,8 @@ constexpr int kRowWarp = kWidenWarp0 + kWidenWarps;
 constexpr int kMlaThreads = (kRowWarp + 1) * 32;
 // What a segment costs beside its tiles, in tiles, when they are dealt: ragged
 // requests to 8192 took 97.3 us with 0, 94.1 with 1, 91.9 with 2, 92.3 with 3.  A chunk's
-// segments cost more, about 6 us, and may be short: ragged chunks to 8192 tokens, one
-// of them a prompt of 200 without a prefix, took 647 us with 2, 552 with 3 or 4.
+// segments may be short, and long ones among them: thirteen ragged requests, three of them
+// prompts without a prefix, take 1485 us with 3, 1492 with 2; prompts alone 557 and 547.
 constexpr int kSegmentCost = 2;
 constexpr int kChunkSegmentCost = 3;
 constexpr int kRing = 3;              // tiles whose rows are known ahead of their use
@@ -162,12 +162,12 @@ __device__ __forceinline__ int entry_len(const MlaArgs& a, int v) {
 
 // ---------------------------------------------------------------- chunks
 // (See the head of the file for the tiles.  Measured: 512 new tokens of 32768 x 128 heads
-// 3.35 ms, 1.38 PFLOP/s or 80 % of the measured sustained rate; seven ragged requests with
-// 556 new tokens to 8192 537 us, 1.21 PFLOP/s; lists of 2048 for 320 tokens 190 us; 16 new
-// tokens of 4096 x 16 heads 19.4 us.  A tile takes 1.95 us and a segment 5 beside its tiles:
-// the last softmax and P V, O's way out (2.0 of them, 2.8 in stores of 16 bytes), the next
-// queries, during which the tensor cores wait.  Under ncu, 128 new tokens of 8192: the data
-// path of shared memory and L1 72 %, the tensor pipe 53 %, DRAM 1 %.)
+// 3.36 ms, 1.38 PFLOP/s or 80 % of the measured sustained rate; seven ragged requests with
+// 556 new tokens to 8192 528 us, 1.23 PFLOP/s; lists of 2048 for 320 tokens 188 us; twelve
+// prompts of 20 to 700 tokens 557 us; 16 new tokens of 4096 x 16 heads 19.8 us.  A tile takes
+// 1.95 us and a segment 4 beside its tiles: the last softmax and P V, O's way out, the
+// next queries, during which the tensor cores wait.  Under ncu, 128 new tokens of 8192: the
+// data path of shared memory and L1 72 %, the tensor pipe 53 %, DRAM 1 %.)
 //
 // Requests with any number of new tokens each (CHUNK).  Request b's queries are the rows
 // [start, start + n) x heads of q, its newest tokens.  What a segment belongs to is a
@@ -366,6 +366,21 @@ __device__ __forceinline__ void tmem_ld8x4(uint32_t t, float* v) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// two runs of 8 consecutive columns of this lane, 64 columns apart
+__device__ __forceinline__ void tmem_ld8x2(uint32_t t, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(t), "r"(t + 64)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 // 32 bytes, 32-byte aligned, in one store
 __device__ __forceinline__ void st_global_32(float* p, const float* v) {
@@ -582,17 +597,16 @@ __device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
   }
 }
 
-// Four rows of queries per widening warp into shared memory, kFly of them in
-// flight: the latent part as fp16, beside the fp16 latents, each row divided by
+// Four rows of queries per widening warp into shared memory, all in flight: the latent part as fp16, beside the fp16 latents, each row divided by
 // the power of two that brings its largest value to [2^14, 2^15) (exact down to
 // 2^-31 of that value, with an error below 2^-39 of it under that); the RoPE
 // part, divided alike, as bf16.  A lane takes unit 32 h + 4 (lane % 8) + lane / 8:
 // chunk 8 h + lane % 8, its unit lane / 8; eight lanes then fill the places of one
 // swizzled row.
-template <bool CHUNK, int kFly>
+template <bool CHUNK>
 __device__ __forceinline__ void load_queries(const MlaArgs& a, uint8_t* smem, Misc* mi, int v,
                                              int rt, int q0, int warp, int lane, int seg) {
-  constexpr int kRows = kCtaRows / kWidenWarps;
+  constexpr int kRows = kCtaRows / kWidenWarps, kFly = kRows;
   uint8_t* sq = smem + kOffQ;
   int row0 = rt * kPairRows + q0;
   int rows = 0;
@@ -725,7 +739,7 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
   // g - 1, V of tile g beside QK of tile g + 1.  Slot s of the rows holds tile
   // g for the (g / kRing)th time.
   const int q0 = static_cast<int>(rank) * kCtaRows;
-  load_queries<CHUNK, 4>(a, smem, mi, mi->start_v, mi->start_rt, q0, w, lane, 0);
+  load_queries<CHUNK>(a, smem, mi, mi->start_v, mi->start_rt, q0, w, lane, 0);
   int seg = 0;
   wait_or_abort(&mi->row_full[0], 0, mi, a.status);
   load_k(0);
@@ -763,10 +777,11 @@ __device__ __forceinline__ void widen_role(const MlaArgs& a, uint8_t* smem, Misc
       const int2 next = mi->seg[slot1];
       // The next tile begins a segment: its queries, beside this one's softmax and
       // output.  (Before V they would be there sooner, but with V's codes in
-      // registers too the tile loop spills, or with two rows in flight costs 2 %.)
+      // registers too the tile loop spills, or with two rows in flight costs 2 %.  Here
+      // four rows in flight are 0.35 us a segment faster than two.)
       if (next.x >= 0) {
         wait_or_abort(&mi->q_free, seg & 1, mi, a.status);
-        load_queries<CHUNK, 2>(a, smem, mi, next.x, next.y, q0, w, lane, ++seg);
+        load_queries<CHUNK>(a, smem, mi, next.x, next.y, q0, w, lane, ++seg);
       }
       load_v(slot1);
       __syncwarp();
@@ -993,26 +1008,48 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       const int d0 = half * 256 + sub * 128;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
+        if (CHUNK && whole && a.wide_out) {
+          // Two lanes write 64 bytes of one's row, then of the other's, 32 each, so that a
+          // store meets 16 lines: with 64 bytes a lane, 32 lines a store, a segment took
+          // 0.6 us more, in stores of 16 bytes 0.75 more still.
+          const bool odd = lane & 1;
+          uint32_t keep[8], give[8];   // this lane's half of its own 64 bytes, and the other
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float o[16];
+            tmem_ld8x2(tq + 8 * c + 128 * h, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t w = bf16x2_bits(o[2 * e] * inv, o[2 * e + 1] * inv);
+              if (h == 0) keep[e] = give[e] = w;
+              else if (odd) keep[e] = w;
+              else give[e] = w;
+            }
+          }
+          float to_even[8], to_odd[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, give[e], 1);
+            to_even[e] = __uint_as_float(odd ? got : keep[e]);
+            to_odd[e] = __uint_as_float(odd ? keep[e] : got);
+          }
+          uint16_t* at = a.out + (orow - odd) * kLatent + d0 + 32 * c + 16 * odd;
+          const int first = row0 + r - odd, rows = CHUNK ? unit.rows : a.entry_rows;
+          if (first < rows) st_global_32(reinterpret_cast<float*>(at), to_even);
+          if (first + 1 < rows) st_global_32(reinterpret_cast<float*>(at + kLatent), to_odd);
+          continue;
+        }
         float o[32];
         tmem_ld8x4(tq + 8 * c, o);
-        if (!mine) continue;
-        if (whole) {
+        if (!mine) {
+          continue;
+        } else if (whole) {
           uint16_t* dst = a.out + orow * kLatent + d0 + 32 * c;
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] *= inv;
-          if (CHUNK && a.wide_out) {
-            // 32 bytes a store: half as many requests (a row a lane, each has its own line)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint4 lo = pack8_bf16(o + 16 * x), hi = pack8_bf16(o + 16 * x + 8);
-              const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-              st_global_32(reinterpret_cast<float*>(dst) + 8 * x, reinterpret_cast<const float*>(w));
-            }
-          } else {
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              reinterpret_cast<uint4*>(dst)[x] = pack8_bf16(o + 8 * x);
-          }
+          for (int x = 0; x < 4; ++x)
+            reinterpret_cast<uint4*>(dst)[x] = pack8_bf16(o + 8 * x);
         } else {
           float* dst = a.part_o + static_cast<size_t>(slot) * kPairRows * kLatent +
                        ((d0 + 32 * c) / 8 * kPairRows + prow) * 8;
