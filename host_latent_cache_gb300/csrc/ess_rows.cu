@@ -42,6 +42,11 @@ __device__ __forceinline__ float2 turn(int32_t pos, unsigned long long freq) {
   return make_float2(__cosf(h), __sinf(h));
 }
 
+// A pair of values turned by it, in one form for rows and queries: equal bits in both.
+__device__ __forceinline__ float2 turned(float a, float b, const float2& cs) {
+  return make_float2(__fmaf_rn(a, cs.x, -__fmul_rn(b, cs.y)), __fmaf_rn(a, cs.y, __fmul_rn(b, cs.x)));
+}
+
 // x modulo 1 as a binary fraction of 2^64
 unsigned long long binary_fraction(double x) {
   const double a = std::fabs(x);
@@ -158,11 +163,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) cache_write_kernel(
       ra &= 0xffffu;
     }
     if (a.pos) {
-      const float2 cs_sn = turn(row.pos, freq);
-      const float cs = cs_sn.x, sn = cs_sn.y;
-      const float xa = bf16_lo(ra), xb = bf16_lo(rb);
-      ra = bf16_bits(xa * cs - xb * sn);
-      rb = bf16_bits(xa * sn + xb * cs);
+      const float2 y = turned(bf16_lo(ra), bf16_lo(rb), turn(row.pos, freq));
+      ra = bf16_bits(y.x);
+      rb = bf16_bits(y.y);
     }
     uint8_t* out = a.rows + row.slot * row_bytes_of(FMT);
     uint16_t* rope;
@@ -322,9 +325,9 @@ __global__ void __launch_bounds__(kTurnThreads) rotate_kernel(const RotateArgs a
         // the first and second value of pair i; halves: 0..3 and 4..7
         float& p = a.halves ? y[i] : y[2 * i];
         float& r = a.halves ? y[4 + i] : y[2 * i + 1];
-        const float u = p * cs[i].x - r * cs[i].y, w = p * cs[i].y + r * cs[i].x;
-        p = u;
-        r = w;
+        const float2 w = turned(p, r, cs[i]);
+        p = w.x;
+        r = w.y;
       }
       const uint4 w = pack8_bf16(y);
       if (a.halves) {

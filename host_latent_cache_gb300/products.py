@@ -84,11 +84,13 @@ class Weight8:
         _check(codes, "codes", E4M3, (n, self.ins), at)
         _check(scales, "scales", torch.float32, (n, _groups(self.ins)), at)
         if out is None:
-            _need(dtype in (_BF16, torch.float32), f"results are bf16 or float32, not {dtype}")
+            if dtype is not _BF16 and dtype is not torch.float32:
+                raise ValueError(f"results are bf16 or float32, not {dtype}")
             out = torch.empty((n, self.outs), dtype=dtype, device=self.device)
         else:
             dtype = out.dtype if isinstance(out, torch.Tensor) else _BF16
-            _need(dtype in (_BF16, torch.float32), f"results are bf16 or float32, not {dtype}")
+            if dtype is not _BF16 and dtype is not torch.float32:
+                raise ValueError(f"results are bf16 or float32, not {dtype}")
             _check_rows(out, "out", dtype, (n, self.outs), at)
             _need(n < 2 or out.stride(0) >= self.outs, "out: rows that do not overlap are needed")
         with _OnDevice(at) as stream:

@@ -207,7 +207,8 @@ class RowCache:
         n = slots.shape[0]
         _check(slots, "slots", _I64, (n,), at)
         _check_rows(kv, "kv", _BF16, (n, ROW), at)
-        _need(pairs in PAIRS, f"pairs {pairs!r} is none of {', '.join(PAIRS)}")
+        if pairs not in PAIRS:
+            raise ValueError(f"pairs {pairs!r} is none of {', '.join(PAIRS)}")
         if gamma is not None:
             _check(gamma, "gamma", _BF16, (LATENT,), at)
         freq, count, axis = None, 1, None
@@ -446,24 +447,34 @@ def rotate(x, pos, inv_freq, pairs: str = "adjacent", axes=None, out=None):
     pos int32 [n], or with `axes` [axes][n].  Into `out`, of any such strides, which may be
     x itself; a new tensor without it.  The inverse is the rotation by -inv_freq."""
     _need(isinstance(x, torch.Tensor) and x.dim() == 3 and x.is_cuda,
-          f"x: a CUDA tensor [n][heads][{ROPE}] is needed")
-    n, heads, dim = x.shape
+          "x: a CUDA tensor [n][heads][64] is needed")
+    shape = x.shape
+    n, heads, dim = shape
     at = x.get_device()
-    _need(dim == ROPE and heads >= 1, f"x: [n][heads][{ROPE}] with at least one head is needed")
-    _need(heads <= MOST, "more than 2^31 - 1 heads")
-    _need(pairs in PAIRS, f"pairs {pairs!r} is none of {', '.join(PAIRS)}")
+    _need(dim == ROPE and 1 <= heads <= MOST,
+          "x: [n][heads][64] with at least one head, and no more than 2^31 - 1, is needed")
+    if pairs not in PAIRS:
+        raise ValueError(f"pairs {pairs!r} is none of {', '.join(PAIRS)}")
     freq, count, axis = _turns(inv_freq, pos, axes, n, at)
     if out is None:
         out = torch.empty((n, heads, ROPE), dtype=_BF16, device=x.device)
-    strides = []
-    for t, name in ((x, "x"), (out, "out")):
-        if not (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.shape == x.shape
-                and t.is_cuda and t.get_device() == at and t.stride(2) == 1):
-            _refuse(t, name, _BF16, x.shape, at)
-        # of a single token or head, any that the kernel takes
-        head = t.stride(1) if heads > 1 else ROPE
-        strides += [t.stride(0) if n > 1 else heads * max(head, ROPE), head]
+    x_row, x_head = _turned_rows(x, "x", shape, at)
+    out_row, out_head = _turned_rows(out, "out", shape, at)
     with _OnDevice(at) as stream:
-        ess.ess_rotate(x, strides[0], strides[1], n, heads, freq, pos, count, axis, PAIRS[pairs],
-                       out, strides[2], strides[3], stream)
+        ess.ess_rotate(x, x_row, x_head, n, heads, freq, pos, count, axis, PAIRS[pairs], out,
+                       out_row, out_head, stream)
     return out
+
+
+def _turned_rows(t, name: str, shape, index: int):
+    """Strides of rows [n][heads][64] with contiguous values; of a single token or head,
+    any that the kernel takes."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.shape == shape
+            and t.get_device() == index):
+        _refuse(t, name, _BF16, shape, index)
+    row, head, one = t.stride()
+    if one != 1:
+        _refuse(t, name, _BF16, shape, index)
+    if shape[1] == 1:
+        head = ROPE
+    return (row if shape[0] > 1 else shape[1] * max(head, ROPE)), head

@@ -140,6 +140,15 @@ def test_rows_of_no_request_stay():
     assert (out[-9:] == 3.0).all() and (lse[-9:] == 3.0).all()
 
 
+@pytest.mark.parametrize("heads", [127, 128])
+def test_results_that_are_not_32_byte_aligned(heads):
+    c = Chunks(19, [(70, 400), (3, 3)], heads)
+    want, _ = c.attend()
+    buf = torch.zeros(c.total * heads * 512 + 8, dtype=torch.bfloat16, device="cuda")
+    got, _ = c.attend(out=buf[8:].view(c.total, heads, 512))
+    assert torch.equal(got, want) and (buf[:8] == 0).all()
+
+
 def test_requests_may_start_behind_the_first_row():
     c = Chunks(5, [(6, 90), (40, 400)], 33, gap=7)
     c.cu = c.cu + 7
