@@ -190,9 +190,21 @@ constexpr int prod_tokens(int bn, bool pair) { return pair ? 128 : bn; }   // of
 constexpr uint32_t prod_fetch_bytes(int bn, bool pair) {
   return (prod_tokens(bn, pair) + prod_blocks(bn, pair)) * prod_run(pair) * 16;
 }
+// Parts of K meet in places for BN tokens and these more: p parts of a tile leave
+// p ceil(BN / p) tokens' sums in a CTA at most.  (For 64 tokens no more than two fit beside
+// a second CTA on the SM, which leaves out seven parts.)
+constexpr int kMaxParts = 8;
+static_assert(kMaxParts <= 8, "portable clusters");
+constexpr int prod_places(int bn) { return bn + (bn <= 32 ? 7 : 2); }
+constexpr bool parts_fit(int bn, int parts) {
+  return parts * ((bn + parts - 1) / parts) <= prod_places(bn);
+}
+static_assert(parts_fit(16, 7) && parts_fit(32, 7) && parts_fit(64, 6) && !parts_fit(64, 7) &&
+                  parts_fit(64, 8),
+              "parts of K");
 constexpr uint32_t prod_smem(int bn, bool pair) {
   return prod_stages(bn, pair) * prod_stage_bytes(bn, pair) +
-         prod_fetches(pair) * prod_fetch_bytes(bn, pair) + (pair ? kEpiWarps * kOutBlock : bn * 512) +
+         prod_fetches(pair) * prod_fetch_bytes(bn, pair) + (pair ? kEpiWarps * kOutBlock : prod_places(bn) * 512) +
          sizeof(ProdMisc);
 }
 
@@ -420,7 +432,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
   // a pair's results on their way out (at multiples of 1024), or the sums of a tile's
   // tokens [part][token of this CTA's share][128] from the cluster's CTAs
   uint8_t* blocks = smem + kStages * kStage;
-  ring = blocks + (PAIR ? kEpiWarps * kOutBlock : BN * 512);
+  ring = blocks + (PAIR ? kEpiWarps * kOutBlock : prod_places(BN) * 512);
   ProdMisc* mi = reinterpret_cast<ProdMisc*>(ring + prod_fetches(PAIR) * kFetch);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -790,42 +802,90 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
   if (warp == kProdMmaWarp) prod_dealloc<PAIR>(tmem, kCols);
 }
 
-template <int BN, bool PAIR, typename Out>
-cudaError_t launch_product(const CUtensorMap& am, const CUtensorMap& bm, const CUtensorMap& om,
-                           const ProdArgs& a, int parts, int ctas, int dev, cudaStream_t st) {
-  auto kernel = product_kernel<BN, PAIR, Out>;
-  constexpr uint32_t kSmem = prod_smem(BN, PAIR);
-  static std::atomic<unsigned long long> done{0};   // allowed once per device
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (!(done.load(std::memory_order_relaxed) & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
-    if (e != cudaSuccess) return e;
-    done.fetch_or(bit, std::memory_order_relaxed);
-  }
+// A launch of the kernel as a programmatic dependent, in clusters of `cluster` CTAs.
+struct ProdLaunch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[3];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
-  at[1].val.sharedMemCarveout = static_cast<int>(cudaSharedmemCarveoutMaxShared);
-  at[2].id = cudaLaunchAttributeClusterDimension;
-  at[2].val.clusterDim.x = PAIR ? 2 : parts;
-  at[2].val.clusterDim.y = at[2].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kProdThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = 3;
-  return cudaLaunchKernelEx(&cfg, kernel, am, bm, om, a);
+  ProdLaunch(int ctas, int cluster, uint32_t smem, cudaStream_t st) {
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+    at[1].val.sharedMemCarveout = static_cast<int>(cudaSharedmemCarveoutMaxShared);
+    at[2].id = cudaLaunchAttributeClusterDimension;
+    at[2].val.clusterDim.x = cluster;
+    at[2].val.clusterDim.y = at[2].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kProdThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 3;
+  }
+};
+
+// The kernel's shared memory, allowed once per device.
+template <int BN, bool PAIR, typename Out>
+cudaError_t allow_prod_smem(int dev) {
+  static std::atomic<unsigned long long> done{0};
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(product_kernel<BN, PAIR, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(prod_smem(BN, PAIR)));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+template <int BN, bool PAIR, typename Out>
+cudaError_t launch_product(const CUtensorMap& am, const CUtensorMap& bm, const CUtensorMap& om,
+                           const ProdArgs& a, int ctas, int cluster, int dev, cudaStream_t st) {
+  const cudaError_t e = allow_prod_smem<BN, PAIR, Out>(dev);
+  if (e != cudaSuccess) return e;
+  ProdLaunch l(ctas, cluster, prod_smem(BN, PAIR), st);
+  return cudaLaunchKernelEx(&l.cfg, product_kernel<BN, PAIR, Out>, am, bm, om, a);
+}
+
+// Clusters of `parts` CTAs, two an SM, that run at once, which depends on how SMs are
+// grouped (of 152: 97 of three, 74 of four, 36 of eight); 0 when the runtime does not say.
+// It is asked about a kernel of the same threads and shared memory, as of one that uses
+// TMEM it counts a single CTA an SM.
+__global__ void __launch_bounds__(kProdThreads, 2) place_kernel() {}
+
+int clusters_at_once(int parts, int dev) {
+  constexpr uint32_t kSmem = prod_smem(64, false);   // the largest of them
+  static std::atomic<int> known[64][kMaxParts + 1];   // the number and 1
+  if (dev < 64) {
+    const int k = known[dev][parts].load(std::memory_order_relaxed);
+    if (k > 0) return k - 1;
+  }
+  int n = 0;
+  ProdLaunch l(parts, parts, kSmem, nullptr);
+  if (cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kSmem)) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, place_kernel, &l.cfg) != cudaSuccess)
+    n = 0;
+  if (dev < 64) known[dev][parts].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+// K is cut into as many parts as still run at once, with two stages each (us): 4 x 4096 x
+// 1600, 13 tiles, takes 10.5 uncut, 7.2 in two parts, 5.1 in four, 4.1 in eight; 16 x 4096 x
+// 4736, 37 tiles, 9.0 in eight parts, of which 36 clusters run at once.
+template <int BN, typename Out>
+cudaError_t launch_single(const CUtensorMap& w, const CUtensorMap& x, const ProdArgs& a, int tiles,
+                          int dev, cudaStream_t st) {
+  int parts = kMaxParts;
+  while (parts > 1 && (a.groups < 2 * parts || !parts_fit(BN, parts) ||
+                       tiles > clusters_at_once(parts, dev)))
+    --parts;
+  return launch_product<BN, false, Out>(w, x, w, a, tiles * parts, parts, dev, st);
 }
 
 template <int BN>
 cudaError_t launch_single(bool fp32, const CUtensorMap& w, const CUtensorMap& x, const ProdArgs& a,
-                          int parts, int ctas, int dev, cudaStream_t st) {
-  return fp32 ? launch_product<BN, false, float>(w, x, w, a, parts, ctas, dev, st)
-              : launch_product<BN, false, __nv_bfloat16>(w, x, w, a, parts, ctas, dev, st);
+                          int tiles, int dev, cudaStream_t st) {
+  return fp32 ? launch_single<BN, float>(w, x, a, tiles, dev, st)
+              : launch_single<BN, __nv_bfloat16>(w, x, a, tiles, dev, st);
 }
 
 int sms_of(int dev) {
@@ -934,16 +994,8 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   a.n_tiles = pair ? cover(outs, bn) : cover(n, bn);
   const long long tiles = static_cast<long long>(a.m_tiles) * a.n_tiles;
   if (tiles > 0x3fffffffLL) return ESS_ERR_UNSUPPORTED;
-  int parts = 1, ctas;
-  if (pair) {
-    ctas = 2 * static_cast<int>(std::min<long long>(tiles, sms / 2));
-  } else {
-    // K is cut as long as two CTAs an SM run at once and each has two stages: 4 x 4096 x
-    // 1600 takes 10.5 us uncut, 7.2 in two parts, 5.1 in four, 4.1 in eight; 128 x 4096 x
-    // 8192 12.8, 13.2, 13.1.
-    while (parts < 8 && tiles * (parts + 1) <= 2 * sms && a.groups >= 2 * (parts + 1)) ++parts;
-    ctas = static_cast<int>(tiles) * parts;
-  }
+  const int ctas = 2 * static_cast<int>(std::min<long long>(tiles, sms / 2));   // of pairs
+  const int some = static_cast<int>(tiles);
   CUtensorMap wm, xm, om;
   if (!encode_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, ins, outs, ins, 128,
                      pair ? bn / 2 : 128) ||
@@ -963,12 +1015,12 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   const bool f = fp32 != 0;
-  if (pair && f) e = launch_product<128, true, float>(xm, wm, om, a, parts, ctas, dev, st);
-  else if (pair && !wide) e = launch_product<128, true, __nv_bfloat16>(xm, wm, om, a, parts, ctas, dev, st);
-  else if (pair) e = launch_product<256, true, __nv_bfloat16>(xm, wm, om, a, parts, ctas, dev, st);
-  else if (bn == 16) e = launch_single<16>(f, wm, xm, a, parts, ctas, dev, st);
-  else if (bn == 32) e = launch_single<32>(f, wm, xm, a, parts, ctas, dev, st);
-  else e = launch_single<64>(f, wm, xm, a, parts, ctas, dev, st);
+  if (pair && f) e = launch_product<128, true, float>(xm, wm, om, a, ctas, 2, dev, st);
+  else if (pair && !wide) e = launch_product<128, true, __nv_bfloat16>(xm, wm, om, a, ctas, 2, dev, st);
+  else if (pair) e = launch_product<256, true, __nv_bfloat16>(xm, wm, om, a, ctas, 2, dev, st);
+  else if (bn == 16) e = launch_single<16>(f, wm, xm, a, some, dev, st);
+  else if (bn == 32) e = launch_single<32>(f, wm, xm, a, some, dev, st);
+  else e = launch_single<64>(f, wm, xm, a, some, dev, st);
   return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
 }
 

@@ -166,6 +166,25 @@ def test_products_of_whole_numbers_are_exact(P, n, ins, outs, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("tiles", [30, 37, 45, 57, 73, 90, 140, 300])
+@pytest.mark.parametrize("n", [15, 16, 31, 64])
+def test_k_in_any_number_of_parts(P, n, tiles, dtype):
+    """From eight parts to one, as there are more tiles; each CTA's sums have their place."""
+    rng = np.random.default_rng(n + tiles)
+    ins, outs = 2048, 128 * tiles - 3
+    x, xc = whole(rng, n, ins)
+    w, wc = whole(rng, outs, ins)
+    ws, wsd = scales_of(rng, (tiles, 16), -2, 2)
+    xs, xsd = scales_of(rng, (n, 16), -2, 2)
+    weight = P.Weight8(wc.cuda(), wsd.cuda())
+    got = [weight.product(xc.cuda(), xsd.cuda(), dtype=dtype) for _ in range(3)]
+    assert weight.poll() == ess.ESS_OK
+    want = (x * spread(xs, 1, n, ins)) @ (w * spread(ws, 128, outs, ins)).T
+    want = torch.from_numpy(want.astype(np.float32)).to(dtype)
+    assert all(torch.equal(g.cpu(), want) for g in got)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("n,ins,outs", [(3, 4096, 300), (40, 16384, 200), (200, 2064, 700), (400, 1024, 5000),
                                         (9, 144, 70), (70, 16384, 4100), (300, 4112, 9800)])
 def test_products_of_quantised_values(P, n, ins, outs, dtype):
