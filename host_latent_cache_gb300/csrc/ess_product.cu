@@ -29,7 +29,7 @@
 // 8192 (tokens x ins x outs) 153 us, 3.6 PFLOP/s or 93 % of twice the measured bf16 rate (a
 // library's product with the same form of scales takes 151); in fp32 209; 8192 x 1024 x
 // 24576 135, 2048 x 4096 x 8192 44, 512 x 4096 x 8192 15.8, 128 x 4096 x 8192 11.9, 333 x 4112
-// x 1601 13.0, 64 x 4096 x 8192 9.6, 32 x 1024 x 24576 6.8 (4.0 TB/s), 4 x 4096 x 1600 4.1; a
+// x 1601 12.9, 64 x 4096 x 8192 9.5, 32 x 1024 x 24576 6.8 (4.0 TB/s), 4 x 4096 x 1600 4.1; a
 // launch that multiplies 16 x 128 x 128 2.9.
 // What bounds them: a large product the tensor pipe, busy for 78 % of an SM's cycles under
 // ncu at 2048 tokens (L2 35 %, its crossbar 41 %, shared memory's banks 17 %), with some
