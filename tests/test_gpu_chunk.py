@@ -196,6 +196,22 @@ def test_threads_on_one_stream():
     assert not bad and len(got) == 80 and all(torch.equal(o, w) for o, w in got)
 
 
+@pytest.mark.parametrize("listed", [False, True], ids=["dense", "listed"])
+def test_rows_past_4_gb(listed):
+    from host_latent_cache_gb300.rows import RowCache
+    c = Chunks(20, [(30, 300), (70, 128)], 24)
+    tokens = c.lists(64) if listed else None
+    want, lse = c.attend(tokens)
+    small = c.cache.rows
+    extra = 11_000_000 // 64                      # pages ahead of them, 4.4 GB
+    big = torch.zeros(extra * 64 + small.shape[0], 400, dtype=torch.uint8, device="cuda")
+    big[extra * 64:] = small
+    c.cache = RowCache(big, "q4", page=64)
+    c.dev_table = c.dev_table + extra
+    got, gl = c.attend(tokens)
+    assert torch.equal(got, want) and torch.equal(gl, lse) and c.cache.poll() == ess.ESS_OK
+
+
 def test_more_queries_than_tokens():
     """The first queries then have no token at all."""
     c = Chunks(4, [(10, 4), (300, 150), (2, 0)], 128)

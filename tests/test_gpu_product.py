@@ -271,6 +271,34 @@ def test_into_a_view(P, n, outs, stride, first, dtype):
     assert (buf == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("stride", [33000, 33001])
+def test_offsets_past_32_bits(P, stride, dtype):
+    """Values, codes and results whose places pass 2^31 elements."""
+    n, outs, ins = 66000, 32993, 16
+    rng = np.random.default_rng(3)
+    x, xc = whole(rng, n, ins)
+    w, wc = whole(rng, outs, ins)
+    one = lambda r: torch.ones(r, 1, device="cuda")
+    weight = P.Weight8(wc.cuda(), one(-(-outs // 128)))
+    out = torch.full((n, stride), 7.0, dtype=dtype, device="cuda")
+    weight.product(xc.cuda(), one(n), out=out[:, :outs])
+    assert weight.poll() == ess.ESS_OK
+    assert (out[:, outs:] == 7.0).all()
+    for rows in (slice(0, 70), slice(n // 2, n // 2 + 70), slice(n - 70, n)):
+        want = torch.from_numpy((x[rows] @ w.T).astype(np.float32)).to(dtype)
+        assert torch.equal(out[rows, :outs].cpu(), want)
+    if dtype is torch.bfloat16 and stride == 33000:
+        wide = out[:, :outs - outs % 8]          # large values, in a view of wide rows
+        for square in (False, True):
+            codes, scales = P.quant_q8(wide, square=square)
+            at = n - n % 128 - 256               # whole blocks near the end
+            c, s = P.quant_q8(wide[at:].contiguous(), square=square)
+            assert torch.equal(codes[at:].view(torch.uint8), c.view(torch.uint8))
+            assert torch.equal(scales[at // 128 if square else at:], s)
+            del codes, scales
+
+
 def test_a_product_repeats_its_bits(P):
     x = torch.randn(70, 4096, device="cuda").to(torch.bfloat16)
     weight = P.Weight8.of(torch.randn(700, 4096, device="cuda").to(torch.bfloat16))

@@ -88,6 +88,19 @@ def test_views_and_places(pairs):
                        rotate(one.contiguous(), pos, FREQ, pairs=pairs).expand(n, heads, 64))
 
 
+def test_offsets_past_32_bits():
+    from host_latent_cache_gb300.rows import rotate
+    n, heads = 300000, 64
+    wide = torch.zeros(n, heads, 128, dtype=torch.bfloat16, device="cuda")   # 2.4e9 values
+    wide[-5:] = torch.randn(5, heads, 128, device="cuda").to(torch.bfloat16)
+    pos = torch.arange(n, device="cuda", dtype=torch.int32)
+    want = rotate(wide[-5:, :, 64:].contiguous(), pos[-5:].contiguous(), FREQ)
+    left = wide[-5:, :, :64].clone()
+    rotate(wide[:, :, 64:], pos, FREQ, out=wide[:, :, 64:])
+    assert torch.equal(wide[-5:, :, 64:], want) and torch.equal(wide[-5:, :, :64], left)
+    assert not wide[:-5].any()
+
+
 def test_the_inverse_is_by_the_negative_frequencies():
     """To bf16's two roundings: each off by 2^-8 of a value below |(a, b)|."""
     from host_latent_cache_gb300.rows import rotate
