@@ -233,6 +233,16 @@ struct UnitWalk {
 };
 constexpr int kMaxChunkBatch = 32768;   // their first units fit the operands' place
 
+// The deal counts tiles and segments in one 64-bit sum, tiles below this bit and segments
+// above it.  Entries are at most 65535 requests x 4 segments, of 2^24 tiles each.  Chunks
+// may have a unit for each query token: calls whose units or tiles could reach these
+// limits are refused, which keeps a pair's tiles within an int as well.
+constexpr int kSegShift = 43;
+constexpr int kChunkSegShift = 37;
+constexpr long long kMaxChunkTiles = 1LL << kChunkSegShift;
+constexpr long long kMaxChunkUnits = 1LL << (63 - kChunkSegShift);
+static_assert(kMaxChunkTiles / kMaxPairs < 0x7fffffffLL, "a pair's tiles");
+
 // Units of all requests; unit0[b], those before request b.  All threads call it.
 __device__ __forceinline__ int chunk_units(const MlaArgs& a, int* unit0, int* sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1128,7 +1138,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   // tiles those positions are left out, as a pair with none but them would lie
   // between two that share a request.  (Few entries are scanned by every warp,
   // without the block: 0.3 us of a small call.)
-  constexpr int kSegShift = 43;   // tiles below, segments above
+  constexpr int kShift = CHUNK ? kChunkSegShift : kSegShift;
   // Chunks scan units, whose requests are found among the requests' first units, kept
   // where the operands will be.
   int* unit0 = reinterpret_cast<int*>(smem);
@@ -1142,12 +1152,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   if (CHUNK) {
     walk0.start(a, unit0, v0, v0 < v1);
     UnitWalk w = walk0;
-    for (int v = v0; v < v1; ++v, w.next(a)) mine += w.tiles(a) + (1LL << kSegShift);
+    for (int v = v0; v < v1; ++v, w.next(a)) mine += w.tiles(a) + (1LL << kShift);
   } else {
     for (int v = v0; v < v1; ++v) {
       const int nt = (entry_len(a, v) + kMt - 1) / kMt;
       if (v == v0) nt0 = nt;
-      if (nt > 0) mine += (static_cast<long long>(nt) + (1LL << kSegShift)) * a.row_tiles;
+      if (nt > 0) mine += (static_cast<long long>(nt) + (1LL << kShift)) * a.row_tiles;
     }
   }
   long long before = mine;
@@ -1171,14 +1181,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     total = __shfl_sync(0xffffffffu, sums, 31);
     before += warp > 0 ? __shfl_sync(0xffffffffu, sums, warp - 1) : 0;
   }
-  constexpr long long kTileMask = (1LL << kSegShift) - 1;
+  constexpr long long kTileMask = (1LL << kShift) - 1;
   const long long tiles = total & kTileMask;
   constexpr int kCost = CHUNK ? kChunkSegmentCost : kSegmentCost;
   const int cost = tiles >= static_cast<long long>(kCost + 1) * pairs ? kCost : 0;
   const long long tiles_before = before & kTileMask;
-  const long long pos0 = tiles_before + cost * (before >> kSegShift);
-  const long long pos1 = pos0 + (mine & kTileMask) + cost * (mine >> kSegShift);
-  const long long all = tiles + cost * (total >> kSegShift);
+  const long long pos0 = tiles_before + cost * (before >> kShift);
+  const long long pos1 = pos0 + (mine & kTileMask) + cost * (mine >> kShift);
+  const long long all = tiles + cost * (total >> kShift);
   // the first all % busy pairs take one position more
   const int busy = tiles < pairs ? max(static_cast<int>(tiles), 1) : pairs;
   const long long share = all < 0x7fffffffLL
@@ -1628,6 +1638,11 @@ ess_status ess_cache_chunk(const void* q, int64_t total, const int32_t* cu, cons
       !aligned_to(page_table, 4) || !aligned_to(T, 4) || !aligned_to(tokens, 4) ||
       !aligned_to(lse, 4) || !aligned_to(status, 4))
     return ESS_ERR_INVALID_ARG;
+  // units and tiles there can be
+  const long long context = static_cast<long long>(max_pages) * page;
+  const long long units = tokens ? total : total * heads / kPairRows + std::min<long long>(total, batch);
+  const long long most = units * (((tokens ? std::min<long long>(k, context) : context) + kMt - 1) / kMt);
+  if (units >= kMaxChunkUnits || most >= kMaxChunkTiles) return ESS_ERR_UNSUPPORTED;
   const ChunkLayout L = chunk_layout();
   if (ws_bytes < L.total) return ESS_ERR_OOM;
   int dev = 0;
@@ -1659,9 +1674,6 @@ ess_status ess_cache_chunk(const void* q, int64_t total, const int32_t* cu, cons
   a.status = status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // no more pairs than tiles there can be
-  const long long context = static_cast<long long>(max_pages) * page;
-  const long long units = tokens ? total : total * heads / kPairRows + std::min<long long>(total, batch);
-  const long long most = units * (((tokens ? std::min<long long>(k, context) : context) + kMt - 1) / kMt);
   a.pairs = static_cast<int>(std::max(1LL, std::min<long long>(most, kMaxPairs)));
   cudaError_t e = allow_smem<true>(dev);
   if (e != cudaSuccess) return ESS_ERR_CUDA;

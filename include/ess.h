@@ -693,8 +693,10 @@ ess_status ess_cache_chunk_bytes(size_t* bytes);
  * status; such a token is left out.  total = 0 launches nothing.
  * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or non-positive argument or a scale
  * that is not finite; ESS_ERR_UNSUPPORTED for more than 128 heads or 32768 requests,
- * another format, more than 2^31 - 1 rows, max_pages * page or k above 2^31 - 256, or
- * total * heads of 2^31 - 384 or more; ESS_ERR_OOM for a workspace that is too small. */
+ * another format, more than 2^31 - 1 rows, max_pages * page or k above 2^31 - 256,
+ * total * heads of 2^31 - 384 or more, 2^26 or more query tokens with lists, or 2^37 or
+ * more tiles of 128 query rows (with lists: a query token's heads) x 128 tokens, as many
+ * as max_pages * page or k allow; ESS_ERR_OOM for a workspace that is too small. */
 ess_status ess_cache_chunk(const void* q, int64_t total, const int32_t* cu, const void* rows,
                            int64_t n_rows, int32_t format, const int32_t* page_table,
                            int32_t max_pages, int32_t page, const int32_t* T, int32_t batch,
