@@ -108,6 +108,7 @@ struct Misc {
   uint64_t row_full[kRing], row_free[kRing];
   uint32_t tmem;
   int abort;
+  int fell;                           // chunks: some offset is below the one before it
   int start_v, start_rt, start_tile;
   long long first_tile, end_tile;     // of all tiles of all requests
   uint32_t mask[kRing][4];            // tokens of a tile that exist
@@ -145,6 +146,7 @@ struct MlaArgs {
   bool wide_out;           // chunks: out is 32-byte aligned
   int pairs;               // chunks: pairs of the launch
   int4* rec;               // chunks: [pairs] which units the pairs cut
+  volatile int* unit0;     // chunks whose offsets fall: [batch + 1] units of the requests before
   int2* span;              // [entries][row_tiles]: first pair * 2 + slot, last pair
   float* part_o;           // [pairs][2][512 / 8][128][8]: a lane's 32 bytes beside its neighbours'
   float4* part_ml;         // [pairs][2][128]: reference, sum, c2 of the row
@@ -189,6 +191,28 @@ __device__ __forceinline__ Chunk chunk_of(const MlaArgs& a, int b) {
 __device__ __forceinline__ int units_of(const MlaArgs& a, int n) {
   return (n * a.heads + a.unit_rows - 1) / a.unit_rows;
 }
+// Where offsets fall, and then rise again, a request that starts ahead of the end of one
+// before it has no units: so a query row belongs to one unit at most, and there are no more
+// units than the host counts.  The units that are left are kept in the workspace then, the
+// same numbers from every CTA, as each walks over them.
+__device__ __forceinline__ int end_before(const MlaArgs& a, int b) {
+  int end = 0;
+  for (int i = 0; i < b; ++i) {
+    const Chunk c = chunk_of(a, i);
+    end = max(end, c.n > 0 ? c.start + c.n : 0);
+  }
+  return end;
+}
+// Units of request b behind those that leave off at `end`, which becomes its own end.
+__device__ __forceinline__ int units_behind(const MlaArgs& a, int b, int* end) {
+  const Chunk c = chunk_of(a, b);
+  const int units = c.start < *end ? 0 : units_of(a, c.n);
+  *end = max(*end, c.n > 0 ? c.start + c.n : 0);
+  return units;
+}
+__device__ __forceinline__ int request_units(const MlaArgs& a, int b, bool fell) {
+  return fell ? a.unit0[b + 1] - a.unit0[b] : units_of(a, chunk_of(a, b).n);
+}
 // Tokens that the last row of unit u of a request sees.
 __device__ __forceinline__ int unit_sees(const MlaArgs& a, int T, int n, int u) {
   const int last = min(n * a.heads, (u + 1) * a.unit_rows) - 1;
@@ -203,14 +227,14 @@ __device__ __forceinline__ int unit_tiles(int len) { return max((len + kMt - 1) 
 
 // A walk over the units of all requests.
 struct UnitWalk {
-  int b, u, units, n, T;
+  const int* unit0;   // [batch + 1]: units of the requests before each
+  int b, u, n, T;
   __device__ __forceinline__ void load(const MlaArgs& a) {
     n = chunk_of(a, b).n;
     T = request_len(a, b);
-    units = units_of(a, n);
   }
-  // unit0[b]: units of the requests before b
-  __device__ __forceinline__ void start(const MlaArgs& a, const int* unit0, int v, bool live) {
+  __device__ __forceinline__ void start(const MlaArgs& a, const int* first, int v, bool live) {
+    unit0 = first;
     int lo = 0, hi = live ? a.batch - 1 : 0;   // the last request that starts at v or before
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -225,13 +249,14 @@ struct UnitWalk {
     return unit_tiles(unit_len(a, T, n, u));
   }
   __device__ __forceinline__ void next(const MlaArgs& a) {
-    for (++u; u >= units && b + 1 < a.batch; u = 0) {
+    for (++u; u >= unit0[b + 1] - unit0[b] && b + 1 < a.batch; u = 0) {
       ++b;
       load(a);
     }
   }
 };
-constexpr int kMaxChunkBatch = 32768;   // their first units fit the operands' place
+constexpr int kMaxChunkBatch = 32768;
+static_assert((kMaxChunkBatch + 1) * sizeof(int) <= kOffMisc, "the first units, in the operands' place");
 
 // The deal counts tiles and segments in one 64-bit sum, tiles below this bit and segments
 // above it.  Entries are at most 65535 requests x 4 segments, of 2^24 tiles each.  Chunks
@@ -244,27 +269,34 @@ constexpr long long kMaxChunkUnits = 1LL << (63 - kChunkSegShift);
 static_assert(kMaxChunkTiles / kMaxPairs < 0x7fffffffLL, "a pair's tiles");
 
 // Units of all requests; unit0[b], those before request b.  All threads call it.
-__device__ __forceinline__ int chunk_units(const MlaArgs& a, int* unit0, int* sums) {
+__device__ __forceinline__ int chunk_units(const MlaArgs& a, int* unit0, int* sums, int* fell_out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.batch + kMlaThreads - 1) / kMlaThreads;
   const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
-  int mine = 0;
-  bool bad = false;
+  int mine = 0, before;
+  bool bad = false, falls = false, fell = false;
   for (int b = b0; b < b1; ++b) {
     const Chunk c = chunk_of(a, b);
     const int T = a.T[b];
     bad |= !c.ok || T < 0 || T > static_cast<long long>(a.max_pages) * a.page;
+    falls |= a.cu[b + 1] < a.cu[b];
     mine += units_of(a, c.n);
   }
   if (bad && blockIdx.x == 0) set_status(a.status, ESS_ERR_DEVICE_CHECK);
-  int before = mine;
+  for (;;) {
+    before = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += x;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += x;
+    }
+    if (lane == 31) sums[warp] = before;
+    if (!__syncthreads_or(falls)) break;
+    fell = true;   // counted again, without the requests that start inside another
+    falls = false;
+    mine = 0;
+    for (int b = b0, end = end_before(a, b0); b < b1; ++b) mine += units_behind(a, b, &end);
   }
-  if (lane == 31) sums[warp] = before;
-  __syncthreads();
   int all = lane < kMlaThreads / 32 ? sums[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -274,9 +306,16 @@ __device__ __forceinline__ int chunk_units(const MlaArgs& a, int* unit0, int* su
   const int total = __shfl_sync(0xffffffffu, all, 31);
   const int earlier = __shfl_sync(0xffffffffu, all, max(warp - 1, 0));
   before += (warp > 0 ? earlier : 0) - mine;
+  int end = fell ? end_before(a, b0) : 0;
   for (int b = b0; b < b1; ++b) {
     unit0[b] = before;
-    before += units_of(a, chunk_of(a, b).n);
+    if (fell) a.unit0[b] = before;
+    before += fell ? units_behind(a, b, &end) : units_of(a, chunk_of(a, b).n);
+  }
+  if (tid == 0) {
+    unit0[a.batch] = total;
+    if (fell) a.unit0[a.batch] = total;
+    *fell_out = fell;
   }
   __syncthreads();
   return total;
@@ -466,14 +505,14 @@ struct Tiles {
   // of a segment: a run of tiles of one entry and row tile
   __device__ __forceinline__ bool first() const { return begins || tile == 0; }
   __device__ __forceinline__ bool last() const { return left == 1 || tile + 1 == nt; }
-  __device__ __forceinline__ void next(const MlaArgs& a) {
+  __device__ __forceinline__ void next(const MlaArgs& a, const Misc* mi) {
     begins = false;
     --left;
     if (++tile == nt && left > 0) {
       tile = 0;
       if (CHUNK) {
         ++rt;
-        while (v + 1 < a.batch && rt >= units_of(a, chunk_of(a, v).n)) {
+        while (v + 1 < a.batch && rt >= request_units(a, v, mi->fell)) {
           rt = 0;
           ++v;
         }
@@ -603,7 +642,7 @@ __device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
       slot = 0;
       ++turn;
     }
-    it.next(a);
+    it.next(a, mi);
   }
 }
 
@@ -869,7 +908,7 @@ __device__ __forceinline__ void mma_role(const MlaArgs& a, uint8_t* smem, Misc* 
     }
     if (!first) pv(g - 1, acc);
     acc = !first;
-    it.next(a);
+    it.next(a, mi);
     if (!it.more()) pv(g, acc);
   }
 }
@@ -988,7 +1027,7 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
     if (lane == 0) mbar_arrive_remote(dsmem_addr(smem_u32(&mi->vp_full[half]), 0));
 
     if (!last) {
-      it.next(a);
+      it.next(a, mi);
     } else {
       const int v = it.v;
       const int row0 = (CHUNK ? 0 : it.rt * kPairRows) + static_cast<int>(rank) * kCtaRows;
@@ -998,7 +1037,7 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
       const bool ends = it.tile + 1 == it.nt;
       const bool whole = seg_first_tile == 0 && ends;
       const int slot = pair * 2 + (seg == 0 ? 0 : 1);
-      it.next(a);
+      it.next(a, mi);
       ++seg;
       // the whole row's sum, then O out of TMEM: final, or a partial
       mi->xch[part][r] = l;
@@ -1142,7 +1181,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
   // Chunks scan units, whose requests are found among the requests' first units, kept
   // where the operands will be.
   int* unit0 = reinterpret_cast<int*>(smem);
-  const int entries = CHUNK ? chunk_units(a, unit0, reinterpret_cast<int*>(mi->xch)) : a.entries;
+  const int entries = CHUNK ? chunk_units(a, unit0, reinterpret_cast<int*>(mi->xch), &mi->fell) : a.entries;
   const int per = (entries + kMlaThreads - 1) / kMlaThreads;
   const bool few = !CHUNK && entries <= 32;   // then each warp scans them
   const int v0 = min(entries, few ? lane : tid * per), v1 = min(entries, v0 + per);
@@ -1505,12 +1544,13 @@ MlaLayout mla_layout(int batch, int ways) {
 }
 
 struct ChunkLayout {
-  size_t rec, part_o, part_ml, total;
+  size_t rec, unit0, part_o, part_ml, total;
 };
 ChunkLayout chunk_layout() {
   ChunkLayout L;
   L.rec = 0;
-  L.part_ml = (kMaxPairs * sizeof(int4) + 255) & ~static_cast<size_t>(255);
+  L.unit0 = (kMaxPairs * sizeof(int4) + 255) & ~static_cast<size_t>(255);
+  L.part_ml = L.unit0 + (((kMaxChunkBatch + 1) * sizeof(int) + 255) & ~static_cast<size_t>(255));
   L.part_o = L.part_ml + static_cast<size_t>(kMaxPairs) * 2 * kPairRows * sizeof(float4);
   L.total = L.part_o + static_cast<size_t>(kMaxPairs) * 2 * kPairRows * kLatent * sizeof(float);
   return L;
@@ -1669,6 +1709,7 @@ ess_status ess_cache_chunk(const void* q, int64_t total, const int32_t* cu, cons
   a.lse = lse;
   char* ws = static_cast<char*>(workspace);
   a.rec = reinterpret_cast<int4*>(ws + L.rec);
+  a.unit0 = reinterpret_cast<int*>(ws + L.unit0);
   a.part_o = reinterpret_cast<float*>(ws + L.part_o);
   a.part_ml = reinterpret_cast<float4*>(ws + L.part_ml);
   a.status = status;

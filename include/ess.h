@@ -688,9 +688,10 @@ ess_status ess_cache_chunk_bytes(size_t* bytes);
  *              share one are ordered by the caller
  * rows, page_table, the results and the roundings are as in ess_cache_mla.  A query that
  * attends to nothing (n above T_b) gets zeros and lse = -infinity.  A length outside its
- * range, offsets that are negative, fall or pass total (the request then has no queries),
- * a token past its query's and a page outside the cache report ESS_ERR_DEVICE_CHECK in
- * status; such a token is left out.  total = 0 launches nothing.
+ * range, offsets that are negative, fall or pass total (the request then has no queries,
+ * nor has one behind them that starts ahead of the end of a request before it), a token
+ * past its query's and a page outside the cache report ESS_ERR_DEVICE_CHECK in status; such
+ * a token is left out.  total = 0 launches nothing.
  * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or non-positive argument or a scale
  * that is not finite; ESS_ERR_UNSUPPORTED for more than 128 heads or 32768 requests,
  * another format, more than 2^31 - 1 rows, max_pages * page or k above 2^31 - 256,
