@@ -156,12 +156,16 @@ constexpr int kMaxStages = 8;
 constexpr uint32_t kOutBlock = 32 * 128;  // results on their way out: 32 tokens, 128 bytes each
 constexpr int kOverlap = 32;             // columns that two accumulators of 256 share
 
-// Groups of K that one accumulator adds up when results are fp32.  The tensor core
+// Groups of K that one accumulator adds up when sums are short.  The tensor core
 // cuts off what an addition shifts out, so a sum drifts towards zero with each of
-// its additions: products of 4096 values were off by 2e-6 of their norm (2^-24 is
-// 6e-8).  Sums of 1024 are added up in registers, rounded, instead: 5e-7.  For bf16
-// results (2^-9) the whole of K is one sum.
+// its additions.  Of values of one sign, in parts of their sum: 2e-6 over 1024 of them,
+// 1e-5 over 4096, 4e-5 over 16384, 1.8e-4 over 65536; of both signs, products of 4096
+// values were off by 2e-6 of their norm (2^-24 is 6e-8).  For fp32 results sums of 1024 are
+// added up in registers, rounded, instead: 2e-6 of one sign for any K.  A bf16 result (half
+// a step is 4e-3 of it) is one sum of up to kOneSum values, and short sums above that: eight
+// sums of 2^19 were 1.8e-3 short, eight of 2^23 1.6e-2.
 constexpr int kSumGroups = 8;
+constexpr int kOneSum = 1 << 16;
 
 constexpr int prod_stages(int bn, bool pair) {
   return pair ? (bn == 256 ? 6 : 8) : bn <= 16 ? 5 : bn <= 32 ? 4 : 3;
@@ -408,12 +412,13 @@ struct ProdShare {
   int first, step, tiles, g0, g1;
 };
 
-template <int BN, bool PAIR, typename Out>
+template <int BN, bool PAIR, typename Out, bool SUMS>
 __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
     product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                    const __grid_constant__ CUtensorMap omap, const ProdArgs a) {
-  constexpr bool kSums = sizeof(Out) == 4;   // short sums, added up in registers
+  constexpr bool kSums = SUMS;               // short sums, added up in registers
   static_assert(!kSums || BN <= 128, "sums in registers");
+  static_assert(kSums || sizeof(Out) == 2, "fp32 results");
   constexpr int kStages = prod_stages(BN, PAIR);
   constexpr uint32_t kStage = prod_stage_bytes(BN, PAIR);
   constexpr int kBRows = prod_b_rows(BN, PAIR);
@@ -824,25 +829,25 @@ struct ProdLaunch {
 };
 
 // The kernel's shared memory, allowed once per device.
-template <int BN, bool PAIR, typename Out>
+template <int BN, bool PAIR, typename Out, bool SUMS>
 cudaError_t allow_prod_smem(int dev) {
   static std::atomic<unsigned long long> done{0};
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
   if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
   const cudaError_t e =
-      cudaFuncSetAttribute(product_kernel<BN, PAIR, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      cudaFuncSetAttribute(product_kernel<BN, PAIR, Out, SUMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(prod_smem(BN, PAIR)));
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
 
-template <int BN, bool PAIR, typename Out>
+template <int BN, bool PAIR, typename Out, bool SUMS>
 cudaError_t launch_product(const CUtensorMap& am, const CUtensorMap& bm, const CUtensorMap& om,
                            const ProdArgs& a, int ctas, int cluster, int dev, cudaStream_t st) {
-  const cudaError_t e = allow_prod_smem<BN, PAIR, Out>(dev);
+  const cudaError_t e = allow_prod_smem<BN, PAIR, Out, SUMS>(dev);
   if (e != cudaSuccess) return e;
   ProdLaunch l(ctas, cluster, prod_smem(BN, PAIR), st);
-  return cudaLaunchKernelEx(&l.cfg, product_kernel<BN, PAIR, Out>, am, bm, om, a);
+  return cudaLaunchKernelEx(&l.cfg, product_kernel<BN, PAIR, Out, SUMS>, am, bm, om, a);
 }
 
 // Clusters of `parts` CTAs, two an SM, that run at once, which depends on how SMs are
@@ -871,21 +876,22 @@ int clusters_at_once(int parts, int dev) {
 // K is cut into as many parts as still run at once, with two stages each (us): 4 x 4096 x
 // 1600, 13 tiles, takes 10.5 uncut, 7.2 in two parts, 5.1 in four, 4.1 in eight; 16 x 4096 x
 // 4736, 37 tiles, 9.0 in eight parts, of which 36 clusters run at once.
-template <int BN, typename Out>
+template <int BN, typename Out, bool SUMS>
 cudaError_t launch_single(const CUtensorMap& w, const CUtensorMap& x, const ProdArgs& a, int tiles,
                           int dev, cudaStream_t st) {
   int parts = kMaxParts;
   while (parts > 1 && (a.groups < 2 * parts || !parts_fit(BN, parts) ||
                        tiles > clusters_at_once(parts, dev)))
     --parts;
-  return launch_product<BN, false, Out>(w, x, w, a, tiles * parts, parts, dev, st);
+  return launch_product<BN, false, Out, SUMS>(w, x, w, a, tiles * parts, parts, dev, st);
 }
 
 template <int BN>
-cudaError_t launch_single(bool fp32, const CUtensorMap& w, const CUtensorMap& x, const ProdArgs& a,
-                          int tiles, int dev, cudaStream_t st) {
-  return fp32 ? launch_single<BN, float>(w, x, a, tiles, dev, st)
-              : launch_single<BN, __nv_bfloat16>(w, x, a, tiles, dev, st);
+cudaError_t launch_single(bool fp32, bool sums, const CUtensorMap& w, const CUtensorMap& x,
+                          const ProdArgs& a, int tiles, int dev, cudaStream_t st) {
+  return fp32   ? launch_single<BN, float, true>(w, x, a, tiles, dev, st)
+         : sums ? launch_single<BN, __nv_bfloat16, true>(w, x, a, tiles, dev, st)
+                : launch_single<BN, __nv_bfloat16, false>(w, x, a, tiles, dev, st);
 }
 
 int sms_of(int dev) {
@@ -985,10 +991,11 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   // 11.7 against 12.6, 333 x 4096 x 1600, 26 tiles, 11.1 against 10.7; up to 64 tokens the
   // others: 64 x 4096 x 8192 9.6 against 11.5.  256 columns once tiles of 128 would take
   // more than one wave: 1024 x 4096 x 1600, 52 of 128, 11.8 against 14.4; 512 x 4096 x
-  // 8192, 128 of 128, 18.8 against 15.8.  fp32 results' sums have registers for 128.
+  // 8192, 128 of 128, 18.8 against 15.8.  Short sums have registers for 128.
   const long long pair_tiles = static_cast<long long>(cover(outs, 128)) * cover(n, 256);
   const bool pair = n > 64 && pair_tiles >= sms / 5;
-  const bool wide = !fp32 && pair_tiles > sms / 2;
+  const bool f = fp32 != 0, sums = f || ins > kOneSum;
+  const bool wide = !sums && pair_tiles > sms / 2;
   const int bn = pair ? (wide ? 256 : 128) : n <= 16 ? 16 : n <= 32 ? 32 : 64;
   a.m_tiles = pair ? cover(n, 256) : cover(outs, 128);
   a.n_tiles = pair ? cover(outs, bn) : cover(n, bn);
@@ -1014,13 +1021,13 @@ ess_status ess_product(const void* x, const float* x_scales, int64_t n, const vo
   if (a.keys) ++key_norms();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  const bool f = fp32 != 0;
-  if (pair && f) e = launch_product<128, true, float>(xm, wm, om, a, ctas, 2, dev, st);
-  else if (pair && !wide) e = launch_product<128, true, __nv_bfloat16>(xm, wm, om, a, ctas, 2, dev, st);
-  else if (pair) e = launch_product<256, true, __nv_bfloat16>(xm, wm, om, a, ctas, 2, dev, st);
-  else if (bn == 16) e = launch_single<16>(f, wm, xm, a, some, dev, st);
-  else if (bn == 32) e = launch_single<32>(f, wm, xm, a, some, dev, st);
-  else e = launch_single<64>(f, wm, xm, a, some, dev, st);
+  if (pair && f) e = launch_product<128, true, float, true>(xm, wm, om, a, ctas, 2, dev, st);
+  else if (pair && sums) e = launch_product<128, true, __nv_bfloat16, true>(xm, wm, om, a, ctas, 2, dev, st);
+  else if (pair && !wide) e = launch_product<128, true, __nv_bfloat16, false>(xm, wm, om, a, ctas, 2, dev, st);
+  else if (pair) e = launch_product<256, true, __nv_bfloat16, false>(xm, wm, om, a, ctas, 2, dev, st);
+  else if (bn == 16) e = launch_single<16>(f, sums, wm, xm, a, some, dev, st);
+  else if (bn == 32) e = launch_single<32>(f, sums, wm, xm, a, some, dev, st);
+  else e = launch_single<64>(f, sums, wm, xm, a, some, dev, st);
   return e == cudaSuccess ? ESS_OK : ESS_ERR_CUDA;
 }
 
