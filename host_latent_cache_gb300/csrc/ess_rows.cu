@@ -340,6 +340,16 @@ __global__ void __launch_bounds__(kTurnThreads) rotate_kernel(const RotateArgs a
   }
 }
 
+// Whether rows of 64 values at every i * row + j * head, i < n, j < heads, keep apart: the
+// heads of a token lie ahead of the next token, or the tokens of a head ahead of the next head.
+bool rows_apart(long long n, long long row, long long heads, long long head) {
+  auto ahead = [](long long count, long long inner, long long outer) {   // count inner ones in an outer one
+    return outer >= 64 && (count < 2 || (inner >= 64 && (outer - 64) / (count - 1) >= inner));
+  };
+  if (n < 2 || heads < 2) return (n < 2 || row >= 64) && (heads < 2 || head >= 64);
+  return ahead(heads, head, row) || ahead(n, row, head);
+}
+
 // Frequencies and axes (axis null: all pairs turn by the first); false for a bad one.
 bool rope_freq(const double* inv_freq, int axes, const int32_t* axis, RopeFreq* fr) {
   for (int i = 0; i < 32; ++i) {
@@ -567,7 +577,7 @@ ess_status ess_rotate(const void* x, int64_t x_row, int64_t x_head, int64_t n, i
   RopeFreq fr = {};
   if (!rope_freq(inv_freq, axes, axis, &fr)) return ESS_ERR_INVALID_ARG;
   if (x_row % 8 != 0 || x_head % 8 != 0 || out_row % 8 != 0 || out_head % 8 != 0 || x_row < 0 ||
-      x_head < 0 || (n > 1 && out_row < 64) || (heads > 1 && out_head < 64))
+      x_head < 0 || out_row < 0 || out_head < 0 || !rows_apart(n, out_row, heads, out_head))
     return ESS_ERR_INVALID_ARG;
   RotateArgs a;
   a.chunks = (heads - 1) / kTurnHeads + 1;

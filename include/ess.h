@@ -598,8 +598,10 @@ ess_status ess_cache_write_axes(const void* kv, int64_t kv_stride, int64_t n, co
  *   inv_freq, pairs         as in ess_cache_write; the inverse rotation (its gradient)
  *                           is that of the negative frequencies
  *   pos, axes, axis         as in ess_cache_write_axes
- *   out       device bf16 [n][heads][64] with strides of its own, at least 64; it may be x
- *             with x's strides, and shares no memory with x otherwise
+ *   out       device bf16 [n][heads][64] with strides of its own, under which no rows meet:
+ *             all heads of a token lie ahead of the next token, or all tokens of a head
+ *             ahead of the next head; it may be x with x's strides, and shares no memory
+ *             with x otherwise
  * Each value is formed in fp32, with the sine's and cosine's bound of ess_cache_write,
  * and rounded once.  What lies between the rows is left as it was.  n = 0 launches nothing.
  * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or negative argument, a stride, axis,
