@@ -254,7 +254,8 @@ class RowCache:
                workspace=None):
         """Attention of q bf16 [batch][ways][heads][576] over the cached tokens
         of each request (page_table int32 [batch][max_pages], T int32
-        [batch]), or over tokens int32 [batch][ways][k].  Returns (out bf16
+        [batch]), or over tokens int32 [batch][ways][k]: the first min(k, T) entries
+        of a list, of which negative ones are no token.  Returns (out bf16
         [batch][ways][heads][512], lse float32 [batch][ways][heads]).  Without
         `workspace` all caches keep one for each current stream (see
         `release_workspaces`), and a captured call takes one from its graph's
@@ -335,7 +336,10 @@ class RowCache:
         """Attention of chunks of new tokens: q bf16 [total][heads][576], of which
         request b has the tokens cu[b] to cu[b + 1] - 1 (cu int32 [batch + 1]), its
         newest of T[b] (int32 [batch]), each attending to itself and all before it
-        (page_table int32 [batch][max_pages]), or to tokens int32 [total][k].
+        (page_table int32 [batch][max_pages]), or to tokens int32 [total][k]: a query
+        token that sees s tokens (itself and those before it) attends to the first
+        min(k, s) entries of its list, of which negative ones are no token.  So a list's
+        tokens stand at its front: what lies behind s entries is not read, nor reported.
         Returns (out bf16 [total][heads][512], lse float32 [total][heads]); tokens of q
         outside all requests leave their places in both as they were.  Workspaces,
         threads and empty arguments as in `attend`."""

@@ -683,7 +683,8 @@ ess_status ess_cache_chunk_bytes(size_t* bytes);
  *   tokens     NULL: token i attends to the tokens t <= T_b - n + i.  Otherwise device
  *              int32 [total][k]: a query token attends to those of its first
  *              min(k, T_b - n + i + 1) entries that are tokens, whatever their order; a
- *              negative entry is no token.
+ *              negative entry is no token.  Entries behind those are not read: a list
+ *              has its tokens at its front.
  *   out        device bf16 [total][heads][512], 16-byte aligned
  *   lse        device float [total][heads], or NULL
  *   workspace  device, 256-byte aligned, at least ess_cache_chunk_bytes; calls that
