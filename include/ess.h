@@ -603,7 +603,8 @@ ess_status ess_cache_write_axes(const void* kv, int64_t kv_stride, int64_t n, co
  *             ahead of the next head; it may be x with x's strides, and shares no memory
  *             with x otherwise
  * Each value is formed in fp32, with the sine's and cosine's bound of ess_cache_write,
- * and rounded once.  What lies between the rows is left as it was.  n = 0 launches nothing.
+ * and rounded once.  What lies between the rows is left as it was.  Rows side by side may be
+ * bf16 indexer keys, as in ess_norm_quant.  n = 0 launches nothing.
  * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or negative argument, a stride, axis,
  * pairs or frequency out of range; ESS_ERR_UNSUPPORTED when n * ceil(heads / 4) is 2^31 or
  * more. */
@@ -724,7 +725,10 @@ ess_status ess_cache_chunk(const void* q, int64_t total, const int32_t* cu, cons
  * e4m3(y / scale).  With dim = 128 a row is an indexer key with its key scale:
  * codes and scales are ess_append's key_row and key_scale, or rows of the bound
  * idx_keys and idx_scale for a prompt: indexer calls that follow on the stream
- * wait for them.
+ * wait for them.  That goes by the call's rows, here and in ess_quant (dim up to 128),
+ * ess_product (bf16, up to 64 columns) and ess_rotate (rows of 64 side by side): keys
+ * written through another view of their memory (two keys as a row of 256 codes) need a
+ * synchronisation of the stream ahead of the indexer, which loads its first keys early.
  * n = 0 launches nothing.  Pointers and strides are 16-byte aligned (scales
  * 4-byte).  Errors: ESS_ERR_INVALID_ARG for a null, misaligned or negative
  * argument, a stride below dim, residual_out without residual, or eps < 0;
@@ -770,7 +774,8 @@ ess_status ess_quant(const void* x, int64_t x_stride, int64_t n, int32_t dim, in
  * values are one such sum, or up to eight for parts of K, added up with a rounding each;
  * of more values they are made of sums of 1024; and they are rounded to bf16 once.  A NaN
  * code makes the outputs it enters NaN, and no others.  One shape always adds in one order.
- * n = 0 launches nothing.
+ * bf16 rows of up to 64 columns may be indexer keys, as in ess_norm_quant.  n = 0 launches
+ * nothing.
  * Errors: ESS_ERR_INVALID_ARG for a null, misaligned or non-positive argument or
  * out_stride below outs; ESS_ERR_UNSUPPORTED when ins is not a multiple of 16 or above
  * 2^26, or n or outs above 2^31 - 256. */
