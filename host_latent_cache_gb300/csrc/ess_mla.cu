@@ -108,7 +108,6 @@ struct Misc {
   uint64_t row_full[kRing], row_free[kRing];
   uint32_t tmem;
   int abort;
-  int fell;                           // chunks: some offset is below the one before it
   int start_v, start_rt, start_tile;
   long long first_tile, end_tile;     // of all tiles of all requests
   uint32_t mask[kRing][4];            // tokens of a tile that exist
@@ -116,6 +115,7 @@ struct Misc {
   float xch[4][kCtaRows];             // a row's statistics from the four threads that share it
   int2 seg[kRing];                    // entry and row tile of a segment that a tile begins, or -1
   int8_t qexp[2][kCtaRows];           // log2 of what a query row was divided by, of two segments
+  int fell;                           // chunks: some offset is below the one before it
 };
 constexpr uint32_t kMlaSmem = 232448;
 static_assert(kOffMisc + sizeof(Misc) <= kMlaSmem, "shared memory of one CTA");
@@ -146,11 +146,11 @@ struct MlaArgs {
   bool wide_out;           // chunks: out is 32-byte aligned
   int pairs;               // chunks: pairs of the launch
   int4* rec;               // chunks: [pairs] which units the pairs cut
-  volatile int* unit0;     // chunks whose offsets fall: [batch + 1] units of the requests before
   int2* span;              // [entries][row_tiles]: first pair * 2 + slot, last pair
   float* part_o;           // [pairs][2][512 / 8][128][8]: a lane's 32 bytes beside its neighbours'
   float4* part_ml;         // [pairs][2][128]: reference, sum, c2 of the row
   int* status;
+  volatile int* unit0;     // chunks whose offsets fall: [batch + 1] units of the requests before
 };
 
 __device__ __forceinline__ int request_len(const MlaArgs& a, int b) {
