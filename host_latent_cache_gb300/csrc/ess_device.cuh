@@ -9,6 +9,8 @@
 #include <cuda_fp8.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ess_internal.h"
 
 namespace ess {
@@ -60,6 +62,43 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     if (abort != nullptr && *abort) return false;
     if (clock64() - t0 > kWaitLimitCycles) return false;
   }
+}
+
+// Arrive on a barrier of any CTA of the cluster.  The default (CTA-scope) release is
+// enough where it orders this CTA's own shared memory or TMEM, which fence.proxy.async or
+// tcgen05.wait and tcgen05.fence have put before it.  A cluster-scope release waits for the
+// warp's loads in flight: with it the scales' fetches of the 8-bit product held up every
+// round of four groups (8192 x 4096 x 8192 183 us instead of 153).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// Bounded wait of a warp's role.  When it gives up, or another role of the CTA has (abort in
+// what they share), the role goes on without waiting, so that every block-wide barrier is
+// still reached; the results are garbage and status says so.
+template <typename Shared>
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Shared* mi,
+                                              int* status) {
+  const uint32_t addr = smem_u32(bar);
+  if (mbar_try_wait(addr, parity)) return true;
+  volatile int* stop = &mi->abort;
+  const long long t0 = clock64();
+  while (!*stop) {
+    if (mbar_try_wait(addr, parity)) return true;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      set_status(status, ESS_ERR_TIMEOUT);
+      *stop = 1;
+    }
+  }
+  return false;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
 }
 
 // ---------------------------------------------------------------- proxies
@@ -205,6 +244,28 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    bar)
                : "memory");
+}
+
+// The same for a pair of CTAs (cta_group::2).
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
+               "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+// arrive on the barrier at this offset in both CTAs when all prior MMAs are done
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
 }
 
 // Instruction descriptor (kind::f16 / kind::f8f6f4): D f32, M=128 rows.
@@ -396,6 +457,19 @@ __device__ __forceinline__ void compact_row_to_bf16(const uint8_t* src, uint16_t
   d[2 * lane] = lo;
   d[2 * lane + 1] = hi;
   if (lane >= 1 && lane < 9) d[64 + lane - 1] = c.extra;   // RoPE: bytes 1024 + 16(lane - 1)
+}
+
+// ---------------------------------------------------------------- host
+// A kernel's dynamic shared memory, allowed once per device.
+template <auto KERNEL>
+cudaError_t allow_smem(int dev, uint32_t bytes) {
+  static std::atomic<unsigned long long> done{0};
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // ---------------------------------------------------------------- misc

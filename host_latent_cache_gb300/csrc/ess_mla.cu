@@ -54,7 +54,6 @@
 // them); a request cut by a boundary leaves fp32 partials, which a second kernel
 // joins.
 #include <algorithm>
-#include <atomic>
 #include <cfloat>
 #include <cmath>
 #include <cstddef>
@@ -322,18 +321,6 @@ __device__ __forceinline__ int chunk_units(const MlaArgs& a, int* unit0, int* su
 }
 
 // ---------------------------------------------------------------- pair PTX
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
-               "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish_pair() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-               : "memory");
-}
 // REUSE: 0 reads A from shared memory, 1 does and keeps it in the collector
 // buffer, 2 takes it from there (the MMA before had the same A).
 template <int REUSE>
@@ -351,48 +338,6 @@ __device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t a_desc, 
   else if (REUSE == 2) ESS_UMMA_PAIR(".collector::a::lastuse");
   else ESS_UMMA_PAIR("");
 #undef ESS_UMMA_PAIR
-}
-// arrive on the barrier at this offset in both CTAs when all prior MMAs are done
-__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(bar),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-// Arrive on a barrier of either CTA.  The default (CTA-scope) release is
-// enough: what it orders are writes to this CTA's own shared memory, which
-// fence.proxy.async has already put before the tensor core's reads of it.  A
-// cluster-scope release would wait for the warp's loads in flight.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-// Bounded wait.  When it gives up (or another warp has) the role goes on
-// without waiting, so that every block-wide barrier is still reached; the
-// results are garbage and status says so.
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Misc* mi,
-                                              int* status) {
-  const uint32_t addr = smem_u32(bar);
-  if (mbar_try_wait(addr, parity)) return true;
-  volatile int* stop = &mi->abort;
-  const long long t0 = clock64();
-  while (!*stop) {
-    if (mbar_try_wait(addr, parity)) return true;
-    if (clock64() - t0 > kWaitLimitCycles) {
-      set_status(status, ESS_ERR_TIMEOUT);
-      *stop = 1;
-    }
-  }
-  return false;
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(p));
-  return p != 0;
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -1514,18 +1459,6 @@ ess_status check_shape(int batch, int ways, int heads) {
   return ESS_OK;
 }
 
-// The kernel's shared memory, allowed once per device.
-template <bool CHUNK>
-cudaError_t allow_smem(int dev) {
-  static std::atomic<unsigned long long> done{0};
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(
-      cache_mla_kernel<CHUNK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMlaSmem));
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
 struct MlaLayout {
   size_t span, part_o, part_ml, total;
 };
@@ -1633,7 +1566,7 @@ ess_status ess_cache_mla(const void* q, const void* rows, int64_t n_rows, int32_
                            kMt - 1) /
                           kMt);
   const int pairs = static_cast<int>(std::min<long long>(most, kMaxPairs));
-  cudaError_t e = allow_smem<false>(dev);
+  cudaError_t e = allow_smem<cache_mla_kernel<false>>(dev, kMlaSmem);
   if (e != cudaSuccess) return ESS_ERR_CUDA;
   e = launch_pdl_once(cache_mla_kernel<false>, dim3(2 * pairs), dim3(kMlaThreads), kMlaSmem, st, a);
   if (e != cudaSuccess) return ESS_ERR_CUDA;
@@ -1716,7 +1649,7 @@ ess_status ess_cache_chunk(const void* q, int64_t total, const int32_t* cu, cons
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // no more pairs than tiles there can be
   a.pairs = static_cast<int>(std::max(1LL, std::min<long long>(most, kMaxPairs)));
-  cudaError_t e = allow_smem<true>(dev);
+  cudaError_t e = allow_smem<cache_mla_kernel<true>>(dev, kMlaSmem);
   if (e != cudaSuccess) return ESS_ERR_CUDA;
   e = launch_pdl_once(cache_mla_kernel<true>, dim3(2 * a.pairs), dim3(kMlaThreads), kMlaSmem, st, a);
   if (e == cudaSuccess && a.pairs > 1) {

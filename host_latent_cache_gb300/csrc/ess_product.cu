@@ -225,32 +225,6 @@ struct ProdArgs {
   int* status;
 };
 
-// Bounded wait (see the cache attention): when it gives up, or another role has,
-// the role goes on without waiting, so that every barrier of the block is reached.
-__device__ __forceinline__ bool prod_wait(uint64_t* bar, uint32_t parity, ProdMisc* mi,
-                                          int* status) {
-  const uint32_t addr = smem_u32(bar);
-  if (mbar_try_wait(addr, parity)) return true;
-  volatile int* stop = &mi->abort;
-  const long long t0 = clock64();
-  while (!*stop) {
-    if (mbar_try_wait(addr, parity)) return true;
-    if (clock64() - t0 > kWaitLimitCycles) {
-      set_status(status, ESS_ERR_TIMEOUT);
-      *stop = 1;
-    }
-  }
-  return false;
-}
-__device__ __forceinline__ bool prod_elect() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(p));
-  return p != 0;
-}
 // a block of shared memory to global memory; what lies outside the tensor is left out
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int x, int y) {
   asm volatile(
@@ -258,14 +232,6 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src,
           reinterpret_cast<uint64_t>(m)),
       "r"(src), "r"(x), "r"(y)
       : "memory");
-}
-// Arrive on a barrier of either CTA of a pair.  The default (CTA-scope) release is enough:
-// what it orders are this CTA's reads and writes of TMEM, which tcgen05.wait and
-// tcgen05.fence have put before it.  A cluster-scope release waits for the warp's loads in
-// flight: the scales' fetches then held up every round of four groups (8192 x 4096 x 8192
-// 183 us instead of 153).
-__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // a load into this CTA that counts its bytes on the even CTA's barrier
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m,
@@ -303,23 +269,14 @@ __device__ __forceinline__ uint32_t mx_idesc(uint32_t M, uint32_t N, uint32_t by
 }
 template <bool PAIR>
 __device__ __forceinline__ void prod_commit(uint32_t bar) {   // in both CTAs of a pair
-  if (PAIR)
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-        "[%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-  else
-    umma_commit(bar);
+  if (PAIR) umma_commit_pair(bar);
+  else umma_commit(bar);
 }
 template <bool PAIR>
 __device__ __forceinline__ void prod_alloc(uint32_t dst, uint32_t cols) {
   if (PAIR) {
-    asm volatile(
-        "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
-        "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(dst),
-        "r"(cols)
-        : "memory");
+    tmem_alloc_pair(dst, cols);
+    tmem_relinquish_pair();
   } else {
     tmem_alloc(dst, cols);
     tmem_relinquish();
@@ -327,11 +284,8 @@ __device__ __forceinline__ void prod_alloc(uint32_t dst, uint32_t cols) {
 }
 template <bool PAIR>
 __device__ __forceinline__ void prod_dealloc(uint32_t taddr, uint32_t cols) {
-  if (PAIR)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols)
-                 : "memory");
-  else
-    tmem_dealloc(taddr, cols);
+  if (PAIR) tmem_dealloc_pair(taddr, cols);
+  else tmem_dealloc(taddr, cols);
 }
 // N consecutive columns of this lane
 template <int N>
@@ -489,13 +443,13 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
   auto n_of = [&](int t) { return (PAIR ? t % a.n_tiles : t / a.m_tiles) * BN; };
 
   if (warp == kTmaWarp) {
-    if (prod_elect()) {
+    if (elect_one()) {
       int stage = 0, turn = 0;
       bool ok = true;   // after a wait that gave up nothing more is loaded
       for (int t = sh.first; ok && t < sh.tiles; t += sh.step) {
         const int m0 = m_of(t), n0 = n_of(t) + (PAIR ? static_cast<int>(rank) * kBRows : 0);
         for (int g = sh.g0; g < sh.g1; ++g) {
-          if (turn > 0) ok = prod_wait(&mi->empty[stage], (turn - 1) & 1, mi, a.status);
+          if (turn > 0) ok = wait_or_abort(&mi->empty[stage], (turn - 1) & 1, mi, a.status);
           if (!ok) break;
           const uint32_t dst = smem_u32(smem + stage * kStage), bar = smem_u32(&mi->full[stage]);
           if (PAIR) {
@@ -520,7 +474,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
       // are counted by the even one, which stays until the cluster's last barrier.)
       for (int i = 0; i < kStages; ++i) {
         const int last = i < stage ? turn : turn - 1;   // the stage's last use
-        if (last < 0 || prod_wait(&mi->empty[i], last & 1, mi, a.status)) continue;
+        if (last < 0 || wait_or_abort(&mi->empty[i], last & 1, mi, a.status)) continue;
         const long long t0 = clock64();
         while ((!PAIR || rank == 0) && !mbar_try_wait(smem_u32(&mi->full[i]), last & 1) &&
                clock64() - t0 < kWaitLimitCycles) {
@@ -530,7 +484,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
     __syncwarp();
   } else if (warp == kProdMmaWarp) {
     if (!PAIR || rank == 0) {
-      const bool lead = prod_elect();
+      const bool lead = elect_one();
       int stage = 0, turn = 0, sb = 0, sturn = 0, i = 0;   // i counts sums
       bool ok = true;
       for (int t = sh.first; t < sh.tiles; t += sh.step) {
@@ -540,13 +494,13 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
           if (first) {
             // the accumulator is read out: where two share columns, the part that the sum
             // before shares with it, and so all of the one before that
-            if (kShared && i > 0) ok = prod_wait(&mi->acc_free[0], (i - 1) & 1, mi, a.status) && ok;
+            if (kShared && i > 0) ok = wait_or_abort(&mi->acc_free[0], (i - 1) & 1, mi, a.status) && ok;
             if (kTwo && i > 1)
-              ok = prod_wait(&mi->acc_free[i & 1], ((i >> 1) - 1) & 1, mi, a.status) && ok;
+              ok = wait_or_abort(&mi->acc_free[i & 1], ((i >> 1) - 1) & 1, mi, a.status) && ok;
           }
           if (g == sh.g0 || (g & 3) == 0)
-            ok = prod_wait(&mi->sf_full[sb], sturn & 1, mi, a.status) && ok;
-          ok = prod_wait(&mi->full[stage], turn & 1, mi, a.status) && ok;
+            ok = wait_or_abort(&mi->sf_full[sb], sturn & 1, mi, a.status) && ok;
+          ok = wait_or_abort(&mi->full[stage], turn & 1, mi, a.status) && ok;
           tc_fence_after();
           const bool cells = (g & 3) == 3 || g + 1 == sh.g1;   // done with a buffer of scales
           if (ok && lead) {
@@ -633,7 +587,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
 #pragma unroll
         for (int c = 0; c < kTokCols; ++c)
           x[c] = scale_word(piece(kTok < 32 ? lane % kTok : 32 * c + lane), &bad);
-        if (sturn > 0) prod_wait(&mi->sf_empty[sb], (sturn - 1) & 1, mi, a.status);
+        if (sturn > 0) wait_or_abort(&mi->sf_empty[sb], (sturn - 1) & 1, mi, a.status);
         tc_fence_after();
         if (PAIR) {
           tmem_put<kTokCols>(ts + sb * kSfBuf, x);
@@ -646,7 +600,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (PAIR) mbar_arrive_pair(dsmem_addr(smem_u32(&mi->sf_full[sb]), 0));
+          if (PAIR) mbar_arrive_remote(dsmem_addr(smem_u32(&mi->sf_full[sb]), 0));
           else mbar_arrive(smem_u32(&mi->sf_full[sb]));
         }
         if (++sb == 2) {
@@ -657,7 +611,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
     }
     for (int i = 0; i < 2; ++i) {   // the last arrivals, which nothing else waits for
       const int last = i < sb ? sturn : sturn - 1;
-      if (last >= 0) prod_wait(&mi->sf_empty[i], last & 1, mi, a.status);
+      if (last >= 0) wait_or_abort(&mi->sf_empty[i], last & 1, mi, a.status);
     }
     cp_async_wait<0>();
     if (q == 0 && bad) set_status(a.status, ESS_ERR_DEVICE_CHECK);
@@ -735,7 +689,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
       tc_fence_before();
       __syncwarp();
       if (lane != 0) return;
-      if (PAIR) mbar_arrive_pair(dsmem_addr(smem_u32(&mi->acc_free[kShared ? 0 : i & 1]), 0));
+      if (PAIR) mbar_arrive_remote(dsmem_addr(smem_u32(&mi->acc_free[kShared ? 0 : i & 1]), 0));
       else mbar_arrive(smem_u32(&mi->acc_free[i & 1]));
     };
     int i = 0;   // counts sums
@@ -745,7 +699,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
 #pragma unroll
         for (int c = 0; c < kAcc; ++c) sum[c] = 0.0f;
         for (int g = sh.g0; g < sh.g1; g += kSumGroups, ++i) {
-          prod_wait(&mi->acc_full[i & 1], (i >> 1) & 1, mi, a.status);
+          wait_or_abort(&mi->acc_full[i & 1], (i >> 1) & 1, mi, a.status);
           tc_fence_after();
 #pragma unroll
           for (int b = 0; b < kAcc; b += 16) {
@@ -763,7 +717,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
           else store(t, b, sum + 32 * b);
         }
       } else {
-        prod_wait(&mi->acc_full[i & 1], (i >> 1) & 1, mi, a.status);
+        wait_or_abort(&mi->acc_full[i & 1], (i >> 1) & 1, mi, a.status);
         tc_fence_after();
 #pragma unroll 1
         for (int j = 0; j < kBlocks; ++j) {
@@ -786,7 +740,7 @@ __global__ void __launch_bounds__(kProdThreads, PAIR ? 1 : 2)
   if (!PAIR && parts > 1) {
     // The cluster's CTAs held the same tile's sums over their parts of K: each adds up
     // the tokens [BN rank / parts, BN (rank + 1) / parts), in the order of the parts.
-    prod_wait(&mi->sums_here, 0, mi, a.status);
+    wait_or_abort(&mi->sums_here, 0, mi, a.status);
     const int t0 = static_cast<int>(BN * rank / parts);
     const int share = static_cast<int>(BN * (rank + 1) / parts) - t0;
     const int f = m_of(sh.first) + (tid & 127);
@@ -828,23 +782,10 @@ struct ProdLaunch {
   }
 };
 
-// The kernel's shared memory, allowed once per device.
-template <int BN, bool PAIR, typename Out, bool SUMS>
-cudaError_t allow_prod_smem(int dev) {
-  static std::atomic<unsigned long long> done{0};
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  const cudaError_t e =
-      cudaFuncSetAttribute(product_kernel<BN, PAIR, Out, SUMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(prod_smem(BN, PAIR)));
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
 template <int BN, bool PAIR, typename Out, bool SUMS>
 cudaError_t launch_product(const CUtensorMap& am, const CUtensorMap& bm, const CUtensorMap& om,
                            const ProdArgs& a, int ctas, int cluster, int dev, cudaStream_t st) {
-  const cudaError_t e = allow_prod_smem<BN, PAIR, Out, SUMS>(dev);
+  const cudaError_t e = allow_smem<product_kernel<BN, PAIR, Out, SUMS>>(dev, prod_smem(BN, PAIR));
   if (e != cudaSuccess) return e;
   ProdLaunch l(ctas, cluster, prod_smem(BN, PAIR), st);
   return cudaLaunchKernelEx(&l.cfg, product_kernel<BN, PAIR, Out, SUMS>, am, bm, om, a);
