@@ -591,16 +591,16 @@ __device__ __forceinline__ void row_role(const MlaArgs& a, Misc* mi) {
   }
 }
 
-// Four rows of queries per widening warp into shared memory, all in flight: the latent part as fp16, beside the fp16 latents, each row divided by
-// the power of two that brings its largest value to [2^14, 2^15) (exact down to
-// 2^-31 of that value, with an error below 2^-39 of it under that); the RoPE
-// part, divided alike, as bf16.  A lane takes unit 32 h + 4 (lane % 8) + lane / 8:
-// chunk 8 h + lane % 8, its unit lane / 8; eight lanes then fill the places of one
-// swizzled row.
+// Four rows of queries per widening warp into shared memory, all in flight: the latent
+// part as fp16, beside the fp16 latents, each row divided by the power of two that brings
+// its largest value to [2^14, 2^15) (exact down to 2^-31 of that value, with an error below
+// 2^-39 of it under that); the RoPE part, divided alike, as bf16.  A lane takes unit
+// 32 h + 4 (lane % 8) + lane / 8: chunk 8 h + lane % 8, its unit lane / 8; eight lanes then
+// fill the places of one swizzled row.
 template <bool CHUNK>
 __device__ __forceinline__ void load_queries(const MlaArgs& a, uint8_t* smem, Misc* mi, int v,
                                              int rt, int q0, int warp, int lane, int seg) {
-  constexpr int kRows = kCtaRows / kWidenWarps, kFly = kRows;
+  constexpr int kRows = kCtaRows / kWidenWarps;
   uint8_t* sq = smem + kOffQ;
   int row0 = rt * kPairRows + q0;
   int rows = 0;
@@ -612,50 +612,47 @@ __device__ __forceinline__ void load_queries(const MlaArgs& a, uint8_t* smem, Mi
     first = static_cast<size_t>(c.start) * a.heads;
   }
   const int un = 4 * (lane & 7) + (lane >> 3);
-#pragma unroll 1
-  for (int i0 = 0; i0 < kRows; i0 += kFly) {
-    uint4 u[kFly][2];
-    uint32_t rope[kFly];
+  uint4 u[kRows][2];
+  uint32_t rope[kRows];
 #pragma unroll
-    for (int i = 0; i < kFly; ++i) {
-      const int row = row0 + warp * kRows + i0 + i;
-      u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      rope[i] = 0u;
-      if (row < (CHUNK ? rows : a.entry_rows)) {
-        const uint16_t* q =
-            a.q + ((CHUNK ? first : static_cast<size_t>(v) * a.entry_rows) + row) * kRowDim;
-        u[i][0] = reinterpret_cast<const uint4*>(q)[un];
-        u[i][1] = reinterpret_cast<const uint4*>(q)[32 + un];
-        rope[i] = reinterpret_cast<const uint32_t*>(q + kLatent)[lane];
-      }
+  for (int i = 0; i < kRows; ++i) {
+    const int row = row0 + warp * kRows + i;
+    u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
+    rope[i] = 0u;
+    if (row < (CHUNK ? rows : a.entry_rows)) {
+      const uint16_t* q =
+          a.q + ((CHUNK ? first : static_cast<size_t>(v) * a.entry_rows) + row) * kRowDim;
+      u[i][0] = reinterpret_cast<const uint4*>(q)[un];
+      u[i][1] = reinterpret_cast<const uint4*>(q)[32 + un];
+      rope[i] = reinterpret_cast<const uint32_t*>(q + kLatent)[lane];
     }
+  }
 #pragma unroll
-    for (int i = 0; i < kFly; ++i) {
-      const int r = warp * kRows + i0 + i;
-      float x[16];
-      unpack8(u[i][0], x);
-      unpack8(u[i][1], x + 8);
-      const float ra = bf16_lo(rope[i]), rb = bf16_hi(rope[i]);
-      const float mx = __uint_as_float(__reduce_max_sync(
-          0xffffffffu, __float_as_uint(fmaxf(fmaxf(amax8(x), amax8(x + 8)),
-                                             fmaxf(fabsf(ra), fabsf(rb))))));
-      // 2^e <= mx < 2^(e + 1); rows of zeros, infinities and NaN as they are
-      const int e = mx > 0.0f && mx < INFINITY
-                        ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 - 14
-                        : 0;
-      const int ec = min(max(e, -126), 126);
-      const float inv = exp2i(-ec);
-      if (lane == 0) mi->qexp[seg & 1][r] = static_cast<int8_t>(ec);
+  for (int i = 0; i < kRows; ++i) {
+    const int r = warp * kRows + i;
+    float x[16];
+    unpack8(u[i][0], x);
+    unpack8(u[i][1], x + 8);
+    const float ra = bf16_lo(rope[i]), rb = bf16_hi(rope[i]);
+    const float mx = __uint_as_float(__reduce_max_sync(
+        0xffffffffu, __float_as_uint(fmaxf(fmaxf(amax8(x), amax8(x + 8)),
+                                           fmaxf(fabsf(ra), fabsf(rb))))));
+    // 2^e <= mx < 2^(e + 1); rows of zeros, infinities and NaN as they are
+    const int e = mx > 0.0f && mx < INFINITY
+                      ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 - 14
+                      : 0;
+    const int ec = min(max(e, -126), 126);
+    const float inv = exp2i(-ec);
+    if (lane == 0) mi->qexp[seg & 1][r] = static_cast<int8_t>(ec);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float* y = x + 8 * h;
-        *reinterpret_cast<uint4*>(sq + (4 * h + (lane >> 3)) * kKBlk + sw128_off(r, lane & 7)) =
-            make_uint4(half2_bits(y[0] * inv, y[1] * inv), half2_bits(y[2] * inv, y[3] * inv),
-                       half2_bits(y[4] * inv, y[5] * inv), half2_bits(y[6] * inv, y[7] * inv));
-      }
-      *reinterpret_cast<uint32_t*>(sq + 8 * kKBlk + sw128_off(r, lane >> 2) + (lane & 3) * 4) =
-          bf16x2_bits(ra * inv, rb * inv);
+    for (int h = 0; h < 2; ++h) {
+      const float* y = x + 8 * h;
+      *reinterpret_cast<uint4*>(sq + (4 * h + (lane >> 3)) * kKBlk + sw128_off(r, lane & 7)) =
+          make_uint4(half2_bits(y[0] * inv, y[1] * inv), half2_bits(y[2] * inv, y[3] * inv),
+                     half2_bits(y[4] * inv, y[5] * inv), half2_bits(y[6] * inv, y[7] * inv));
     }
+    *reinterpret_cast<uint32_t*>(sq + 8 * kKBlk + sw128_off(r, lane >> 2) + (lane & 3) * 4) =
+        bf16x2_bits(ra * inv, rb * inv);
   }
   fence_proxy_async_smem();
   __syncwarp();
@@ -1028,9 +1025,9 @@ __device__ __forceinline__ void softmax_role(const MlaArgs& a, uint8_t* smem, Mi
             to_odd[e] = __uint_as_float(odd ? keep[e] : got);
           }
           uint16_t* at = a.out + (orow - odd) * kLatent + d0 + 32 * c + 16 * odd;
-          const int first = row0 + r - odd, rows = CHUNK ? unit.rows : a.entry_rows;
-          if (first < rows) st_global_32(reinterpret_cast<float*>(at), to_even);
-          if (first + 1 < rows) st_global_32(reinterpret_cast<float*>(at + kLatent), to_odd);
+          const int first = row0 + r - odd;
+          if (first < unit.rows) st_global_32(reinterpret_cast<float*>(at), to_even);
+          if (first + 1 < unit.rows) st_global_32(reinterpret_cast<float*>(at + kLatent), to_odd);
           continue;
         }
         float o[32];
