@@ -163,12 +163,13 @@ __device__ __forceinline__ int entry_len(const MlaArgs& a, int v) {
 
 // ---------------------------------------------------------------- chunks
 // (See the head of the file for the tiles.  Measured: 512 new tokens of 32768 x 128 heads
-// 3.36 ms, 1.38 PFLOP/s or 80 % of the measured sustained rate; seven ragged requests with
-// 556 new tokens to 8192 528 us, 1.23 PFLOP/s; lists of 2048 for 320 tokens 188 us; twelve
-// prompts of 20 to 700 tokens 557 us; 16 new tokens of 4096 x 16 heads 19.8 us.  A tile takes
-// 1.95 us and a segment 4 beside its tiles: the last softmax and P V, O's way out, the
-// next queries, during which the tensor cores wait.  Under ncu, 128 new tokens of 8192: the
-// data path of shared memory and L1 72 %, the tensor pipe 53 %, DRAM 1 %.)
+// 3.34 ms, 1.39 PFLOP/s or 81 % of the measured sustained rate; seven ragged requests with
+// 556 new tokens to 8192 528 us, 1.23 PFLOP/s; lists of 2048 for 320 tokens 187 us, with 16
+// heads 167; twelve prompts of 20 to 700 tokens 557 us; 16 new tokens of 4096 x 16 heads
+// 19.8 us; 1000 requests of 3 new tokens of 70 x 16 heads 98 us.  A tile takes 1.95 us and a
+// segment 4 beside its tiles: the last softmax and P V, O's way out, the next queries,
+// during which the tensor cores wait.  Under ncu, 128 new tokens of 8192: the data path of
+// shared memory and L1 72 %, the tensor pipe 53 %, DRAM 1 %.)
 //
 // Requests with any number of new tokens each (CHUNK).  Request b's queries are the rows
 // [start, start + n) x heads of q, its newest tokens.  What a segment belongs to is a
@@ -255,7 +256,8 @@ struct UnitWalk {
   }
 };
 constexpr int kMaxChunkBatch = 32768;
-static_assert((kMaxChunkBatch + 1) * sizeof(int) <= kOffMisc, "the first units, in the operands' place");
+static_assert((kMaxChunkBatch + 1) * sizeof(int) <= kOffMisc,
+              "the first units, in the operands' place");
 
 // The deal counts tiles and segments in one 64-bit sum, tiles below this bit and segments
 // above it.  Entries are at most 65535 requests x 4 segments, of 2^24 tiles each.  Chunks

@@ -25,12 +25,13 @@
 // accumulators of 256 columns and the scales need 536 of 512, so they share 32, which are
 // read first.  Few such tiles, and fp32 results, take 128 columns.
 //
-// Measured (time; flops or the bytes that the call cannot do without / time): 8192 x 4096 x
-// 8192 (tokens x ins x outs) 153 us, 3.6 PFLOP/s or 93 % of twice the measured bf16 rate (a
-// library's product with the same form of scales takes 151); in fp32 209; 8192 x 1024 x
-// 24576 135, 2048 x 4096 x 8192 44, 512 x 4096 x 8192 15.8, 128 x 4096 x 8192 11.9, 333 x 4112
-// x 1601 12.9, 64 x 4096 x 8192 9.5, 32 x 1024 x 24576 6.8 (4.0 TB/s), 4 x 4096 x 1600 4.1; a
-// launch that multiplies 16 x 128 x 128 2.9.
+// Measured, back to back on one set of inputs for a few milliseconds, so that L2 holds
+// weights and codes (time; flops): 8192 x 4096 x 8192 (tokens x ins x outs) 148 to 153 us, 3.6
+// PFLOP/s or 93 % of twice the measured bf16 rate (a library's product with the same form of
+// scales takes 151); in fp32 208 to 225; 8192 x 1024 x 24576 131 to 138, 2048 x 4096 x 8192 44,
+// 512 x 4096 x 8192 15.9, 128 x 4096 x 8192 11.8, 333 x 4112 x 1601 12.9, 64 x 4096 x 8192 9.5, 32 x
+// 1024 x 24576 6.4 to 6.8, 4 x 4096 x 1600 4.1; a launch that multiplies 16 x 128 x 128 2.9.  The
+// first one on end, at the power limit: 174 to 186 us, 86 to 92 % of twice the sustained rate.
 // What bounds them: a large product the tensor pipe, busy for 78 % of an SM's cycles under
 // ncu at 2048 tokens (L2 35 %, its crossbar 41 %, shared memory's banks 17 %), with some
 // 1000 cycles between two tiles; seconds on end the power limit.  Rows of K that are not
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const QuantAr
 }
 
 // One CTA a block of 128 x 128: eight lanes a row, 32 rows at a time.  16384 x 4096 take
-// 37.2 us (5.4 TB/s), 1600 x 4096 3.0; with 512 threads 39.7, with 1024 45.9: all of a
+// 36.7 us (5.5 TB/s), 1600 x 4096 (from L2) 2.9; with 512 threads 39.7, with 1024 45.9: all of a
 // block is loaded before any of it leaves, so several small CTAs an SM do better.
 __global__ void __launch_bounds__(kQuantThreads) quant_square_kernel(const QuantArgs a) {
   __shared__ float part[kQuantThreads / 32];
